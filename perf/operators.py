@@ -109,8 +109,8 @@ def work(case):
         return {"bytes": T * (H * es * (4 if case["residual"] else 3) + 4) + H * (es + 4), "flops": 10 * T * H}
     V = case["V"]
     if op == "logprob":
-        return {"bytes": T * (V * es + 8 + 12 + 12 * case["k"]), "flops": 6 * T * V}
-    return {"bytes": T * (2 * V * es + 8 + 16), "flops": 8 * T * V}
+        return {"bytes": T * (V * es + 8 + 24 + 12 * case["k"]), "flops": 6 * T * V}
+    return {"bytes": T * (2 * V * es + 8 + 20), "flops": 8 * T * V}
 
 
 # ---------------------------------------------------------------------------- inputs
@@ -168,14 +168,13 @@ def prepare(case, seed):
         s["scale_b"] = 0.001 + 0.002 * torch.rand(N, generator=g, device=dev)
     else:
         s["logits"], s["tokens"] = _logits(case, g, dev)
-        if op == "logprob_grad":
-            m = s["logits"].amax(-1).float().clamp_min(torch.finfo(torch.float32).min)
-            t = s["logits"].float() - m[:, None]
+        if op == "logprob_grad":             # what the forward call left: each row's peak, log z and entropy
+            peak = s["logits"].amax(-1).float()
+            t = s["logits"].float() - peak.clamp_min(torch.finfo(torch.float32).min)[:, None]
             e = t.exp()
             z = e.sum(-1)
-            s["lse"] = m + z.log()
-            s["entropy"] = torch.where(z > 0, z.log() - (e * t.clamp_min(-1e4)).sum(-1) / z, 0.0)
-            s["lse"] = torch.where(z > 0, s["lse"], -math.inf)
+            entropy = torch.where(z > 0, z.log() - (e * t.clamp_min(-1e4)).sum(-1) / z, 0.0)
+            s["stats"] = torch.stack([peak, z.log(), entropy], 1)
             s["grad_logprob"] = -torch.rand(case["T"], generator=g, device=dev)      # weights of a summed loss
             s["grad_entropy"] = 0.1 * randn(case["T"])
     return s
@@ -224,31 +223,33 @@ def _plain_logprob(s):
     e = t.exp()
     z = e.sum(-1)
     some = z > 0
-    lse = torch.where(some, m + z.log(), -math.inf)
-    entropy = torch.where(some, z.log() - (e * t.clamp_min(-1e4)).sum(-1) / z, 0.0)
-    del t, e
+    logz = z.log()
+    entropy = torch.where(some, logz - (e * t.clamp_min(-1e4)).sum(-1) / z, 0.0)
+    del e
     keep = s["tokens"] != _IGNORE
-    at = x.gather(1, torch.where(keep, s["tokens"], 0)[:, None])[:, 0]
-    logprob = torch.where(keep, torch.where(some, at - lse, -math.inf), 0.0)
+    at = t.gather(1, torch.where(keep, s["tokens"], 0)[:, None])[:, 0]
+    logprob = torch.where(keep, torch.where(some, at - logz, -math.inf), 0.0)
+    stats = torch.stack([x.amax(-1), logz, entropy], 1)
     # one 64-bit key for each logit: its order among floats above, the lower index first below
     bits = (x + 0.0).view(torch.int32)
     order = torch.where(bits < 0, bits ^ 0x7FFFFFFF, bits).to(torch.int64)
     key = order * (1 << 32) + ((1 << 31) - 1 - torch.arange(V, device=x.device))
     top = key.topk(k, dim=-1).values
     ids = (1 << 31) - 1 - (top & 0xFFFFFFFF)
-    lead = torch.where(some[:, None], x.gather(1, ids) - lse[:, None], -math.inf)
-    return logprob, entropy, lse, lead, ids
+    lead = torch.where(some[:, None], t.gather(1, ids) - logz[:, None], -math.inf)
+    return logprob, entropy, torch.where(some, m + logz, -math.inf), stats, lead, ids
 
 
 def _plain_logprob_grad(s):
     x = s["logits"].float()
     V = x.shape[1]
-    some = (s["lse"] > -math.inf)[:, None]
-    lp = torch.where(some, x - s["lse"][:, None], -math.inf)
+    peak, logz, entropy = (c[:, None] for c in s["stats"].unbind(1))
+    some = peak > -math.inf
+    lp = torch.where(some, x - peak - logz, -math.inf)
     p = lp.exp()
     g = torch.where(s["tokens"] != _IGNORE, s["grad_logprob"], 0.0)[:, None]
     hot = (torch.arange(V, device=x.device) == s["tokens"][:, None]) & some
-    out = g * (hot.float() - p) - s["grad_entropy"][:, None] * p * (lp.clamp_min(-1e4) + s["entropy"][:, None])
+    out = g * (hot.float() - p) - s["grad_entropy"][:, None] * p * (lp.clamp_min(-1e4) + entropy)
     return out.to(s["logits"].dtype)
 
 
@@ -277,7 +278,7 @@ def run(state):
         if op == "int8":
             return {"out": _plain_int8(s)}
         if op == "logprob":
-            logprob, entropy, lse, lead, ids = _plain_logprob(s)
+            logprob, entropy, lse, stats, lead, ids = _plain_logprob(s)
         else:
             return {"grad_logits": _plain_logprob_grad(s)}
     else:
@@ -293,13 +294,13 @@ def run(state):
             return {"out": fw.int8_scaled_mm(s["a"], s["w"].t(), s["scale_a"], s["scale_b"],
                                              out_dtype=_DT[case["dtype"]])}
         if op == "logprob":
-            logprob, entropy, lse, lead, ids = fw.token_logprobs(s["logits"], s["tokens"], top_k=case["k"],
-                                                                 ignore_index=_IGNORE)
+            logprob, entropy, lse, stats, lead, ids = fw.token_logprobs(s["logits"], s["tokens"], top_k=case["k"],
+                                                                        ignore_index=_IGNORE)
         else:
-            return {"grad_logits": fw.token_logprobs_backward(s["logits"], s["tokens"], s["lse"], s["entropy"],
+            return {"grad_logits": fw.token_logprobs_backward(s["logits"], s["tokens"], s["stats"],
                                                               s["grad_logprob"], s["grad_entropy"],
                                                               ignore_index=_IGNORE)}
-    out = {"logprob": logprob, "entropy": entropy, "lse": lse}
+    out = {"logprob": logprob, "entropy": entropy, "lse": lse, "stats": stats}
     if case["k"] > 0:
         out["top_logprobs"], out["top_ids"] = lead, ids
     return out
@@ -357,18 +358,20 @@ def exact(case, seed):
         pad = s["tokens"] == _IGNORE
         at = x[torch.arange(case["T"], device=x.device), s["tokens"].masked_fill(pad, 0)]
         logprob = (at - lse).masked_fill(empty, -math.inf).masked_fill(pad, 0.0)
-        out = {"logprob": logprob, "entropy": entropy, "lse": lse}
+        peak = torch.max(x, dim=1).values
+        out = {"logprob": logprob, "entropy": entropy, "lse": lse,
+               "stats": torch.stack([peak, (lse - peak).masked_fill(empty, -math.inf), entropy], dim=1)}
         if case["k"] > 0:
             lead = torch.topk(x, case["k"], dim=1).values - lse.unsqueeze(1)
             out["top_logprobs"] = lead.masked_fill(empty.unsqueeze(1), -math.inf)
             out["top_ids"] = None
         return out
     # d logprob / d x_v = [v = token] - p_v;  d entropy / d x_v = -p_v (log p_v + entropy)
-    lp = x - s["lse"].to(f64).unsqueeze(1)
-    p = torch.exp(lp)
+    peak, logz, entropy = s["stats"].to(f64).unsqueeze(2).unbind(1)
+    p = torch.exp(x - peak - logz)
     pad = s["tokens"] == _IGNORE
     gl = s["grad_logprob"].to(f64).masked_fill(pad, 0.0)
-    part = torch.special.entr(p) - p * s["entropy"].to(f64).unsqueeze(1)
+    part = torch.special.entr(p) - p * entropy
     gx = part * s["grad_entropy"].to(f64).unsqueeze(1) - gl.unsqueeze(1) * p
     rows = torch.arange(case["T"], device=x.device)
     gx[rows, s["tokens"].masked_fill(pad, 0)] += gl
