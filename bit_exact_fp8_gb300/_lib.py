@@ -23,11 +23,18 @@ EMU_OUT_F16 = 2
 EMU_OUT_E4M3FN = 3
 EMU_OUT_E5M2 = 4
 
+EMU_Q_E4M3FN = 0
+EMU_Q_E5M2 = 1
+EMU_Q_INT8 = 2
+
 #: every symbol include/emu_fp8.h declares
 EXPORTED = ("emu_preset_get", "emu_workspace_bytes", "emu_scaled_mm", "emu_last_error",
             "emu_abi_version", "emu_scaled_mm_noalloc", "emu_device_status",
             "emu_selftest_wait_timeout", "emu_scaled_mm_ex", "emu_host_staging_bytes",
-            "emu_scaled_mm_host", "emu_tile_for", "emu_tc_selftest")
+            "emu_scaled_mm_host", "emu_tile_for", "emu_tc_selftest", "emu_rms_norm_quant",
+            "emu_rms_norm_backward_workspace_bytes", "emu_rms_norm_backward",
+            "emu_int8_workspace_bytes", "emu_int8_scaled_mm", "emu_token_logprobs",
+            "emu_token_logprobs_backward", "emu_ops_last_error", "emu_ops_device_status")
 
 #: size of the static scratch of emu_scaled_mm_noalloc (EMU_NOALLOC_SCRATCH_BYTES)
 EMU_NOALLOC_SCRATCH_BYTES = 4 << 20
@@ -93,6 +100,26 @@ def load(path: str = LIB) -> ctypes.CDLL:
                                ctypes.c_int32, ctypes.POINTER(emu_preset_t), ctypes.c_int32,
                                ctypes.c_char_p, ctypes.c_size_t]
     L.emu_tile_for.restype = ctypes.c_int
+    # the operators around the product: called by ops.py with addresses and sizes as ints
+    I, I64, Z, F = ctypes.c_int, ctypes.c_int64, ctypes.c_size_t, ctypes.c_float
+    L.emu_rms_norm_quant.argtypes = [P, I64, P, I64, P, I, I, I64, I64, F, P, I, P, P, P, I64, P, P]
+    L.emu_rms_norm_quant.restype = I
+    L.emu_rms_norm_backward_workspace_bytes.argtypes = [I64, I64]
+    L.emu_rms_norm_backward_workspace_bytes.restype = Z
+    L.emu_rms_norm_backward.argtypes = [P, I64, P, I64, P, P, I, P, I64, I, I64, I64, P, P, P, Z, P]
+    L.emu_rms_norm_backward.restype = I
+    L.emu_int8_workspace_bytes.argtypes = [I64, I64, I64]
+    L.emu_int8_workspace_bytes.restype = Z
+    L.emu_int8_scaled_mm.argtypes = [P, I64, P, I64, I64, I64, I64, P, I64, P, I64, P, I, P, Z, P]
+    L.emu_int8_scaled_mm.restype = I
+    L.emu_token_logprobs.argtypes = [P, I64, I, P, I64, I64, ctypes.c_int32, I64, P, P, P, P, P, P, P]
+    L.emu_token_logprobs.restype = I
+    L.emu_token_logprobs_backward.argtypes = [P, I64, I, P, I64, I64, I64, P, P, P, P, I64, P]
+    L.emu_token_logprobs_backward.restype = I
+    L.emu_ops_last_error.argtypes = []
+    L.emu_ops_last_error.restype = ctypes.c_char_p
+    L.emu_ops_device_status.argtypes = [ctypes.POINTER(ctypes.c_int32), ctypes.c_int32]
+    L.emu_ops_device_status.restype = I
     L.emu_last_error.argtypes = []
     L.emu_last_error.restype = ctypes.c_char_p
     L.emu_abi_version.argtypes = []
@@ -115,6 +142,19 @@ def emu_workspace_bytes(M: int, N: int, split_S: int) -> int:
 
 def emu_last_error() -> str:
     return load().emu_last_error().decode(errors="replace")
+
+
+def emu_ops_last_error() -> str:
+    return load().emu_ops_last_error().decode(errors="replace")
+
+
+def emu_ops_device_status(reset: bool = False) -> int:
+    """The operators' device status word (0 ok, 1 a bounded wait gave up); synchronous."""
+    v = ctypes.c_int32(0)
+    st = load().emu_ops_device_status(ctypes.byref(v), int(bool(reset)))
+    if st != EMU_OK:
+        raise RuntimeError(f"emu_ops_device_status failed: {emu_ops_last_error()}")
+    return int(v.value)
 
 
 def emu_abi_version() -> int:

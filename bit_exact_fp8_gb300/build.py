@@ -3,8 +3,9 @@ microbenchmark bench.py divides by) in-tree with nvcc for sm_103a (GB300).
 
     python -m bit_exact_fp8_gb300.build [--force]
 
-One translation unit per library, one -gencode, no cmake; the two compile in
-parallel, and each is rebuilt only when one of its sources or headers is newer.
+One -gencode, no cmake; the two libraries and the GEMM library's translation units
+compile in parallel, and each library is rebuilt only when one of its sources or
+headers is newer.
 """
 from __future__ import annotations
 
@@ -19,14 +20,15 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libemufp8.so")
 PEAKS_LIB = os.path.join(PKG, "libemupeaks.so")
-SOURCES = [os.path.join(CSRC, "emu_api.cu")]
+SOURCES = [os.path.join(CSRC, f) for f in ("emu_api.cu", "ops_norm.cu", "ops_int8.cu",
+                                           "ops_logprob.cu")]
 PEAKS_SOURCES = [os.path.join(CSRC, "emu_peaks.cu")]
 PEAKS_DEPS = PEAKS_SOURCES + [os.path.join(INCLUDE, "emu_peaks.h")]
 DEPS = SOURCES + [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cuh", ".h"))] \
     + [os.path.join(INCLUDE, "emu_fp8.h")]
 
 NVCC_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a", "-O3", "-lineinfo", "-std=c++17",
-              "-Xcompiler", "-fPIC", "-shared", "-I" + INCLUDE, "-I" + CSRC]
+              "-Xcompiler", "-fPIC", "-shared", "--threads", "0", "-I" + INCLUDE, "-I" + CSRC]
 
 
 def nvcc_path() -> str:

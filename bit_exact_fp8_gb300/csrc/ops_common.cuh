@@ -1,0 +1,77 @@
+// ops_common.cuh -- what the operators around the 8-bit product share: element types,
+// 16-byte loads, warp reductions, and the host side's errors and checks.  (The GEMM's own
+// header holds kernels that belong to one translation unit, so nothing is taken from it.)
+#pragma once
+
+#include "emu_fp8.h"
+
+#include <cstdint>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+// host side (ops_norm.cu): records the message emu_ops_last_error returns; gives `code`
+int emu_ops_fail(int code, const char* fmt, ...) __attribute__((format(printf, 2, 3)));
+void emu_ops_begin();                          // clears the message and a stale launch error
+int emu_ops_launched(const char* what);        // EMU_OK, or EMU_ECUDA with the launch's error
+int emu_ops_sm_count();                        // SMs of the current device
+int emu_ops_device_status_int8(int* status, bool reset);   // ops_int8.cu
+
+namespace emu_ops {
+
+inline bool aligned(const void* p, size_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
+inline size_t elem_bytes(emu_out_t t) { return t == EMU_OUT_F32 ? 4 : 2; }
+inline bool is_float_type(emu_out_t t) { return t == EMU_OUT_F32 || t == EMU_OUT_BF16 || t == EMU_OUT_F16; }
+
+// rows x cols elements of `esz` bytes, rows `ld` elements apart: the bytes they span
+struct Span {
+  uintptr_t lo, hi;
+  Span(const void* p, int64_t rows, int64_t ld, int64_t cols, size_t esz)
+      : lo(reinterpret_cast<uintptr_t>(p)), hi(lo) {
+    if (p && rows > 0 && cols > 0) hi = lo + ((size_t)(rows - 1) * (size_t)ld + (size_t)cols) * esz;
+  }
+  bool meets(const Span& o) const { return lo < o.hi && o.lo < hi; }
+};
+
+__device__ __forceinline__ float to_f(float v) { return v; }
+__device__ __forceinline__ float to_f(__nv_bfloat16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ float to_f(__half v) { return __half2float(v); }
+template <class T> __device__ __forceinline__ T from_f(float v);
+template <> __device__ __forceinline__ float from_f<float>(float v) { return v; }
+template <> __device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
+template <> __device__ __forceinline__ __half from_f<__half>(float v) { return __float2half_rn(v); }
+
+// VEC elements loaded or stored at once (VEC * sizeof(T) = 16 bytes, or one element)
+template <class T, int VEC> struct alignas(sizeof(T) * VEC) Pack {
+  T v[VEC];
+};
+template <class T, int VEC> __device__ __forceinline__ void load_f(const T* p, float (&f)[VEC]) {
+  const Pack<T, VEC> q = *reinterpret_cast<const Pack<T, VEC>*>(p);
+#pragma unroll
+  for (int i = 0; i < VEC; ++i) f[i] = to_f(q.v[i]);
+}
+template <class T, int VEC> __device__ __forceinline__ void store_f(T* p, const float (&f)[VEC]) {
+  Pack<T, VEC> q;
+#pragma unroll
+  for (int i = 0; i < VEC; ++i) q.v[i] = from_f<T>(f[i]);
+  *reinterpret_cast<Pack<T, VEC>*>(p) = q;
+}
+
+// the larger of two, NaN if either is NaN
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+  return v;
+}
+__device__ __forceinline__ float warp_max_nan(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v = max_nan(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
+  return v;
+}
+
+}  // namespace emu_ops

@@ -288,6 +288,120 @@ int emu_selftest_wait_timeout(void* stream);
  */
 int emu_tc_selftest(uint32_t* mismatches);
 
+/*
+ * ---- Operators around an 8-bit product.  (Additions of this library; the pages have no
+ * counterpart: they describe the product alone.)  What makes its 8-bit operand (RMS norm
+ * with the residual's addition), the product of the other 8-bit type, and what reads the
+ * logits that a model's last product leaves; each with its gradient where training needs
+ * one.  As everywhere here, arguments are checked on the host before any launch, nothing
+ * allocates or synchronises, the work is enqueued on the caller's stream, results do not
+ * depend on what outputs and workspaces held before, and a call may be captured in a CUDA
+ * graph.  All results are the same from run to run.  Errors leave their message in
+ * emu_ops_last_error.  Tensors are row-major with the given row strides (in elements);
+ * any alignment of whole elements is accepted, 16-byte alignment of rows is faster.
+ */
+
+/* 8-bit formats of a quantised output: the two FP8 formats, and signed integers. */
+typedef enum { EMU_Q_E4M3FN = 0, EMU_Q_E5M2 = 1, EMU_Q_INT8 = 2 } emu_q_t;
+
+/*
+ * RMS norm of T rows of H values with an 8-bit output:
+ *   h = x + residual (fp32; residual NULL: h = x),  rstd = 1 / sqrt(mean(h^2) + eps),
+ *   y = h * rstd * weight,  q = y / scale rounded to nearest even and saturated.
+ *
+ *   x, residual   [T,H] of `type` (fp32, bf16 or fp16), rows ldx and ldr elements apart
+ *   weight        [H], of `type` or fp32 (weight_type)
+ *   scale         device pointer to one fp32, the scale of every row (what emu_scaled_mm
+ *                 takes as scale_a); or NULL: each row's own, max|y| / qmax but at least
+ *                 2^-126, written to scale_out [T] (qmax: 448, 57344 or 127)
+ *   q             [T,H] codes, contiguous
+ *   residual_out  [T,H] of `type`, rows ldo apart: h rounded once; NULL: not wanted.  May
+ *                 be x or residual itself, and may not overlap them otherwise
+ *   rstd          [T] fp32, for the gradient
+ * Sums are fp32.  |h * weight| has to stay within fp32's normal range (or be 0), and so has
+ * a given scale.  A row holding NaN or Inf
+ * gives NaN for its own scale and codes of NaN or 0 (a NaN becomes FP8's NaN, int8's 0),
+ * and touches no other row.  Sizes: T < 2^31, 1 <= H <= 2^22.
+ */
+int emu_rms_norm_quant(const void* x, int64_t ldx, const void* residual, int64_t ldr,
+                       const void* weight, emu_out_t weight_type, emu_out_t type,
+                       int64_t T, int64_t H, float eps, const float* scale, emu_q_t q_format,
+                       void* q, float* scale_out, void* residual_out, int64_t ldo, float* rstd,
+                       void* stream);
+
+/*
+ * Gradient of y = h * rstd * weight, straight through the 8-bit rounding, given grad_y and
+ * (NULL: none) the gradient grad_residual that reaches h by the residual stream:
+ *   g = grad_y * weight,
+ *   grad_x = rstd * (g - h * rstd^2 * mean(g * h)) + grad_residual,
+ *   grad_weight = sum over the rows of grad_y * h * rstd    (fp32 [H], written, not added)
+ * hidden is h as the forward call stored it (x where there was no residual); grad_x [T,H]
+ * (contiguous, of `type`) is the gradient of x and of residual alike, and may not overlap
+ * an input.  workspace: emu_rms_norm_backward_workspace_bytes(T, H), 16-byte aligned.
+ */
+size_t emu_rms_norm_backward_workspace_bytes(int64_t T, int64_t H);
+int emu_rms_norm_backward(const void* grad_y, int64_t ldy, const void* hidden, int64_t ldh,
+                          const float* rstd, const void* weight, emu_out_t weight_type,
+                          const void* grad_residual, int64_t ldg, emu_out_t type,
+                          int64_t T, int64_t H, void* grad_x, float* grad_weight,
+                          void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * out[M,N] = (fp32(A @ B) * scale_a[m]) * scale_b[n] of signed 8-bit integers: the sums are
+ * exact in 32 bits, converted to fp32 and scaled in this order, then rounded to out_dtype
+ * (fp32, bf16, fp16).
+ *   A  [M,K] row-major, rows lda apart;  B  [K,N] column-major, columns ldb apart (the
+ *      w.t() of a row-major [N,K] weight);  scale_a M values or one, scale_b N or one
+ *   out [M,N] contiguous
+ *   workspace: emu_int8_workspace_bytes(M, N, K) bytes, 256-byte aligned (NULL where 0)
+ * Sizes: M, N < 2^31, K <= 131071 (EMU_EUNSUPPORTED above: the sums could overflow).
+ * K == 0 gives zeros times the scales.
+ */
+size_t emu_int8_workspace_bytes(int64_t M, int64_t N, int64_t K);
+int emu_int8_scaled_mm(const int8_t* A, int64_t lda, const int8_t* B, int64_t ldb,
+                       int64_t M, int64_t N, int64_t K, const float* scale_a, int64_t scale_a_count,
+                       const float* scale_b, int64_t scale_b_count, void* out, emu_out_t out_dtype,
+                       void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Log probabilities of given tokens, with the entropy and the top_k alternatives of each
+ * of T rows of V logits (type fp32, bf16 or fp16, rows ldx apart):
+ *   lse = log sum_v e^x_v,  logprob = x[token] - lse,  entropy = -sum_v p_v log p_v,
+ *   top_logprobs, top_ids [T,top_k]: the largest log probabilities in falling order and
+ *   where they are (equal logits: the lower id first)
+ *   stats [T,3]: for the gradient, the row's largest logit m, log sum_v e^(x_v - m), entropy
+ * all fp32, ids int64; 0 <= top_k <= 32 (and <= V).  tokens: int64; a token equal to
+ * ignore_index has logprob 0, any other one outside [0, V) has NaN.  -inf logits have
+ * probability 0.  A row of nothing but -inf has lse, logprob and top_logprobs -inf and
+ * entropy 0; a row holding NaN or +inf has NaN for all of them and -1 for its ids.
+ */
+int emu_token_logprobs(const void* logits, int64_t ldx, emu_out_t type, const int64_t* tokens,
+                       int64_t T, int64_t V, int32_t top_k, int64_t ignore_index, float* logprob,
+                       float* entropy, float* lse, float* stats, float* top_logprobs,
+                       int64_t* top_ids, void* stream);
+
+/*
+ * Gradient of the above by the logits, of their type, rows ldo apart:
+ *   grad_logits = grad_logprob ([v = token] - p) - grad_entropy p (log p + entropy)
+ * grad_logprob and grad_entropy [T] fp32 (either may be NULL: zero); stats as the forward
+ * call gave them.  Rows of ignored tokens get
+ * the entropy's part alone, empty rows zeros, rows of tokens outside [0, V) NaN.
+ * grad_logits may be the logits themselves, and may not overlap them otherwise.
+ */
+int emu_token_logprobs_backward(const void* logits, int64_t ldx, emu_out_t type,
+                                const int64_t* tokens, int64_t T, int64_t V, int64_t ignore_index,
+                                const float* stats, const float* grad_logprob,
+                                const float* grad_entropy, void* grad_logits, int64_t ldo,
+                                void* stream);
+
+/* Message of the last error an operator above returned on the calling host thread. */
+const char* emu_ops_last_error(void);
+
+/* Device status of the operators above on the current device, as emu_device_status gives
+   it for the FP8 product: *status = 0, or 1 when a kernel's bounded wait gave up.
+   Synchronous. */
+int emu_ops_device_status(int32_t* status, int32_t reset);
+
 /* Message of the last error returned on the calling host thread ("" if none). */
 const char* emu_last_error(void);
 
