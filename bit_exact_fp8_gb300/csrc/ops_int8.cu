@@ -5,14 +5,24 @@
 // kernel that took it.
 #include "ops_common.cuh"
 
+#include <cuda.h>             // CUtensorMap (the type only; the driver is called through an entry point)
+#include <cudaTypedefs.h>
+
+#include <atomic>
+#include <mutex>
+
 namespace emu_ops {
+
+// 1 once a bounded wait of the pipeline gave up (the outputs of that call are not valid)
+__device__ int g_ops_status = 0;
 
 constexpr int64_t kInt8MaxK = 131071;             // K * 128 * 128 < 2^31
 
 struct Int8Params {
   const int8_t* a; int64_t lda;                   // [M, K]
   const int8_t* b; int64_t ldb;                   // [N, K]
-  int64_t M, N;
+  int64_t M, N;                                   // N: also the output's row stride
+  int64_t cols;                                   // columns of B here (a slab of the N)
   int K;
   const float* scale_a; int sa_step;              // 0: one scale for all
   const float* scale_b; int sb_step;
@@ -34,40 +44,26 @@ __device__ __forceinline__ int dot16(const uint4& a, const uint4& b, int acc) {
   return __dp4a((int)a.w, (int)b.w, acc);
 }
 
-// A warp takes MT rows by NT columns, its lanes 16 codes of K each in turn (one code where
-// rows are not 16-byte aligned), and adds the lanes' sums up.
-template <int MT, int NT, bool VEC>
+// One token, or a few: a warp takes MT rows by NT columns, its lanes 16 codes of K each in turn,
+// and adds the lanes' sums up.  Bound by reading B once.
+template <int MT, int NT>
 __global__ void __launch_bounds__(128)
 int8_dot_kernel(const Int8Params p) {
   const int lane = threadIdx.x & 31;
   const int64_t n0 = ((int64_t)blockIdx.x * 4 + (threadIdx.x >> 5)) * NT;
   if (n0 >= p.N) return;
-  for (int64_t m0 = (int64_t)blockIdx.y * MT; m0 < p.M; m0 += (int64_t)gridDim.y * MT) {
+  for (int64_t m0 = 0; m0 < p.M; m0 += MT) {
     int acc[MT][NT] = {};
-    if constexpr (VEC) {
-      for (int k = lane * 16; k < p.K; k += 512) {
-        uint4 b[NT];
+    for (int k = lane * 16; k < p.K; k += 512) {
+      uint4 b[NT];
 #pragma unroll
-        for (int j = 0; j < NT; ++j)
-          b[j] = *reinterpret_cast<const uint4*>(p.b + (n0 + j < p.N ? n0 + j : p.N - 1) * p.ldb + k);
+      for (int j = 0; j < NT; ++j)
+        b[j] = *reinterpret_cast<const uint4*>(p.b + (n0 + j < p.N ? n0 + j : p.N - 1) * p.ldb + k);
 #pragma unroll
-        for (int i = 0; i < MT; ++i) {
-          const uint4 a = *reinterpret_cast<const uint4*>(p.a + (m0 + i < p.M ? m0 + i : p.M - 1) * p.lda + k);
+      for (int i = 0; i < MT; ++i) {
+        const uint4 a = *reinterpret_cast<const uint4*>(p.a + (m0 + i < p.M ? m0 + i : p.M - 1) * p.lda + k);
 #pragma unroll
-          for (int j = 0; j < NT; ++j) acc[i][j] = dot16(a, b[j], acc[i][j]);
-        }
-      }
-    } else {
-      for (int k = lane; k < p.K; k += 32) {
-        int b[NT];
-#pragma unroll
-        for (int j = 0; j < NT; ++j) b[j] = p.b[(n0 + j < p.N ? n0 + j : p.N - 1) * p.ldb + k];
-#pragma unroll
-        for (int i = 0; i < MT; ++i) {
-          const int a = p.a[(m0 + i < p.M ? m0 + i : p.M - 1) * p.lda + k];
-#pragma unroll
-          for (int j = 0; j < NT; ++j) acc[i][j] += a * b[j];
-        }
+        for (int j = 0; j < NT; ++j) acc[i][j] = dot16(a, b[j], acc[i][j]);
       }
     }
 #pragma unroll
@@ -80,29 +76,394 @@ int8_dot_kernel(const Int8Params p) {
   }
 }
 
-template <bool VEC> void launch_dot(const Int8Params& p, cudaStream_t st) {
+template <int MT> int launch_dot(const Int8Params& p, cudaStream_t st) {
   constexpr int NT = 4;
-  const unsigned gx = (unsigned)((p.N + 4 * NT - 1) / (4 * NT));
-  const int64_t tiles = (p.M + 7) / 8;
-  const unsigned gy = (unsigned)(tiles < 65535 ? tiles : 65535);
-  if (p.M == 1) int8_dot_kernel<1, NT, VEC><<<dim3(gx, 1), 128, 0, st>>>(p);
-  else int8_dot_kernel<8, NT, VEC><<<dim3(gx, gy), 128, 0, st>>>(p);
+  int8_dot_kernel<MT, NT><<<(unsigned)((p.N + 4 * NT - 1) / (4 * NT)), 128, 0, st>>>(p);
+  return EMU_OK;
+}
+
+__device__ __forceinline__ uint32_t smem_addr(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
+
+// Four codes as fp16 (exact: |code| <= 128 has at most eight significant bits).  With the sign
+// bit flipped a code is u = code + 128 in 0..255; the fp16 word 0x6400 | u is 1024 + u.
+__device__ __forceinline__ void codes_to_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  const uint32_t u = w ^ 0x80808080u;
+  const __half2 bias = __half2half2(__ushort_as_half(0x6480));          // 1152
+  uint32_t a = __byte_perm(u, 0x64646464u, 0x4140), b = __byte_perm(u, 0x64646464u, 0x4342);
+  const __half2 x = __hsub2(*reinterpret_cast<__half2*>(&a), bias), y = __hsub2(*reinterpret_cast<__half2*>(&b), bias);
+  lo = *reinterpret_cast<const uint32_t*>(&x);
+  hi = *reinterpret_cast<const uint32_t*>(&y);
+}
+
+// ---------------------------------------------------------------------------------------
+// Rows copied to 16-byte aligned rows of `ldo` codes, zeros after the K-th: for operands whose
+// rows the vector kernels cannot read as they are.  One warp a row and step.
+__global__ void __launch_bounds__(256)
+int8_align_kernel(const int8_t* in, int64_t ld, int64_t rows, int K, int8_t* out, int64_t ldo) {
+  const int words = (int)(ldo / 4);
+  for (int64_t row = blockIdx.x; row < rows; row += gridDim.x) {
+    const int8_t* r = in + row * ld;
+    for (int i = threadIdx.x; i < words; i += 256) {
+      uint32_t w = 0;
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (4 * i + j < K) w |= (uint32_t)(uint8_t)r[4 * i + j] << (8 * j);
+      reinterpret_cast<uint32_t*>(out + row * ldo)[i] = w;
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------------------
+// A few to a few hundred tokens: fp16 warp products of the codes.  mma.sync on int8 runs at
+// the rate of the dp4a instruction here (75 TMAC/s measured), on fp16 four times faster (303),
+// and 1024 products of at most 2^14 in magnitude sum exactly in fp32: so the codes become
+// fp16 in registers, and every 1024 of K the fp32 sums move into 32-bit integers.
+//
+// A CTA takes BM x BN outputs and one of S slices of K; its warps hold MT x NT fragments of
+// 16 x 8.  Stages of 128 codes of K come by cp.async into a ring of NS.  The order of K inside a
+// product is free as long as both operands agree: each thread reads 16 consecutive codes of
+// its row, four of them for each of four 16-wide steps.  A row's 16-byte chunks are permuted
+// by its number so that the eight threads of a shared-memory phase read distinct banks.
+// The S slices are the CTAs of a cluster: each leaves its integer sums in shared memory and
+// adds up its share of the tile over all of them.
+template <int WM, int WN, int MT, int NT> struct MmaShape {
+  static constexpr int BM = WM * MT * 16, BN = WN * NT * 8, THREADS = WM * WN * 32, NS = 4;
+  static constexpr int STAGE = (BM + BN) * 128;
+  static constexpr int SUMS = BM * BN * 4;
+  static constexpr int SMEM = NS * STAGE > SUMS ? NS * STAGE : SUMS;
+};
+
+__device__ __forceinline__ int chunk_at(int row, int c) { return c ^ (((row & 1) << 2) | ((row >> 1) & 3)); }
+
+__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
+}
+
+template <int WM, int WN, int MT, int NT>
+__global__ void __launch_bounds__(WM * WN * 32)
+int8_mma_kernel(const Int8Params p, int S) {
+  using SH = MmaShape<WM, WN, MT, NT>;
+  constexpr int BM = SH::BM, BN = SH::BN, NS = SH::NS, NTH = SH::THREADS;
+  extern __shared__ __align__(128) unsigned char smem[];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int wm = warp % WM, wn = warp / WM;
+  const int slice = blockIdx.x % S;
+  const int64_t n0 = (int64_t)(blockIdx.x / S) * BN, m0 = (int64_t)blockIdx.y * BM;
+  // this slice's stages of 128 codes
+  const int all = (p.K + 127) / 128, first = (int)((int64_t)all * slice / S);
+  const int count = (int)((int64_t)all * (slice + 1) / S) - first;
+
+  auto fill = [&](int st) {
+    unsigned char* base = smem + (st % NS) * SH::STAGE;
+    const int k0 = (first + st) * 128;
+    for (int i = tid; i < (BM + BN) * 8; i += NTH) {
+      const int row = i >> 3, c = i & 7, k = k0 + c * 16;
+      const bool is_a = row < BM;
+      const int64_t r = is_a ? m0 + row : n0 + (row - BM);
+      const bool in = k < p.K && r < (is_a ? p.M : p.N);
+      const int8_t* src = is_a ? p.a + (in ? r * p.lda + k : 0) : p.b + (in ? r * p.ldb + k : 0);
+      const uint32_t dst = smem_addr(base + row * 128 + chunk_at(row, c) * 16);
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
+    }
+  };
+#pragma unroll
+  for (int st = 0; st < NS - 1; ++st) {
+    if (st < count) fill(st);
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  }
+
+  float acc[MT][NT][4] = {};
+  int sum[MT][NT][4] = {};
+  const int g = lane >> 2, t = lane & 3;
+  for (int st = 0; st < count; ++st) {
+    asm volatile("cp.async.wait_group %0;" ::"n"(NS - 2) : "memory");
+    __syncthreads();                       // stage st landed; stage st - 1 read by all
+    if (st + NS - 1 < count) fill(st + NS - 1);
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    const unsigned char* sa = smem + (st % NS) * SH::STAGE + wm * MT * 16 * 128;
+    const unsigned char* sb = smem + (st % NS) * SH::STAGE + (BM + wn * NT * 8) * 128;
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      uint4 aw[MT][2], bw[NT];
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int r = i * 16 + h * 8 + g;
+          aw[i][h] = *reinterpret_cast<const uint4*>(sa + r * 128 + chunk_at(r, half * 4 + t) * 16);
+        }
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        const int r = j * 8 + g;
+        bw[j] = *reinterpret_cast<const uint4*>(sb + r * 128 + chunk_at(r, half * 4 + t) * 16);
+      }
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        auto word = [q](const uint4& v) { return q == 0 ? v.x : q == 1 ? v.y : q == 2 ? v.z : v.w; };
+        uint32_t bf[NT][2];
+#pragma unroll
+        for (int j = 0; j < NT; ++j) codes_to_f16(word(bw[j]), bf[j][0], bf[j][1]);
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+          uint32_t af[4];
+          codes_to_f16(word(aw[i][0]), af[0], af[2]);
+          codes_to_f16(word(aw[i][1]), af[1], af[3]);
+#pragma unroll
+          for (int j = 0; j < NT; ++j) mma_f16(acc[i][j], af, bf[j]);
+        }
+      }
+    }
+    if ((st & 7) == 7 || st + 1 == count) {  // 1024 products a sum at most
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            sum[i][j][e] += __float2int_rn(acc[i][j][e]);
+            acc[i][j][e] = 0.0f;
+          }
+    }
+  }
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
+
+  if (S == 1) {
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int64_t m = m0 + (wm * MT + i) * 16 + (e >> 1) * 8 + g;
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          const int64_t n = n0 + (wn * NT + j) * 8 + 2 * t + (e & 1);
+          if (m < p.M && n < p.N) store_out(p, m, n, sum[i][j][e]);
+        }
+      }
+    return;
+  }
+  __syncthreads();                         // the ring is free: the sums take its place
+  int* own = reinterpret_cast<int*>(smem);
+#pragma unroll
+  for (int i = 0; i < MT; ++i)
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; e += 2)
+        *reinterpret_cast<int2*>(own + ((wm * MT + i) * 16 + (e >> 1) * 8 + g) * BN + (wn * NT + j) * 8 + 2 * t) =
+            make_int2(sum[i][j][e], sum[i][j][e + 1]);
+  asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  for (int i = slice * NTH + tid; i < BM * BN; i += S * NTH) {
+    const int64_t m = m0 + i / BN, n = n0 + i % BN;
+    int v = 0;
+    for (int r = 0; r < S; ++r) {
+      uint32_t at;
+      int x;
+      asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_addr(own + i)), "r"(r));
+      asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(x) : "r"(at) : "memory");
+      v += x;
+    }
+    if (m < p.M && n < p.N) store_out(p, m, n, v);
+  }
+  asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// the dynamic shared memory limit of a kernel, set once a device
+template <class K> bool allow_smem(K kernel, int bytes, std::atomic<bool> (&done)[64]) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return false;
+  if (dev >= 0 && dev < 64 && done[dev].load(std::memory_order_acquire)) return true;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return false;
+  if (dev >= 0 && dev < 64) done[dev].store(true, std::memory_order_release);
+  return true;
+}
+
+template <int WM, int WN, int MT, int NT> int launch_mma(const Int8Params& p, cudaStream_t st) {
+  using SH = MmaShape<WM, WN, MT, NT>;
+  auto kernel = int8_mma_kernel<WM, WN, MT, NT>;
+  static std::atomic<bool> done[64];
+  if (!allow_smem(kernel, SH::SMEM, done)) return emu_ops_launched("cudaFuncSetAttribute");
+  const int64_t tn = (p.N + SH::BN - 1) / SH::BN;
+  // as many slices as fill the SMs twice over, of four stages at least
+  const int sms = emu_ops_sm_count();
+  int S = 1;
+  const int64_t tiles = tn * ((p.M + SH::BM - 1) / SH::BM);
+  while (S < 8 && tiles * S < 2 * sms && (p.K + 127) / 128 >= 8 * S) S *= 2;
+  // rows of tiles on grid.y, at most 65535 a launch
+  for (int64_t m = 0; m < p.M; m += (int64_t)65535 * SH::BM) {
+    Int8Params q = p;
+    q.M = p.M - m < (int64_t)65535 * SH::BM ? p.M - m : (int64_t)65535 * SH::BM;
+    q.a += m * p.lda;
+    q.scale_a += m * p.sa_step;
+    q.out = static_cast<unsigned char*>(p.out) + (size_t)(m * p.N) * elem_bytes((emu_out_t)p.out_type);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(tn * S), (unsigned)((q.M + SH::BM - 1) / SH::BM));
+    cfg.blockDim = dim3(SH::THREADS);
+    cfg.dynamicSmemBytes = SH::SMEM;
+    cfg.stream = st;
+    cudaLaunchAttribute at;
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim.x = (unsigned)S;
+    at.val.clusterDim.y = at.val.clusterDim.z = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = S > 1 ? 1 : 0;
+    if (cudaLaunchKernelEx(&cfg, kernel, q, S) != cudaSuccess) return emu_ops_launched("emu_int8_scaled_mm");
+  }
+  return EMU_OK;
+}
+
+}  // namespace emu_ops
+
+#include "ops_int8_tc.cuh"
+
+namespace emu_ops {
+
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* ptr = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
+  });
+  return fn;
+}
+
+// fp16 rows of Kp values, boxes of 64 values by `box` rows under the 128-byte swizzle
+int f16_map(CUtensorMap* map, const uint16_t* at, int64_t rows, int64_t Kp, int box) {
+  PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+  if (!enc) return emu_ops_fail(EMU_ECUDA, "cuTensorMapEncodeTiled is not available from the driver");
+  const cuuint64_t dims[2] = {(cuuint64_t)Kp, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)Kp * 2};
+  const cuuint32_t boxes[2] = {64u, (cuuint32_t)box}, step[2] = {1u, 1u};
+  const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, const_cast<uint16_t*>(at), dims, strides, boxes, step,
+                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? EMU_OK : emu_ops_fail(EMU_ECUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
+}
+
+inline size_t round256(size_t v) { return (v + 255) & ~(size_t)255; }
+inline int64_t round_up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
+
+// How a product is computed, by its sizes alone.
+enum class Int8Kind { dot, mma, tensor };
+struct Plan {
+  Int8Kind kind;
+  int64_t Kp;                    // operands laid out in rows of Kp values (mma: only where not aligned)
+  int64_t rows_a, rows_b;        // tensor: the rows laid out at a time
+  size_t a_bytes, b_bytes;       // workspace: A's part, then B's
+};
+constexpr size_t kSlabBytes = (size_t)128 << 20;   // fp16 rows at a time, so that the workspace stays small
+
+Plan plan_for(int64_t M, int64_t N, int64_t K, bool aligned16) {
+  Plan pl = {};
+  pl.kind = M <= 4 ? Int8Kind::dot : M >= 256 && N >= 128 && K >= 128 ? Int8Kind::tensor : Int8Kind::mma;
+  if (pl.kind == Int8Kind::tensor) {
+    pl.Kp = round_up(K, kTcBK);
+    const int64_t most = (int64_t)(kSlabBytes / (2 * (size_t)pl.Kp)) / kTcBN * kTcBN;   // K < 2^17: 512 rows at least
+    pl.rows_a = M < most ? M : most;
+    pl.rows_b = N < most ? N : most;
+    pl.a_bytes = round256((size_t)pl.rows_a * (size_t)pl.Kp * 2);
+    pl.b_bytes = round256((size_t)pl.rows_b * (size_t)pl.Kp * 2);
+  } else if (!aligned16) {
+    pl.Kp = round_up(K, 16);
+    pl.a_bytes = round256((size_t)M * (size_t)pl.Kp);
+    pl.b_bytes = round256((size_t)N * (size_t)pl.Kp);
+  }
+  return pl;
+}
+
+int launch_tc(const Int8Params& p, const Plan& pl, bool vec, unsigned char* ws, cudaStream_t st) {
+  static std::atomic<bool> done[64];
+  if (!allow_smem(int8_tc_kernel, kTcSmem, done)) return emu_ops_launched("cudaFuncSetAttribute");
+  uint16_t* a16 = reinterpret_cast<uint16_t*>(ws);
+  uint16_t* b16 = reinterpret_cast<uint16_t*>(ws + pl.a_bytes);
+  const int sms = emu_ops_sm_count();
+  const size_t es = elem_bytes((emu_out_t)p.out_type);
+  const uint32_t chunks = (uint32_t)(pl.Kp / 16);
+  for (int64_t m = 0; m < p.M; m += pl.rows_a) {
+    const int64_t rows_a = p.M - m < pl.rows_a ? p.M - m : pl.rows_a;
+    for (int64_t n = 0; n < p.N; n += pl.rows_b) {
+      const int64_t rows_b = p.N - n < pl.rows_b ? p.N - n : pl.rows_b;
+      const uint32_t lay_a = n == 0 ? (uint32_t)rows_a : 0u;
+      const bool lay_b = m == 0 || pl.rows_b < p.N;
+      const uint64_t work = ((uint64_t)lay_a + (lay_b ? (uint64_t)rows_b : 0u)) * chunks;
+      if (work > 0) {
+        const uint64_t blocks = (work + 255) / 256;
+        int8_to_f16_kernel<<<(unsigned)(blocks < 16384 ? blocks : 16384), 256, 0, st>>>(
+            p.a + m * p.lda, p.lda, lay_a, a16, p.b + n * p.ldb, p.ldb, lay_b ? (uint32_t)rows_b : 0u, b16, p.K, chunks, vec);
+      }
+      CUtensorMap map_a, map_b;
+      int rc = f16_map(&map_a, a16, rows_a, pl.Kp, kTcBM);
+      if (rc == EMU_OK) rc = f16_map(&map_b, b16, rows_b, pl.Kp, kTcBN);
+      if (rc != EMU_OK) return rc;
+      Int8Params q = p;
+      q.M = rows_a;
+      q.cols = rows_b;
+      q.scale_a += m * p.sa_step;
+      q.scale_b += n * p.sb_step;
+      q.out = static_cast<unsigned char*>(p.out) + (size_t)(m * p.N + n) * es;
+      const TcTiles tl = {(int)((rows_a + kTcBM - 1) / kTcBM), (int)((rows_b + kTcBN - 1) / kTcBN), (int)(pl.Kp / kTcBK)};
+      const int tiles = tl.tiles_m * tl.tiles_n;
+      int8_tc_kernel<<<(unsigned)(tiles < sms ? tiles : sms), kTcThreads, kTcSmem, st>>>(q, tl, map_a, map_b);
+    }
+  }
+  return EMU_OK;
+}
+
+int run_plan(const Int8Params& p, bool vec, void* workspace, cudaStream_t st) {
+  const Plan pl = plan_for(p.M, p.N, p.K, vec);
+  unsigned char* ws = static_cast<unsigned char*>(workspace);
+  if (pl.kind == Int8Kind::tensor) {
+    const int rc = launch_tc(p, pl, vec, ws, st);
+    return rc == EMU_OK ? emu_ops_launched("emu_int8_scaled_mm") : rc;
+  }
+  Int8Params q = p;
+  if (!vec && p.K > 0) {
+    int8_t* a = reinterpret_cast<int8_t*>(ws);
+    int8_t* b = reinterpret_cast<int8_t*>(ws + pl.a_bytes);
+    int8_align_kernel<<<(unsigned)(p.M < 8192 ? p.M : 8192), 256, 0, st>>>(p.a, p.lda, p.M, p.K, a, pl.Kp);
+    int8_align_kernel<<<(unsigned)(p.N < 8192 ? p.N : 8192), 256, 0, st>>>(p.b, p.ldb, p.N, p.K, b, pl.Kp);
+    q.a = a;
+    q.b = b;
+    q.lda = q.ldb = pl.Kp;
+    q.K = (int)pl.Kp;
+  }
+  int rc;
+  if (pl.kind == Int8Kind::dot) rc = q.M == 1 ? launch_dot<1>(q, st) : launch_dot<4>(q, st);
+  else if (q.M <= 16) rc = launch_mma<1, 4, 1, 2>(q, st);
+  else if (q.M <= 32) rc = launch_mma<1, 4, 2, 2>(q, st);
+  else rc = launch_mma<2, 2, 2, 4>(q, st);
+  return rc == EMU_OK ? emu_ops_launched("emu_int8_scaled_mm") : rc;
 }
 
 }  // namespace emu_ops
 
 using namespace emu_ops;
 
-int emu_ops_device_status_int8(int* status, bool) {
-  *status = 0;
+int emu_ops_device_status_int8(int* status, bool reset) {
+  int v = 0;
+  cudaError_t e = cudaMemcpyFromSymbol(&v, g_ops_status, sizeof v);
+  if (e != cudaSuccess) return emu_ops_fail(EMU_ECUDA, "reading the device status failed: %s", cudaGetErrorString(e));
+  *status = v;
+  if (reset) {
+    const int zero = 0;
+    e = cudaMemcpyToSymbol(g_ops_status, &zero, sizeof zero);
+    if (e != cudaSuccess) return emu_ops_fail(EMU_ECUDA, "clearing the device status failed: %s", cudaGetErrorString(e));
+  }
   return EMU_OK;
 }
 
 extern "C" {
 
-size_t emu_int8_workspace_bytes(int64_t M, int64_t N, int64_t K) {
-  (void)M; (void)N; (void)K;
-  return 0;
+size_t emu_int8_workspace_bytes(int64_t M, int64_t N, int64_t K, int32_t aligned16) {
+  if (M < 1 || N < 1 || K < 1 || K > kInt8MaxK || M >= ((int64_t)1 << 31) || N >= ((int64_t)1 << 31)) return 0;
+  const Plan plan = plan_for(M, N, K, aligned16 != 0);
+  return plan.a_bytes + plan.b_bytes;
 }
 
 int emu_int8_scaled_mm(const int8_t* A, int64_t lda, const int8_t* B, int64_t ldb, int64_t M, int64_t N, int64_t K,
@@ -124,19 +485,17 @@ int emu_int8_scaled_mm(const int8_t* A, int64_t lda, const int8_t* B, int64_t ld
   const size_t es = elem_bytes(out_dtype);
   if (!aligned(out, es) || !aligned(scale_a, 4) || !aligned(scale_b, 4))
     return emu_ops_fail(EMU_EINVAL, "a tensor is not aligned to its elements");
-  const size_t need = emu_int8_workspace_bytes(M, N, K);
+  const bool vec = K % 16 == 0 && lda % 16 == 0 && ldb % 16 == 0 && aligned(A, 16) && aligned(B, 16);
+  const size_t need = emu_int8_workspace_bytes(M, N, K, vec);
   if (need > 0 && (!workspace || workspace_bytes < need || !aligned(workspace, 256)))
     return emu_ops_fail(EMU_EINVAL, "workspace of %zu bytes needed, 256-byte aligned (got %zu)", need, workspace_bytes);
   Int8Params p;
-  p.a = A; p.lda = lda; p.b = B; p.ldb = ldb; p.M = M; p.N = N; p.K = (int)K;
+  p.a = A; p.lda = lda; p.b = B; p.ldb = ldb; p.M = M; p.N = N; p.cols = N; p.K = (int)K;
   p.scale_a = scale_a; p.sa_step = scale_a_count == 1 ? 0 : 1;
   p.scale_b = scale_b; p.sb_step = scale_b_count == 1 ? 0 : 1;
   p.out = out; p.out_type = (int)out_dtype;
-  const bool vec = K % 16 == 0 && lda % 16 == 0 && ldb % 16 == 0 && aligned(A, 16) && aligned(B, 16);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (vec) launch_dot<true>(p, st);
-  else launch_dot<false>(p, st);
-  return emu_ops_launched("emu_int8_scaled_mm");
+  return run_plan(p, vec, workspace, st);
 }
 
 }  // extern "C"

@@ -1,0 +1,302 @@
+// ops_int8_tc.cuh -- the int8 product on the 5th-generation tensor cores, for many tokens.
+//
+// sm_103a's tcgen05 has no int8 kind, but a code is exact in fp16, a product of two is at
+// most 2^14 in magnitude, and 1024 of them sum exactly in the fp32 accumulator (every partial
+// sum is a whole number of at most 2^24).  So the codes are laid out once as fp16, rows padded
+// with zeros to a multiple of 64, and multiplied by tcgen05.mma kind::f16; after every 1024 of
+// K the accumulator is read back and added up in 32-bit integers, while the MMAs go on in the
+// other of two accumulators.
+#pragma once
+#include "ops_common.cuh"
+
+namespace emu_ops {
+
+constexpr int kTcBM = 128, kTcBN = 256, kTcBK = 64, kTcNS = 4;
+constexpr int kTcChunk = 1024 / kTcBK;                       // K blocks that one accumulator takes
+constexpr int kTcStage = (kTcBM + kTcBN) * kTcBK * 2;        // 48 KB
+constexpr int kTcStageRow = 33;                              // floats of a staged output row
+constexpr int kTcOut = kTcNS * kTcStage;                     // eight warps' staging, 32 x 33 floats each
+constexpr int kTcBars = kTcOut + 8 * 32 * kTcStageRow * 4;
+constexpr int kTcSmem = kTcBars + 128 + 1024;                // and what aligning to 1024 may take
+constexpr int kTcThreads = 384;
+constexpr uint32_t kTcPolls = 1u << 20;
+
+struct TcTiles {
+  int tiles_m, tiles_n, k_blocks;
+};
+
+// ---- barriers, TMA and tcgen05 (inline PTX)
+__device__ __forceinline__ void bar_init(uint32_t bar, uint32_t count) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
+}
+__device__ __forceinline__ void bar_arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void bar_expect(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred P;\n mbarrier.try_wait.parity.shared::cta.b64 P, [%1], %2;\n selp.u32 %0, 1, 0, P;\n}"
+      : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+  return ok != 0u;
+}
+// Waits for the phase of this parity; false once the limit is reached or another role gave up.
+__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile int* given_up) {
+  for (uint32_t i = 0; i < kTcPolls; ++i) {
+    if (bar_try(bar, parity)) return true;
+    if (*given_up) return false;
+  }
+  *given_up = 1;
+  return false;
+}
+// the same at a failed role's end, for what it still has in flight
+__device__ __forceinline__ void bar_drain(uint32_t bar, uint32_t parity) {
+  for (uint32_t i = 0; i < kTcPolls; ++i)
+    if (bar_try(bar, parity)) return;
+}
+__device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
+      ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar) : "memory");
+}
+// shared-memory matrix descriptor: K-major rows of 128 bytes under the 128-byte swizzle, groups of
+// eight rows 1024 bytes apart
+__device__ __forceinline__ uint64_t tc_desc(uint32_t addr) {
+  return (uint64_t)((addr >> 4) & 0x3FFFu) | (1ull << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
+}
+// instruction descriptor of kind::f16: fp16 operands, both K-major, fp32 accumulator
+__device__ __forceinline__ uint32_t tc_idesc(int m, int n) {
+  return (1u << 4) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
+}
+__device__ __forceinline__ void tc_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t add) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(add)
+      : "memory");
+}
+__device__ __forceinline__ void tc_commit(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+// 32 columns of this warp's 32 lanes
+__device__ __forceinline__ void tc_read32(uint32_t addr, float (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]), "=f"(r[8]),
+        "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15]), "=f"(r[16]),
+        "=f"(r[17]), "=f"(r[18]), "=f"(r[19]), "=f"(r[20]), "=f"(r[21]), "=f"(r[22]), "=f"(r[23]), "=f"(r[24]),
+        "=f"(r[25]), "=f"(r[26]), "=f"(r[27]), "=f"(r[28]), "=f"(r[29]), "=f"(r[30]), "=f"(r[31])
+      : "r"(addr)
+      : "memory");
+}
+
+// Codes to fp16 rows of Kp values, zeros after the K-th: rows_a rows of A, then rows_b of B.  A
+// thread takes 16 codes.
+__global__ void __launch_bounds__(256)
+int8_to_f16_kernel(const int8_t* a, int64_t lda, uint32_t rows_a, uint16_t* a16, const int8_t* b, int64_t ldb,
+                   uint32_t rows_b, uint16_t* b16, int K, uint32_t chunks, bool vec) {
+  const uint32_t total = (rows_a + rows_b) * chunks;
+  for (uint32_t i = blockIdx.x * 256u + threadIdx.x; i < total; i += gridDim.x * 256u) {
+    const uint32_t row = i / chunks, c = i - row * chunks;
+    const bool is_a = row < rows_a;
+    const uint32_t r = is_a ? row : row - rows_a;
+    const int8_t* src = is_a ? a + (int64_t)r * lda : b + (int64_t)r * ldb;
+    const int k = (int)c * 16;
+    uint32_t w[4] = {0u, 0u, 0u, 0u};
+    if (vec) {
+      if (k < K) {
+        const uint4 q = *reinterpret_cast<const uint4*>(src + k);
+        w[0] = q.x; w[1] = q.y; w[2] = q.z; w[3] = q.w;
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 16; ++j)
+        if (k + j < K) w[j >> 2] |= (uint32_t)(uint8_t)src[k + j] << (8 * (j & 3));
+    }
+    uint4* dst = reinterpret_cast<uint4*>((is_a ? a16 : b16) + (size_t)r * chunks * 16 + (size_t)c * 16);
+    uint32_t h[8];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) codes_to_f16(w[j], h[2 * j], h[2 * j + 1]);
+    dst[0] = make_uint4(h[0], h[1], h[2], h[3]);
+    dst[1] = make_uint4(h[4], h[5], h[6], h[7]);
+  }
+}
+
+// Persistent: one CTA an SM, tiles of 128 x 256 outputs in turn.  Warp 0 loads the stages by TMA,
+// warp 1 issues the MMAs, warp 2 owns the tensor memory, warps 4 to 11 read the accumulators
+// back: each holds 32 rows x 128 columns of sums in registers, scales them and writes rows of 32
+// columns through shared memory.  All waits are bounded; a role that gives up sets the status
+// and takes the others along.
+__global__ void __launch_bounds__(kTcThreads, 1)
+int8_tc_kernel(const Int8Params p, const TcTiles tl, const __grid_constant__ CUtensorMap map_a,
+               const __grid_constant__ CUtensorMap map_b) {
+  extern __shared__ unsigned char raw[];
+  unsigned char* const smem = raw + ((1024u - (smem_addr(raw) & 1023u)) & 1023u);
+  const uint32_t base = smem_addr(smem);
+  const uint32_t full = base + kTcBars, empty = full + 8 * kTcNS, tfull = empty + 8 * kTcNS, tempty = tfull + 16,
+                 drained = tempty + 16;
+  uint32_t* const slot = reinterpret_cast<uint32_t*>(smem + kTcBars + 8 * (2 * kTcNS + 5));
+  volatile int* const given_up = reinterpret_cast<volatile int*>(slot + 1);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+
+  if (tid == 0) {
+    for (int i = 0; i < kTcNS; ++i) {
+      bar_init(full + 8 * i, 1);
+      bar_init(empty + 8 * i, 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      bar_init(tfull + 8 * i, 1);
+      bar_init(tempty + 8 * i, 8);                // one arrival a reading warp
+    }
+    bar_init(drained, 1);
+    *given_up = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 2) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_addr(slot)) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *slot;
+  const int tiles = tl.tiles_m * tl.tiles_n;
+
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+    if (warp == 0 && lane == 0) {
+      uint32_t it = 0;
+      bool ok = true;
+      for (int tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
+        const int m0 = tile % tl.tiles_m * kTcBM, n0 = tile / tl.tiles_m * kTcBN;
+        for (int kb = 0; kb < tl.k_blocks; ++kb, ++it) {
+          const uint32_t s = it % kTcNS, bar = full + 8 * s, dst = base + s * kTcStage;
+          if (it >= kTcNS && !bar_wait(empty + 8 * s, (it / kTcNS - 1) & 1, given_up)) {
+            ok = false;
+            break;
+          }
+          bar_expect(bar, kTcStage);
+          tma_load(dst, &map_a, kb * kTcBK, m0, bar);
+          tma_load(dst + kTcBM * kTcBK * 2, &map_b, kb * kTcBK, n0, bar);
+        }
+      }
+      if (!ok)                                    // the loads issued last, one a stage at most
+        for (uint32_t i = it > kTcNS ? it - kTcNS : 0; i < it; ++i) bar_drain(full + 8 * (i % kTcNS), (i / kTcNS) & 1);
+    } else if (warp == 1 && lane == 0) {
+      const uint32_t idesc = tc_idesc(kTcBM, kTcBN);
+      uint32_t it = 0, unit = 0;
+      bool ok = true;
+      for (int tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
+        for (int k0 = 0; k0 < tl.k_blocks && ok; k0 += kTcChunk, ++unit) {
+          const uint32_t buf = unit & 1;
+          if (unit >= 2 && !bar_wait(tempty + 8 * buf, ((unit >> 1) - 1) & 1, given_up)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const int k1 = k0 + kTcChunk < tl.k_blocks ? k0 + kTcChunk : tl.k_blocks;
+          for (int kb = k0; kb < k1; ++kb, ++it) {
+            const uint32_t s = it % kTcNS;
+            if (!bar_wait(full + 8 * s, (it / kTcNS) & 1, given_up)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const uint64_t da = tc_desc(base + s * kTcStage), db = tc_desc(base + s * kTcStage + kTcBM * kTcBK * 2);
+#pragma unroll
+            for (int k = 0; k < kTcBK / 16; ++k)
+              tc_mma(tmem + buf * 256, da + 2 * k, db + 2 * k, idesc, kb > k0 || k > 0);
+            tc_commit(empty + 8 * s);
+          }
+          if (ok) tc_commit(tfull + 8 * buf);
+        }
+      }
+      tc_commit(drained);                         // the MMAs are done before the tensor memory goes back
+      bar_drain(drained, 0);
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
+    const int quad = warp & 3, half = (warp - 4) >> 2;
+    float* const stage = reinterpret_cast<float*>(smem + kTcOut) + (warp - 4) * 32 * kTcStageRow;
+    const bool pairs = p.out_type != EMU_OUT_F32 && p.N % 2 == 0 && p.cols % 2 == 0 && ((uintptr_t)p.out & 3u) == 0;
+    uint32_t unit = 0;
+    bool ok = true;
+    for (int tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
+      const int64_t m0 = (int64_t)(tile % tl.tiles_m) * kTcBM + quad * 32;
+      const int64_t n0 = (int64_t)(tile / tl.tiles_m) * kTcBN + half * 128;
+      int sum[128];
+      for (int k0 = 0; k0 < tl.k_blocks; k0 += kTcChunk, ++unit) {
+        const uint32_t buf = unit & 1;
+        ok = __all_sync(0xFFFFFFFFu, bar_wait(tfull + 8 * buf, (unit >> 1) & 1, given_up));
+        if (!ok) break;
+        tc_fence_after();
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          float r[32];
+          tc_read32(tmem + ((uint32_t)(quad * 32) << 16) + buf * 256 + half * 128 + c * 32, r);
+          if (k0 == 0) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) sum[c * 32 + i] = __float2int_rn(r[i]);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) sum[c * 32 + i] += __float2int_rn(r[i]);
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) bar_arrive(tempty + 8 * buf);
+      }
+      if (!ok) break;
+      const float sa = m0 + lane < p.M ? p.scale_a[(m0 + lane) * p.sa_step] : 0.0f;
+      const int rows = p.M - m0 < 32 ? (int)(p.M - m0) : 32;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const int64_t nc = n0 + c * 32;
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 32; ++i) stage[lane * kTcStageRow + i] = (float)sum[c * 32 + i] * sa;
+        __syncwarp();
+        if (pairs) {
+          const int64_t n = nc + (lane & 15) * 2;
+          if (n < p.cols) {
+            const float s0 = p.scale_b[n * p.sb_step], s1 = p.scale_b[(n + 1) * p.sb_step];
+            for (int r = lane >> 4; r < rows; r += 2) {
+              const float* v = stage + r * kTcStageRow + (lane & 15) * 2;
+              const int64_t at = (m0 + r) * p.N + n;
+              if (p.out_type == EMU_OUT_BF16)
+                *reinterpret_cast<__nv_bfloat162*>(static_cast<__nv_bfloat16*>(p.out) + at) =
+                    __floats2bfloat162_rn(v[0] * s0, v[1] * s1);
+              else
+                *reinterpret_cast<__half2*>(static_cast<__half*>(p.out) + at) = __floats2half2_rn(v[0] * s0, v[1] * s1);
+            }
+          }
+        } else {
+          const int64_t n = nc + lane;
+          if (n < p.cols) {
+            const float sb = p.scale_b[n * p.sb_step];
+            for (int r = 0; r < rows; ++r) {
+              const float v = stage[r * kTcStageRow + lane] * sb;
+              const int64_t at = (m0 + r) * p.N + n;
+              if (p.out_type == EMU_OUT_F32) static_cast<float*>(p.out)[at] = v;
+              else if (p.out_type == EMU_OUT_BF16) static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(v);
+              else static_cast<__half*>(p.out)[at] = __float2half_rn(v);
+            }
+          }
+        }
+      }
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (tid == 0 && *given_up) atomicExch(&g_ops_status, 1);
+  if (warp == 2) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+}
+
+}  // namespace emu_ops

@@ -184,8 +184,9 @@ def rms_norm_backward(grad_y: torch.Tensor, hidden: torch.Tensor, rstd: torch.Te
 
 
 def int8_workspace_bytes(M: int, N: int, K: int) -> int:
-    """Device workspace bytes ``int8_scaled_mm`` needs for these sizes."""
-    return int(_lib.load().emu_int8_workspace_bytes(M, N, K))
+    """Device workspace bytes ``int8_scaled_mm`` needs for these sizes, whatever the
+    operands' alignment."""
+    return int(_lib.load().emu_int8_workspace_bytes(M, N, K, 0))
 
 
 def int8_scaled_mm(mat1: torch.Tensor, mat2: torch.Tensor, scale_a: torch.Tensor, scale_b: torch.Tensor, *,
@@ -220,13 +221,14 @@ def int8_scaled_mm(mat1: torch.Tensor, mat2: torch.Tensor, scale_a: torch.Tensor
     elif out.shape != (M, N) or out.dtype != out_dtype or not out.is_contiguous() or out.device != dev:
         raise ValueError("out must be a contiguous [M, N] tensor of out_dtype on the device")
     L = _lib.load()
-    need = L.emu_int8_workspace_bytes(M, N, K)
+    pa, pb = mat1.data_ptr(), mat2.data_ptr()
+    need = L.emu_int8_workspace_bytes(M, N, K, (K | lda | ldb | pa | pb) % 16 == 0)
     wp = 0
     if need > 0:
         if workspace is None or workspace.numel() * workspace.element_size() < need or workspace.data_ptr() % 256:
             workspace = torch.empty(need, dtype=torch.uint8, device=dev)
         wp = workspace.data_ptr()
-    _call(L.emu_int8_scaled_mm, dev, "int8_scaled_mm", mat1.data_ptr(), lda, mat2.data_ptr(), ldb, M, N, K, sa, na,
+    _call(L.emu_int8_scaled_mm, dev, "int8_scaled_mm", pa, lda, pb, ldb, M, N, K, sa, na,
           sb, nb, out.data_ptr(), _FLOAT[out_dtype], wp, need)
     return out
 
