@@ -37,99 +37,385 @@ __device__ __forceinline__ float key_value(uint32_t k) {
   return __uint_as_float((k & 0x80000000u) ? (k & 0x7FFFFFFFu) : ~k);
 }
 
-// Running (m, z, u) of a part of a row; m = -inf: nothing above -inf yet.
+// Running (m, z, u) of a part of a row: z and u are relative to m, the largest logit so far or,
+// before any, the lowest finite number (so that x - m is never -inf - -inf).  z == 0: nothing
+// above -inf yet.  NaN and +inf end in z = NaN, which every later step keeps.
 struct Soft {
   float m, z, u;
 };
+constexpr float kLowest = -3.40282347e38f;
 __device__ __forceinline__ Soft soft_join(const Soft& a, const Soft& b) {
   const float m = fmaxf(a.m, b.m);
-  if (m == -INFINITY) return Soft{m, a.z + b.z, a.u + b.u};      // zeros, or a NaN that is kept
-  Soft r{m, 0.0f, 0.0f};
-  if (a.m != -INFINITY || a.z != 0.0f) {
-    const float d = fmaxf(a.m - m, -1e4f), f = exp2_approx(d * kLog2e);
-    r.z += a.z * f;
-    r.u += (a.u + a.z * d) * f;
-  }
-  if (b.m != -INFINITY || b.z != 0.0f) {
-    const float d = fmaxf(b.m - m, -1e4f), f = exp2_approx(d * kLog2e);
-    r.z += b.z * f;
-    r.u += (b.u + b.z * d) * f;
-  }
-  return r;
+  const float da = fmaxf(a.m - m, -1e4f), db = fmaxf(b.m - m, -1e4f);    // e^-1e4 is 0
+  const float fa = exp2_approx(da * kLog2e), fb = exp2_approx(db * kLog2e);
+  return Soft{m, a.z * fa + b.z * fb, (a.u + a.z * da) * fa + (b.u + b.z * db) * fb};
 }
-__device__ __forceinline__ Soft soft_shfl(const Soft& a, int o) {
-  return Soft{__shfl_xor_sync(0xFFFFFFFFu, a.m, o), __shfl_xor_sync(0xFFFFFFFFu, a.z, o),
-              __shfl_xor_sync(0xFFFFFFFFu, a.u, o)};
+__device__ __forceinline__ Soft soft_warp(Soft a) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+    a = soft_join(a, Soft{__shfl_xor_sync(0xFFFFFFFFu, a.m, o), __shfl_xor_sync(0xFFFFFFFFu, a.z, o),
+                          __shfl_xor_sync(0xFFFFFFFFu, a.u, o)});
+  return a;
+}
+
+// A row as 16-byte vectors at 16-byte addresses: vector v holds the logits v * VEC - off + j, those
+// outside [0, V) read as -inf.
+template <class T> struct Row {
+  static constexpr int VEC = 16 / sizeof(T);
+  const T* base;           // the row's start, rounded down to 16 bytes
+  int off, V, nvec;
+  __device__ __forceinline__ Row(const T* x, int V_) : V(V_) {
+    off = (int)((reinterpret_cast<uintptr_t>(x) & 15u) / sizeof(T));
+    base = x - off;
+    nvec = (V + off + VEC - 1) / VEC;
+  }
+  __device__ __forceinline__ int first(int v) const { return v * VEC - off; }
+  __device__ __forceinline__ bool whole(int v) const { return first(v) >= 0 && first(v) + VEC <= V; }
+  __device__ __forceinline__ void load(int v, float (&f)[VEC]) const {
+    if (whole(v)) {
+      load_f<T, VEC>(base + (int64_t)v * VEC, f);
+    } else {
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) {
+        const int i = first(v) + j;
+        f[j] = i >= 0 && i < V ? to_f(base[off + i]) : -INFINITY;
+      }
+    }
+  }
+};
+
+// (key, position) of a logit as one number: the larger key first, then the lower position
+__device__ __forceinline__ unsigned long long ranked(uint32_t key, uint32_t pos) {
+  return ((unsigned long long)key << 32) | (0xFFFFFFFFu - pos);
+}
+
+// A thread's pass over the vectors v0, v0 + step, ... below v1: its Soft, and where in its vectors its
+// largest logit first stands.
+template <class T>
+__device__ __forceinline__ Soft stream(const Row<T>& row, int v0, int v1, int step, int& at) {
+  constexpr int VEC = Row<T>::VEC, U = 4;
+  Soft s{kLowest, 0.0f, 0.0f};
+  at = v0;
+  for (int v = v0; v < v1; v += step * U) {
+    float f[U][VEC];
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      if (v + i * step < v1) {
+        row.load(v + i * step, f[i]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) f[i][j] = -INFINITY;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      float m = f[i][0];
+#pragma unroll
+      for (int j = 1; j < VEC; ++j) m = fmaxf(m, f[i][j]);
+      if (m > s.m || (m == s.m && s.z == 0.0f)) {        // the latter: the lowest finite number itself
+        const float d = fmaxf(s.m - m, -1e4f), e = exp2_approx(d * kLog2e);
+        s.u = (s.u + s.z * d) * e;
+        s.z *= e;
+        s.m = m;
+        at = v + i * step;
+      }
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) {
+        const float t = f[i][j] - s.m, e = exp2_approx(t * kLog2e);
+        s.z += e;
+        s.u = fmaf(e, fmaxf(t, -1e4f), s.u);
+      }
+    }
+  }
+  return s;
 }
 
 // the row's outputs but its alternatives; x - m is exact where it matters, so logprob is (x - m) - log z
 template <class T>
-__device__ __forceinline__ void finish_row(const LogprobParams& p, int64_t row, float m, float z, float u, const T* x) {
-  const bool empty = m == -INFINITY && z == 0.0f;
-  const float logz = logf(z);
-  const float entropy = empty ? 0.0f : logz - u / z;
+__device__ __forceinline__ void finish_row(const LogprobParams& p, int64_t row, const Soft& s) {
+  const T* x = static_cast<const T*>(p.x) + row * p.ldx;
+  const bool empty = s.z == 0.0f;
+  const float logz = logf(s.z);
+  const float entropy = empty ? 0.0f : logz - s.u / s.z;
   const int64_t tok = p.tokens[row];
   p.logprob[row] = tok == p.ignore ? 0.0f
                    : tok < 0 || tok >= p.V ? NAN
-                   : empty ? -INFINITY : to_f(x[tok]) - m - logz;
+                   : empty ? -INFINITY : to_f(x[tok]) - s.m - logz;
   p.entropy[row] = entropy;
-  p.lse[row] = empty ? -INFINITY : m + logz;
+  p.lse[row] = empty ? -INFINITY : s.m + logz;
   float* st = p.stats + row * 3;
-  st[0] = m;
+  st[0] = empty ? -INFINITY : s.m;
   st[1] = logz;
   st[2] = entropy;
 }
+// alternative `rank` of the row: logit of this key at this id
+__device__ __forceinline__ void put_top(const LogprobParams& p, int64_t row, int rank, unsigned long long c, const Soft& s) {
+  const bool bad = s.z != s.z;
+  p.top_val[row * p.k + rank] = bad ? NAN : s.z == 0.0f ? -INFINITY : key_value((uint32_t)(c >> 32)) - s.m - logf(s.z);
+  p.top_id[row * p.k + rank] = bad ? -1 : (int64_t)(0xFFFFFFFFu - (uint32_t)c);
+}
 
-// One CTA a row; each thread takes every 256th logit.  The alternatives: k times the
-// largest (key, lowest index) below the last one found.
+// The top k of a row in one more look at a few of its logits.  The pass above leaves each group of
+// threads with its largest logit, its head.  The k-th largest head bounds the k-th largest logit
+// from below (at least k logits reach it), so only the k groups with the largest heads hold
+// logits to be taken, and of theirs only those from that bound on: for most rows little more
+// than k.  They are listed, and each counts those above itself.  Heads and bound are compared
+// with their vectors' positions, so equal logits come out by lower id and a row of equal ones
+// lists few.  A list too short (many large logits at one period) is made up for by k searches.
+//
+// One warp a row: for short rows.
+constexpr int kWarpRows = 8, kWarpList = 256;
 template <class T>
-__global__ void __launch_bounds__(256)
-logprob_kernel(const LogprobParams p) {
-  __shared__ Soft sm[8];
-  __shared__ unsigned long long best[8];
-  const int64_t row = blockIdx.x;
-  const T* x = static_cast<const T*>(p.x) + row * p.ldx;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  Soft s{-INFINITY, 0.0f, 0.0f};
-  for (int v = tid; v < p.V; v += 256) {
-    const float f = to_f(x[v]);
-    if (f == -INFINITY) continue;
-    s = soft_join(s, f != f || f == INFINITY ? Soft{s.m, NAN, NAN} : Soft{f, 1.0f, 0.0f});
+__global__ void __launch_bounds__(32 * kWarpRows)
+logprob_warp_kernel(const LogprobParams p) {
+  __shared__ unsigned long long list_all[kWarpRows][kWarpList];
+  __shared__ int count_all[kWarpRows];
+  constexpr int VEC = Row<T>::VEC;
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  const int64_t r = (int64_t)blockIdx.x * kWarpRows + w;
+  if (r >= p.T) return;
+  const Row<T> row(static_cast<const T*>(p.x) + r * p.ldx, p.V);
+  int at;
+  const Soft mine = stream(row, lane, row.nvec, 32, at);
+  const Soft s = soft_warp(mine);
+  if (lane == 0) finish_row<T>(p, r, s);
+  if (p.k == 0) return;
+  unsigned long long* list = list_all[w];
+  int& count = count_all[w];
+  if (lane == 0) count = 0;
+  const unsigned long long head =
+      lane < row.nvec ? ranked(order_key(mine.z == 0.0f ? -INFINITY : mine.m), (uint32_t)at) : 0ull;
+  int above = 0;
+#pragma unroll
+  for (int i = 0; i < 32; ++i) above += __shfl_sync(0xFFFFFFFFu, head, i) > head;
+  const uint32_t kth = __ballot_sync(0xFFFFFFFFu, head != 0ull && above == p.k - 1);
+  const unsigned long long bound = kth ? __shfl_sync(0xFFFFFFFFu, head, __ffs(kth) - 1) : 0ull;
+  __syncwarp();
+  if (head != 0ull && above < p.k) {
+    for (int v = lane; v < row.nvec; v += 32) {
+      float f[VEC];
+      row.load(v, f);
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) {
+        const int id = row.first(v) + j;
+        const uint32_t key = order_key(f[j]);
+        if (id >= 0 && id < p.V && ranked(key, (uint32_t)v) >= bound) {
+          const int n = atomicAdd(&count, 1);
+          if (n < kWarpList) list[n] = ranked(key, (uint32_t)id);
+        }
+      }
+    }
   }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) s = soft_join(s, soft_shfl(s, o));
-  if (lane == 0) sm[warp] = s;
-  __syncthreads();
-  s = sm[0];
-#pragma unroll
-  for (int w = 1; w < 8; ++w) s = soft_join(s, sm[w]);
-  const bool empty = s.m == -INFINITY && s.z == 0.0f;
-  const float logz = logf(s.z);
-  if (tid == 0) finish_row(p, row, s.m, s.z, s.u, x);
+  __syncwarp();
+  const int n = count;
+  if (n <= kWarpList) {
+    for (int i = lane; i < n; i += 32) {
+      const unsigned long long c = list[i];
+      int rank = 0;
+      for (int j = 0; j < n; ++j) rank += list[j] > c;
+      if (rank < p.k) put_top(p, r, rank, c, s);
+    }
+    return;
+  }
   unsigned long long last = ~0ull;
   for (int i = 0; i < p.k; ++i) {
-    unsigned long long mine = 0ull;
-    for (int v = tid; v < p.V; v += 256) {
-      const unsigned long long c = ((unsigned long long)order_key(to_f(x[v])) << 32) | (0xFFFFFFFFu - (uint32_t)v);
-      if (c < last && c > mine) mine = c;
+    unsigned long long best = 0ull;
+    for (int v = lane; v < p.V; v += 32) {
+      const unsigned long long c = ranked(order_key(to_f(row.base[row.off + v])), (uint32_t)v);
+      if (c < last && c > best) best = c;
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
-      const unsigned long long c = __shfl_xor_sync(0xFFFFFFFFu, mine, o);
-      mine = c > mine ? c : mine;
+      const unsigned long long c = __shfl_xor_sync(0xFFFFFFFFu, best, o);
+      best = c > best ? c : best;
+    }
+    last = best;
+    if (lane == 0) put_top(p, r, i, last, s);
+  }
+}
+
+__device__ __forceinline__ uint32_t in_cluster(const void* ptr, int rank) {
+  uint32_t a;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"((uint32_t)__cvta_generic_to_shared(ptr)), "r"(rank));
+  return a;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// A CTA, or the C CTAs of a cluster, a row: for long rows, and more CTAs a row the fewer rows there
+// are.  Each CTA takes a run of the row's vectors; the first one joins the sums and the k
+// largest of each through distributed shared memory.
+constexpr int kGroups = 128, kList = 1024, kMaxCluster = 8;
+template <class T, int NT>
+__global__ void __launch_bounds__(NT)
+logprob_row_kernel(const LogprobParams p, int C) {
+  constexpr int VEC = Row<T>::VEC, NW = NT / 32, GT = NT / kGroups;      // GT threads a group
+  __shared__ Soft warp_soft[NW];
+  __shared__ __align__(16) unsigned long long heads[kGroups];
+  __shared__ int cand[kMaxTop];
+  __shared__ unsigned long long bound;
+  __shared__ int count;
+  __shared__ unsigned long long list[kList];
+  __shared__ Soft parts[kMaxCluster];                                    // of the first CTA: all CTAs'
+  __shared__ unsigned long long tops[kMaxCluster][kMaxTop];
+  __shared__ unsigned long long best_of[NW];
+  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+  const int64_t r = blockIdx.x / C;
+  const int part = blockIdx.x % C;
+  const Row<T> row(static_cast<const T*>(p.x) + r * p.ldx, p.V);
+  const int v0 = (int)((int64_t)row.nvec * part / C), v1 = (int)((int64_t)row.nvec * (part + 1) / C);
+  int at;
+  const Soft mine = stream(row, v0 + tid, v1, NT, at);
+  const Soft ws = soft_warp(mine);
+  if (lane == 0) warp_soft[w] = ws;
+  if (p.k > 0) {
+    unsigned long long head =
+        v0 + tid < v1 ? ranked(order_key(mine.z == 0.0f ? -INFINITY : mine.m), (uint32_t)at) : 0ull;
+#pragma unroll
+    for (int o = 1; o < GT; o <<= 1) {
+      const unsigned long long c = __shfl_xor_sync(0xFFFFFFFFu, head, o);
+      head = c > head ? c : head;
+    }
+    if (tid % GT == 0) heads[tid / GT] = head;
+    if (tid == 0) {
+      count = 0;
+      bound = 0ull;
+    }
+    if (tid < kMaxTop) cand[tid] = -1;
+  }
+  __syncthreads();
+  Soft s = warp_soft[0];
+#pragma unroll
+  for (int i = 1; i < NW; ++i) s = soft_join(s, warp_soft[i]);
+
+  if (p.k > 0) {
+    if (tid < kGroups) {
+      const unsigned long long head = heads[tid];
+      int above = 0;
+#pragma unroll 16
+      for (int i = 0; i < kGroups; i += 2) {
+        const ulonglong2 h = *reinterpret_cast<const ulonglong2*>(heads + i);
+        above += (h.x > head) + (h.y > head);
+      }
+      if (head != 0ull && above < p.k) {
+        cand[above] = tid;
+        if (above == p.k - 1) bound = head;
+      }
     }
     __syncthreads();
-    if (lane == 0) best[warp] = mine;
-    __syncthreads();
-    last = best[0];
+    for (int c = w; c < p.k; c += NW) {                // one warp a group taken
+      const int g = cand[c];
+      if (g < 0) break;
+      for (int i = lane;; i += 32) {                   // its i-th vector
+        const int v = v0 + i / GT * NT + g * GT + i % GT;
+        if (v >= v1) break;
+        float f[VEC];
+        row.load(v, f);
 #pragma unroll
-    for (int w = 1; w < 8; ++w) last = best[w] > last ? best[w] : last;
-    if (tid == 0) {
-      const bool bad = logz != logz;
-      p.top_val[row * p.k + i] = bad ? NAN : empty ? -INFINITY : key_value((uint32_t)(last >> 32)) - s.m - logz;
-      p.top_id[row * p.k + i] = bad ? -1 : (int64_t)(0xFFFFFFFFu - (uint32_t)last);
+        for (int j = 0; j < VEC; ++j) {
+          const int id = row.first(v) + j;
+          const uint32_t key = order_key(f[j]);
+          if (id >= 0 && id < p.V && ranked(key, (uint32_t)v) >= bound) {
+            const int n = atomicAdd(&count, 1);
+            if (n < kList) list[n] = ranked(key, (uint32_t)id);
+          }
+        }
+      }
+    }
+    __syncthreads();
+    const int n = count;
+    const int id0 = max(row.first(v0), 0), id1 = min(row.first(v1), p.V);
+    if (tid < kMaxTop) tops[part][tid] = 0ull;         // fewer logits than k in this run
+    __syncthreads();
+    if (n <= kList) {
+      for (int i = tid; i < n; i += NT) {
+        const unsigned long long c = list[i];
+        int rank = 0;
+        for (int j = 0; j < n; ++j) rank += list[j] > c;
+        if (rank < p.k) tops[part][rank] = c;
+      }
+      __syncthreads();
+    } else {
+      unsigned long long last = ~0ull;
+      for (int i = 0; i < p.k; ++i) {
+        unsigned long long best = 0ull;
+        for (int id = id0 + tid; id < id1; id += NT) {
+          const unsigned long long c = ranked(order_key(to_f(row.base[row.off + id])), (uint32_t)id);
+          if (c < last && c > best) best = c;
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+          const unsigned long long c = __shfl_xor_sync(0xFFFFFFFFu, best, o);
+          best = c > best ? c : best;
+        }
+        if (lane == 0) best_of[w] = best;
+        __syncthreads();
+        last = best_of[0];
+#pragma unroll
+        for (int q = 1; q < NW; ++q) last = best_of[q] > last ? best_of[q] : last;
+        __syncthreads();
+        if (tid == 0) tops[part][i] = last;
+      }
+      __syncthreads();
     }
   }
+
+  if (C > 1) {
+    cluster_sync();                                    // every CTA of the cluster runs
+    if (part > 0) {
+      if (tid == 0) {
+        const uint32_t a = in_cluster(&parts[part], 0);
+        asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(a), "f"(s.m) : "memory");
+        asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(a + 4), "f"(s.z) : "memory");
+        asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(a + 8), "f"(s.u) : "memory");
+      }
+      if (tid < p.k)
+        asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(in_cluster(&tops[part][tid], 0)), "l"(tops[part][tid])
+                     : "memory");
+    }
+    cluster_sync();
+    if (part > 0) return;
+    for (int i = 1; i < C; ++i) s = soft_join(s, parts[i]);
+  }
+  if (tid == 0) finish_row<T>(p, r, s);
+  for (int i = tid; i < C * kMaxTop; i += NT) {
+    const int q = i / kMaxTop, j = i % kMaxTop;
+    const unsigned long long c = j < p.k ? tops[q][j] : 0ull;
+    if (c == 0ull) continue;
+    int rank = j;                                      // within its own part
+    for (int o = 0; o < C; ++o)
+      if (o != q)
+        for (int l = 0; l < p.k && tops[o][l] > c; ++l) ++rank;
+    if (rank < p.k) put_top(p, r, rank, c, s);
+  }
+}
+
+template <class T, int NT> int launch_row(const LogprobParams& p, int C, cudaStream_t st) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.blockDim = dim3(NT);
+  cfg.stream = st;
+  cudaLaunchAttribute at;
+  at.id = cudaLaunchAttributeClusterDimension;
+  at.val.clusterDim.x = (unsigned)C;
+  at.val.clusterDim.y = at.val.clusterDim.z = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = C > 1 ? 1 : 0;
+  cfg.gridDim = dim3((unsigned)(p.T * C));               // C > 1 only for few rows
+  if (cudaLaunchKernelEx(&cfg, logprob_row_kernel<T, NT>, p, C) != cudaSuccess) return emu_ops_launched("emu_token_logprobs");
+  return EMU_OK;
+}
+
+template <class T> int pick_logprob(const LogprobParams& p, cudaStream_t st) {
+  const int nvec = (int)(((int64_t)p.V + Row<T>::VEC - 1) / Row<T>::VEC);
+  if (nvec <= 256) {
+    logprob_warp_kernel<T><<<(unsigned)((p.T + kWarpRows - 1) / kWarpRows), 32 * kWarpRows, 0, st>>>(p);
+    return EMU_OK;
+  }
+  if (nvec <= 1024 && p.T >= 2 * emu_ops_sm_count()) return launch_row<T, 128>(p, 1, st);
+  int C = 1;                                            // until two CTAs an SM, four vectors a thread
+  while (C < kMaxCluster && p.T * C < 2 * emu_ops_sm_count() && nvec >= 2 * C * 512 * 4) C *= 2;
+  return launch_row<T, 512>(p, C, st);
 }
 
 struct LogprobGradParams {
@@ -142,28 +428,74 @@ struct LogprobGradParams {
   void* gx; int64_t ldo;
 };
 
-// gx = gl ([v = token] - p) - ge p (log p + H), log p = (x - m) - log z, one CTA a row
-template <class T>
+// gx = gl ([v = token] - p) - ge p (log p + H), log p = (x - m) - log z.  TPR threads a row and part of
+// it, four vectors each; `same` says that logits and gradient rows lie alike about 16-byte
+// addresses.
+template <class T, int TPR>
 __global__ void __launch_bounds__(256)
-logprob_grad_kernel(const LogprobGradParams p) {
-  const int64_t row = blockIdx.x;
-  const T* x = static_cast<const T*>(p.x) + row * p.ldx;
-  T* gx = static_cast<T*>(p.gx) + row * p.ldo;
-  const float m = p.stats[row * 3], logz = p.stats[row * 3 + 1], H = p.stats[row * 3 + 2];
-  const int64_t tok = p.tokens[row];
+logprob_grad_kernel(const LogprobGradParams p, int parts, bool same) {
+  constexpr int VEC = Row<T>::VEC, U = 4;
+  const int t = threadIdx.x % TPR;
+  const int64_t unit = (int64_t)blockIdx.x * (256 / TPR) + threadIdx.x / TPR;
+  const int64_t r = unit / parts;
+  if (r >= p.T) return;
+  const Row<T> row(static_cast<const T*>(p.x) + r * p.ldx, p.V);
+  T* gx = static_cast<T*>(p.gx) + r * p.ldo;
+  const float m = p.stats[r * 3], logz = p.stats[r * 3 + 1], H = p.stats[r * 3 + 2];
+  const int64_t tok = p.tokens[r];
   const bool out_of_range = tok != p.ignore && (tok < 0 || tok >= p.V);
-  const float gl = tok == p.ignore || !p.g_logprob ? 0.0f : out_of_range ? NAN : p.g_logprob[row];
-  const float ge = p.g_entropy ? p.g_entropy[row] : 0.0f;
+  const float gl = tok == p.ignore || !p.g_logprob ? 0.0f : out_of_range ? NAN : p.g_logprob[r];
+  const float ge = p.g_entropy ? p.g_entropy[r] : 0.0f;
   const bool empty = m == -INFINITY && logz == -INFINITY;
-  for (int v = threadIdx.x; v < p.V; v += 256) {
-    float r = 0.0f;
-    if (!empty) {
-      const float lp = to_f(x[v]) - m - logz;
+  const int hot = tok >= 0 && tok < p.V ? (int)tok : -1;
+  const int v0 = (int)(unit - r * parts) * (TPR * U) + t;
+  float f[U][VEC];
+#pragma unroll
+  for (int i = 0; i < U; ++i)
+    if (v0 + i * TPR < row.nvec) row.load(v0 + i * TPR, f[i]);
+#pragma unroll
+  for (int i = 0; i < U; ++i) {
+    const int v = v0 + i * TPR;
+    if (v >= row.nvec) break;
+    const int id0 = row.first(v);
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) {
+      const float lp = f[i][j] - m - logz;
       const float pr = exp2_approx(lp * kLog2e);
-      r = -pr * fmaf(ge, max_nan(lp, -1e4f) + H, gl);
-      if (v == tok) r += gl;
+      float g = -pr * fmaf(ge, max_nan(lp, -1e4f) + H, gl);
+      if (id0 + j == hot) g += gl;
+      f[i][j] = empty ? 0.0f : g;
     }
-    gx[v] = from_f<T>(r);
+    if (same && row.whole(v)) {
+      store_f<T, VEC>(gx + id0, f[i]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < VEC; ++j)
+        if (id0 + j >= 0 && id0 + j < p.V) gx[id0 + j] = from_f<T>(f[i][j]);
+    }
+  }
+}
+
+template <class T> void pick_logprob_grad(const LogprobGradParams& p, cudaStream_t st) {
+  const int nvec = p.V / Row<T>::VEC + 2;                // at most, wherever a row starts
+  const bool same = ((reinterpret_cast<uintptr_t>(p.x) ^ reinterpret_cast<uintptr_t>(p.gx)) & 15u) == 0 &&
+                    ((p.ldx - p.ldo) * (int64_t)sizeof(T)) % 16 == 0;
+  // rows of parts, at most 2^31 - 1 CTAs a launch
+  const int tpr = nvec <= 256 ? 32 : 256;
+  const int parts = (nvec + tpr * 4 - 1) / (tpr * 4);
+  const int64_t rows = ((int64_t)1 << 30) / parts;
+  for (int64_t r = 0; r < p.T; r += rows) {
+    LogprobGradParams q = p;
+    q.T = p.T - r < rows ? p.T - r : rows;
+    q.x = static_cast<const T*>(p.x) + r * p.ldx;
+    q.gx = static_cast<T*>(p.gx) + r * p.ldo;
+    q.tokens += r;
+    q.stats += 3 * r;
+    if (q.g_logprob) q.g_logprob += r;
+    if (q.g_entropy) q.g_entropy += r;
+    const int64_t units = q.T * parts;
+    if (tpr == 32) logprob_grad_kernel<T, 32><<<(unsigned)((units + 7) / 8), 256, 0, st>>>(q, parts, same);
+    else logprob_grad_kernel<T, 256><<<(unsigned)units, 256, 0, st>>>(q, parts, same);
   }
 }
 
@@ -207,9 +539,10 @@ int emu_token_logprobs(const void* logits, int64_t ldx, emu_out_t type, const in
   p.T = T; p.V = (int)V; p.k = top_k;
   p.logprob = logprob; p.entropy = entropy; p.lse = lse; p.stats = stats; p.top_val = top_logprobs; p.top_id = top_ids;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (type == EMU_OUT_F32) logprob_kernel<float><<<(unsigned)T, 256, 0, st>>>(p);
-  else if (type == EMU_OUT_BF16) logprob_kernel<__nv_bfloat16><<<(unsigned)T, 256, 0, st>>>(p);
-  else logprob_kernel<__half><<<(unsigned)T, 256, 0, st>>>(p);
+  if (type == EMU_OUT_F32) rc = pick_logprob<float>(p, st);
+  else if (type == EMU_OUT_BF16) rc = pick_logprob<__nv_bfloat16>(p, st);
+  else rc = pick_logprob<__half>(p, st);
+  if (rc != EMU_OK) return rc;
   return emu_ops_launched("emu_token_logprobs");
 }
 
@@ -231,9 +564,9 @@ int emu_token_logprobs_backward(const void* logits, int64_t ldx, emu_out_t type,
   p.stats = stats; p.g_logprob = grad_logprob; p.g_entropy = grad_entropy;
   p.gx = grad_logits; p.ldo = ldo;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (type == EMU_OUT_F32) logprob_grad_kernel<float><<<(unsigned)T, 256, 0, st>>>(p);
-  else if (type == EMU_OUT_BF16) logprob_grad_kernel<__nv_bfloat16><<<(unsigned)T, 256, 0, st>>>(p);
-  else logprob_grad_kernel<__half><<<(unsigned)T, 256, 0, st>>>(p);
+  if (type == EMU_OUT_F32) pick_logprob_grad<float>(p, st);
+  else if (type == EMU_OUT_BF16) pick_logprob_grad<__nv_bfloat16>(p, st);
+  else pick_logprob_grad<__half>(p, st);
   return emu_ops_launched("emu_token_logprobs_backward");
 }
 
