@@ -71,16 +71,21 @@ template <class T> struct Row {
   }
   __device__ __forceinline__ int first(int v) const { return v * VEC - off; }
   __device__ __forceinline__ bool whole(int v) const { return first(v) >= 0 && first(v) + VEC <= V; }
-  __device__ __forceinline__ void load(int v, float (&f)[VEC]) const {
-    if (whole(v)) {
-      load_f<T, VEC>(base + (int64_t)v * VEC, f);
-    } else {
+  __device__ __forceinline__ uint4 load_raw(int v) const {
+    if (whole(v)) return *reinterpret_cast<const uint4*>(base + (int64_t)v * VEC);
+    Pack<T, VEC> q;
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) {
-        const int i = first(v) + j;
-        f[j] = i >= 0 && i < V ? to_f(base[off + i]) : -INFINITY;
-      }
+    for (int j = 0; j < VEC; ++j) {
+      const int i = first(v) + j;
+      q.v[j] = i >= 0 && i < V ? base[off + i] : from_f<T>(-INFINITY);
     }
+    return *reinterpret_cast<const uint4*>(&q);
+  }
+  __device__ __forceinline__ void load(int v, float (&f)[VEC]) const { unpack(load_raw(v), f); }
+  static __device__ __forceinline__ void unpack(const uint4& raw, float (&f)[VEC]) {
+    const Pack<T, VEC> q = *reinterpret_cast<const Pack<T, VEC>*>(&raw);
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) f[j] = to_f(q.v[j]);
   }
 };
 
@@ -89,43 +94,161 @@ __device__ __forceinline__ unsigned long long ranked(uint32_t key, uint32_t pos)
   return ((unsigned long long)key << 32) | (0xFFFFFFFFu - pos);
 }
 
-// A thread's pass over the vectors v0, v0 + step, ... below v1: its Soft, and where in its vectors its
-// largest logit first stands.
-template <class T>
-__device__ __forceinline__ Soft stream(const Row<T>& row, int v0, int v1, int step, int& at) {
-  constexpr int VEC = Row<T>::VEC, U = 4;
-  Soft s{kLowest, 0.0f, 0.0f};
-  at = v0;
-  for (int v = v0; v < v1; v += step * U) {
-    float f[U][VEC];
+// The largest and the smallest of N vectors' logits (NaN left out), two at a time in 16-bit types.
+template <int N> __device__ __forceinline__ void extremes(const uint4 (&raw)[N], float& hi, float& lo, float) {
+  hi = -INFINITY;
+  lo = INFINITY;
 #pragma unroll
-    for (int i = 0; i < U; ++i) {
-      if (v + i * step < v1) {
-        row.load(v + i * step, f[i]);
-      } else {
+  for (int i = 0; i < N; ++i) {
+    float f[4];
+    Row<float>::unpack(raw[i], f);
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) f[i][j] = -INFINITY;
+    for (int j = 0; j < 4; ++j) {
+      hi = fmaxf(hi, f[j]);
+      lo = fminf(lo, f[j]);
+    }
+  }
+}
+template <class P, int N> __device__ __forceinline__ void extremes2(const uint4 (&raw)[N], P& h, P& l) {
+  h = l = *reinterpret_cast<const P*>(&raw[0].x);
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const P* q = reinterpret_cast<const P*>(&raw[i]);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      h = __hmax2(h, q[j]);
+      l = __hmin2(l, q[j]);
+    }
+  }
+}
+template <int N> __device__ __forceinline__ void extremes(const uint4 (&raw)[N], float& hi, float& lo, __nv_bfloat16) {
+  __nv_bfloat162 h, l;
+  extremes2(raw, h, l);
+  hi = fmaxf(__bfloat162float(h.x), __bfloat162float(h.y));
+  lo = fminf(__bfloat162float(l.x), __bfloat162float(l.y));
+}
+template <int N> __device__ __forceinline__ void extremes(const uint4 (&raw)[N], float& hi, float& lo, __half) {
+  __half2 h, l;
+  extremes2(raw, h, l);
+  hi = fmaxf(__half2float(h.x), __half2float(h.y));
+  lo = fminf(__half2float(l.x), __half2float(l.y));
+}
+
+// fp32 pairs: one instruction for two logits
+typedef unsigned long long f2;
+__device__ __forceinline__ f2 pair(float a, float b) {
+  f2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void halves(f2 v, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+__device__ __forceinline__ f2 add2(f2 a, f2 b) {
+  f2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+  f2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
+// A thread's part of a row.  Vectors whose logits are all within +-1e6 take the fast form: with
+// L = log2 e and c = fp32(m L), a = x L - c is one rounding, e = 2^a, and the sums of e and e a
+// run in fp32 pairs, about five instructions a logit.  (c differs from m L by a rounding that is
+// the same for every logit, below 0.1; it is taken out at the end as d = c - m L.)  The others,
+// -inf among them, and the row's ragged ends go by x - m one by one.
+template <class T> struct Streamed {
+  static constexpr int VEC = Row<T>::VEC;
+  float m = kLowest, c = kLowest;      // of the fast form
+  f2 z = 0ull, w = 0ull;               // sums of e, of e a
+  Soft slow{kLowest, 0.0f, 0.0f};
+  float top = -INFINITY;               // the largest logit and the vector where it first stands
+  int at;
+
+  template <int N> __device__ __forceinline__ void take(const uint4 (&raw)[N], int v, int step) {
+    float hi, lo;
+    extremes(raw, hi, lo, T());
+    if (hi > top) {
+      top = hi;
+#pragma unroll
+      for (int i = N - 1; i >= 0; --i) {
+        const uint4 one[1] = {raw[i]};
+        float h, l;
+        extremes(one, h, l, T());
+        if (h == hi) at = v + i * step;
       }
     }
-#pragma unroll
-    for (int i = 0; i < U; ++i) {
-      float m = f[i][0];
-#pragma unroll
-      for (int j = 1; j < VEC; ++j) m = fmaxf(m, f[i][j]);
-      if (m > s.m || (m == s.m && s.z == 0.0f)) {        // the latter: the lowest finite number itself
-        const float d = fmaxf(s.m - m, -1e4f), e = exp2_approx(d * kLog2e);
-        s.u = (s.u + s.z * d) * e;
-        s.z *= e;
-        s.m = m;
-        at = v + i * step;
+    if (lo >= -1e6f && hi <= 1e6f) {
+      if (hi > m) {
+        const float cn = hi * kLog2e, d = fmaxf(c - cn, -1e4f), e = exp2_approx(d);
+        const f2 e2 = pair(e, e);
+        w = fma2(fma2(pair(d, d), z, w), e2, 0ull);
+        z = fma2(z, e2, 0ull);
+        m = hi;
+        c = cn;
       }
+      const f2 L2 = pair(kLog2e, kLog2e), c2 = pair(-c, -c);
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        float f[VEC];
+        Row<T>::unpack(raw[i], f);
+#pragma unroll
+        for (int j = 0; j < VEC; j += 2) {
+          const f2 a = fma2(pair(f[j], f[j + 1]), L2, c2);
+          float a0, a1;
+          halves(a, a0, a1);
+          const f2 e = pair(exp2_approx(a0), exp2_approx(a1));
+          z = add2(z, e);
+          w = fma2(e, a, w);
+        }
+      }
+      return;
+    }
+    if (hi > slow.m) {
+      const float d = fmaxf(slow.m - hi, -1e4f), e = exp2_approx(d * kLog2e);
+      slow.u = (slow.u + slow.z * d) * e;
+      slow.z *= e;
+      slow.m = hi;
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      float f[VEC];
+      Row<T>::unpack(raw[i], f);
 #pragma unroll
       for (int j = 0; j < VEC; ++j) {
-        const float t = f[i][j] - s.m, e = exp2_approx(t * kLog2e);
-        s.z += e;
-        s.u = fmaf(e, fmaxf(t, -1e4f), s.u);
+        const float t = f[j] - slow.m, e = exp2_approx(t * kLog2e);
+        slow.z += e;
+        slow.u = fmaf(e, fmaxf(t, -1e4f), slow.u);
       }
     }
+  }
+  __device__ __forceinline__ Soft sums() const {
+    float z0, z1, w0, w1;
+    halves(z, z0, z1);
+    halves(w, w0, w1);
+    const float d = m > kLowest ? fmaf(-m, kLog2e, c) : 0.0f, e = exp2_approx(d);
+    const float zz = z0 + z1;
+    return soft_join(Soft{m, zz * e, (w0 + w1 + d * zz) * e * 0.693147181f}, slow);
+  }
+};
+
+// the vectors v0, v0 + step, ... below v1
+template <class T>
+__device__ __forceinline__ Streamed<T> stream(const Row<T>& row, int v0, int v1, int step) {
+  constexpr int U = 4;
+  Streamed<T> s;
+  s.at = v0;
+  int v = v0;
+  for (; v + (U - 1) * step < v1; v += step * U) {
+    uint4 raw[U];
+#pragma unroll
+    for (int i = 0; i < U; ++i) raw[i] = row.load_raw(v + i * step);
+    s.take(raw, v, step);
+  }
+  for (; v < v1; v += step) {
+    const uint4 raw[1] = {row.load_raw(v)};
+    s.take(raw, v, step);
   }
   return s;
 }
@@ -175,16 +298,15 @@ logprob_warp_kernel(const LogprobParams p) {
   const int64_t r = (int64_t)blockIdx.x * kWarpRows + w;
   if (r >= p.T) return;
   const Row<T> row(static_cast<const T*>(p.x) + r * p.ldx, p.V);
-  int at;
-  const Soft mine = stream(row, lane, row.nvec, 32, at);
-  const Soft s = soft_warp(mine);
+  const Streamed<T> mine = stream(row, lane, row.nvec, 32);
+  const Soft s = soft_warp(mine.sums());
   if (lane == 0) finish_row<T>(p, r, s);
   if (p.k == 0) return;
   unsigned long long* list = list_all[w];
   int& count = count_all[w];
   if (lane == 0) count = 0;
   const unsigned long long head =
-      lane < row.nvec ? ranked(order_key(mine.z == 0.0f ? -INFINITY : mine.m), (uint32_t)at) : 0ull;
+      lane < row.nvec ? ranked(order_key(mine.top), (uint32_t)mine.at) : 0ull;
   int above = 0;
 #pragma unroll
   for (int i = 0; i < 32; ++i) above += __shfl_sync(0xFFFFFFFFu, head, i) > head;
@@ -265,13 +387,12 @@ logprob_row_kernel(const LogprobParams p, int C) {
   const int part = blockIdx.x % C;
   const Row<T> row(static_cast<const T*>(p.x) + r * p.ldx, p.V);
   const int v0 = (int)((int64_t)row.nvec * part / C), v1 = (int)((int64_t)row.nvec * (part + 1) / C);
-  int at;
-  const Soft mine = stream(row, v0 + tid, v1, NT, at);
-  const Soft ws = soft_warp(mine);
+  const Streamed<T> mine = stream(row, v0 + tid, v1, NT);
+  const Soft ws = soft_warp(mine.sums());
   if (lane == 0) warp_soft[w] = ws;
   if (p.k > 0) {
     unsigned long long head =
-        v0 + tid < v1 ? ranked(order_key(mine.z == 0.0f ? -INFINITY : mine.m), (uint32_t)at) : 0ull;
+        v0 + tid < v1 ? ranked(order_key(mine.top), (uint32_t)mine.at) : 0ull;
 #pragma unroll
     for (int o = 1; o < GT; o <<= 1) {
       const unsigned long long c = __shfl_xor_sync(0xFFFFFFFFu, head, o);
