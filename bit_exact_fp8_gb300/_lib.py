@@ -5,9 +5,11 @@ missing, every call raises."""
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
 
-from .build import LIB
+from .build import LIB, OPS_LIB
 
 EMU_OK = 0
 EMU_EINVAL = -1
@@ -126,6 +128,20 @@ def load(path: str = LIB) -> ctypes.CDLL:
     L.emu_abi_version.restype = ctypes.c_int
     _handle = L
     return L
+
+
+def load_ops(path: str = OPS_LIB):
+    """The extension module of the operators' torch-facing calls (ops_torch.cpp), beside the
+    libemufp8 it is linked to; raises OSError if it has not been built."""
+    load()
+    if not os.path.exists(path):
+        raise OSError(f"the operators' extension is not built ({path} missing): run "
+                      "python -m bit_exact_fp8_gb300.build")
+    loader = importlib.machinery.ExtensionFileLoader("_ops_torch", path)
+    spec = importlib.util.spec_from_file_location("_ops_torch", path, loader=loader)
+    module = importlib.util.module_from_spec(spec)
+    loader.exec_module(module)
+    return module
 
 
 def emu_preset_get(name: str) -> emu_preset_t:

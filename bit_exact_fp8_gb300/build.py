@@ -1,5 +1,6 @@
 """Build libemufp8.so (the GEMM library) and libemupeaks.so (the instruction-rate
-microbenchmark bench.py divides by) in-tree with nvcc for sm_103a (GB300).
+microbenchmark bench.py divides by) in-tree with nvcc for sm_103a (GB300), and the
+operators' torch-facing calls (_ops_torch.so) with the host compiler.
 
     python -m bit_exact_fp8_gb300.build [--force]
 
@@ -13,6 +14,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -20,12 +22,16 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libemufp8.so")
 PEAKS_LIB = os.path.join(PKG, "libemupeaks.so")
+OPS_LIB = os.path.join(PKG, "_ops_torch.so")
 SOURCES = [os.path.join(CSRC, f) for f in ("emu_api.cu", "ops_norm.cu", "ops_int8.cu",
                                            "ops_logprob.cu")]
 PEAKS_SOURCES = [os.path.join(CSRC, "emu_peaks.cu")]
 PEAKS_DEPS = PEAKS_SOURCES + [os.path.join(INCLUDE, "emu_peaks.h")]
 DEPS = SOURCES + [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cuh", ".h"))] \
     + [os.path.join(INCLUDE, "emu_fp8.h")]
+
+OPS_SOURCES = [os.path.join(CSRC, "ops_torch.cpp")]
+OPS_DEPS = OPS_SOURCES + [os.path.join(INCLUDE, "emu_fp8.h")]
 
 NVCC_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a", "-O3", "-lineinfo", "-std=c++17",
               "-Xcompiler", "-fPIC", "-shared", "--threads", "0", "-I" + INCLUDE, "-I" + CSRC]
@@ -49,12 +55,35 @@ def _up_to_date(lib: str, deps) -> bool:
 
 
 def up_to_date() -> bool:
-    return _up_to_date(LIB, DEPS) and _up_to_date(PEAKS_LIB, PEAKS_DEPS)
+    return _up_to_date(LIB, DEPS) and _up_to_date(PEAKS_LIB, PEAKS_DEPS) and _up_to_date(OPS_LIB, OPS_DEPS)
+
+
+def ops_commands(out: str) -> "tuple[list, list]":
+    """The host compiler's commands that make the operators' extension from its source: one
+    that compiles, and one that links it to torch and to the libemufp8 beside it."""
+    import torch
+    from torch.utils.cpp_extension import include_paths, library_paths
+    cuda = os.path.dirname(os.path.dirname(nvcc_path()))
+    obj = out + ".o"
+    includes = [INCLUDE] + include_paths() + [os.path.join(cuda, "include"), sysconfig.get_paths()["include"]]
+    compile_ = ["g++", "-O2", "-std=c++17", "-fPIC", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"]
+    compile_ += [f"-I{d}" for d in includes] + ["-c"] + OPS_SOURCES + ["-o", obj]
+    link = ["g++", "-shared", obj, "-o", out, f"-L{PKG}", "-l:" + os.path.basename(LIB), "-Wl,-rpath,$ORIGIN"]
+    link += [f"-L{d}" for d in library_paths()] + ["-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10"]
+    return compile_, link
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile whichever of the two libraries is stale; returns the GEMM library's path."""
+    """Compile whichever of the two libraries and the operators' extension is stale; returns the
+    GEMM library's path."""
     jobs = []
+    ops_tmp = OPS_LIB + f".tmp{os.getpid()}"
+    ops_stale = force or not _up_to_date(OPS_LIB, OPS_DEPS)
+    if ops_stale:
+        ops_compile, ops_link = ops_commands(ops_tmp)
+        if verbose:
+            print(" ".join(ops_compile), file=sys.stderr)
+        ops_proc = subprocess.Popen(ops_compile)
     for lib, srcs, deps in ((LIB, SOURCES, DEPS), (PEAKS_LIB, PEAKS_SOURCES, PEAKS_DEPS)):
         if force or not _up_to_date(lib, deps):
             tmp = lib + f".tmp{os.getpid()}"
@@ -63,10 +92,16 @@ def build(force: bool = False, verbose: bool = False) -> str:
                 print(" ".join(cmd), file=sys.stderr)
             jobs.append((lib, tmp, subprocess.Popen(cmd)))
     failed = [lib for lib, _, proc in jobs if proc.wait() != 0]
+    if ops_stale and ops_proc.wait() != 0:
+        failed.append(OPS_LIB)
     if failed:
-        raise subprocess.CalledProcessError(1, f"nvcc ({', '.join(failed)})")
+        raise subprocess.CalledProcessError(1, f"nvcc or g++ ({', '.join(failed)})")
     for lib, tmp, _ in jobs:
         os.replace(tmp, lib)
+    if ops_stale:
+        subprocess.run(ops_link, check=True)
+        os.replace(ops_tmp, OPS_LIB)
+        os.remove(ops_tmp + ".o")
     return LIB
 
 

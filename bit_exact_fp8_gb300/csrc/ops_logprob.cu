@@ -134,6 +134,21 @@ template <int N> __device__ __forceinline__ void extremes(const uint4 (&raw)[N],
   lo = fminf(__half2float(l.x), __half2float(l.y));
 }
 
+// Logits below about -65504 moved up to there (NaN kept): next to one of -6e4 or more their weight is 0
+// as it was, and x - m is finite.
+__device__ __forceinline__ void floor_at(uint4& raw, float) {
+  float* f = reinterpret_cast<float*>(&raw);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) f[j] = max_nan(f[j], -65536.0f);
+}
+template <class P> __device__ __forceinline__ void floor2(uint4& raw, P low) {
+  P* q = reinterpret_cast<P*>(&raw);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) q[j] = __hmax2_nan(q[j], low);
+}
+__device__ __forceinline__ void floor_at(uint4& raw, __nv_bfloat16) { floor2(raw, __float2bfloat162_rn(-65536.0f)); }
+__device__ __forceinline__ void floor_at(uint4& raw, __half) { floor2(raw, __float2half2_rn(-65504.0f)); }
+
 // fp32 pairs: one instruction for two logits
 typedef unsigned long long f2;
 __device__ __forceinline__ f2 pair(float a, float b) {
@@ -153,11 +168,11 @@ __device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
   return r;
 }
 
-// A thread's part of a row.  Vectors whose logits are all within +-1e6 take the fast form: with
-// L = log2 e and c = fp32(m L), a = x L - c is one rounding, e = 2^a, and the sums of e and e a
-// run in fp32 pairs, about five instructions a logit.  (c differs from m L by a rounding that is
-// the same for every logit, below 0.1; it is taken out at the end as d = c - m L.)  The others,
-// -inf among them, and the row's ragged ends go by x - m one by one.
+// A thread's part of a row.  Vectors whose largest logit is within -6e4 and 1e6 take the fast form:
+// with L = log2 e and c = fp32(m L), a = x L - c is one rounding, e = 2^a, and the sums of e and
+// e a run in fp32 pairs, about five instructions a logit.  (c differs from m L by a rounding that
+// is the same for every logit, below 0.1; it is taken out at the end as d = c - m L.)  The others
+// (masked whole, or out of range) go by x - m one by one.
 template <class T> struct Streamed {
   static constexpr int VEC = Row<T>::VEC;
   float m = kLowest, c = kLowest;      // of the fast form
@@ -166,7 +181,7 @@ template <class T> struct Streamed {
   float top = -INFINITY;               // the largest logit and the vector where it first stands
   int at;
 
-  template <int N> __device__ __forceinline__ void take(const uint4 (&raw)[N], int v, int step) {
+  template <int N> __device__ __forceinline__ void take(uint4 (&raw)[N], int v, int step) {
     float hi, lo;
     extremes(raw, hi, lo, T());
     if (hi > top) {
@@ -179,7 +194,11 @@ template <class T> struct Streamed {
         if (h == hi) at = v + i * step;
       }
     }
-    if (lo >= -1e6f && hi <= 1e6f) {
+    if (hi >= -6e4f && hi <= 1e6f) {
+      if (!(lo >= -65504.0f)) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) floor_at(raw[i], T());
+      }
       if (hi > m) {
         const float cn = hi * kLog2e, d = fmaxf(c - cn, -1e4f), e = exp2_approx(d);
         const f2 e2 = pair(e, e);
@@ -247,7 +266,7 @@ __device__ __forceinline__ Streamed<T> stream(const Row<T>& row, int v0, int v1,
     s.take(raw, v, step);
   }
   for (; v < v1; v += step) {
-    const uint4 raw[1] = {row.load_raw(v)};
+    uint4 raw[1] = {row.load_raw(v)};
     s.take(raw, v, step);
   }
   return s;
@@ -286,14 +305,39 @@ __device__ __forceinline__ void put_top(const LogprobParams& p, int64_t row, int
 // with their vectors' positions, so equal logits come out by lower id and a row of equal ones
 // lists few.  A list too short (many large logits at one period) is made up for by k searches.
 //
+// The logits of one vector that reach the bound, onto the list.
+template <class T>
+__device__ __forceinline__ void collect_vector(const Row<T>& row, int v, const uint4& raw, float least,
+                                               unsigned long long bound, unsigned long long* list, int room, int* count) {
+  constexpr int VEC = Row<T>::VEC;
+  float hi, lo;
+  const uint4 one[1] = {raw};
+  extremes(one, hi, lo, T());
+  if (!(hi >= least)) return;
+  float f[VEC];
+  Row<T>::unpack(raw, f);
+#pragma unroll
+  for (int j = 0; j < VEC; ++j) {
+    const int id = row.first(v) + j;
+    const uint32_t key = order_key(f[j]);
+    if (id >= 0 && id < row.V && ranked(key, (uint32_t)v) >= bound) {
+      const int n = atomicAdd(count, 1);
+      if (n < room) list[n] = ranked(key, (uint32_t)id);
+    }
+  }
+}
+__device__ __forceinline__ float least_of(unsigned long long bound) {
+  return bound ? key_value((uint32_t)(bound >> 32)) : -INFINITY;
+}
+
 // One warp a row: for short rows.
-constexpr int kWarpRows = 8, kWarpList = 256;
+constexpr int kWarpRows = 4, kWarpList = 256;
 template <class T>
 __global__ void __launch_bounds__(32 * kWarpRows)
 logprob_warp_kernel(const LogprobParams p) {
   __shared__ unsigned long long list_all[kWarpRows][kWarpList];
+  __shared__ int cand_all[kWarpRows][kMaxTop];
   __shared__ int count_all[kWarpRows];
-  constexpr int VEC = Row<T>::VEC;
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int64_t r = (int64_t)blockIdx.x * kWarpRows + w;
   if (r >= p.T) return;
@@ -312,21 +356,23 @@ logprob_warp_kernel(const LogprobParams p) {
   for (int i = 0; i < 32; ++i) above += __shfl_sync(0xFFFFFFFFu, head, i) > head;
   const uint32_t kth = __ballot_sync(0xFFFFFFFFu, head != 0ull && above == p.k - 1);
   const unsigned long long bound = kth ? __shfl_sync(0xFFFFFFFFu, head, __ffs(kth) - 1) : 0ull;
+  if (head != 0ull && above < p.k) cand_all[w][above] = lane;
+  const int taken = __popc(__ballot_sync(0xFFFFFFFFu, head != 0ull && above < p.k));
   __syncwarp();
-  if (head != 0ull && above < p.k) {
-    for (int v = lane; v < row.nvec; v += 32) {
-      float f[VEC];
-      row.load(v, f);
+  const float least = least_of(bound);
+  const int len = (row.nvec + 31) / 32;                // a lane's vectors
+  for (int q0 = lane; q0 < taken * len; q0 += 128) {   // those of the lanes taken, four at a time
+    uint4 raw[4];
+    int at[4];
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) {
-        const int id = row.first(v) + j;
-        const uint32_t key = order_key(f[j]);
-        if (id >= 0 && id < p.V && ranked(key, (uint32_t)v) >= bound) {
-          const int n = atomicAdd(&count, 1);
-          if (n < kWarpList) list[n] = ranked(key, (uint32_t)id);
-        }
-      }
+    for (int u = 0; u < 4; ++u) {
+      const int q = q0 + u * 32, c = q / len;
+      at[u] = q < taken * len ? (q - c * len) * 32 + cand_all[w][c] : row.nvec;
+      if (at[u] < row.nvec) raw[u] = row.load_raw(at[u]);
     }
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      if (at[u] < row.nvec) collect_vector(row, at[u], raw[u], least, bound, list, kWarpList, &count);
   }
   __syncwarp();
   const int n = count;
@@ -370,14 +416,14 @@ __device__ __forceinline__ void cluster_sync() {
 // largest of each through distributed shared memory.
 constexpr int kGroups = 128, kList = 1024, kMaxCluster = 8;
 template <class T, int NT>
-__global__ void __launch_bounds__(NT)
+__global__ void __launch_bounds__(NT, 1280 / NT)
 logprob_row_kernel(const LogprobParams p, int C) {
-  constexpr int VEC = Row<T>::VEC, NW = NT / 32, GT = NT / kGroups;      // GT threads a group
+  constexpr int NW = NT / 32, GT = NT / kGroups;      // GT threads a group
   __shared__ Soft warp_soft[NW];
   __shared__ __align__(16) unsigned long long heads[kGroups];
   __shared__ int cand[kMaxTop];
   __shared__ unsigned long long bound;
-  __shared__ int count;
+  __shared__ int count, taken;
   __shared__ unsigned long long list[kList];
   __shared__ Soft parts[kMaxCluster];                                    // of the first CTA: all CTAs'
   __shared__ unsigned long long tops[kMaxCluster][kMaxTop];
@@ -400,10 +446,9 @@ logprob_row_kernel(const LogprobParams p, int C) {
     }
     if (tid % GT == 0) heads[tid / GT] = head;
     if (tid == 0) {
-      count = 0;
+      count = taken = 0;
       bound = 0ull;
     }
-    if (tid < kMaxTop) cand[tid] = -1;
   }
   __syncthreads();
   Soft s = warp_soft[0];
@@ -421,27 +466,22 @@ logprob_row_kernel(const LogprobParams p, int C) {
       }
       if (head != 0ull && above < p.k) {
         cand[above] = tid;
+        atomicAdd(&taken, 1);
         if (above == p.k - 1) bound = head;
       }
     }
     __syncthreads();
-    for (int c = w; c < p.k; c += NW) {                // one warp a group taken
-      const int g = cand[c];
-      if (g < 0) break;
-      for (int i = lane;; i += 32) {                   // its i-th vector
-        const int v = v0 + i / GT * NT + g * GT + i % GT;
-        if (v >= v1) break;
-        float f[VEC];
-        row.load(v, f);
+    const float least = least_of(bound);
+    for (int c = w; c < taken; c += NW) {              // a warp a group taken, four vectors a lane at a time
+      constexpr int ROUND = 32 / GT * NT;
+      for (int v = v0 + lane / GT * NT + cand[c] * GT + lane % GT; v < v1; v += 4 * ROUND) {
+        uint4 raw[4];
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) {
-          const int id = row.first(v) + j;
-          const uint32_t key = order_key(f[j]);
-          if (id >= 0 && id < p.V && ranked(key, (uint32_t)v) >= bound) {
-            const int n = atomicAdd(&count, 1);
-            if (n < kList) list[n] = ranked(key, (uint32_t)id);
-          }
-        }
+        for (int u = 0; u < 4; ++u)
+          if (v + u * ROUND < v1) raw[u] = row.load_raw(v + u * ROUND);
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+          if (v + u * ROUND < v1) collect_vector(row, v + u * ROUND, raw[u], least, bound, list, kList, &count);
       }
     }
     __syncthreads();
@@ -504,10 +544,16 @@ logprob_row_kernel(const LogprobParams p, int C) {
     const int q = i / kMaxTop, j = i % kMaxTop;
     const unsigned long long c = j < p.k ? tops[q][j] : 0ull;
     if (c == 0ull) continue;
-    int rank = j;                                      // within its own part
-    for (int o = 0; o < C; ++o)
-      if (o != q)
-        for (int l = 0; l < p.k && tops[o][l] > c; ++l) ++rank;
+    int rank = j;                                      // within its own part; and those above it in the others
+    for (int o = 0; o < C; ++o) {
+      if (o == q) continue;
+      int n = 0;                                       // the parts' lists fall: a search by halves
+#pragma unroll
+      for (int h = kMaxTop / 2; h > 0; h >>= 1)
+        if (n + h <= p.k && tops[o][n + h - 1] > c) n += h;
+      if (n < p.k && tops[o][n] > c) ++n;
+      rank += n;
+    }
     if (rank < p.k) put_top(p, r, rank, c, s);
   }
 }
@@ -529,14 +575,13 @@ template <class T, int NT> int launch_row(const LogprobParams& p, int C, cudaStr
 
 template <class T> int pick_logprob(const LogprobParams& p, cudaStream_t st) {
   const int nvec = (int)(((int64_t)p.V + Row<T>::VEC - 1) / Row<T>::VEC);
-  if (nvec <= 256) {
+  if (nvec <= 1024) {
     logprob_warp_kernel<T><<<(unsigned)((p.T + kWarpRows - 1) / kWarpRows), 32 * kWarpRows, 0, st>>>(p);
     return EMU_OK;
   }
-  if (nvec <= 1024 && p.T >= 2 * emu_ops_sm_count()) return launch_row<T, 128>(p, 1, st);
   int C = 1;                                            // until two CTAs an SM, four vectors a thread
-  while (C < kMaxCluster && p.T * C < 2 * emu_ops_sm_count() && nvec >= 2 * C * 512 * 4) C *= 2;
-  return launch_row<T, 512>(p, C, st);
+  while (C < kMaxCluster && p.T * C < 2 * emu_ops_sm_count() && nvec >= 2 * C * 256 * 4) C *= 2;
+  return launch_row<T, 256>(p, C, st);
 }
 
 struct LogprobGradParams {
