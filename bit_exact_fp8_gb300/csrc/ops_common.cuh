@@ -5,6 +5,7 @@
 
 #include "emu_fp8.h"
 
+#include <atomic>
 #include <cstdint>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -15,7 +16,9 @@ int emu_ops_fail(int code, const char* fmt, ...) __attribute__((format(printf, 2
 void emu_ops_begin();                          // clears the message and a stale launch error
 int emu_ops_launched(const char* what);        // EMU_OK, or EMU_ECUDA with the launch's error
 int emu_ops_sm_count();                        // SMs of the current device
-int emu_ops_device_status_int8(int* status, bool reset);   // ops_int8.cu
+int emu_ops_int8_status(int* status, bool reset);          // ops_int8.cu's device status word
+// the dynamic shared memory a kernel may take, set once a device (`done`: one flag a device)
+bool emu_ops_allow_smem(const void* kernel, int bytes, std::atomic<bool>* done);
 
 namespace emu_ops {
 
@@ -50,11 +53,57 @@ template <class T, int VEC> __device__ __forceinline__ void load_f(const T* p, f
 #pragma unroll
   for (int i = 0; i < VEC; ++i) f[i] = to_f(q.v[i]);
 }
+constexpr int kMaxSmem = 227 * 1024;              // dynamic shared memory of a CTA at most
+
 template <class T, int VEC> __device__ __forceinline__ void store_f(T* p, const float (&f)[VEC]) {
   Pack<T, VEC> q;
 #pragma unroll
   for (int i = 0; i < VEC; ++i) q.v[i] = from_f<T>(f[i]);
   *reinterpret_cast<Pack<T, VEC>*>(p) = q;
+}
+
+__device__ __forceinline__ uint32_t smem_addr(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
+
+// mbarriers and bulk copies (inline PTX)
+__device__ __forceinline__ void bar_init(uint32_t bar, uint32_t count) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
+}
+__device__ __forceinline__ void bar_init_fence() { asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory"); }
+__device__ __forceinline__ void bar_arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void bar_expect(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred P;\n mbarrier.try_wait.parity.shared::cta.b64 P, [%1], %2;\n selp.u32 %0, 1, 0, P;\n}"
+      : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+  return ok != 0u;
+}
+// polls before a wait gives up; each suspends the thread for a short time set by the hardware, so a wait
+// ends well within seconds
+constexpr uint32_t kPolls = 1u << 20;
+// Waits for the phase of this parity to complete; false once the limit is reached.
+__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity) {
+  for (uint32_t i = 0; i < kPolls; ++i)
+    if (bar_try(bar, parity)) return true;
+  return false;
+}
+// `bytes` (a multiple of 16) from 16-byte aligned memory to 16-byte aligned shared memory
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(src), "r"(bytes), "r"(bar) : "memory");
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// the address of `p`, of this CTA's shared memory, in that of the cluster's CTA `rank`
+__device__ __forceinline__ uint32_t in_cluster(const void* p, int rank) {
+  uint32_t a;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_addr(p)), "r"(rank));
+  return a;
 }
 
 // the larger of two, NaN if either is NaN

@@ -82,8 +82,6 @@ template <int MT> int launch_dot(const Int8Params& p, cudaStream_t st) {
   return EMU_OK;
 }
 
-__device__ __forceinline__ uint32_t smem_addr(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
-
 // Four codes as fp16 (exact: |code| <= 128 has at most eight significant bits).  With the sign
 // bit flipped a code is u = code + 128 in 0..255; the fp16 word 0x6400 | u is 1024 + u.
 __device__ __forceinline__ void codes_to_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
@@ -255,37 +253,25 @@ int8_mma_kernel(const Int8Params p, int S) {
       for (int e = 0; e < 4; e += 2)
         *reinterpret_cast<int2*>(own + ((wm * MT + i) * 16 + (e >> 1) * 8 + g) * BN + (wn * NT + j) * 8 + 2 * t) =
             make_int2(sum[i][j][e], sum[i][j][e + 1]);
-  asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  cluster_sync();
   for (int i = slice * NTH + tid; i < BM * BN; i += S * NTH) {
     const int64_t m = m0 + i / BN, n = n0 + i % BN;
     int v = 0;
     for (int r = 0; r < S; ++r) {
-      uint32_t at;
       int x;
-      asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_addr(own + i)), "r"(r));
-      asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(x) : "r"(at) : "memory");
+      asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(x) : "r"(in_cluster(own + i, r)) : "memory");
       v += x;
     }
     if (m < p.M && n < p.N) store_out(p, m, n, v);
   }
-  asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-
-// the dynamic shared memory limit of a kernel, set once a device
-template <class K> bool allow_smem(K kernel, int bytes, std::atomic<bool> (&done)[64]) {
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return false;
-  if (dev >= 0 && dev < 64 && done[dev].load(std::memory_order_acquire)) return true;
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return false;
-  if (dev >= 0 && dev < 64) done[dev].store(true, std::memory_order_release);
-  return true;
+  cluster_sync();
 }
 
 template <int WM, int WN, int MT, int NT> int launch_mma(const Int8Params& p, cudaStream_t st) {
   using SH = MmaShape<WM, WN, MT, NT>;
   auto kernel = int8_mma_kernel<WM, WN, MT, NT>;
   static std::atomic<bool> done[64];
-  if (!allow_smem(kernel, SH::SMEM, done)) return emu_ops_launched("cudaFuncSetAttribute");
+  if (!emu_ops_allow_smem(reinterpret_cast<const void*>(kernel), SH::SMEM, done)) return emu_ops_launched("cudaFuncSetAttribute");
   const int64_t tn = (p.N + SH::BN - 1) / SH::BN;
   // as many slices as fill the SMs twice over, of four stages at least
   const int sms = emu_ops_sm_count();
@@ -379,7 +365,7 @@ Plan plan_for(int64_t M, int64_t N, int64_t K, bool aligned16) {
 
 int launch_tc(const Int8Params& p, const Plan& pl, bool vec, unsigned char* ws, cudaStream_t st) {
   static std::atomic<bool> done[64];
-  if (!allow_smem(int8_tc_kernel, kTcSmem, done)) return emu_ops_launched("cudaFuncSetAttribute");
+  if (!emu_ops_allow_smem(reinterpret_cast<const void*>(int8_tc_kernel), kTcSmem, done)) return emu_ops_launched("cudaFuncSetAttribute");
   uint16_t* a16 = reinterpret_cast<uint16_t*>(ws);
   uint16_t* b16 = reinterpret_cast<uint16_t*>(ws + pl.a_bytes);
   const int sms = emu_ops_sm_count();
@@ -445,7 +431,7 @@ int run_plan(const Int8Params& p, bool vec, void* workspace, cudaStream_t st) {
 
 using namespace emu_ops;
 
-int emu_ops_device_status_int8(int* status, bool reset) {
+int emu_ops_int8_status(int* status, bool reset) {
   int v = 0;
   cudaError_t e = cudaMemcpyFromSymbol(&v, g_ops_status, sizeof v);
   if (e != cudaSuccess) return emu_ops_fail(EMU_ECUDA, "reading the device status failed: %s", cudaGetErrorString(e));

@@ -19,42 +19,20 @@ constexpr int kTcOut = kTcNS * kTcStage;                     // eight warps' sta
 constexpr int kTcBars = kTcOut + 8 * 32 * kTcStageRow * 4;
 constexpr int kTcSmem = kTcBars + 128 + 1024;                // and what aligning to 1024 may take
 constexpr int kTcThreads = 384;
-constexpr uint32_t kTcPolls = 1u << 20;
 
 struct TcTiles {
   int tiles_m, tiles_n, k_blocks;
 };
 
 // ---- barriers, TMA and tcgen05 (inline PTX)
-__device__ __forceinline__ void bar_init(uint32_t bar, uint32_t count) {
-  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
-}
-__device__ __forceinline__ void bar_arrive(uint32_t bar) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-__device__ __forceinline__ void bar_expect(uint32_t bar, uint32_t bytes) {
-  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n .reg .pred P;\n mbarrier.try_wait.parity.shared::cta.b64 P, [%1], %2;\n selp.u32 %0, 1, 0, P;\n}"
-      : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
-  return ok != 0u;
-}
 // Waits for the phase of this parity; false once the limit is reached or another role gave up.
-__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile int* given_up) {
-  for (uint32_t i = 0; i < kTcPolls; ++i) {
+__device__ __forceinline__ bool bar_wait_all(uint32_t bar, uint32_t parity, volatile int* given_up) {
+  for (uint32_t i = 0; i < kPolls; ++i) {
     if (bar_try(bar, parity)) return true;
     if (*given_up) return false;
   }
   *given_up = 1;
   return false;
-}
-// the same at a failed role's end, for what it still has in flight
-__device__ __forceinline__ void bar_drain(uint32_t bar, uint32_t parity) {
-  for (uint32_t i = 0; i < kTcPolls; ++i)
-    if (bar_try(bar, parity)) return;
 }
 __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
   asm volatile(
@@ -155,7 +133,7 @@ int8_tc_kernel(const Int8Params p, const TcTiles tl, const __grid_constant__ CUt
     }
     bar_init(drained, 1);
     *given_up = 0;
-    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    bar_init_fence();
   }
   if (warp == 2) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_addr(slot)) : "memory");
@@ -176,7 +154,7 @@ int8_tc_kernel(const Int8Params p, const TcTiles tl, const __grid_constant__ CUt
         const int m0 = tile % tl.tiles_m * kTcBM, n0 = tile / tl.tiles_m * kTcBN;
         for (int kb = 0; kb < tl.k_blocks; ++kb, ++it) {
           const uint32_t s = it % kTcNS, bar = full + 8 * s, dst = base + s * kTcStage;
-          if (it >= kTcNS && !bar_wait(empty + 8 * s, (it / kTcNS - 1) & 1, given_up)) {
+          if (it >= kTcNS && !bar_wait_all(empty + 8 * s, (it / kTcNS - 1) & 1, given_up)) {
             ok = false;
             break;
           }
@@ -186,7 +164,7 @@ int8_tc_kernel(const Int8Params p, const TcTiles tl, const __grid_constant__ CUt
         }
       }
       if (!ok)                                    // the loads issued last, one a stage at most
-        for (uint32_t i = it > kTcNS ? it - kTcNS : 0; i < it; ++i) bar_drain(full + 8 * (i % kTcNS), (i / kTcNS) & 1);
+        for (uint32_t i = it > kTcNS ? it - kTcNS : 0; i < it; ++i) (void)bar_wait(full + 8 * (i % kTcNS), (i / kTcNS) & 1);
     } else if (warp == 1 && lane == 0) {
       const uint32_t idesc = tc_idesc(kTcBM, kTcBN);
       uint32_t it = 0, unit = 0;
@@ -194,7 +172,7 @@ int8_tc_kernel(const Int8Params p, const TcTiles tl, const __grid_constant__ CUt
       for (int tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
         for (int k0 = 0; k0 < tl.k_blocks && ok; k0 += kTcChunk, ++unit) {
           const uint32_t buf = unit & 1;
-          if (unit >= 2 && !bar_wait(tempty + 8 * buf, ((unit >> 1) - 1) & 1, given_up)) {
+          if (unit >= 2 && !bar_wait_all(tempty + 8 * buf, ((unit >> 1) - 1) & 1, given_up)) {
             ok = false;
             break;
           }
@@ -202,7 +180,7 @@ int8_tc_kernel(const Int8Params p, const TcTiles tl, const __grid_constant__ CUt
           const int k1 = k0 + kTcChunk < tl.k_blocks ? k0 + kTcChunk : tl.k_blocks;
           for (int kb = k0; kb < k1; ++kb, ++it) {
             const uint32_t s = it % kTcNS;
-            if (!bar_wait(full + 8 * s, (it / kTcNS) & 1, given_up)) {
+            if (!bar_wait_all(full + 8 * s, (it / kTcNS) & 1, given_up)) {
               ok = false;
               break;
             }
@@ -217,7 +195,7 @@ int8_tc_kernel(const Int8Params p, const TcTiles tl, const __grid_constant__ CUt
         }
       }
       tc_commit(drained);                         // the MMAs are done before the tensor memory goes back
-      bar_drain(drained, 0);
+      (void)bar_wait(drained, 0);
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
@@ -232,7 +210,7 @@ int8_tc_kernel(const Int8Params p, const TcTiles tl, const __grid_constant__ CUt
       int sum[128];
       for (int k0 = 0; k0 < tl.k_blocks; k0 += kTcChunk, ++unit) {
         const uint32_t buf = unit & 1;
-        ok = __all_sync(0xFFFFFFFFu, bar_wait(tfull + 8 * buf, (unit >> 1) & 1, given_up));
+        ok = __all_sync(0xFFFFFFFFu, bar_wait_all(tfull + 8 * buf, (unit >> 1) & 1, given_up));
         if (!ok) break;
         tc_fence_after();
 #pragma unroll

@@ -402,15 +402,6 @@ logprob_warp_kernel(const LogprobParams p) {
   }
 }
 
-__device__ __forceinline__ uint32_t in_cluster(const void* ptr, int rank) {
-  uint32_t a;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"((uint32_t)__cvta_generic_to_shared(ptr)), "r"(rank));
-  return a;
-}
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-
 // A CTA, or the C CTAs of a cluster, a row: for long rows, and more CTAs a row the fewer rows there
 // are.  Each CTA takes a run of the row's vectors; the first one joins the sums and the k
 // largest of each through distributed shared memory.

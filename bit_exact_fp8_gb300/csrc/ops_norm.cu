@@ -31,6 +31,14 @@ int emu_ops_launched(const char* what) {
   const cudaError_t e = cudaGetLastError();
   return e == cudaSuccess ? EMU_OK : emu_ops_fail(EMU_ECUDA, "%s: CUDA launch failed: %s", what, cudaGetErrorString(e));
 }
+bool emu_ops_allow_smem(const void* kernel, int bytes, std::atomic<bool>* done) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return false;
+  if (dev >= 0 && dev < 64 && done[dev].load(std::memory_order_acquire)) return true;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return false;
+  if (dev >= 0 && dev < 64) done[dev].store(true, std::memory_order_release);
+  return true;
+}
 int emu_ops_sm_count() {
   static std::atomic<int> cached[64];
   int dev = 0;
@@ -45,6 +53,9 @@ int emu_ops_sm_count() {
 }
 
 namespace emu_ops {
+
+// 1 once a bounded wait gave up (the outputs of that call are not valid)
+__device__ int g_norm_status = 0;
 
 constexpr float kScaleMin = 1.17549435e-38f;      // 2^-126, the smallest scale of a row
 
@@ -62,8 +73,8 @@ struct NormParams {
   float* rstd;
 };
 
-template <class T, int VEC>
-__device__ __forceinline__ void load_weight(const NormParams& p, int col, float (&w)[VEC]) {
+template <class T, int VEC, class P>
+__device__ __forceinline__ void load_weight(const P& p, int col, float (&w)[VEC]) {
   if (p.weight_f32) {
     constexpr int V4 = VEC < 4 ? VEC : 4;
 #pragma unroll
@@ -246,6 +257,150 @@ struct NormGradParams {
   float* part;                                    // [gridDim.x, H]
 };
 
+// The gradient in one pass.  A CTA takes rows blockIdx.x, + gridDim.x, ...; a thread has IT vectors of
+// columns, and keeps their weights and their sums of gy h rstd in registers over all its rows.  A
+// row's sum of g h (g = gy w) has to be known before its first output, so a row is looked at twice:
+// both times in shared memory, where a ring of S rows is filled ahead by bulk copies, so that HBM
+// is read once and without a pause between rows.  (Rows that are not 16-byte aligned: `ring` false,
+// read from memory twice.)  At the end the eight CTAs of a cluster add their column sums up
+// through distributed shared memory, so that only gridDim / 8 parts of H sums go through memory to
+// the joining kernel.  Bound by HBM: four tensors of T H values.
+constexpr int kGradCluster = 8, kGradStages = 8;
+template <class T, int VEC, int IT, int MAXT, int MINB>
+__global__ void __launch_bounds__(MAXT, MINB)
+norm_grad_kernel(const NormGradParams p, int S) {
+  constexpr bool RING = VEC > 1;
+  extern __shared__ __align__(16) unsigned char dyn[];      // the ring; then the column sums, [H] fp32
+  __shared__ float sm[2][32];
+  __shared__ __align__(8) uint64_t full[kGradStages];
+  const int t = threadIdx.x, nt = blockDim.x, lane = t & 31, warp = t >> 5, warps = nt >> 5;
+  const uint32_t row_bytes = (uint32_t)p.H * sizeof(T), inputs = p.gh ? 3u : 2u, stage_bytes = inputs * row_bytes;
+  const int64_t rows = p.T > blockIdx.x ? (p.T - blockIdx.x + gridDim.x - 1) / gridDim.x : 0;
+  auto fill = [&](int64_t i, int s) {                       // one thread: row i of this CTA into stage s
+    const int64_t row = blockIdx.x + i * gridDim.x;
+    const uint32_t bar = smem_addr(&full[s]), dst = smem_addr(dyn) + s * stage_bytes;
+    bar_expect(bar, stage_bytes);
+    bulk_load(dst, static_cast<const T*>(p.gy) + row * p.ldy, row_bytes, bar);
+    bulk_load(dst + row_bytes, static_cast<const T*>(p.h) + row * p.ldh, row_bytes, bar);
+    if (p.gh) bulk_load(dst + 2 * row_bytes, static_cast<const T*>(p.gh) + row * p.ldg, row_bytes, bar);
+  };
+  if (RING) {
+    if (t == 0) {
+      for (int i = 0; i < S; ++i) bar_init(smem_addr(&full[i]), 1);
+      bar_init_fence();
+      for (int i = 0; i < S && i < rows; ++i) fill(i, i);
+    }
+    __syncthreads();
+  }
+  float w[IT][VEC], dw[IT][VEC];
+#pragma unroll
+  for (int i = 0; i < IT; ++i) {
+    const int col = (i * nt + t) * VEC;
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) dw[i][j] = 0.0f;
+    if (col < p.H) load_weight<T, VEC>(p, col, w[i]);
+  }
+  bool ok = true;
+  int s = 0, before = S - 1;                                // row k's stage and row k - 1's
+  uint32_t phase = 0;
+  for (int64_t k = 0; k < rows; ++k) {
+    const int64_t row = blockIdx.x + k * gridDim.x;
+    const float rstd = p.rstd[row];
+    const T *gy, *h, *gh = nullptr;
+    if (RING) {
+      ok = bar_wait(smem_addr(&full[s]), phase);
+      gy = reinterpret_cast<const T*>(dyn + s * stage_bytes);
+      h = gy + p.H;
+      if (p.gh) gh = h + p.H;
+    } else {
+      gy = static_cast<const T*>(p.gy) + row * p.ldy;
+      h = static_cast<const T*>(p.h) + row * p.ldh;
+      if (p.gh) gh = static_cast<const T*>(p.gh) + row * p.ldg;
+    }
+    float sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < IT; ++i) {
+      const int col = (i * nt + t) * VEC;
+      if (col < p.H) {
+        float y[VEC], x[VEC];
+        load_f<T, VEC>(gy + col, y);
+        load_f<T, VEC>(h + col, x);
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) sum = fmaf(y[j] * w[i][j], x[j], sum);
+      }
+    }
+    sum = warp_sum(sum);
+    if (lane == 0) sm[k & 1][warp] = sum;                   // the other half of sm is the row before's
+    if (__syncthreads_or(!ok)) {
+      ok = false;
+      break;
+    }
+    if (RING) {                                             // all are past the row before
+      if (t == 0 && k >= 1 && k - 1 + S < rows) fill(k - 1 + S, before);
+      before = s;
+      if (++s == S) {
+        s = 0;
+        phase ^= 1u;
+      }
+    }
+    sum = 0.0f;
+    for (int i = 0; i < warps; ++i) sum += sm[k & 1][i];
+    const float coef = __fdiv_rn(sum, (float)p.H) * rstd * rstd;
+    T* gx = static_cast<T*>(p.gx) + row * p.H;
+#pragma unroll
+    for (int i = 0; i < IT; ++i) {
+      const int col = (i * nt + t) * VEC;
+      if (col < p.H) {
+        float y[VEC], x[VEC];
+        load_f<T, VEC>(gy + col, y);
+        load_f<T, VEC>(h + col, x);
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) {
+          dw[i][j] = fmaf(y[j], x[j] * rstd, dw[i][j]);
+          y[j] = rstd * (y[j] * w[i][j] - x[j] * coef);
+        }
+        if (gh) {
+          load_f<T, VEC>(gh + col, x);
+#pragma unroll
+          for (int j = 0; j < VEC; ++j) y[j] += x[j];
+        }
+        store_f<T, VEC>(gx + col, y);
+      }
+    }
+  }
+  if (!ok && t == 0) {                                      // a copy that never came: wait for the others, then end
+    atomicExch(&g_norm_status, 1);
+    for (int s = 0; s < S; ++s) {
+      (void)bar_wait(smem_addr(&full[s]), 0);
+      (void)bar_wait(smem_addr(&full[s]), 1);
+    }
+  }
+  __syncthreads();
+  float* const column_sums = reinterpret_cast<float*>(dyn);
+#pragma unroll
+  for (int i = 0; i < IT; ++i)
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) {
+      const int col = (i * nt + t) * VEC + j;
+      if (col < p.H) column_sums[col] = dw[i][j];
+    }
+  cluster_sync();
+  const int rank = blockIdx.x % kGradCluster;
+  for (int col = rank * nt + t; col < p.H; col += kGradCluster * nt) {
+    float v[kGradCluster];
+#pragma unroll
+    for (int r = 0; r < kGradCluster; ++r)
+      asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v[r]) : "r"(in_cluster(column_sums + col, r)) : "memory");
+    float s = 0.0f;
+#pragma unroll
+    for (int r = 0; r < kGradCluster; ++r) s += v[r];
+    p.part[(int64_t)(blockIdx.x / kGradCluster) * p.H + col] = s;
+  }
+  cluster_sync();
+}
+
+// Rows too long for a CTA's registers, in two passes over them.
+//
 // Row t: g = gy w, c = rstd^2 mean(g h), gx = rstd (g - h c) + gh.  One element a thread and
 // step, the row read twice.
 template <class T>
@@ -301,9 +456,59 @@ norm_grad_join_kernel(const float* part, int parts, int H, float* gw) {
   }
 }
 
-template <class T> void pick_norm_grad(const NormGradParams& p, int parts, cudaStream_t st) {
+// Launches the kernel; the parts that it leaves for the joining kernel, 0 if it failed.
+template <class T, int VEC, int IT, int MAXT, int MINB>
+int launch_grad(const NormGradParams& p, int threads, cudaStream_t st) {
+  auto kernel = norm_grad_kernel<T, VEC, IT, MAXT, MINB>;
+  static std::atomic<bool> done[64];
+  if (!emu_ops_allow_smem(reinterpret_cast<const void*>(kernel), kMaxSmem - 1024, done)) return 0;
+  // CTAs an SM by threads and registers (MAXT * MINB threads have theirs), and a ring that lets that many
+  // share its memory: two rows at least, kGradStages at most
+  int resident = MAXT * MINB / threads < 16 ? MAXT * MINB / threads : 16, S = 0;
+  size_t bytes = (size_t)p.H * 4;
+  if (VEC > 1) {
+    const size_t stage = (size_t)p.H * sizeof(T) * (p.gh ? 3 : 2);
+    while (resident > 1 && (kMaxSmem / resident - 2048) / stage < 3) --resident;
+    S = (int)((kMaxSmem / resident - 2048) / stage);
+    if (S > kGradStages) S = kGradStages;
+    if (bytes < S * stage) bytes = S * stage;
+  } else {
+    while (resident > 1 && kMaxSmem / resident - 2048 < (int)bytes) --resident;
+  }
+  const int64_t most = (int64_t)emu_ops_sm_count() * resident;
+  int64_t clusters = ((p.T < most ? p.T : most) + kGradCluster - 1) / kGradCluster;
+  if (clusters > kGradParts) clusters = kGradParts;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(clusters * kGradCluster));
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = bytes;
+  cfg.stream = st;
+  cudaLaunchAttribute at;
+  at.id = cudaLaunchAttributeClusterDimension;
+  at.val.clusterDim.x = kGradCluster;
+  at.val.clusterDim.y = at.val.clusterDim.z = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, p, S) == cudaSuccess ? (int)clusters : 0;
+}
+
+// The fewest vectors a thread that leave a CTA within its threads; 0: a launch failed.
+template <class T> int pick_norm_grad(const NormGradParams& p, bool vec, cudaStream_t st) {
+  constexpr int V = 16 / sizeof(T);
+  auto threads = [](int n, int it) { return ((n + it - 1) / it + 31) / 32 * 32; };
+  if (vec) {
+    const int nv = p.H / V;
+    if (nv <= 256) return launch_grad<T, V, 1, 256, 5>(p, threads(nv, 1), st);
+    if (nv <= 1024) return launch_grad<T, V, 2, 512, 2>(p, threads(nv, 2), st);
+    if (nv <= 2048) return launch_grad<T, V, 4, 512, 1>(p, threads(nv, 4), st);
+  } else if (p.H <= 8192) {
+    return p.H <= 2048 ? launch_grad<T, 1, 8, 256, 4>(p, threads(p.H, 8), st)
+                       : launch_grad<T, 1, 8, 1024, 1>(p, threads(p.H, 8), st);
+  }
+  const int parts = (int)(p.T < kGradParts ? p.T : kGradParts);
   norm_grad_rows_kernel<T><<<(unsigned)p.T, 256, 0, st>>>(p);
   norm_grad_weight_kernel<T><<<dim3((unsigned)parts, (unsigned)((p.H + 255) / 256)), 256, 0, st>>>(p);
+  return parts;
 }
 
 int check_rows(const char* what, int64_t T, int64_t H) {
@@ -325,9 +530,15 @@ int emu_ops_device_status(int32_t* status, int32_t reset) {
   emu_ops_begin();
   if (!status) return emu_ops_fail(EMU_EINVAL, "status is null");
   int v = 0;
-  const int rc = emu_ops_device_status_int8(&v, reset != 0);
-  if (rc == EMU_OK) *status = v;
-  return rc;
+  const int rc = emu_ops_int8_status(&v, reset != 0);
+  if (rc != EMU_OK) return rc;
+  int n = 0;
+  if (cudaMemcpyFromSymbol(&n, g_norm_status, sizeof n) != cudaSuccess) return emu_ops_launched("emu_ops_device_status");
+  const int zero = 0;
+  if (reset && cudaMemcpyToSymbol(g_norm_status, &zero, sizeof zero) != cudaSuccess)
+    return emu_ops_launched("emu_ops_device_status");
+  *status = v | n;
+  return EMU_OK;
 }
 
 int emu_rms_norm_quant(const void* x, int64_t ldx, const void* residual, int64_t ldr,
@@ -420,10 +631,13 @@ int emu_rms_norm_backward(const void* grad_y, int64_t ldy, const void* hidden, i
   p.gy = grad_y; p.ldy = ldy; p.h = hidden; p.ldh = ldh; p.gh = grad_residual; p.ldg = ldg;
   p.weight = weight; p.weight_f32 = weight_type == EMU_OUT_F32; p.rstd = rstd;
   p.T = T; p.H = (int)H; p.gx = grad_x; p.part = static_cast<float*>(workspace);
-  const int parts = (int)(T < kGradParts ? T : kGradParts);
-  if (type == EMU_OUT_F32) pick_norm_grad<float>(p, parts, st);
-  else if (type == EMU_OUT_BF16) pick_norm_grad<__nv_bfloat16>(p, parts, st);
-  else pick_norm_grad<__half>(p, parts, st);
+  const int64_t v = 16 / (int64_t)es;
+  const bool vec = H % v == 0 && ldy % v == 0 && ldh % v == 0 && (!grad_residual || ldg % v == 0) && aligned(grad_y, 16) &&
+                   aligned(hidden, 16) && aligned(grad_residual, 16) && aligned(grad_x, 16) && aligned(weight, 16);
+  const int parts = type == EMU_OUT_F32    ? pick_norm_grad<float>(p, vec, st)
+                    : type == EMU_OUT_BF16 ? pick_norm_grad<__nv_bfloat16>(p, vec, st)
+                                           : pick_norm_grad<__half>(p, vec, st);
+  if (parts == 0) return emu_ops_launched("emu_rms_norm_backward");
   norm_grad_join_kernel<<<(unsigned)((H + 31) / 32), 256, 0, st>>>(p.part, parts, p.H, grad_weight);
   return emu_ops_launched("emu_rms_norm_backward");
 }
