@@ -149,25 +149,6 @@ template <class P> __device__ __forceinline__ void floor2(uint4& raw, P low) {
 __device__ __forceinline__ void floor_at(uint4& raw, __nv_bfloat16) { floor2(raw, __float2bfloat162_rn(-65536.0f)); }
 __device__ __forceinline__ void floor_at(uint4& raw, __half) { floor2(raw, __float2half2_rn(-65504.0f)); }
 
-// fp32 pairs: one instruction for two logits
-typedef unsigned long long f2;
-__device__ __forceinline__ f2 pair(float a, float b) {
-  f2 r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ void halves(f2 v, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
-__device__ __forceinline__ f2 add2(f2 a, f2 b) {
-  f2 r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
-  f2 r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-
 // A thread's part of a row.  Vectors whose largest logit is within -6e4 and 1e6 take the fast form:
 // with L = log2 e and c = fp32(m L), a = x L - c is one rounding, e = 2^a, and the sums of e and
 // e a run in fp32 pairs, about five instructions a logit.  (c differs from m L by a rounding that
@@ -202,8 +183,8 @@ template <class T> struct Streamed {
       if (hi > m) {
         const float cn = hi * kLog2e, d = fmaxf(c - cn, -1e4f), e = exp2_approx(d);
         const f2 e2 = pair(e, e);
-        w = fma2(fma2(pair(d, d), z, w), e2, 0ull);
-        z = fma2(z, e2, 0ull);
+        w = mul2(fma2(pair(d, d), z, w), e2);
+        z = mul2(z, e2);
         m = hi;
         c = cn;
       }

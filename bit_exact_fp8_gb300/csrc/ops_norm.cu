@@ -118,6 +118,110 @@ template <int VEC> __device__ __forceinline__ void store_codes(uint8_t* q, const
   }
 }
 
+// ---- rows through shared memory.  A row of a tensor is held as the 16-byte vectors that it touches:
+// vector v has the values of columns v * VEC - off + j, `off` values of the row before it in its
+// first one.  Tensors whose rows lie alike about 16-byte addresses share off, and the rows
+// of one CTA (a multiple of 8 apart) do too, so a thread's columns, weights and sums of columns
+// stay its own over all its rows, whatever the row's length.
+constexpr int kStages = 8;
+struct Ring {
+  int S;                        // rows held at once
+  uint32_t pitch;               // bytes of one row's vectors
+  bool q_vec;                   // codes can be stored a vector at a time
+};
+// EDGES: rows that begin or end inside a vector
+template <class T, bool EDGES> struct Columns {
+  static constexpr int VEC = 16 / sizeof(T);
+  int first, lo, hi;            // of a thread's vector: the column of value 0, its valid values [lo, hi)
+  __device__ __forceinline__ Columns(int v, int off, int H) : first(v * VEC - (EDGES ? off : 0)) {
+    lo = EDGES && first < 0 ? -first : 0;
+    hi = !EDGES ? (first < H ? VEC : 0) : H - first < VEC ? H - first : VEC;
+  }
+  __device__ __forceinline__ bool any() const { return hi > lo; }
+  __device__ __forceinline__ bool whole() const { return !EDGES || (lo == 0 && hi == VEC); }
+};
+// One thread: row `row` of a [rows, H] tensor into shared memory at dst, by a bulk copy of the vectors
+// that lie within the tensor; values of others (the tensor's very ends) one by one.
+template <class T>
+__device__ __forceinline__ void fill_row(unsigned char* dst, const T* base, int64_t ld, int64_t row, int64_t rows, int H,
+                                         uint32_t bar) {
+  const uintptr_t start = reinterpret_cast<uintptr_t>(base + row * ld), end = start + (size_t)H * sizeof(T);
+  const uintptr_t tensor_end = reinterpret_cast<uintptr_t>(base + (rows - 1) * ld) + (size_t)H * sizeof(T);
+  const uintptr_t from = start & ~(uintptr_t)15;
+  uintptr_t lo = from, hi = (end + 15) & ~(uintptr_t)15;
+  if (lo < reinterpret_cast<uintptr_t>(base)) lo += 16;
+  if (hi > tensor_end) hi -= 16;
+  if (lo > start || hi < end) {
+    for (uintptr_t a = start; a < end && a < lo; a += sizeof(T))
+      *reinterpret_cast<T*>(dst + (a - from)) = *reinterpret_cast<const T*>(a);
+    for (uintptr_t a = hi > start ? hi : start; a < end; a += sizeof(T))
+      if (a >= lo) *reinterpret_cast<T*>(dst + (a - from)) = *reinterpret_cast<const T*>(a);
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // before a later row's copy takes their place
+  }
+  const uint32_t bytes = hi > lo ? (uint32_t)(hi - lo) : 0u;
+  bar_expect(bar, bytes);
+  if (bytes) bulk_load(smem_addr(dst + (lo - from)), reinterpret_cast<const void*>(lo), bytes, bar);
+}
+template <class T> __device__ __forceinline__ int offset_of(const void* base, int64_t ld, int64_t row) {
+  return (int)((reinterpret_cast<uintptr_t>(static_cast<const T*>(base) + row * ld) & 15u) / sizeof(T));
+}
+// a thread's vector from shared memory as pairs; values outside the row as 0
+template <class T, bool EDGES>
+__device__ __forceinline__ void read_pairs(const unsigned char* at, const Columns<T, EDGES>& c, f2 (&f)[8 / sizeof(T)]) {
+  constexpr int VEC = Columns<T, EDGES>::VEC;
+  float v[VEC];
+  load_f<T, VEC>(reinterpret_cast<const T*>(at), v);
+  if (!c.whole()) {
+    asm volatile("");           // a branch for the two vectors of a row, not selects for all
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) v[j] = j >= c.lo && j < c.hi ? v[j] : 0.0f;
+  }
+#pragma unroll
+  for (int j = 0; j < VEC; j += 2) f[j / 2] = pair(v[j], v[j + 1]);
+}
+template <class T, bool EDGES>
+__device__ __forceinline__ void write_pairs(T* row, const Columns<T, EDGES>& c, const f2 (&f)[8 / sizeof(T)]) {
+  constexpr int VEC = Columns<T, EDGES>::VEC;
+  float v[VEC];
+#pragma unroll
+  for (int j = 0; j < VEC; j += 2) halves(f[j / 2], v[j], v[j + 1]);
+  if (c.whole()) {
+    store_f<T, VEC>(row + c.first, v);
+  } else {
+#pragma unroll
+    for (int j = 0; j < VEC; ++j)
+      if (j >= c.lo && j < c.hi) row[c.first + j] = from_f<T>(v[j]);
+  }
+}
+template <class T, bool EDGES, class P>
+__device__ __forceinline__ void weight_pairs(const P& p, const Columns<T, EDGES>& c, f2 (&w)[8 / sizeof(T)]) {
+  constexpr int VEC = Columns<T, EDGES>::VEC;
+  float v[VEC];
+#pragma unroll
+  for (int j = 0; j < VEC; ++j) {
+    v[j] = 0.0f;
+    if (j >= c.lo && j < c.hi)
+      v[j] = p.weight_f32 ? static_cast<const float*>(p.weight)[c.first + j]
+                          : to_f(static_cast<const T*>(p.weight)[c.first + j]);
+  }
+#pragma unroll
+  for (int j = 0; j < VEC; j += 2) w[j / 2] = pair(v[j], v[j + 1]);
+}
+// the sum of what the first `warps` warps left in part (16 places, zeros after theirs)
+__device__ __forceinline__ float sum16(const float* part) {
+  const float4* q = reinterpret_cast<const float4*>(part);
+  const float4 a = q[0], b = q[1], c = q[2], d = q[3];
+  return ((a.x + a.y) + (a.z + a.w)) + ((b.x + b.y) + (b.z + b.w)) + (((c.x + c.y) + (c.z + c.w)) + ((d.x + d.y) + (d.z + d.w)));
+}
+
+__device__ __forceinline__ float max16(const float* part) {
+  const float4* q = reinterpret_cast<const float4*>(part);
+  float m = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) m = max_nan(m, max_nan(max_nan(q[i].x, q[i].y), max_nan(q[i].z, q[i].w)));
+  return m;
+}
+
 // the sums (and maxima) of the TPR threads of a row: shuffles, then one barrier
 template <int TPR>
 __device__ __forceinline__ void row_reduce(float& sum, float& mx, float (*sm)[2]) {
@@ -226,21 +330,175 @@ template <class T, int VEC, int TPR, int IT> void launch_norm(const NormParams& 
   norm_quant_kernel<T, VEC, TPR, IT><<<(unsigned)blocks, TPR == 32 ? 128 : TPR, 0, st>>>(p);
 }
 
-// the fewest threads whose registers hold the row
-template <class T> void pick_norm(const NormParams& p, bool vec, cudaStream_t st) {
-  constexpr int V = 16 / sizeof(T);
-  if (vec) {
-    const int nv = p.H / V;
-    if (nv <= 128) return launch_norm<T, V, 32, 4>(p, st);
-    if (nv <= 256) return launch_norm<T, V, 128, 2>(p, st);
-    if (nv <= 1024) return launch_norm<T, V, 256, 4>(p, st);
-    if (nv <= 2048) return launch_norm<T, V, 512, 4>(p, st);
-    return launch_norm<T, V, 512, 0>(p, st);
+// Many rows: a CTA takes rows blockIdx.x, + gridDim.x, ..., staged ahead in a ring in shared memory by
+// bulk copies, so that HBM is read without a pause between rows; a thread keeps the weights of its
+// IT vectors of columns in registers.  The rest is as above.  Bound by HBM: x, residual, h and q.
+template <class T, int IT, int MAXT, int MINB, bool EDGES>
+__global__ void __launch_bounds__(MAXT, MINB)
+norm_quant_ring_kernel(const NormParams p, const Ring ring) {
+  constexpr int VEC = 16 / sizeof(T), NP = VEC / 2;
+  extern __shared__ __align__(16) unsigned char dyn[];
+  __shared__ __align__(16) float sums[2][16], tops[2][16];
+  __shared__ __align__(8) uint64_t full[kStages];
+  const int t = threadIdx.x, nt = blockDim.x, lane = t & 31, warp = t >> 5;
+  const int inputs = p.residual ? 2 : 1;
+  const uint32_t stage_bytes = (uint32_t)inputs * ring.pitch;
+  const int rows = (int)(p.T > blockIdx.x ? (p.T - blockIdx.x + gridDim.x - 1) / gridDim.x : 0);
+  const int second = nt > 32 ? 32 : 1;                      // the thread that fetches the residual
+  auto fill = [&](int i, int s) {
+    const int64_t row = blockIdx.x + (int64_t)i * gridDim.x;
+    unsigned char* dst = dyn + s * stage_bytes;
+    if (t == 0) fill_row(dst, static_cast<const T*>(p.x), p.ldx, row, p.T, p.H, smem_addr(&full[s]));
+    else fill_row(dst + ring.pitch, static_cast<const T*>(p.residual), p.ldr, row, p.T, p.H, smem_addr(&full[s]));
+  };
+  const bool fetches = t == 0 || (t == second && inputs == 2);
+  if (t < 16) sums[0][t] = sums[1][t] = tops[0][t] = tops[1][t] = 0.0f;
+  if (t == 0) {
+    for (int i = 0; i < ring.S; ++i) bar_init(smem_addr(&full[i]), inputs);
+    bar_init_fence();
   }
-  if (p.H <= 256) return launch_norm<T, 1, 32, 8>(p, st);
-  if (p.H <= 2048) return launch_norm<T, 1, 256, 8>(p, st);
-  if (p.H <= 8192) return launch_norm<T, 1, 1024, 8>(p, st);
-  return launch_norm<T, 1, 1024, 0>(p, st);
+  __syncthreads();
+  if (fetches)
+    for (int i = 0; i < ring.S && i < rows; ++i) fill(i, i);
+  const int off = offset_of<T>(p.x, p.ldx, blockIdx.x);
+  f2 w[IT][NP];
+#pragma unroll
+  for (int i = 0; i < IT; ++i) weight_pairs(p, Columns<T, EDGES>(i * nt + t, off, p.H), w[i]);
+  const float inv_h = __fdiv_rn(1.0f, (float)p.H), inv_qmax = __fdiv_rn(1.0f, p.qmax);
+  const float inv_static = p.scale ? __fdiv_rn(1.0f, __ldg(p.scale)) : 0.0f;
+  bool ok = true;
+  int s = 0, before = ring.S - 1;
+  uint32_t phase = 0;
+  for (int k = 0; k < rows; ++k) {
+    const int64_t row = blockIdx.x + (int64_t)k * gridDim.x;
+    ok = bar_wait(smem_addr(&full[s]), phase);
+    const unsigned char* in = dyn + s * stage_bytes;
+    T* ho = p.residual_out ? static_cast<T*>(p.residual_out) + row * p.ldo : nullptr;
+    f2 hw[IT][NP], sq = 0ull;
+    float mx = 0.0f;
+#pragma unroll
+    for (int i = 0; i < IT; ++i) {
+      const Columns<T, EDGES> c(i * nt + t, off, p.H);
+      if (!c.any()) continue;
+      read_pairs(in + (i * nt + t) * 16, c, hw[i]);
+      if (inputs == 2) {
+        f2 r[NP];
+        read_pairs(in + ring.pitch + (i * nt + t) * 16, c, r);
+#pragma unroll
+        for (int j = 0; j < NP; ++j) hw[i][j] = add2(hw[i][j], r[j]);
+      }
+      if (ho) write_pairs(ho, c, hw[i]);
+#pragma unroll
+      for (int j = 0; j < NP; ++j) {
+        sq = fma2(hw[i][j], hw[i][j], sq);
+        hw[i][j] = mul2(hw[i][j], w[i][j]);
+        float a, b;
+        halves(hw[i][j], a, b);
+        mx = max_nan(mx, max_nan(fabsf(a), fabsf(b)));
+      }
+    }
+    float s0, s1;
+    halves(sq, s0, s1);
+    const float part = warp_sum(s0 + s1);
+    mx = warp_max_nan(mx);
+    if (lane == 0) {                                        // the other halves are the row before's
+      sums[k & 1][warp] = part;
+      tops[k & 1][warp] = mx;
+    }
+    if (__syncthreads_or(!ok)) {
+      ok = false;
+      break;
+    }
+    if (fetches && k >= 1 && k - 1 + ring.S < rows) fill(k - 1 + ring.S, before);   // all are past the row before
+    before = s;
+    if (++s == ring.S) {
+      s = 0;
+      phase ^= 1u;
+    }
+    const float rstd = rsqrtf(fmaf(sum16(sums[k & 1]), inv_h, p.eps));
+    float inv = inv_static;
+    if (!p.scale) {
+      const float scale = max_nan(max16(tops[k & 1]) * rstd * inv_qmax, kScaleMin);
+      if (t == 0) p.scale_out[row] = scale;
+      inv = __fdiv_rn(1.0f, scale);
+    }
+    if (t == 0) p.rstd[row] = rstd;
+    uint8_t* q = p.q + row * p.H;
+#pragma unroll
+    for (int i = 0; i < IT; ++i) {
+      const Columns<T, EDGES> c(i * nt + t, off, p.H);
+      if (!c.any()) continue;
+      float v[VEC];
+#pragma unroll
+      for (int j = 0; j < NP; ++j) {
+        float a, b;
+        halves(hw[i][j], a, b);
+        v[2 * j] = a * rstd * inv;
+        v[2 * j + 1] = b * rstd * inv;
+      }
+      if (ring.q_vec && c.whole()) {
+        store_codes<VEC>(q + c.first, v, p.q_format);
+      } else {
+#pragma unroll
+        for (int j = 0; j < VEC; ++j)
+          if (j >= c.lo && j < c.hi) q[c.first + j] = (uint8_t)code_pair(v[j], 0.0f, p.q_format);
+      }
+    }
+  }
+  if (!ok && t == 0) {                                      // a copy that never came: wait for the others, then end
+    atomicExch(&g_norm_status, 1);
+    for (int i = 0; i < ring.S; ++i) {
+      (void)bar_wait(smem_addr(&full[i]), 0);
+      (void)bar_wait(smem_addr(&full[i]), 1);
+    }
+  }
+}
+
+// The ring for rows of `inputs` tensors in CTAs of `threads` threads, of which registers let `most` live
+// on an SM: CTAs an SM (at least three rows in each, if that leaves one) and rows a CTA.
+Ring ring_for(int64_t H, size_t es, bool aligned16, int inputs, int most, int* resident) {
+  Ring r = {};
+  r.pitch = (uint32_t)((size_t)H * es);
+  if (!aligned16) r.pitch = (r.pitch + 30u) & ~15u;
+  const size_t stage = (size_t)inputs * r.pitch;
+  int n = most < 16 ? most : 16;
+  while (n > 1 && (size_t)(kMaxSmem / n - 2048) / stage < 3) --n;
+  const size_t S = (size_t)(kMaxSmem / n - 2048) / stage;
+  r.S = S < kStages ? (int)S : kStages;
+  *resident = n;
+  return r;
+}
+int threads_for(int n, int it) { return ((n + it - 1) / it + 31) / 32 * 32; }
+
+template <class T, int IT, int MAXT, int MINB>
+int launch_norm_ring(const NormParams& p, int threads, bool aligned16, bool q_vec, cudaStream_t st) {
+  auto kernel = aligned16 ? norm_quant_ring_kernel<T, IT, MAXT, MINB, false> : norm_quant_ring_kernel<T, IT, MAXT, MINB, true>;
+  static std::atomic<bool> flags[2][64];
+  std::atomic<bool>* done = flags[aligned16];
+  if (!emu_ops_allow_smem(reinterpret_cast<const void*>(kernel), kMaxSmem - 1024, done))
+    return emu_ops_launched("cudaFuncSetAttribute");
+  int resident;
+  Ring ring = ring_for(p.H, sizeof(T), aligned16, p.residual ? 2 : 1, MAXT * MINB / threads, &resident);
+  ring.q_vec = q_vec;
+  const int64_t most = (int64_t)emu_ops_sm_count() * resident;
+  int64_t ctas = p.T < most ? p.T : most;
+  if (!aligned16) ctas = (ctas + 7) / 8 * 8;               // a CTA's rows lie alike
+  kernel<<<(unsigned)ctas, threads, (size_t)ring.S * (p.residual ? 2 : 1) * ring.pitch, st>>>(p, ring);
+  return EMU_OK;
+}
+
+template <class T> int pick_norm(const NormParams& p, bool alike, bool aligned16, bool q_vec, cudaStream_t st) {
+  constexpr int V = 16 / sizeof(T);
+  const int nv = aligned16 ? p.H / V : (p.H + 2 * V - 2) / V;       // vectors that a row can touch
+  if (alike && nv <= 2048) {
+    if (nv <= 256) return launch_norm_ring<T, 1, 256, 5>(p, threads_for(nv, 1), aligned16, q_vec, st);
+    if (nv <= 1024) return launch_norm_ring<T, 2, 512, 2>(p, threads_for(nv, 2), aligned16, q_vec, st);
+    return launch_norm_ring<T, 4, 512, 1>(p, threads_for(nv, 4), aligned16, q_vec, st);
+  }
+  if (aligned16 && alike) launch_norm<T, V, 512, 0>(p, st);
+  else if (p.H <= 256) launch_norm<T, 1, 32, 8>(p, st);
+  else launch_norm<T, 1, 512, 0>(p, st);
+  return EMU_OK;
 }
 
 // ------------------------------------------------------------------------- gradient
@@ -257,133 +515,130 @@ struct NormGradParams {
   float* part;                                    // [gridDim.x, H]
 };
 
-// The gradient in one pass.  A CTA takes rows blockIdx.x, + gridDim.x, ...; a thread has IT vectors of
-// columns, and keeps their weights and their sums of gy h rstd in registers over all its rows.  A
-// row's sum of g h (g = gy w) has to be known before its first output, so a row is looked at twice:
-// both times in shared memory, where a ring of S rows is filled ahead by bulk copies, so that HBM
-// is read once and without a pause between rows.  (Rows that are not 16-byte aligned: `ring` false,
-// read from memory twice.)  At the end the eight CTAs of a cluster add their column sums up
-// through distributed shared memory, so that only gridDim / 8 parts of H sums go through memory to
-// the joining kernel.  Bound by HBM: four tensors of T H values.
-constexpr int kGradCluster = 8, kGradStages = 8;
-template <class T, int VEC, int IT, int MAXT, int MINB>
+// The gradient in one pass.  As in the forward kernel, a CTA takes rows a grid apart through a ring in
+// shared memory.  A row's sum of g h (g = gy w) has to be known before its first output, so each
+// row is looked at twice, both times in shared memory.  A thread keeps the weights and the sums of
+// gy h rstd of its IT vectors of columns in registers over all its rows; at the end the two CTAs
+// of a cluster add theirs up through distributed shared memory, so that half as many parts of H
+// sums go through memory to the joining kernel (clusters of eight did not all fit on the SMs at
+// once: 95 us for 8192 x 5760).  Bound by HBM: four tensors of T H values.
+constexpr int kGradCluster = 2;
+template <class T, int IT, int MAXT, int MINB, bool EDGES>
 __global__ void __launch_bounds__(MAXT, MINB)
-norm_grad_kernel(const NormGradParams p, int S) {
-  constexpr bool RING = VEC > 1;
+norm_grad_kernel(const NormGradParams p, const Ring ring) {
+  constexpr int VEC = 16 / sizeof(T), NP = VEC / 2;
   extern __shared__ __align__(16) unsigned char dyn[];      // the ring; then the column sums, [H] fp32
-  __shared__ float sm[2][32];
-  __shared__ __align__(8) uint64_t full[kGradStages];
-  const int t = threadIdx.x, nt = blockDim.x, lane = t & 31, warp = t >> 5, warps = nt >> 5;
-  const uint32_t row_bytes = (uint32_t)p.H * sizeof(T), inputs = p.gh ? 3u : 2u, stage_bytes = inputs * row_bytes;
-  const int64_t rows = p.T > blockIdx.x ? (p.T - blockIdx.x + gridDim.x - 1) / gridDim.x : 0;
-  auto fill = [&](int64_t i, int s) {                       // one thread: row i of this CTA into stage s
-    const int64_t row = blockIdx.x + i * gridDim.x;
-    const uint32_t bar = smem_addr(&full[s]), dst = smem_addr(dyn) + s * stage_bytes;
-    bar_expect(bar, stage_bytes);
-    bulk_load(dst, static_cast<const T*>(p.gy) + row * p.ldy, row_bytes, bar);
-    bulk_load(dst + row_bytes, static_cast<const T*>(p.h) + row * p.ldh, row_bytes, bar);
-    if (p.gh) bulk_load(dst + 2 * row_bytes, static_cast<const T*>(p.gh) + row * p.ldg, row_bytes, bar);
+  __shared__ __align__(16) float sums[2][16];
+  __shared__ __align__(8) uint64_t full[kStages];
+  const int t = threadIdx.x, nt = blockDim.x, lane = t & 31, warp = t >> 5;
+  const int inputs = p.gh ? 3 : 2;
+  const uint32_t stage_bytes = (uint32_t)inputs * ring.pitch;
+  const int rows = (int)(p.T > blockIdx.x ? (p.T - blockIdx.x + gridDim.x - 1) / gridDim.x : 0);
+  const int apart = nt > 64 ? 32 : 1;                       // threads 0, 1, 2 of these fetch a tensor each
+  const bool fetches = t % apart == 0 && t / apart < inputs;
+  auto fill = [&](int i, int s) {
+    const int64_t row = blockIdx.x + (int64_t)i * gridDim.x;
+    const int which = t / apart;
+    const T* base = static_cast<const T*>(which == 0 ? p.gy : which == 1 ? p.h : p.gh);
+    fill_row(dyn + s * stage_bytes + which * ring.pitch, base, which == 0 ? p.ldy : which == 1 ? p.ldh : p.ldg, row, p.T,
+             p.H, smem_addr(&full[s]));
   };
-  if (RING) {
-    if (t == 0) {
-      for (int i = 0; i < S; ++i) bar_init(smem_addr(&full[i]), 1);
-      bar_init_fence();
-      for (int i = 0; i < S && i < rows; ++i) fill(i, i);
-    }
-    __syncthreads();
+  if (t < 16) sums[0][t] = sums[1][t] = 0.0f;
+  if (t == 0) {
+    for (int i = 0; i < ring.S; ++i) bar_init(smem_addr(&full[i]), inputs);
+    bar_init_fence();
   }
-  float w[IT][VEC], dw[IT][VEC];
+  __syncthreads();
+  if (fetches)
+    for (int i = 0; i < ring.S && i < rows; ++i) fill(i, i);
+  const int off = offset_of<T>(p.gy, p.ldy, blockIdx.x);
+  f2 w[IT][NP], dw[IT][NP];
 #pragma unroll
   for (int i = 0; i < IT; ++i) {
-    const int col = (i * nt + t) * VEC;
+    weight_pairs(p, Columns<T, EDGES>(i * nt + t, off, p.H), w[i]);
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) dw[i][j] = 0.0f;
-    if (col < p.H) load_weight<T, VEC>(p, col, w[i]);
+    for (int j = 0; j < NP; ++j) dw[i][j] = 0ull;
   }
+  const float inv_h = __fdiv_rn(1.0f, (float)p.H);
   bool ok = true;
-  int s = 0, before = S - 1;                                // row k's stage and row k - 1's
+  int s = 0, before = ring.S - 1;                           // row k's stage and row k - 1's
   uint32_t phase = 0;
-  for (int64_t k = 0; k < rows; ++k) {
-    const int64_t row = blockIdx.x + k * gridDim.x;
+  for (int k = 0; k < rows; ++k) {
+    const int64_t row = blockIdx.x + (int64_t)k * gridDim.x;
     const float rstd = p.rstd[row];
-    const T *gy, *h, *gh = nullptr;
-    if (RING) {
-      ok = bar_wait(smem_addr(&full[s]), phase);
-      gy = reinterpret_cast<const T*>(dyn + s * stage_bytes);
-      h = gy + p.H;
-      if (p.gh) gh = h + p.H;
-    } else {
-      gy = static_cast<const T*>(p.gy) + row * p.ldy;
-      h = static_cast<const T*>(p.h) + row * p.ldh;
-      if (p.gh) gh = static_cast<const T*>(p.gh) + row * p.ldg;
-    }
-    float sum = 0.0f;
+    ok = bar_wait(smem_addr(&full[s]), phase);
+    const unsigned char* in = dyn + s * stage_bytes;
+    f2 sum2 = 0ull;
 #pragma unroll
     for (int i = 0; i < IT; ++i) {
-      const int col = (i * nt + t) * VEC;
-      if (col < p.H) {
-        float y[VEC], x[VEC];
-        load_f<T, VEC>(gy + col, y);
-        load_f<T, VEC>(h + col, x);
+      const Columns<T, EDGES> c(i * nt + t, off, p.H);
+      if (!c.any()) continue;
+      f2 y[NP], x[NP];
+      read_pairs(in + (i * nt + t) * 16, c, y);
+      read_pairs(in + ring.pitch + (i * nt + t) * 16, c, x);
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) sum = fmaf(y[j] * w[i][j], x[j], sum);
-      }
+      for (int j = 0; j < NP; ++j) sum2 = fma2(mul2(y[j], w[i][j]), x[j], sum2);
     }
-    sum = warp_sum(sum);
-    if (lane == 0) sm[k & 1][warp] = sum;                   // the other half of sm is the row before's
+    float s0, s1;
+    halves(sum2, s0, s1);
+    const float part = warp_sum(s0 + s1);
+    if (lane == 0) sums[k & 1][warp] = part;                // the other half is the row before's
     if (__syncthreads_or(!ok)) {
       ok = false;
       break;
     }
-    if (RING) {                                             // all are past the row before
-      if (t == 0 && k >= 1 && k - 1 + S < rows) fill(k - 1 + S, before);
-      before = s;
-      if (++s == S) {
-        s = 0;
-        phase ^= 1u;
-      }
+    if (fetches && k >= 1 && k - 1 + ring.S < rows) fill(k - 1 + ring.S, before);   // all are past the row before
+    before = s;
+    if (++s == ring.S) {
+      s = 0;
+      phase ^= 1u;
     }
-    sum = 0.0f;
-    for (int i = 0; i < warps; ++i) sum += sm[k & 1][i];
-    const float coef = __fdiv_rn(sum, (float)p.H) * rstd * rstd;
+    // gx = (gy rstd) w + (gh - x coef), coef = rstd^3 mean(g h)
+    const float coef = sum16(sums[k & 1]) * inv_h * rstd * rstd * rstd;
+    const f2 r2 = pair(rstd, rstd), k2 = pair(-coef, -coef);
     T* gx = static_cast<T*>(p.gx) + row * p.H;
 #pragma unroll
     for (int i = 0; i < IT; ++i) {
-      const int col = (i * nt + t) * VEC;
-      if (col < p.H) {
-        float y[VEC], x[VEC];
-        load_f<T, VEC>(gy + col, y);
-        load_f<T, VEC>(h + col, x);
+      const Columns<T, EDGES> c(i * nt + t, off, p.H);
+      if (!c.any()) continue;
+      f2 y[NP], x[NP], g[NP];
+      read_pairs(in + (i * nt + t) * 16, c, y);
+      read_pairs(in + ring.pitch + (i * nt + t) * 16, c, x);
+      if (inputs == 3) {
+        read_pairs(in + 2 * ring.pitch + (i * nt + t) * 16, c, g);
+      } else {
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) {
-          dw[i][j] = fmaf(y[j], x[j] * rstd, dw[i][j]);
-          y[j] = rstd * (y[j] * w[i][j] - x[j] * coef);
-        }
-        if (gh) {
-          load_f<T, VEC>(gh + col, x);
-#pragma unroll
-          for (int j = 0; j < VEC; ++j) y[j] += x[j];
-        }
-        store_f<T, VEC>(gx + col, y);
+        for (int j = 0; j < NP; ++j) g[j] = 0ull;
       }
+#pragma unroll
+      for (int j = 0; j < NP; ++j) {
+        const f2 yr = mul2(y[j], r2);
+        dw[i][j] = fma2(yr, x[j], dw[i][j]);
+        g[j] = fma2(yr, w[i][j], fma2(x[j], k2, g[j]));
+      }
+      write_pairs(gx, c, g);
     }
   }
   if (!ok && t == 0) {                                      // a copy that never came: wait for the others, then end
     atomicExch(&g_norm_status, 1);
-    for (int s = 0; s < S; ++s) {
-      (void)bar_wait(smem_addr(&full[s]), 0);
-      (void)bar_wait(smem_addr(&full[s]), 1);
+    for (int i = 0; i < ring.S; ++i) {
+      (void)bar_wait(smem_addr(&full[i]), 0);
+      (void)bar_wait(smem_addr(&full[i]), 1);
     }
   }
   __syncthreads();
   float* const column_sums = reinterpret_cast<float*>(dyn);
 #pragma unroll
-  for (int i = 0; i < IT; ++i)
+  for (int i = 0; i < IT; ++i) {
+    const Columns<T, EDGES> c(i * nt + t, off, p.H);
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) {
-      const int col = (i * nt + t) * VEC + j;
-      if (col < p.H) column_sums[col] = dw[i][j];
+    for (int j = 0; j < NP; ++j) {
+      float a, b;
+      halves(dw[i][j], a, b);
+      if (2 * j >= c.lo && 2 * j < c.hi) column_sums[c.first + 2 * j] = a;
+      if (2 * j + 1 >= c.lo && 2 * j + 1 < c.hi) column_sums[c.first + 2 * j + 1] = b;
     }
+  }
   cluster_sync();
   const int rank = blockIdx.x % kGradCluster;
   for (int col = rank * nt + t; col < p.H; col += kGradCluster * nt) {
@@ -391,10 +646,10 @@ norm_grad_kernel(const NormGradParams p, int S) {
 #pragma unroll
     for (int r = 0; r < kGradCluster; ++r)
       asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v[r]) : "r"(in_cluster(column_sums + col, r)) : "memory");
-    float s = 0.0f;
+    float a = v[0];
 #pragma unroll
-    for (int r = 0; r < kGradCluster; ++r) s += v[r];
-    p.part[(int64_t)(blockIdx.x / kGradCluster) * p.H + col] = s;
+    for (int r = 1; r < kGradCluster; ++r) a += v[r];
+    p.part[(int64_t)(blockIdx.x / kGradCluster) * p.H + col] = a;
   }
   cluster_sync();
 }
@@ -457,29 +712,22 @@ norm_grad_join_kernel(const float* part, int parts, int H, float* gw) {
 }
 
 // Launches the kernel; the parts that it leaves for the joining kernel, 0 if it failed.
-template <class T, int VEC, int IT, int MAXT, int MINB>
-int launch_grad(const NormGradParams& p, int threads, cudaStream_t st) {
-  auto kernel = norm_grad_kernel<T, VEC, IT, MAXT, MINB>;
-  static std::atomic<bool> done[64];
+template <class T, int IT, int MAXT, int MINB>
+int launch_grad(const NormGradParams& p, int threads, bool aligned16, cudaStream_t st) {
+  auto kernel = aligned16 ? norm_grad_kernel<T, IT, MAXT, MINB, false> : norm_grad_kernel<T, IT, MAXT, MINB, true>;
+  static std::atomic<bool> flags[2][64];
+  std::atomic<bool>* done = flags[aligned16];
   if (!emu_ops_allow_smem(reinterpret_cast<const void*>(kernel), kMaxSmem - 1024, done)) return 0;
-  // CTAs an SM by threads and registers (MAXT * MINB threads have theirs), and a ring that lets that many
-  // share its memory: two rows at least, kGradStages at most
-  int resident = MAXT * MINB / threads < 16 ? MAXT * MINB / threads : 16, S = 0;
-  size_t bytes = (size_t)p.H * 4;
-  if (VEC > 1) {
-    const size_t stage = (size_t)p.H * sizeof(T) * (p.gh ? 3 : 2);
-    while (resident > 1 && (kMaxSmem / resident - 2048) / stage < 3) --resident;
-    S = (int)((kMaxSmem / resident - 2048) / stage);
-    if (S > kGradStages) S = kGradStages;
-    if (bytes < S * stage) bytes = S * stage;
-  } else {
-    while (resident > 1 && kMaxSmem / resident - 2048 < (int)bytes) --resident;
-  }
+  int resident;
+  const int inputs = p.gh ? 3 : 2;
+  const Ring ring = ring_for(p.H, sizeof(T), aligned16, inputs, MAXT * MINB / threads, &resident);
   const int64_t most = (int64_t)emu_ops_sm_count() * resident;
-  int64_t clusters = ((p.T < most ? p.T : most) + kGradCluster - 1) / kGradCluster;
-  if (clusters > kGradParts) clusters = kGradParts;
+  int64_t ctas = p.T < most ? p.T : most;
+  if (ctas > kGradParts * kGradCluster) ctas = kGradParts * kGradCluster;
+  ctas = (ctas + 7) / 8 * 8;                               // whole clusters, and a CTA's rows lie alike
+  const size_t bytes = (size_t)ring.S * inputs * ring.pitch;   // two rows of two tensors at least: room for [H] fp32
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(clusters * kGradCluster));
+  cfg.gridDim = dim3((unsigned)ctas);
   cfg.blockDim = dim3((unsigned)threads);
   cfg.dynamicSmemBytes = bytes;
   cfg.stream = st;
@@ -489,21 +737,17 @@ int launch_grad(const NormGradParams& p, int threads, cudaStream_t st) {
   at.val.clusterDim.y = at.val.clusterDim.z = 1;
   cfg.attrs = &at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, p, S) == cudaSuccess ? (int)clusters : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, p, ring) == cudaSuccess ? (int)(ctas / kGradCluster) : 0;
 }
 
 // The fewest vectors a thread that leave a CTA within its threads; 0: a launch failed.
-template <class T> int pick_norm_grad(const NormGradParams& p, bool vec, cudaStream_t st) {
+template <class T> int pick_norm_grad(const NormGradParams& p, bool alike, bool aligned16, cudaStream_t st) {
   constexpr int V = 16 / sizeof(T);
-  auto threads = [](int n, int it) { return ((n + it - 1) / it + 31) / 32 * 32; };
-  if (vec) {
-    const int nv = p.H / V;
-    if (nv <= 256) return launch_grad<T, V, 1, 256, 5>(p, threads(nv, 1), st);
-    if (nv <= 1024) return launch_grad<T, V, 2, 512, 2>(p, threads(nv, 2), st);
-    if (nv <= 2048) return launch_grad<T, V, 4, 512, 1>(p, threads(nv, 4), st);
-  } else if (p.H <= 8192) {
-    return p.H <= 2048 ? launch_grad<T, 1, 8, 256, 4>(p, threads(p.H, 8), st)
-                       : launch_grad<T, 1, 8, 1024, 1>(p, threads(p.H, 8), st);
+  const int nv = aligned16 ? p.H / V : (p.H + 2 * V - 2) / V;       // vectors that a row can touch
+  if (alike && nv <= 2048) {
+    if (nv <= 256) return launch_grad<T, 1, 256, 5>(p, threads_for(nv, 1), aligned16, st);
+    if (nv <= 1024) return launch_grad<T, 2, 512, 2>(p, threads_for(nv, 2), aligned16, st);
+    return launch_grad<T, 4, 512, 1>(p, threads_for(nv, 4), aligned16, st);
   }
   const int parts = (int)(p.T < kGradParts ? p.T : kGradParts);
   norm_grad_rows_kernel<T><<<(unsigned)p.T, 256, 0, st>>>(p);
@@ -580,20 +824,26 @@ int emu_rms_norm_quant(const void* x, int64_t ldx, const void* residual, int64_t
   p.scale = scale; p.q_format = (int)q_format;
   p.q = static_cast<uint8_t*>(q); p.scale_out = scale_out;
   p.residual_out = residual_out; p.ldo = ldo; p.rstd = rstd;
+  // do all rows start on 16 bytes, or at least all tensors' alike
+  auto at = [](const void* t) { return reinterpret_cast<uintptr_t>(t); };
+  const uintptr_t starts = (at(x) ^ (residual ? at(residual) : at(x))) | (at(x) ^ (residual_out ? at(residual_out) : at(x)));
+  const int64_t strides = (ldx - (residual ? ldr : ldx)) | (ldx - (residual_out ? ldo : ldx));
   const int64_t v = 16 / (int64_t)es;
-  const bool vec = H % v == 0 && ldx % v == 0 && (!residual || ldr % v == 0) && (!residual_out || ldo % v == 0) &&
-                   aligned(x, 16) && aligned(residual, 16) && aligned(residual_out, 16) && aligned(weight, 16) &&
-                   aligned(q, (size_t)v);
+  const bool alike = starts % 16 == 0 && strides % v == 0;
+  const bool aligned16 = alike && aligned(x, 16) && ldx % v == 0 && H % v == 0 && aligned(weight, 16) && aligned(q, (size_t)v);
+  const bool q_vec = at(q) % v == at(x) / es % v && (H - ldx) % v == 0;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (type == EMU_OUT_F32) pick_norm<float>(p, vec, st);
-  else if (type == EMU_OUT_BF16) pick_norm<__nv_bfloat16>(p, vec, st);
-  else pick_norm<__half>(p, vec, st);
+  rc = type == EMU_OUT_F32    ? pick_norm<float>(p, alike, aligned16, q_vec, st)
+       : type == EMU_OUT_BF16 ? pick_norm<__nv_bfloat16>(p, alike, aligned16, q_vec, st)
+                              : pick_norm<__half>(p, alike, aligned16, q_vec, st);
+  if (rc != EMU_OK) return rc;
   return emu_ops_launched("emu_rms_norm_quant");
 }
 
 size_t emu_rms_norm_backward_workspace_bytes(int64_t T, int64_t H) {
   if (T < 1 || H < 1 || H > (1 << 22)) return 0;
-  return (size_t)(T < kGradParts ? T : kGradParts) * (size_t)H * sizeof(float);
+  const int64_t parts = T < 4 ? 4 : T < kGradParts ? T : kGradParts;   // eight CTAs, four clusters at least
+  return (size_t)parts * (size_t)H * sizeof(float);
 }
 
 int emu_rms_norm_backward(const void* grad_y, int64_t ldy, const void* hidden, int64_t ldh,
@@ -631,12 +881,17 @@ int emu_rms_norm_backward(const void* grad_y, int64_t ldy, const void* hidden, i
   p.gy = grad_y; p.ldy = ldy; p.h = hidden; p.ldh = ldh; p.gh = grad_residual; p.ldg = ldg;
   p.weight = weight; p.weight_f32 = weight_type == EMU_OUT_F32; p.rstd = rstd;
   p.T = T; p.H = (int)H; p.gx = grad_x; p.part = static_cast<float*>(workspace);
+  // do all rows start on 16 bytes, or at least all tensors' alike
+  auto at = [](const void* t) { return reinterpret_cast<uintptr_t>(t); };
+  const uintptr_t bases = (at(grad_y) ^ at(hidden)) | (at(grad_y) ^ at(grad_x)) |
+                          (at(grad_y) ^ (grad_residual ? at(grad_residual) : at(grad_y)));
+  const int64_t strides = (ldy - ldh) | (ldy - H) | (ldy - (grad_residual ? ldg : ldy));
   const int64_t v = 16 / (int64_t)es;
-  const bool vec = H % v == 0 && ldy % v == 0 && ldh % v == 0 && (!grad_residual || ldg % v == 0) && aligned(grad_y, 16) &&
-                   aligned(hidden, 16) && aligned(grad_residual, 16) && aligned(grad_x, 16) && aligned(weight, 16);
-  const int parts = type == EMU_OUT_F32    ? pick_norm_grad<float>(p, vec, st)
-                    : type == EMU_OUT_BF16 ? pick_norm_grad<__nv_bfloat16>(p, vec, st)
-                                           : pick_norm_grad<__half>(p, vec, st);
+  const bool alike = bases % 16 == 0 && strides % v == 0;
+  const bool aligned16 = alike && aligned(grad_y, 16) && ldy % v == 0 && H % v == 0;
+  const int parts = type == EMU_OUT_F32    ? pick_norm_grad<float>(p, alike, aligned16, st)
+                    : type == EMU_OUT_BF16 ? pick_norm_grad<__nv_bfloat16>(p, alike, aligned16, st)
+                                           : pick_norm_grad<__half>(p, alike, aligned16, st);
   if (parts == 0) return emu_ops_launched("emu_rms_norm_backward");
   norm_grad_join_kernel<<<(unsigned)((H + 31) / 32), 256, 0, st>>>(p.part, parts, p.H, grad_weight);
   return emu_ops_launched("emu_rms_norm_backward");
