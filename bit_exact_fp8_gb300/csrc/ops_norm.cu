@@ -487,12 +487,16 @@ int launch_norm_ring(const NormParams& p, int threads, bool aligned16, bool q_ve
   return EMU_OK;
 }
 
+// A row's step has a fixed part for each warp (reduction, barrier, scale), so rows take few threads of
+// many vectors: 8192 x 5760 bf16 in 52.7 us with four vectors a thread, 54.5 with two.  (Few rows would be
+// done a little sooner by more threads, 64 x 5760 in 3.6 us with two vectors, 4.0 with four; but the
+// choice goes by the row's length alone, so that a row's codes do not depend on the rows beside it.)
 template <class T> int pick_norm(const NormParams& p, bool alike, bool aligned16, bool q_vec, cudaStream_t st) {
   constexpr int V = 16 / sizeof(T);
   const int nv = aligned16 ? p.H / V : (p.H + 2 * V - 2) / V;       // vectors that a row can touch
   if (alike && nv <= 2048) {
-    if (nv <= 256) return launch_norm_ring<T, 1, 256, 5>(p, threads_for(nv, 1), aligned16, q_vec, st);
-    if (nv <= 1024) return launch_norm_ring<T, 2, 512, 2>(p, threads_for(nv, 2), aligned16, q_vec, st);
+    if (nv <= 256) return launch_norm_ring<T, 2, 128, 8>(p, threads_for(nv, 2), aligned16, q_vec, st);
+    if (nv <= 1024) return launch_norm_ring<T, 4, 256, 2>(p, threads_for(nv, 4), aligned16, q_vec, st);
     return launch_norm_ring<T, 4, 512, 1>(p, threads_for(nv, 4), aligned16, q_vec, st);
   }
   if (aligned16 && alike) launch_norm<T, V, 512, 0>(p, st);
@@ -502,7 +506,15 @@ template <class T> int pick_norm(const NormParams& p, bool alike, bool aligned16
 }
 
 // ------------------------------------------------------------------------- gradient
-constexpr int kGradParts = 304;                   // two CTAs on each of 152 SMs
+// The parts of column sums that there can be: one of every two CTAs, of up to 608 CTAs, or of up to 2432
+// where rows are short and many CTAs live on an SM (2.5 MB in all).  A multiple of four, as CTAs
+// come by eights.
+int64_t parts_for(int64_t T, int64_t H) {
+  int64_t most = ((int64_t)1 << 20) * 10 / 16 / H;
+  most = most < 304 ? 304 : most > 1216 ? 1216 : most / 4 * 4;
+  const int64_t n = (T + 7) / 8 * 4;
+  return n < most ? n : most;
+}
 
 struct NormGradParams {
   const void* gy; int64_t ldy;
@@ -543,6 +555,7 @@ norm_grad_kernel(const NormGradParams p, const Ring ring) {
     fill_row(dyn + s * stage_bytes + which * ring.pitch, base, which == 0 ? p.ldy : which == 1 ? p.ldh : p.ldg, row, p.T,
              p.H, smem_addr(&full[s]));
   };
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the joining kernel waits for this one's end
   if (t < 16) sums[0][t] = sums[1][t] = 0.0f;
   if (t == 0) {
     for (int i = 0; i < ring.S; ++i) bar_init(smem_addr(&full[i]), inputs);
@@ -693,21 +706,29 @@ norm_grad_weight_kernel(const NormGradParams p) {
                to_f(static_cast<const T*>(p.h)[row * p.ldh + c]) * p.rstd[row], acc);
   p.part[(int64_t)blockIdx.x * p.H + c] = acc;
 }
-// gw[c] = sum of the parts, in order: 32 columns a CTA, eight threads a column
-__global__ void __launch_bounds__(256)
+// gw[c] = sum of the parts: 32 columns a CTA, sixteen threads a column.  Launched while the kernel before
+// it still runs (its parts are waited for here).
+__global__ void __launch_bounds__(512)
 norm_grad_join_kernel(const float* part, int parts, int H, float* gw) {
-  __shared__ float sm[8][33];
+  __shared__ float sm[16][33];
   const int lane = threadIdx.x & 31, g = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + lane;
-  float acc = 0.0f;
-  if (c < H)
-    for (int b = g; b < parts; b += 8) acc += part[(int64_t)b * H + c];
-  sm[g][lane] = acc;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  if (c < H) {
+    int b = g;
+    for (; b + 48 < parts; b += 64)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[i] += part[(int64_t)(b + 16 * i) * H + c];
+    for (; b < parts; b += 16) acc[0] += part[(int64_t)b * H + c];
+  }
+  sm[g][lane] = (acc[0] + acc[1]) + (acc[2] + acc[3]);
   __syncthreads();
   if (g == 0 && c < H) {
+    float a = 0.0f;
 #pragma unroll
-    for (int i = 1; i < 8; ++i) acc += sm[i][lane];
-    gw[c] = acc;
+    for (int i = 0; i < 16; ++i) a += sm[i][lane];
+    gw[c] = a;
   }
 }
 
@@ -722,9 +743,8 @@ int launch_grad(const NormGradParams& p, int threads, bool aligned16, cudaStream
   const int inputs = p.gh ? 3 : 2;
   const Ring ring = ring_for(p.H, sizeof(T), aligned16, inputs, MAXT * MINB / threads, &resident);
   const int64_t most = (int64_t)emu_ops_sm_count() * resident;
-  int64_t ctas = p.T < most ? p.T : most;
-  if (ctas > kGradParts * kGradCluster) ctas = kGradParts * kGradCluster;
-  ctas = (ctas + 7) / 8 * 8;                               // whole clusters, and a CTA's rows lie alike
+  int64_t ctas = ((p.T < most ? p.T : most) + 7) / 8 * 8;  // whole clusters, and a CTA's rows lie alike
+  if (ctas > parts_for(p.T, p.H) * kGradCluster) ctas = parts_for(p.T, p.H) * kGradCluster;
   const size_t bytes = (size_t)ring.S * inputs * ring.pitch;   // two rows of two tensors at least: room for [H] fp32
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)ctas);
@@ -745,11 +765,11 @@ template <class T> int pick_norm_grad(const NormGradParams& p, bool alike, bool 
   constexpr int V = 16 / sizeof(T);
   const int nv = aligned16 ? p.H / V : (p.H + 2 * V - 2) / V;       // vectors that a row can touch
   if (alike && nv <= 2048) {
-    if (nv <= 256) return launch_grad<T, 1, 256, 5>(p, threads_for(nv, 1), aligned16, st);
-    if (nv <= 1024) return launch_grad<T, 2, 512, 2>(p, threads_for(nv, 2), aligned16, st);
+    if (nv <= 256) return launch_grad<T, 2, 128, 6>(p, threads_for(nv, 2), aligned16, st);
+    if (nv <= 1024) return launch_grad<T, 4, 256, 2>(p, threads_for(nv, 4), aligned16, st);
     return launch_grad<T, 4, 512, 1>(p, threads_for(nv, 4), aligned16, st);
   }
-  const int parts = (int)(p.T < kGradParts ? p.T : kGradParts);
+  const int parts = (int)parts_for(p.T, p.H);
   norm_grad_rows_kernel<T><<<(unsigned)p.T, 256, 0, st>>>(p);
   norm_grad_weight_kernel<T><<<dim3((unsigned)parts, (unsigned)((p.H + 255) / 256)), 256, 0, st>>>(p);
   return parts;
@@ -842,8 +862,7 @@ int emu_rms_norm_quant(const void* x, int64_t ldx, const void* residual, int64_t
 
 size_t emu_rms_norm_backward_workspace_bytes(int64_t T, int64_t H) {
   if (T < 1 || H < 1 || H > (1 << 22)) return 0;
-  const int64_t parts = T < 4 ? 4 : T < kGradParts ? T : kGradParts;   // eight CTAs, four clusters at least
-  return (size_t)parts * (size_t)H * sizeof(float);
+  return (size_t)parts_for(T, H) * (size_t)H * sizeof(float);
 }
 
 int emu_rms_norm_backward(const void* grad_y, int64_t ldy, const void* hidden, int64_t ldh,
@@ -893,7 +912,18 @@ int emu_rms_norm_backward(const void* grad_y, int64_t ldy, const void* hidden, i
                     : type == EMU_OUT_BF16 ? pick_norm_grad<__nv_bfloat16>(p, alike, aligned16, st)
                                            : pick_norm_grad<__half>(p, alike, aligned16, st);
   if (parts == 0) return emu_ops_launched("emu_rms_norm_backward");
-  norm_grad_join_kernel<<<(unsigned)((H + 31) / 32), 256, 0, st>>>(p.part, parts, p.H, grad_weight);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((H + 31) / 32));
+  cfg.blockDim = dim3(512);
+  cfg.stream = st;
+  cudaLaunchAttribute early;
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &early;
+  cfg.numAttrs = 1;
+  const float* sums = p.part;
+  if (cudaLaunchKernelEx(&cfg, norm_grad_join_kernel, sums, parts, p.H, grad_weight) != cudaSuccess)
+    return emu_ops_launched("emu_rms_norm_backward");
   return emu_ops_launched("emu_rms_norm_backward");
 }
 
