@@ -566,50 +566,68 @@ struct LogprobGradParams {
   void* gx; int64_t ldo;
 };
 
-// gx = gl ([v = token] - p) - ge p (log p + H), log p = (x - m) - log z.  TPR threads a row and part of
-// it, four vectors each; `same` says that logits and gradient rows lie alike about 16-byte
-// addresses.
+// gx = gl ([v = token] - p) - ge p (log p + H) = p (-ge log p - (ge H + gl)) + gl [v = token], with
+// log p = (x - m) - log z.  TPR threads a row and part of it, four vectors each, in fp32 pairs;
+// `same` says that logits and gradient rows lie alike about 16-byte addresses.
 template <class T, int TPR>
 __global__ void __launch_bounds__(256)
-logprob_grad_kernel(const LogprobGradParams p, int parts, bool same) {
+logprob_grad_kernel(const LogprobGradParams p, uint32_t parts, bool same) {
   constexpr int VEC = Row<T>::VEC, U = 4;
   const int t = threadIdx.x % TPR;
-  const int64_t unit = (int64_t)blockIdx.x * (256 / TPR) + threadIdx.x / TPR;
-  const int64_t r = unit / parts;
+  const uint32_t unit = blockIdx.x * (256 / TPR) + threadIdx.x / TPR;
+  const uint32_t r32 = unit / parts;
+  const int64_t r = r32;
   if (r >= p.T) return;
   const Row<T> row(static_cast<const T*>(p.x) + r * p.ldx, p.V);
   T* gx = static_cast<T*>(p.gx) + r * p.ldo;
+  const int v0 = (int)(unit - r32 * parts) * (TPR * U) + t;
+  uint4 raw[U];
+#pragma unroll
+  for (int i = 0; i < U; ++i)
+    if (v0 + i * TPR < row.nvec) raw[i] = row.load_raw(v0 + i * TPR);
   const float m = p.stats[r * 3], logz = p.stats[r * 3 + 1], H = p.stats[r * 3 + 2];
   const int64_t tok = p.tokens[r];
   const bool out_of_range = tok != p.ignore && (tok < 0 || tok >= p.V);
   const float gl = tok == p.ignore || !p.g_logprob ? 0.0f : out_of_range ? NAN : p.g_logprob[r];
   const float ge = p.g_entropy ? p.g_entropy[r] : 0.0f;
   const bool empty = m == -INFINITY && logz == -INFINITY;
-  const int hot = tok >= 0 && tok < p.V ? (int)tok : -1;
-  const int v0 = (int)(unit - r * parts) * (TPR * U) + t;
-  float f[U][VEC];
-#pragma unroll
-  for (int i = 0; i < U; ++i)
-    if (v0 + i * TPR < row.nvec) row.load(v0 + i * TPR, f[i]);
+  const int hot = !empty && tok >= 0 && tok < p.V ? (int)tok : -1;
+  const f2 m2 = pair(-m, -m), z2 = pair(-logz, -logz), L2 = pair(kLog2e, kLog2e), e2 = pair(-ge, -ge);
+  const float rest = -fmaf(ge, H, gl);
+  const f2 c2 = pair(rest, rest);
 #pragma unroll
   for (int i = 0; i < U; ++i) {
     const int v = v0 + i * TPR;
     if (v >= row.nvec) break;
     const int id0 = row.first(v);
+    float f[VEC];
+    Row<T>::unpack(raw[i], f);
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) {
-      const float lp = f[i][j] - m - logz;
-      const float pr = exp2_approx(lp * kLog2e);
-      float g = -pr * fmaf(ge, max_nan(lp, -1e4f) + H, gl);
-      if (id0 + j == hot) g += gl;
-      f[i][j] = empty ? 0.0f : g;
+    for (int j = 0; j < VEC; j += 2) {
+      const f2 lp = add2(add2(pair(f[j], f[j + 1]), m2), z2);
+      float l0, l1, a0, a1;
+      halves(lp, l0, l1);
+      halves(mul2(lp, L2), a0, a1);
+      const f2 pr = pair(exp2_approx(a0), exp2_approx(a1));
+      // p = 0 where log p is -inf: a finite number in its place
+      halves(mul2(pr, fma2(pair(max_nan(l0, -1e4f), max_nan(l1, -1e4f)), e2, c2)), f[j], f[j + 1]);
+    }
+    if (empty) {
+      asm volatile("");                                  // branches: few rows and vectors take them
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) f[j] = 0.0f;
+    }
+    if ((uint32_t)(hot - id0) < (uint32_t)VEC && hot >= 0) {
+      asm volatile("");
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) f[j] += id0 + j == hot ? gl : 0.0f;
     }
     if (same && row.whole(v)) {
-      store_f<T, VEC>(gx + id0, f[i]);
+      store_f<T, VEC>(gx + id0, f);
     } else {
 #pragma unroll
       for (int j = 0; j < VEC; ++j)
-        if (id0 + j >= 0 && id0 + j < p.V) gx[id0 + j] = from_f<T>(f[i][j]);
+        if (id0 + j >= 0 && id0 + j < p.V) gx[id0 + j] = from_f<T>(f[j]);
     }
   }
 }
@@ -620,7 +638,7 @@ template <class T> void pick_logprob_grad(const LogprobGradParams& p, cudaStream
                     ((p.ldx - p.ldo) * (int64_t)sizeof(T)) % 16 == 0;
   // rows of parts, at most 2^31 - 1 CTAs a launch
   const int tpr = nvec <= 256 ? 32 : 256;
-  const int parts = (nvec + tpr * 4 - 1) / (tpr * 4);
+  const uint32_t parts = (uint32_t)((nvec + tpr * 4 - 1) / (tpr * 4));
   const int64_t rows = ((int64_t)1 << 30) / parts;
   for (int64_t r = 0; r < p.T; r += rows) {
     LogprobGradParams q = p;
