@@ -29,12 +29,39 @@ struct Int8Params {
   void* out; int out_type;                        // [M, N] contiguous
 };
 
-__device__ __forceinline__ void store_out(const Int8Params& p, int64_t m, int64_t n, int acc) {
-  const float v = ((float)acc * p.scale_a[m * p.sa_step]) * p.scale_b[n * p.sb_step];
+// the scales by the read-only path, so that their loads need not wait for the stores before them
+__device__ __forceinline__ float scale_a(const Int8Params& p, int64_t m) { return __ldg(p.scale_a + m * p.sa_step); }
+__device__ __forceinline__ float scale_b(const Int8Params& p, int64_t n) { return __ldg(p.scale_b + n * p.sb_step); }
+__device__ __forceinline__ void store_out(const Int8Params& p, int64_t m, int64_t n, int acc, float sa, float sb) {
+  const float v = ((float)acc * sa) * sb;
   const int64_t i = m * p.N + n;
   if (p.out_type == EMU_OUT_F32) static_cast<float*>(p.out)[i] = v;
   else if (p.out_type == EMU_OUT_BF16) static_cast<__nv_bfloat16*>(p.out)[i] = __float2bfloat16_rn(v);
   else static_cast<__half*>(p.out)[i] = __float2half_rn(v);
+}
+// outputs (m, n) to (m, n + N - 1), of which the matrix may have fewer; `together`: it has all or none of
+// them, and they can be stored at once
+template <int N>
+__device__ __forceinline__ void store_row(const Int8Params& p, int64_t m, int64_t n, const int (&acc)[N], float sa,
+                                          const float (&sb)[N], bool together) {
+  if (m >= p.M || n >= p.N) return;
+  if (together) {
+    float v[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = ((float)acc[i] * sa) * sb[i];
+    const int64_t at = m * p.N + n;
+    if (p.out_type == EMU_OUT_F32) store_f<float, N>(static_cast<float*>(p.out) + at, v);
+    else if (p.out_type == EMU_OUT_BF16) store_f<__nv_bfloat16, N>(static_cast<__nv_bfloat16*>(p.out) + at, v);
+    else store_f<__half, N>(static_cast<__half*>(p.out) + at, v);
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (n + i < p.N) store_out(p, m, n + i, acc[i], sa, sb[i]);
+  }
+}
+template <int N> __device__ __forceinline__ bool stores_together(const Int8Params& p) {
+  const uintptr_t es = p.out_type == EMU_OUT_F32 ? 4 : 2;
+  return p.N % N == 0 && (reinterpret_cast<uintptr_t>(p.out) & (N * es - 1)) == 0;
 }
 
 __device__ __forceinline__ int dot16(const uint4& a, const uint4& b, int acc) {
@@ -71,7 +98,7 @@ int8_dot_kernel(const Int8Params p) {
 #pragma unroll
       for (int j = 0; j < NT; ++j) {
         const int s = __reduce_add_sync(0xFFFFFFFFu, acc[i][j]);
-        if (lane == (i * NT + j) % 32 && m0 + i < p.M && n0 + j < p.N) store_out(p, m0 + i, n0 + j, s);
+        if (lane == (i * NT + j) % 32 && m0 + i < p.M && n0 + j < p.N) store_out(p, m0 + i, n0 + j, s, scale_a(p, m0 + i), scale_b(p, n0 + j));
       }
   }
 }
@@ -94,211 +121,33 @@ __device__ __forceinline__ void codes_to_f16(uint32_t w, uint32_t& lo, uint32_t&
 }
 
 // ---------------------------------------------------------------------------------------
-// Rows copied to 16-byte aligned rows of `ldo` codes, zeros after the K-th: for operands whose
-// rows the vector kernels cannot read as they are.  One warp a row and step.
+// Rows of A, then of B, copied to 16-byte aligned rows of `ldo` codes, zeros after the K-th: for operands
+// whose rows the vector kernels cannot read as they are.  A thread takes 16 codes.
 __global__ void __launch_bounds__(256)
-int8_align_kernel(const int8_t* in, int64_t ld, int64_t rows, int K, int8_t* out, int64_t ldo) {
-  const int words = (int)(ldo / 4);
-  for (int64_t row = blockIdx.x; row < rows; row += gridDim.x) {
-    const int8_t* r = in + row * ld;
-    for (int i = threadIdx.x; i < words; i += 256) {
-      uint32_t w = 0;
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (4 * i + j < K) w |= (uint32_t)(uint8_t)r[4 * i + j] << (8 * j);
-      reinterpret_cast<uint32_t*>(out + row * ldo)[i] = w;
+int8_align_kernel(const int8_t* a, int64_t lda, int64_t rows_a, const int8_t* b, int64_t ldb, int64_t rows_b, int K,
+                  int8_t* out_a, int8_t* out_b, int ldo) {
+  const uint32_t chunks = (uint32_t)ldo / 16;
+  const int64_t rows = rows_a + rows_b, total = rows * chunks;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
+    int64_t row;
+    uint32_t c;
+    if (total <= 0xFFFFFFFFll) {
+      const uint32_t q = (uint32_t)i / chunks;
+      row = q;
+      c = (uint32_t)i - q * chunks;
+    } else {
+      row = i / chunks;
+      c = (uint32_t)(i - row * chunks);
     }
+    const bool is_a = row < rows_a;
+    const int64_t r = is_a ? row : row - rows_a;
+    const int8_t* src = (is_a ? a + r * lda : b + r * ldb) + c * 16;
+    uint32_t w[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+    for (int j = 0; j < 16; ++j)
+      if ((int)c * 16 + j < K) w[j >> 2] |= (uint32_t)(uint8_t)src[j] << (8 * (j & 3));
+    *reinterpret_cast<uint4*>((is_a ? out_a : out_b) + r * ldo + c * 16) = make_uint4(w[0], w[1], w[2], w[3]);
   }
-}
-
-// ---------------------------------------------------------------------------------------
-// A few to a few hundred tokens: fp16 warp products of the codes.  mma.sync on int8 runs at
-// the rate of the dp4a instruction here (75 TMAC/s measured), on fp16 four times faster (303),
-// and 1024 products of at most 2^14 in magnitude sum exactly in fp32: so the codes become
-// fp16 in registers, and every 1024 of K the fp32 sums move into 32-bit integers.
-//
-// A CTA takes BM x BN outputs and one of S slices of K; its warps hold MT x NT fragments of
-// 16 x 8.  Stages of 128 codes of K come by cp.async into a ring of NS.  The order of K inside a
-// product is free as long as both operands agree: each thread reads 16 consecutive codes of
-// its row, four of them for each of four 16-wide steps.  A row's 16-byte chunks are permuted
-// by its number so that the eight threads of a shared-memory phase read distinct banks.
-// The S slices are the CTAs of a cluster: each leaves its integer sums in shared memory and
-// adds up its share of the tile over all of them.
-template <int WM, int WN, int MT, int NT> struct MmaShape {
-  static constexpr int BM = WM * MT * 16, BN = WN * NT * 8, THREADS = WM * WN * 32, NS = 4;
-  static constexpr int STAGE = (BM + BN) * 128;
-  static constexpr int SUMS = BM * BN * 4;
-  static constexpr int SMEM = NS * STAGE > SUMS ? NS * STAGE : SUMS;
-};
-
-__device__ __forceinline__ int chunk_at(int row, int c) { return c ^ (((row & 1) << 2) | ((row >> 1) & 3)); }
-
-__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-      "{%0, %1, %2, %3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
-}
-
-template <int WM, int WN, int MT, int NT>
-__global__ void __launch_bounds__(WM * WN * 32)
-int8_mma_kernel(const Int8Params p, int S) {
-  using SH = MmaShape<WM, WN, MT, NT>;
-  constexpr int BM = SH::BM, BN = SH::BN, NS = SH::NS, NTH = SH::THREADS;
-  extern __shared__ __align__(128) unsigned char smem[];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int wm = warp % WM, wn = warp / WM;
-  const int slice = blockIdx.x % S;
-  const int64_t n0 = (int64_t)(blockIdx.x / S) * BN, m0 = (int64_t)blockIdx.y * BM;
-  // this slice's stages of 128 codes
-  const int all = (p.K + 127) / 128, first = (int)((int64_t)all * slice / S);
-  const int count = (int)((int64_t)all * (slice + 1) / S) - first;
-
-  auto fill = [&](int st) {
-    unsigned char* base = smem + (st % NS) * SH::STAGE;
-    const int k0 = (first + st) * 128;
-    for (int i = tid; i < (BM + BN) * 8; i += NTH) {
-      const int row = i >> 3, c = i & 7, k = k0 + c * 16;
-      const bool is_a = row < BM;
-      const int64_t r = is_a ? m0 + row : n0 + (row - BM);
-      const bool in = k < p.K && r < (is_a ? p.M : p.N);
-      const int8_t* src = is_a ? p.a + (in ? r * p.lda + k : 0) : p.b + (in ? r * p.ldb + k : 0);
-      const uint32_t dst = smem_addr(base + row * 128 + chunk_at(row, c) * 16);
-      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
-    }
-  };
-#pragma unroll
-  for (int st = 0; st < NS - 1; ++st) {
-    if (st < count) fill(st);
-    asm volatile("cp.async.commit_group;" ::: "memory");
-  }
-
-  float acc[MT][NT][4] = {};
-  int sum[MT][NT][4] = {};
-  const int g = lane >> 2, t = lane & 3;
-  for (int st = 0; st < count; ++st) {
-    asm volatile("cp.async.wait_group %0;" ::"n"(NS - 2) : "memory");
-    __syncthreads();                       // stage st landed; stage st - 1 read by all
-    if (st + NS - 1 < count) fill(st + NS - 1);
-    asm volatile("cp.async.commit_group;" ::: "memory");
-    const unsigned char* sa = smem + (st % NS) * SH::STAGE + wm * MT * 16 * 128;
-    const unsigned char* sb = smem + (st % NS) * SH::STAGE + (BM + wn * NT * 8) * 128;
-#pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      uint4 aw[MT][2], bw[NT];
-#pragma unroll
-      for (int i = 0; i < MT; ++i)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int r = i * 16 + h * 8 + g;
-          aw[i][h] = *reinterpret_cast<const uint4*>(sa + r * 128 + chunk_at(r, half * 4 + t) * 16);
-        }
-#pragma unroll
-      for (int j = 0; j < NT; ++j) {
-        const int r = j * 8 + g;
-        bw[j] = *reinterpret_cast<const uint4*>(sb + r * 128 + chunk_at(r, half * 4 + t) * 16);
-      }
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        auto word = [q](const uint4& v) { return q == 0 ? v.x : q == 1 ? v.y : q == 2 ? v.z : v.w; };
-        uint32_t bf[NT][2];
-#pragma unroll
-        for (int j = 0; j < NT; ++j) codes_to_f16(word(bw[j]), bf[j][0], bf[j][1]);
-#pragma unroll
-        for (int i = 0; i < MT; ++i) {
-          uint32_t af[4];
-          codes_to_f16(word(aw[i][0]), af[0], af[2]);
-          codes_to_f16(word(aw[i][1]), af[1], af[3]);
-#pragma unroll
-          for (int j = 0; j < NT; ++j) mma_f16(acc[i][j], af, bf[j]);
-        }
-      }
-    }
-    if ((st & 7) == 7 || st + 1 == count) {  // 1024 products a sum at most
-#pragma unroll
-      for (int i = 0; i < MT; ++i)
-#pragma unroll
-        for (int j = 0; j < NT; ++j)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            sum[i][j][e] += __float2int_rn(acc[i][j][e]);
-            acc[i][j][e] = 0.0f;
-          }
-    }
-  }
-  asm volatile("cp.async.wait_group 0;" ::: "memory");
-
-  if (S == 1) {
-#pragma unroll
-    for (int i = 0; i < MT; ++i)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int64_t m = m0 + (wm * MT + i) * 16 + (e >> 1) * 8 + g;
-#pragma unroll
-        for (int j = 0; j < NT; ++j) {
-          const int64_t n = n0 + (wn * NT + j) * 8 + 2 * t + (e & 1);
-          if (m < p.M && n < p.N) store_out(p, m, n, sum[i][j][e]);
-        }
-      }
-    return;
-  }
-  __syncthreads();                         // the ring is free: the sums take its place
-  int* own = reinterpret_cast<int*>(smem);
-#pragma unroll
-  for (int i = 0; i < MT; ++i)
-#pragma unroll
-    for (int j = 0; j < NT; ++j)
-#pragma unroll
-      for (int e = 0; e < 4; e += 2)
-        *reinterpret_cast<int2*>(own + ((wm * MT + i) * 16 + (e >> 1) * 8 + g) * BN + (wn * NT + j) * 8 + 2 * t) =
-            make_int2(sum[i][j][e], sum[i][j][e + 1]);
-  cluster_sync();
-  for (int i = slice * NTH + tid; i < BM * BN; i += S * NTH) {
-    const int64_t m = m0 + i / BN, n = n0 + i % BN;
-    int v = 0;
-    for (int r = 0; r < S; ++r) {
-      int x;
-      asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(x) : "r"(in_cluster(own + i, r)) : "memory");
-      v += x;
-    }
-    if (m < p.M && n < p.N) store_out(p, m, n, v);
-  }
-  cluster_sync();
-}
-
-template <int WM, int WN, int MT, int NT> int launch_mma(const Int8Params& p, cudaStream_t st) {
-  using SH = MmaShape<WM, WN, MT, NT>;
-  auto kernel = int8_mma_kernel<WM, WN, MT, NT>;
-  static std::atomic<bool> done[64];
-  if (!emu_ops_allow_smem(reinterpret_cast<const void*>(kernel), SH::SMEM, done)) return emu_ops_launched("cudaFuncSetAttribute");
-  const int64_t tn = (p.N + SH::BN - 1) / SH::BN;
-  // as many slices as fill the SMs twice over, of four stages at least
-  const int sms = emu_ops_sm_count();
-  int S = 1;
-  const int64_t tiles = tn * ((p.M + SH::BM - 1) / SH::BM);
-  while (S < 8 && tiles * S < 2 * sms && (p.K + 127) / 128 >= 8 * S) S *= 2;
-  // rows of tiles on grid.y, at most 65535 a launch
-  for (int64_t m = 0; m < p.M; m += (int64_t)65535 * SH::BM) {
-    Int8Params q = p;
-    q.M = p.M - m < (int64_t)65535 * SH::BM ? p.M - m : (int64_t)65535 * SH::BM;
-    q.a += m * p.lda;
-    q.scale_a += m * p.sa_step;
-    q.out = static_cast<unsigned char*>(p.out) + (size_t)(m * p.N) * elem_bytes((emu_out_t)p.out_type);
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(tn * S), (unsigned)((q.M + SH::BM - 1) / SH::BM));
-    cfg.blockDim = dim3(SH::THREADS);
-    cfg.dynamicSmemBytes = SH::SMEM;
-    cfg.stream = st;
-    cudaLaunchAttribute at;
-    at.id = cudaLaunchAttributeClusterDimension;
-    at.val.clusterDim.x = (unsigned)S;
-    at.val.clusterDim.y = at.val.clusterDim.z = 1;
-    cfg.attrs = &at;
-    cfg.numAttrs = S > 1 ? 1 : 0;
-    if (cudaLaunchKernelEx(&cfg, kernel, q, S) != cudaSuccess) return emu_ops_launched("emu_int8_scaled_mm");
-  }
-  return EMU_OK;
 }
 
 }  // namespace emu_ops
@@ -336,10 +185,10 @@ inline size_t round256(size_t v) { return (v + 255) & ~(size_t)255; }
 inline int64_t round_up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
 
 // How a product is computed, by its sizes alone.
-enum class Int8Kind { dot, mma, tensor };
+enum class Int8Kind { dot, few, tensor };
 struct Plan {
   Int8Kind kind;
-  int64_t Kp;                    // operands laid out in rows of Kp values (mma: only where not aligned)
+  int64_t Kp;                    // operands laid out in rows of Kp values (others: only where not aligned)
   int64_t rows_a, rows_b;        // tensor: the rows laid out at a time
   size_t a_bytes, b_bytes;       // workspace: A's part, then B's
 };
@@ -347,7 +196,7 @@ constexpr size_t kSlabBytes = (size_t)128 << 20;   // fp16 rows at a time, so th
 
 Plan plan_for(int64_t M, int64_t N, int64_t K, bool aligned16) {
   Plan pl = {};
-  pl.kind = M <= 4 ? Int8Kind::dot : M >= 256 && N >= 128 && K >= 128 ? Int8Kind::tensor : Int8Kind::mma;
+  pl.kind = M <= 4 || K == 0 ? Int8Kind::dot : M >= 256 && N >= 128 && K >= 128 ? Int8Kind::tensor : Int8Kind::few;
   if (pl.kind == Int8Kind::tensor) {
     pl.Kp = round_up(K, kTcBK);
     const int64_t most = (int64_t)(kSlabBytes / (2 * (size_t)pl.Kp)) / kTcBN * kTcBN;   // K < 2^17: 512 rows at least
@@ -401,6 +250,48 @@ int launch_tc(const Int8Params& p, const Plan& pl, bool vec, unsigned char* ws, 
   return EMU_OK;
 }
 
+template <int BT> int launch_few(const Int8Params& p, cudaStream_t st) {
+  using SH = FewShape<BT>;
+  // slices of K: rounds of CTAs (`resident` an SM) times the stages of a slice and, in stages, a CTA's fixed time
+  const int64_t tn = (p.N + 127) / 128, tiles = tn * ((p.M + BT - 1) / BT), room = (int64_t)emu_ops_sm_count() * SH::RESIDENT;
+  const int stages = (p.K + 127) / 128;
+  int S = 1;
+  int64_t best = 0;
+  for (int n = 1; n <= kMaxSlices && n <= stages; ++n) {
+    const int64_t cost = (tiles * n + room - 1) / room * ((stages + n - 1) / n + kFixedStages);
+    if (n == 1 || cost < best) {
+      best = cost;
+      S = n;
+    }
+  }
+  const bool is_long = (stages + S - 1) / S > 8;
+  auto kernel = is_long ? int8_few_kernel<BT, true> : int8_few_kernel<BT, false>;
+  static std::atomic<bool> done[2][64];
+  if (!emu_ops_allow_smem(reinterpret_cast<const void*>(kernel), SH::SMEM, done[is_long]))
+    return emu_ops_launched("cudaFuncSetAttribute");
+  // rows of tiles on grid.y, at most 65535 a launch
+  for (int64_t m = 0; m < p.M; m += (int64_t)65535 * BT) {
+    Int8Params q = p;
+    q.M = p.M - m < (int64_t)65535 * BT ? p.M - m : (int64_t)65535 * BT;
+    q.a += m * p.lda;
+    q.scale_a += m * p.sa_step;
+    q.out = static_cast<unsigned char*>(p.out) + (size_t)(m * p.N) * elem_bytes((emu_out_t)p.out_type);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(tn * S), (unsigned)((q.M + BT - 1) / BT));
+    cfg.blockDim = dim3(kFewThreads);
+    cfg.dynamicSmemBytes = SH::SMEM;
+    cfg.stream = st;
+    cudaLaunchAttribute at;
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim.x = (unsigned)S;
+    at.val.clusterDim.y = at.val.clusterDim.z = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = S > 1 ? 1 : 0;
+    if (cudaLaunchKernelEx(&cfg, kernel, q, S) != cudaSuccess) return emu_ops_launched("emu_int8_scaled_mm");
+  }
+  return EMU_OK;
+}
+
 int run_plan(const Int8Params& p, bool vec, void* workspace, cudaStream_t st) {
   const Plan pl = plan_for(p.M, p.N, p.K, vec);
   unsigned char* ws = static_cast<unsigned char*>(workspace);
@@ -412,8 +303,9 @@ int run_plan(const Int8Params& p, bool vec, void* workspace, cudaStream_t st) {
   if (!vec && p.K > 0) {
     int8_t* a = reinterpret_cast<int8_t*>(ws);
     int8_t* b = reinterpret_cast<int8_t*>(ws + pl.a_bytes);
-    int8_align_kernel<<<(unsigned)(p.M < 8192 ? p.M : 8192), 256, 0, st>>>(p.a, p.lda, p.M, p.K, a, pl.Kp);
-    int8_align_kernel<<<(unsigned)(p.N < 8192 ? p.N : 8192), 256, 0, st>>>(p.b, p.ldb, p.N, p.K, b, pl.Kp);
+    const int64_t work = (p.M + p.N) * (pl.Kp / 16), blocks = (work + 255) / 256;
+    int8_align_kernel<<<(unsigned)(blocks < 16384 ? blocks : 16384), 256, 0, st>>>(p.a, p.lda, p.M, p.b, p.ldb, p.N, p.K, a, b,
+                                                                                  (int)pl.Kp);
     q.a = a;
     q.b = b;
     q.lda = q.ldb = pl.Kp;
@@ -421,9 +313,10 @@ int run_plan(const Int8Params& p, bool vec, void* workspace, cudaStream_t st) {
   }
   int rc;
   if (pl.kind == Int8Kind::dot) rc = q.M == 1 ? launch_dot<1>(q, st) : launch_dot<4>(q, st);
-  else if (q.M <= 16) rc = launch_mma<1, 4, 1, 2>(q, st);
-  else if (q.M <= 32) rc = launch_mma<1, 4, 2, 2>(q, st);
-  else rc = launch_mma<2, 2, 2, 4>(q, st);
+  else if (q.M <= 16) rc = launch_few<16>(q, st);
+  else if (q.M <= 32) rc = launch_few<32>(q, st);
+  else if (q.M <= 64) rc = launch_few<64>(q, st);
+  else rc = launch_few<128>(q, st);
   return rc == EMU_OK ? emu_ops_launched("emu_int8_scaled_mm") : rc;
 }
 

@@ -1,11 +1,12 @@
-// ops_int8_tc.cuh -- the int8 product on the 5th-generation tensor cores, for many tokens.
+// ops_int8_tc.cuh -- the int8 product on the 5th-generation tensor cores.
 //
-// sm_103a's tcgen05 has no int8 kind, but a code is exact in fp16, a product of two is at
-// most 2^14 in magnitude, and 1024 of them sum exactly in the fp32 accumulator (every partial
-// sum is a whole number of at most 2^24).  So the codes are laid out once as fp16, rows padded
-// with zeros to a multiple of 64, and multiplied by tcgen05.mma kind::f16; after every 1024 of
-// K the accumulator is read back and added up in 32-bit integers, while the MMAs go on in the
-// other of two accumulators.
+// sm_103a's tcgen05 has no int8 kind (and mma.sync on int8 runs at the rate of the dp4a
+// instruction, 75 TMAC/s measured), but a code is exact in fp16, a product of two is at most
+// 2^14 in magnitude, and 1024 of them sum exactly in the fp32 accumulator: every partial sum is
+// a whole number of at most 2^24.  So the codes are multiplied as fp16 by tcgen05.mma
+// kind::f16, and after every 1024 of K the accumulator is read back and added up in 32-bit
+// integers.  Two kernels: for many tokens, operands laid out as fp16 by a kernel before and
+// loaded by TMA; for few, codes converted on the way into shared memory, and K in slices.
 #pragma once
 #include "ops_common.cuh"
 
@@ -73,6 +74,238 @@ __device__ __forceinline__ void tc_read32(uint32_t addr, float (&r)[32]) {
       : "memory");
 }
 
+// ---------------------------------------------------------------------------------------
+// Up to a few hundred tokens, where reading B and the latency of each step count.  A CTA takes 128
+// columns of B (the M side of the MMA) by BT tokens (its N side) and one of S slices of K.  Eight
+// warps load codes straight into registers, some stages of 128 of K ahead, convert them and store
+// them as K-major fp16 rows under the 128-byte swizzle in one of two buffers; a ninth issues the
+// eight MMAs of a stage (issuing them takes as long as they run, about 740 cycles at 64 tokens, so
+// a converting warp would hold the others up).  The S slices are the CTAs of a cluster: each
+// leaves its integer sums in shared memory and adds up its share of the tile over all of them.
+// (The same on mma.sync, each warp converting its own fragments, took 13.4 us for
+// 64 x 5760 x 1920: six times the instructions, as fragments are converted again by each warp.)
+constexpr int kMaxSlices = 8, kFixedStages = 4;
+template <int BT> struct FewShape {
+  static constexpr int ROWS = 128 + BT, ATOM = ROWS * 128, STAGE = 2 * ATOM;   // an atom: 64 of K
+  static constexpr int PIECES = (ROWS * 8 + 255) / 256;                        // of 16 codes, a thread
+  static constexpr int SMEM = 2 * STAGE + 1024;
+  static constexpr int RESIDENT = 228 * 1024 / (SMEM + 2048) < 2 ? 1 : 2;      // CTAs an SM
+  static constexpr int COLS = BT < 32 ? 32 : BT;                               // of tensor memory
+  static constexpr int OWN = BT < 32 ? 16 : BT / 2;                            // tokens a thread reads back
+  static constexpr int AHEAD = BT < 64 ? 3 : 2;                                // stages in registers
+  static_assert(BT * 128 * 4 <= 2 * STAGE, "the sums take the buffers' place");
+};
+
+template <int N> __device__ __forceinline__ void tc_read(uint32_t addr, float (&r)[N]) {
+  if constexpr (N == 16) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
+        "[%16];\ntcgen05.wait::ld.sync.aligned;"
+        : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]), "=f"(r[8]),
+          "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15])
+        : "r"(addr)
+        : "memory");
+  } else {
+    tc_read32(addr, r);
+  }
+}
+
+// LONG: slices of more than eight stages, whose sums are taken out of the tensor memory every 1024 of K
+constexpr int kFewThreads = 288;
+template <int BT, bool LONG>
+__global__ void __launch_bounds__(kFewThreads, FewShape<BT>::RESIDENT)
+int8_few_kernel(const Int8Params p, int S) {
+  using SH = FewShape<BT>;
+  constexpr int PP = SH::PIECES, AHEAD = SH::AHEAD, STEP = SH::OWN < 32 ? 16 : 32;
+  extern __shared__ unsigned char raw_smem[];
+  __shared__ __align__(8) uint64_t bars[5];                 // full[2], empty[2], read (sums taken)
+  __shared__ uint32_t slot;
+  __shared__ int gave_up;
+  unsigned char* const smem = raw_smem + ((1024u - (smem_addr(raw_smem) & 1023u)) & 1023u);
+  const uint32_t base = smem_addr(smem), full = smem_addr(bars), empty = full + 16, taken = full + 32;
+  volatile int* const given_up = &gave_up;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const uint32_t slice = blockIdx.x % (uint32_t)S;
+  const int64_t n0 = (int64_t)(blockIdx.x / (uint32_t)S) * 128, m0 = (int64_t)blockIdx.y * BT;
+  const uint32_t all = (uint32_t)(p.K + 127) / 128, first = all * slice / (uint32_t)S;
+  const int count = (int)(all * (slice + 1) / (uint32_t)S - first);     // stages of 128 codes
+  // piece i of a thread: codes 16 c8 to 16 c8 + 15 of a stage, of row r8 + 32 i (B's 128 rows, then tokens)
+  const int c8 = tid & 7, r8 = (tid & 255) >> 3;
+  const int8_t* at[PP];
+  uint4 w[AHEAD][PP];
+  auto load = [&](int st, uint4 (&v)[PP]) {
+    const int k = (int)(first + st) * 128 + c8 * 16;
+    const bool in = st < count && k < p.K;
+#pragma unroll
+    for (int i = 0; i < PP; ++i) {
+      v[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (in && at[i]) v[i] = *reinterpret_cast<const uint4*>(at[i] + k);
+    }
+  };
+  if (warp < 8) {
+#pragma unroll
+    for (int i = 0; i < PP; ++i) {
+      const int64_t r = i < 4 ? n0 + r8 + 32 * i : m0 + r8 + 32 * (i - 4);
+      const bool in = r < (i < 4 ? p.N : p.M) && (i < 4 || r8 + 32 * (i - 4) < BT);
+      at[i] = in ? (i < 4 ? p.b + r * p.ldb : p.a + r * p.lda) : nullptr;
+    }
+#pragma unroll
+    for (int u = 0; u < AHEAD; ++u) load(u, w[u]);
+  } else {
+    if (lane == 0) {
+      for (int i = 0; i < 2; ++i) {
+        bar_init(full + 8 * i, 8);                          // one arrival a converting warp
+        bar_init(empty + 8 * i, 1);                         // a stage's MMAs
+      }
+      bar_init(taken, 8);
+      gave_up = 0;
+      bar_init_fence();
+    }
+    __syncwarp();
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&slot)), "r"(SH::COLS) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = slot;
+  // the tokens of a lane (a column of B): half of them for each four warps; of 16, warps 4 to 7 read none
+  const int quad = warp & 3, t0 = BT < 32 ? 0 : (warp >> 2) * SH::OWN;
+  const bool reads = warp < (BT >= 32 ? 8 : 4);
+  int sum[SH::OWN];
+  if (LONG) {
+#pragma unroll
+    for (int i = 0; i < SH::OWN; ++i) sum[i] = 0;
+  }
+  bool ok = true;
+  if (warp == 8) {
+    if (lane == 0) {
+      int st = 0;
+      for (; st < count && ok; ++st) {
+        if (LONG && (st & 7) == 0 && st > 0) ok = bar_wait_all(taken, ((st >> 3) - 1) & 1, given_up);   // 1024 products a sum
+        ok = ok && bar_wait_all(full + 8 * (st & 1), (st >> 1) & 1, given_up);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t buf = base + (st & 1) * SH::STAGE;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const uint32_t atom = buf + (k >> 2) * SH::ATOM;
+          tc_mma(tmem, tc_desc(atom) + 2 * (k & 3), tc_desc(atom + 128 * 128) + 2 * (k & 3), tc_idesc(128, BT),
+                 k > 0 || (LONG ? (st & 7) != 0 : st > 0));
+        }
+        tc_commit(empty + 8 * (st & 1));
+      }
+      if (!ok)                                              // the MMAs issued end before their memory is given back
+        for (int i = st > 2 ? st - 2 : 0; i < st; ++i) (void)bar_wait(empty + 8 * (i & 1), (i >> 1) & 1);
+    }
+    __syncwarp();
+  } else {
+    auto take = [&](int st) {                               // stage st and all before it are multiplied: their sums
+      ok = __all_sync(0xFFFFFFFFu, bar_wait_all(empty + 8 * (st & 1), (st >> 1) & 1, given_up));
+      if (!ok) return;
+      tc_fence_after();
+      if (reads) {
+#pragma unroll
+        for (int c = 0; c < SH::OWN; c += STEP) {
+          float r[STEP];
+          tc_read<STEP>(tmem + ((uint32_t)(quad * 32) << 16) + t0 + c, r);
+#pragma unroll
+          for (int i = 0; i < STEP; ++i) sum[c + i] = (LONG ? sum[c + i] : 0) + __float2int_rn(r[i]);
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (LONG && lane == 0) bar_arrive(taken);
+    };
+    for (int s0 = 0; s0 < count && ok; s0 += AHEAD) {
+#pragma unroll
+      for (int u = 0; u < AHEAD; ++u) {
+        const int st = s0 + u;
+        if (st >= count || !ok) break;
+        if (st >= 2) {                                      // its buffer has been read
+          ok = __all_sync(0xFFFFFFFFu, bar_wait_all(empty + 8 * (st & 1), ((st >> 1) - 1) & 1, given_up));
+          if (!ok) break;
+        }
+        unsigned char* const buf = smem + (st & 1) * SH::STAGE + (c8 >> 2) * SH::ATOM;
+#pragma unroll
+        for (int i = 0; i < PP; ++i) {
+          const int row = r8 + 32 * i;
+          if (PP * 32 != SH::ROWS && row >= SH::ROWS) break;
+          uint32_t h[8];
+          codes_to_f16(w[u][i].x, h[0], h[1]);
+          codes_to_f16(w[u][i].y, h[2], h[3]);
+          codes_to_f16(w[u][i].z, h[4], h[5]);
+          codes_to_f16(w[u][i].w, h[6], h[7]);
+          const uint4 lo = make_uint4(h[0], h[1], h[2], h[3]), hi = make_uint4(h[4], h[5], h[6], h[7]);
+          // the two atoms' chunks share banks: their threads store odd and even chunks in turn
+          const int odd = c8 >> 2, chunk = (c8 & 3) * 2;
+          *reinterpret_cast<uint4*>(buf + row * 128 + (((chunk + odd) ^ (row & 7)) << 4)) = odd ? hi : lo;
+          *reinterpret_cast<uint4*>(buf + row * 128 + (((chunk + 1 - odd) ^ (row & 7)) << 4)) = odd ? lo : hi;
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) bar_arrive(full + 8 * (st & 1));
+        load(st + AHEAD, w[u]);
+        if (LONG && (st & 7) == 7 && st + 1 < count) take(st);
+      }
+    }
+    if (ok && count > 0) take(count - 1);
+  }
+  __syncthreads();
+  if (tid == 0 && *given_up) atomicExch(&g_ops_status, 1);
+  tc_fence_after();
+  if (warp == 8) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(SH::COLS) : "memory");
+
+  const int nl = quad * 32 + lane;
+  if (S == 1) {
+    const int64_t n = n0 + nl;
+    if (reads && n < p.N) {
+      const float sb = scale_b(p, n);
+#pragma unroll
+      for (int i = 0; i < SH::OWN; ++i) {
+        const int64_t m = m0 + t0 + i;
+        if (m < p.M) store_out(p, m, n, sum[i], scale_a(p, m), sb);
+      }
+    }
+    return;
+  }
+  int* const own = reinterpret_cast<int*>(smem);            // [BT][128]
+  if (reads) {
+#pragma unroll
+    for (int i = 0; i < SH::OWN; ++i) own[(t0 + i) * 128 + nl] = sum[i];
+  }
+  // this thread's four columns are the same in each of its rows
+  const bool together = stores_together<4>(p);
+  const int64_t n = n0 + (tid * 4) % 128;
+  float sb[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) sb[j] = n + j < p.N ? scale_b(p, n + j) : 0.0f;
+  cluster_sync();
+  // four sums at a time, all slices' in flight at once
+  for (int i = ((int)slice * 256 + tid) * 4; tid < 256 && i < BT * 128; i += S * 1024) {
+    const int64_t m = m0 + i / 128;
+    const float sa = m < p.M ? scale_a(p, m) : 0.0f;
+    int4 x[kMaxSlices];
+#pragma unroll
+    for (int r = 0; r < kMaxSlices; ++r)
+      if (r < S)
+        asm volatile("ld.shared::cluster.v4.s32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(x[r].x), "=r"(x[r].y), "=r"(x[r].z), "=r"(x[r].w) : "r"(in_cluster(own + i, r)) : "memory");
+    int v[4] = {x[0].x, x[0].y, x[0].z, x[0].w};
+#pragma unroll
+    for (int r = 1; r < kMaxSlices; ++r)
+      if (r < S) {
+        v[0] += x[r].x;
+        v[1] += x[r].y;
+        v[2] += x[r].z;
+        v[3] += x[r].w;
+      }
+    store_row<4>(p, m, n, v, sa, sb, together);
+  }
+  cluster_sync();
+}
+
+// ---------------------------------------------------------------------------------------
 // Codes to fp16 rows of Kp values, zeros after the K-th: rows_a rows of A, then rows_b of B.  A
 // thread takes 16 codes.
 __global__ void __launch_bounds__(256)
