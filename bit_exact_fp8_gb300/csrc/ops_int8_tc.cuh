@@ -80,8 +80,8 @@ __device__ __forceinline__ void tc_read32(uint32_t addr, float (&r)[32]) {
 // warps load codes straight into registers, some stages of 128 of K ahead, convert them and store
 // them as K-major fp16 rows under the 128-byte swizzle in one of two buffers; a ninth issues the
 // eight MMAs of a stage (issuing them takes as long as they run, about 740 cycles at 64 tokens, so
-// a converting warp would hold the others up).  The S slices are the CTAs of a cluster: each
-// leaves its integer sums in shared memory and adds up its share of the tile over all of them.
+// a converting warp would hold the others up).  The S slices are the CTAs of a cluster and
+// share out the tile's tokens: each sends the others its integer sums of theirs.
 // (The same on mma.sync, each warp converting its own fragments, took 13.4 us for
 // 64 x 5760 x 1920: six times the instructions, as fragments are converted again by each warp.)
 constexpr int kMaxSlices = 8, kFixedStages = 4;
@@ -252,6 +252,7 @@ int8_few_kernel(const Int8Params p, int S) {
     if (ok && count > 0) take(count - 1);
   }
   __syncthreads();
+  if (S > 1) cluster_arrive();
   if (tid == 0 && *given_up) atomicExch(&g_ops_status, 1);
   tc_fence_after();
   if (warp == 8) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(SH::COLS) : "memory");
@@ -269,40 +270,45 @@ int8_few_kernel(const Int8Params p, int S) {
     }
     return;
   }
-  int* const own = reinterpret_cast<int*>(smem);            // [BT][128]
-  if (reads) {
-#pragma unroll
-    for (int i = 0; i < SH::OWN; ++i) own[(t0 + i) * 128 + nl] = sum[i];
-  }
-  // this thread's four columns are the same in each of its rows
+  // slice s adds up the tokens s, s + S, ...: every slice writes its sums of them there, once that CTA is
+  // past its last MMA, and each then finds all it needs in its own shared memory, [S][slots][128]
+  int* const sums = reinterpret_cast<int*>(smem);
+  const int slots = (BT + S - 1) / S;
   const bool together = stores_together<4>(p);
-  const int64_t n = n0 + (tid * 4) % 128;
+  const int64_t n = n0 + (tid * 4) % 128;                   // a thread's four columns
   float sb[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j) sb[j] = n + j < p.N ? scale_b(p, n + j) : 0.0f;
+  cluster_wait();
+  if (reads) {
+    int owner = t0 % S, slot_of = t0 / S;
+#pragma unroll
+    for (int i = 0; i < SH::OWN; ++i) {
+      asm volatile("st.shared::cluster.s32 [%0], %1;"
+                   ::"r"(in_cluster(sums + ((int)slice * slots + slot_of) * 128 + nl, owner)), "r"(sum[i]) : "memory");
+      if (++owner == S) {
+        owner = 0;
+        ++slot_of;
+      }
+    }
+  }
   cluster_sync();
-  // four sums at a time, all slices' in flight at once
-  for (int i = ((int)slice * 256 + tid) * 4; tid < 256 && i < BT * 128; i += S * 1024) {
-    const int64_t m = m0 + i / 128;
-    const float sa = m < p.M ? scale_a(p, m) : 0.0f;
-    int4 x[kMaxSlices];
+  for (int q = tid / 32; tid < 256 && q * S + (int)slice < BT; q += 8) {
+    const int64_t m = m0 + q * S + slice;
+    if (m >= p.M) break;
+    const float sa = scale_a(p, m);
+    int v[4] = {0, 0, 0, 0};
 #pragma unroll
     for (int r = 0; r < kMaxSlices; ++r)
-      if (r < S)
-        asm volatile("ld.shared::cluster.v4.s32 {%0, %1, %2, %3}, [%4];"
-                     : "=r"(x[r].x), "=r"(x[r].y), "=r"(x[r].z), "=r"(x[r].w) : "r"(in_cluster(own + i, r)) : "memory");
-    int v[4] = {x[0].x, x[0].y, x[0].z, x[0].w};
-#pragma unroll
-    for (int r = 1; r < kMaxSlices; ++r)
       if (r < S) {
-        v[0] += x[r].x;
-        v[1] += x[r].y;
-        v[2] += x[r].z;
-        v[3] += x[r].w;
+        const int4 x = *reinterpret_cast<const int4*>(sums + (r * slots + q) * 128 + lane * 4);
+        v[0] += x.x;
+        v[1] += x.y;
+        v[2] += x.z;
+        v[3] += x.w;
       }
     store_row<4>(p, m, n, v, sa, sb, together);
   }
-  cluster_sync();
 }
 
 // ---------------------------------------------------------------------------------------
