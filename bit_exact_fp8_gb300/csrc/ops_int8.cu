@@ -196,7 +196,11 @@ constexpr size_t kSlabBytes = (size_t)128 << 20;   // fp16 rows at a time, so th
 
 Plan plan_for(int64_t M, int64_t N, int64_t K, bool aligned16) {
   Plan pl = {};
-  pl.kind = M <= 4 || K == 0 ? Int8Kind::dot : M >= 256 && N >= 128 && K >= 128 ? Int8Kind::tensor : Int8Kind::few;
+  // Laying the operands out and filling 128 x 256 tiles pays for many tokens and from about ten stages of
+  // 128 x 128 x 128 an SM on (200 x 5760 x 1920, 8.9 of them: 20.8 us as few, 22.9 as many;
+  // 400 x 5760 x 1920, 17.8: 35.9 and 24.5); few tokens never repay the laying out of B.
+  const int64_t stages = ((M + 127) / 128) * ((N + 127) / 128) * ((K + 127) / 128);
+  pl.kind = M <= 4 || K == 0 ? Int8Kind::dot : M > 128 && stages > 10 * 152 ? Int8Kind::tensor : Int8Kind::few;
   if (pl.kind == Int8Kind::tensor) {
     pl.Kp = round_up(K, kTcBK);
     const int64_t most = (int64_t)(kSlabBytes / (2 * (size_t)pl.Kp)) / kTcBN * kTcBN;   // K < 2^17: 512 rows at least
@@ -244,7 +248,19 @@ int launch_tc(const Int8Params& p, const Plan& pl, bool vec, unsigned char* ws, 
       q.out = static_cast<unsigned char*>(p.out) + (size_t)(m * p.N + n) * es;
       const TcTiles tl = {(int)((rows_a + kTcBM - 1) / kTcBM), (int)((rows_b + kTcBN - 1) / kTcBN), (int)(pl.Kp / kTcBK)};
       const int tiles = tl.tiles_m * tl.tiles_n;
-      int8_tc_kernel<<<(unsigned)(tiles < sms ? tiles : sms), kTcThreads, kTcSmem, st>>>(q, tl, map_a, map_b);
+      // launched while the operands are still laid out, if they are: it waits for them itself
+      cudaLaunchConfig_t cfg = {};
+      cfg.gridDim = dim3((unsigned)(tiles < sms ? tiles : sms));
+      cfg.blockDim = dim3(kTcThreads);
+      cfg.dynamicSmemBytes = kTcSmem;
+      cfg.stream = st;
+      cudaLaunchAttribute early;
+      early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+      early.val.programmaticStreamSerializationAllowed = 1;
+      cfg.attrs = &early;
+      cfg.numAttrs = work > 0 ? 1 : 0;
+      if (cudaLaunchKernelEx(&cfg, int8_tc_kernel, q, tl, map_a, map_b) != cudaSuccess)
+        return emu_ops_launched("emu_int8_scaled_mm");
     }
   }
   return EMU_OK;

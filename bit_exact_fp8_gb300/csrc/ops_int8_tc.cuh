@@ -318,6 +318,7 @@ __global__ void __launch_bounds__(256)
 int8_to_f16_kernel(const int8_t* a, int64_t lda, uint32_t rows_a, uint16_t* a16, const int8_t* b, int64_t ldb,
                    uint32_t rows_b, uint16_t* b16, int K, uint32_t chunks, bool vec) {
   const uint32_t total = (rows_a + rows_b) * chunks;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the product waits for this kernel's end
   for (uint32_t i = blockIdx.x * 256u + threadIdx.x; i < total; i += gridDim.x * 256u) {
     const uint32_t row = i / chunks, c = i - row * chunks;
     const bool is_a = row < rows_a;
@@ -387,6 +388,7 @@ int8_tc_kernel(const Int8Params p, const TcTiles tl, const __grid_constant__ CUt
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
     if (warp == 0 && lane == 0) {
+      asm volatile("griddepcontrol.wait;" ::: "memory");       // the operands are laid out
       uint32_t it = 0;
       bool ok = true;
       for (int tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
