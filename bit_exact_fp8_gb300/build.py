@@ -69,7 +69,7 @@ def ops_commands(out: str) -> "tuple[list, list]":
     compile_ = ["g++", "-O2", "-std=c++17", "-fPIC", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"]
     compile_ += [f"-I{d}" for d in includes] + ["-c"] + OPS_SOURCES + ["-o", obj]
     link = ["g++", "-shared", obj, "-o", out, f"-L{PKG}", "-l:" + os.path.basename(LIB), "-Wl,-rpath,$ORIGIN"]
-    link += [f"-L{d}" for d in library_paths()] + ["-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10"]
+    link += [f"-L{d}" for d in library_paths()] + ["-ltorch_python", "-ltorch_cuda", "-ltorch_cpu", "-lc10_cuda", "-lc10"]
     return compile_, link
 
 

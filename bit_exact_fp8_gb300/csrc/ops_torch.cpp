@@ -5,6 +5,7 @@
 #include "emu_fp8.h"
 
 #include <ATen/ATen.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/core/GradMode.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
@@ -83,8 +84,9 @@ void* vector_of(const at::Tensor& t, const char* name, int64_t count, c10::Scala
         ", got " + text(t));
   return t.data_ptr();
 }
+// from the caching allocator on the current stream, as torch.empty, without its dispatch
 at::Tensor make(at::IntArrayRef sizes, c10::ScalarType type, c10::Device dev) {
-  return at::empty(sizes, at::TensorOptions().dtype(type).device(dev));
+  return at::Tensor(at::detail::empty_cuda(sizes, type, dev, std::nullopt));
 }
 at::Tensor given(PyObject* o, const char* name, int64_t rows, int64_t cols, c10::ScalarType type, c10::Device dev) {
   const at::Tensor& t = tensor(o, name);
