@@ -233,13 +233,24 @@ template <class T> struct Streamed {
   }
 };
 
-// the vectors v0, v0 + step, ... below v1
-template <class T>
+// the vectors v0, v0 + step, ... below v1, LOADS of them asked for at a time
+template <int LOADS, class T>
 __device__ __forceinline__ Streamed<T> stream(const Row<T>& row, int v0, int v1, int step) {
   constexpr int U = 4;
   Streamed<T> s;
   s.at = v0;
   int v = v0;
+  if (LOADS == 2 * U) {
+    for (; v + (2 * U - 1) * step < v1; v += step * 2 * U) {
+      uint4 a[U], b[U];
+#pragma unroll
+      for (int i = 0; i < U; ++i) a[i] = row.load_raw(v + i * step);
+#pragma unroll
+      for (int i = 0; i < U; ++i) b[i] = row.load_raw(v + (U + i) * step);
+      s.take(a, v, step);
+      s.take(b, v + U * step, step);
+    }
+  }
   for (; v + (U - 1) * step < v1; v += step * U) {
     uint4 raw[U];
 #pragma unroll
@@ -253,17 +264,18 @@ __device__ __forceinline__ Streamed<T> stream(const Row<T>& row, int v0, int v1,
   return s;
 }
 
+// the given token's logit, asked for before the row's pass; NaN outside [0, V)
+template <class T> __device__ __forceinline__ float token_logit(const LogprobParams& p, int64_t row, bool& ignored) {
+  const int64_t tok = p.tokens[row];
+  ignored = tok == p.ignore;
+  return tok < 0 || tok >= p.V ? NAN : to_f((static_cast<const T*>(p.x) + row * p.ldx)[tok]);
+}
 // the row's outputs but its alternatives; x - m is exact where it matters, so logprob is (x - m) - log z
-template <class T>
-__device__ __forceinline__ void finish_row(const LogprobParams& p, int64_t row, const Soft& s) {
-  const T* x = static_cast<const T*>(p.x) + row * p.ldx;
+__device__ __forceinline__ void finish_row(const LogprobParams& p, int64_t row, const Soft& s, float logit, bool ignored) {
   const bool empty = s.z == 0.0f;
   const float logz = logf(s.z);
   const float entropy = empty ? 0.0f : logz - s.u / s.z;
-  const int64_t tok = p.tokens[row];
-  p.logprob[row] = tok == p.ignore ? 0.0f
-                   : tok < 0 || tok >= p.V ? NAN
-                   : empty ? -INFINITY : to_f(x[tok]) - s.m - logz;
+  p.logprob[row] = ignored ? 0.0f : empty && logit == logit ? -INFINITY : logit - s.m - logz;
   p.entropy[row] = entropy;
   p.lse[row] = empty ? -INFINITY : s.m + logz;
   float* st = p.stats + row * 3;
@@ -323,9 +335,11 @@ logprob_warp_kernel(const LogprobParams p) {
   const int64_t r = (int64_t)blockIdx.x * kWarpRows + w;
   if (r >= p.T) return;
   const Row<T> row(static_cast<const T*>(p.x) + r * p.ldx, p.V);
-  const Streamed<T> mine = stream(row, lane, row.nvec, 32);
+  bool ignored = false;
+  const float logit = lane == 0 ? token_logit<T>(p, r, ignored) : 0.0f;
+  const Streamed<T> mine = stream<4>(row, lane, row.nvec, 32);
   const Soft s = soft_warp(mine.sums());
-  if (lane == 0) finish_row<T>(p, r, s);
+  if (lane == 0) finish_row(p, r, s, logit, ignored);
   if (p.k == 0) return;
   unsigned long long* list = list_all[w];
   int& count = count_all[w];
@@ -388,9 +402,10 @@ logprob_warp_kernel(const LogprobParams p) {
 // largest of each through distributed shared memory.
 constexpr int kGroups = 128, kList = 1024, kMaxCluster = 8;
 template <class T, int NT>
-__global__ void __launch_bounds__(NT, 1280 / NT)
+__global__ void __launch_bounds__(NT, NT == 512 ? 1 : 5)
 logprob_row_kernel(const LogprobParams p, int C) {
   constexpr int NW = NT / 32, GT = NT / kGroups;      // GT threads a group
+  constexpr bool FEW = NT == 512;                      // the form for few rows
   __shared__ Soft warp_soft[NW];
   __shared__ __align__(16) unsigned long long heads[kGroups];
   __shared__ int cand[kMaxTop];
@@ -405,7 +420,10 @@ logprob_row_kernel(const LogprobParams p, int C) {
   const int part = blockIdx.x % C;
   const Row<T> row(static_cast<const T*>(p.x) + r * p.ldx, p.V);
   const int v0 = (int)((int64_t)row.nvec * part / C), v1 = (int)((int64_t)row.nvec * (part + 1) / C);
-  const Streamed<T> mine = stream(row, v0 + tid, v1, NT);
+  // the last thread writes the row's own outputs, while the others rank its alternatives
+  bool ignored = false;
+  const float logit = tid == NT - 1 && part == 0 ? token_logit<T>(p, r, ignored) : 0.0f;
+  const Streamed<T> mine = stream<FEW ? 8 : 4>(row, v0 + tid, v1, NT);
   const Soft ws = soft_warp(mine.sums());
   if (lane == 0) warp_soft[w] = ws;
   if (p.k > 0) {
@@ -428,32 +446,53 @@ logprob_row_kernel(const LogprobParams p, int C) {
   for (int i = 1; i < NW; ++i) s = soft_join(s, warp_soft[i]);
 
   if (p.k > 0) {
-    if (tid < kGroups) {
-      const unsigned long long head = heads[tid];
+    {                                                  // GT threads a head, each with its share of the others
+      const unsigned long long head = heads[tid / GT];
       int above = 0;
 #pragma unroll 16
-      for (int i = 0; i < kGroups; i += 2) {
+      for (int i = 2 * (tid % GT); i < kGroups; i += 2 * GT) {
         const ulonglong2 h = *reinterpret_cast<const ulonglong2*>(heads + i);
         above += (h.x > head) + (h.y > head);
       }
-      if (head != 0ull && above < p.k) {
-        cand[above] = tid;
+#pragma unroll
+      for (int o = 1; o < GT; o <<= 1) above += __shfl_xor_sync(0xFFFFFFFFu, above, o);
+      if (tid % GT == 0 && head != 0ull && above < p.k) {
+        cand[above] = tid / GT;
         atomicAdd(&taken, 1);
         if (above == p.k - 1) bound = head;
       }
     }
     __syncthreads();
     const float least = least_of(bound);
-    for (int c = w; c < taken; c += NW) {              // a warp a group taken, four vectors a lane at a time
-      constexpr int ROUND = 32 / GT * NT;
-      for (int v = v0 + lane / GT * NT + cand[c] * GT + lane % GT; v < v1; v += 4 * ROUND) {
+    // 32 vectors of a group taken at a time for each warp, four loads in flight: of one group, or (few rows,
+    // whose parts have few vectors a group) of several
+    constexpr int ROUND = 32 / GT * NT;
+    if (FEW) {
+      const int rounds = (v1 - v0 + ROUND - 1) / ROUND, all = taken * rounds;
+      for (int q0 = w; q0 < all; q0 += 4 * NW) {
         uint4 raw[4];
+        int v[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int q = q0 + u * NW, c = q / rounds;
+          v[u] = q < all ? v0 + (q - c * rounds) * ROUND + lane / GT * NT + cand[c] * GT + lane % GT : v1;
+          if (v[u] < v1) raw[u] = row.load_raw(v[u]);
+        }
 #pragma unroll
         for (int u = 0; u < 4; ++u)
-          if (v + u * ROUND < v1) raw[u] = row.load_raw(v + u * ROUND);
+          if (v[u] < v1) collect_vector(row, v[u], raw[u], least, bound, list, kList, &count);
+      }
+    } else {
+      for (int c = w; c < taken; c += NW) {
+        for (int v = v0 + lane / GT * NT + cand[c] * GT + lane % GT; v < v1; v += 4 * ROUND) {
+          uint4 raw[4];
 #pragma unroll
-        for (int u = 0; u < 4; ++u)
-          if (v + u * ROUND < v1) collect_vector(row, v + u * ROUND, raw[u], least, bound, list, kList, &count);
+          for (int u = 0; u < 4; ++u)
+            if (v + u * ROUND < v1) raw[u] = row.load_raw(v + u * ROUND);
+#pragma unroll
+          for (int u = 0; u < 4; ++u)
+            if (v + u * ROUND < v1) collect_vector(row, v + u * ROUND, raw[u], least, bound, list, kList, &count);
+        }
       }
     }
     __syncthreads();
@@ -511,7 +550,7 @@ logprob_row_kernel(const LogprobParams p, int C) {
     if (part > 0) return;
     for (int i = 1; i < C; ++i) s = soft_join(s, parts[i]);
   }
-  if (tid == 0) finish_row<T>(p, r, s);
+  if (tid == NT - 1) finish_row(p, r, s, logit, ignored);
   for (int i = tid; i < C * kMaxTop; i += NT) {
     const int q = i / kMaxTop, j = i % kMaxTop;
     const unsigned long long c = j < p.k ? tops[q][j] : 0ull;
@@ -552,8 +591,8 @@ template <class T> int pick_logprob(const LogprobParams& p, cudaStream_t st) {
     return EMU_OK;
   }
   int C = 1;                                            // until two CTAs an SM, four vectors a thread
-  while (C < kMaxCluster && p.T * C < 2 * emu_ops_sm_count() && nvec >= 2 * C * 256 * 4) C *= 2;
-  return launch_row<T, 256>(p, C, st);
+  while (C < kMaxCluster && p.T * C < 2 * emu_ops_sm_count() && nvec >= 2 * C * 512 * 4) C *= 2;
+  return C > 1 ? launch_row<T, 512>(p, C, st) : launch_row<T, 256>(p, 1, st);
 }
 
 struct LogprobGradParams {
