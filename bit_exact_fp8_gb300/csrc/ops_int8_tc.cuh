@@ -15,14 +15,23 @@ namespace emu_ops {
 constexpr int kTcBM = 128, kTcBN = 256, kTcBK = 64, kTcNS = 4;
 constexpr int kTcChunk = 1024 / kTcBK;                       // K blocks that one accumulator takes
 constexpr int kTcStage = (kTcBM + kTcBN) * kTcBK * 2;        // 48 KB
-constexpr int kTcStageRow = 33;                              // floats of a staged output row
-constexpr int kTcOut = kTcNS * kTcStage;                     // eight warps' staging, 32 x 33 floats each
-constexpr int kTcBars = kTcOut + 8 * 32 * kTcStageRow * 4;
+constexpr int kTcStageRow = 128;                             // bytes of a staged output row
+constexpr int kTcOut = kTcNS * kTcStage;                     // eight warps' staging, 32 rows each
+constexpr int kTcBars = kTcOut + 8 * 32 * kTcStageRow;
 constexpr int kTcSmem = kTcBars + 128 + 1024;                // and what aligning to 1024 may take
+static_assert(kTcSmem <= 227 * 1024, "one CTA an SM");
 constexpr int kTcThreads = 384;
 
 struct TcTiles {
   int tiles_m, tiles_n, k_blocks;
+  // eight rows of tiles at a time, column by column, so that the CTAs at work share both operands' rows
+  // (4096^3: 107 us with all rows at a time, 103 with eight)
+  __device__ __forceinline__ void at(int tile, int& m, int& n) const {
+    const int group = tile / (8 * tiles_n), first = group * 8, rows = tiles_m - first < 8 ? tiles_m - first : 8;
+    const int in = tile - group * 8 * tiles_n;
+    m = first + in % rows;
+    n = in / rows;
+  }
 };
 
 // ---- barriers, TMA and tcgen05 (inline PTX)
@@ -345,10 +354,56 @@ int8_to_f16_kernel(const int8_t* a, int64_t lda, uint32_t rows_a, uint16_t* a16,
   }
 }
 
+// A warp's 32 rows x 128 columns of sums, a row a lane, scaled and written out: 128 bytes of each row at a time go through shared memory (16 bytes a lane, a row's chunks
+// permuted by its number: no two lanes of a phase meet in a bank), so that whole lines are stored.
+// sb: scale_b of columns lane, lane + 32, ...
+template <class T>
+__device__ __forceinline__ void write_tile(const Int8Params& p, const int (&sum)[128], const float (&sb)[4], float sa,
+                                           unsigned char* stage, int64_t m0, int64_t n0, int lane) {
+  constexpr int COLS = 128 / sizeof(T), VEC = 16 / sizeof(T);
+  const int rows = p.M - m0 < 32 ? (int)(p.M - m0) : 32;
+  T* const out = static_cast<T*>(p.out);
+  const bool vec = p.N % VEC == 0 && p.cols % VEC == 0 && (reinterpret_cast<uintptr_t>(out) & 15u) == 0;
+#pragma unroll
+  for (int c = 0; c < 128; c += COLS) {
+    const int64_t nc = n0 + c;
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < COLS; i += VEC) {
+      float v[VEC];
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) {
+        const int n = c + i + j;
+        v[j] = ((float)sum[n] * sa) * __shfl_sync(0xFFFFFFFFu, sb[n / 32], n % 32);
+      }
+      store_f<T, VEC>(reinterpret_cast<T*>(stage + lane * kTcStageRow + (((i / VEC) ^ (lane & 7)) * 16)), v);
+    }
+    __syncwarp();
+    if (vec) {
+      const int64_t n = nc + (lane & 7) * VEC;
+      if (n < p.cols) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const int r = k * 4 + (lane >> 3);
+          if (r < rows)
+            *reinterpret_cast<uint4*>(out + (m0 + r) * p.N + n) =
+                *reinterpret_cast<const uint4*>(stage + r * kTcStageRow + (((lane & 7) ^ (r & 7)) * 16));
+        }
+      }
+    } else {
+      for (int r = 0; r < rows; ++r)
+#pragma unroll
+        for (int i = 0; i < COLS; i += 32)
+          if (nc + i + lane < p.cols)
+            out[(m0 + r) * p.N + nc + i + lane] =
+                reinterpret_cast<const T*>(stage + r * kTcStageRow + ((((i + lane) / VEC) ^ (r & 7)) * 16))[lane % VEC];
+    }
+  }
+}
+
 // Persistent: one CTA an SM, tiles of 128 x 256 outputs in turn.  Warp 0 loads the stages by TMA,
 // warp 1 issues the MMAs, warp 2 owns the tensor memory, warps 4 to 11 read the accumulators
-// back: each holds 32 rows x 128 columns of sums in registers, scales them and writes rows of 32
-// columns through shared memory.  All waits are bounded; a role that gives up sets the status
+// back: each holds 32 rows x 128 columns of sums in registers.  All waits are bounded; a role that gives up sets the status
 // and takes the others along.
 __global__ void __launch_bounds__(kTcThreads, 1)
 int8_tc_kernel(const Int8Params p, const TcTiles tl, const __grid_constant__ CUtensorMap map_a,
@@ -392,7 +447,9 @@ int8_tc_kernel(const Int8Params p, const TcTiles tl, const __grid_constant__ CUt
       uint32_t it = 0;
       bool ok = true;
       for (int tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
-        const int m0 = tile % tl.tiles_m * kTcBM, n0 = tile / tl.tiles_m * kTcBN;
+        int tm, tn;
+        tl.at(tile, tm, tn);
+        const int m0 = tm * kTcBM, n0 = tn * kTcBN;
         for (int kb = 0; kb < tl.k_blocks; ++kb, ++it) {
           const uint32_t s = it % kTcNS, bar = full + 8 * s, dst = base + s * kTcStage;
           if (it >= kTcNS && !bar_wait_all(empty + 8 * s, (it / kTcNS - 1) & 1, given_up)) {
@@ -441,13 +498,18 @@ int8_tc_kernel(const Int8Params p, const TcTiles tl, const __grid_constant__ CUt
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
     const int quad = warp & 3, half = (warp - 4) >> 2;
-    float* const stage = reinterpret_cast<float*>(smem + kTcOut) + (warp - 4) * 32 * kTcStageRow;
-    const bool pairs = p.out_type != EMU_OUT_F32 && p.N % 2 == 0 && p.cols % 2 == 0 && ((uintptr_t)p.out & 3u) == 0;
+    unsigned char* const stage = smem + kTcOut + (warp - 4) * 32 * kTcStageRow;
     uint32_t unit = 0;
     bool ok = true;
     for (int tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
-      const int64_t m0 = (int64_t)(tile % tl.tiles_m) * kTcBM + quad * 32;
-      const int64_t n0 = (int64_t)(tile / tl.tiles_m) * kTcBN + half * 128;
+      int tm, tn;
+      tl.at(tile, tm, tn);
+      const int64_t m0 = (int64_t)tm * kTcBM + quad * 32;
+      const int64_t n0 = (int64_t)tn * kTcBN + half * 128;
+      const float sa = m0 + lane < p.M ? scale_a(p, m0 + lane) : 0.0f;
+      float sb[4];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) sb[c] = n0 + c * 32 + lane < p.cols ? scale_b(p, n0 + c * 32 + lane) : 0.0f;
       int sum[128];
       for (int k0 = 0; k0 < tl.k_blocks; k0 += kTcChunk, ++unit) {
         const uint32_t buf = unit & 1;
@@ -471,43 +533,9 @@ int8_tc_kernel(const Int8Params p, const TcTiles tl, const __grid_constant__ CUt
         if (lane == 0) bar_arrive(tempty + 8 * buf);
       }
       if (!ok) break;
-      const float sa = m0 + lane < p.M ? p.scale_a[(m0 + lane) * p.sa_step] : 0.0f;
-      const int rows = p.M - m0 < 32 ? (int)(p.M - m0) : 32;
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const int64_t nc = n0 + c * 32;
-        __syncwarp();
-#pragma unroll
-        for (int i = 0; i < 32; ++i) stage[lane * kTcStageRow + i] = (float)sum[c * 32 + i] * sa;
-        __syncwarp();
-        if (pairs) {
-          const int64_t n = nc + (lane & 15) * 2;
-          if (n < p.cols) {
-            const float s0 = p.scale_b[n * p.sb_step], s1 = p.scale_b[(n + 1) * p.sb_step];
-            for (int r = lane >> 4; r < rows; r += 2) {
-              const float* v = stage + r * kTcStageRow + (lane & 15) * 2;
-              const int64_t at = (m0 + r) * p.N + n;
-              if (p.out_type == EMU_OUT_BF16)
-                *reinterpret_cast<__nv_bfloat162*>(static_cast<__nv_bfloat16*>(p.out) + at) =
-                    __floats2bfloat162_rn(v[0] * s0, v[1] * s1);
-              else
-                *reinterpret_cast<__half2*>(static_cast<__half*>(p.out) + at) = __floats2half2_rn(v[0] * s0, v[1] * s1);
-            }
-          }
-        } else {
-          const int64_t n = nc + lane;
-          if (n < p.cols) {
-            const float sb = p.scale_b[n * p.sb_step];
-            for (int r = 0; r < rows; ++r) {
-              const float v = stage[r * kTcStageRow + lane] * sb;
-              const int64_t at = (m0 + r) * p.N + n;
-              if (p.out_type == EMU_OUT_F32) static_cast<float*>(p.out)[at] = v;
-              else if (p.out_type == EMU_OUT_BF16) static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(v);
-              else static_cast<__half*>(p.out)[at] = __float2half_rn(v);
-            }
-          }
-        }
-      }
+      if (p.out_type == EMU_OUT_F32) write_tile<float>(p, sum, sb, sa, stage, m0, n0, lane);
+      else if (p.out_type == EMU_OUT_BF16) write_tile<__nv_bfloat16>(p, sum, sb, sa, stage, m0, n0, lane);
+      else write_tile<__half>(p, sum, sb, sa, stage, m0, n0, lane);
     }
   }
   __syncwarp();
