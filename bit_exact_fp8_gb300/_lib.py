@@ -110,7 +110,7 @@ def load(path: str = LIB) -> ctypes.CDLL:
     L.emu_rms_norm_backward_workspace_bytes.restype = Z
     L.emu_rms_norm_backward.argtypes = [P, I64, P, I64, P, P, I, P, I64, I, I64, I64, P, P, P, Z, P]
     L.emu_rms_norm_backward.restype = I
-    L.emu_int8_workspace_bytes.argtypes = [I64, I64, I64, ctypes.c_int32]
+    L.emu_int8_workspace_bytes.argtypes = [I64, I64, I64]
     L.emu_int8_workspace_bytes.restype = Z
     L.emu_int8_scaled_mm.argtypes = [P, I64, P, I64, I64, I64, I64, P, I64, P, I64, P, I, P, Z, P]
     L.emu_int8_scaled_mm.restype = I

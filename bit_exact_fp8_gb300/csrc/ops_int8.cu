@@ -10,6 +10,7 @@
 
 #include <atomic>
 #include <mutex>
+#include <type_traits>
 
 namespace emu_ops {
 
@@ -21,6 +22,7 @@ constexpr int64_t kInt8MaxK = 131071;             // K * 128 * 128 < 2^31
 struct Int8Params {
   const int8_t* a; int64_t lda;                   // [M, K]
   const int8_t* b; int64_t ldb;                   // [N, K]
+  uintptr_t a_end, b_end;                         // where their memory ends
   int64_t M, N;                                   // N: also the output's row stride
   int64_t cols;                                   // columns of B here (a slab of the N)
   int K;
@@ -64,6 +66,68 @@ template <int N> __device__ __forceinline__ bool stores_together(const Int8Param
   return p.N % N == 0 && (reinterpret_cast<uintptr_t>(p.out) & (N * es - 1)) == 0;
 }
 
+// 16 bytes of the 32 in a and b, from the at-th on (0 to 16)
+__device__ __forceinline__ uint4 bytes_from(const uint4& a, const uint4& b, int at) {
+  const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  uint32_t x[6], y[5];
+#pragma unroll
+  for (int i = 0; i < 6; ++i) x[i] = at & 8 ? w[i + 2] : w[i];
+#pragma unroll
+  for (int i = 0; i < 5; ++i) y[i] = at & 4 ? x[i + 1] : x[i];
+  const uint32_t shift = (uint32_t)(at & 3) * 8;
+  if (at == 16) return b;
+  return make_uint4(__funnelshift_r(y[0], y[1], shift), __funnelshift_r(y[1], y[2], shift),
+                    __funnelshift_r(y[2], y[3], shift), __funnelshift_r(y[3], y[4], shift));
+}
+
+// 16 codes of a row from the k-th on, zeros after the K-th, in two steps, so that a thread's loads are all
+// asked for before the first is waited for.  Rows that are 16-byte aligned (VEC): one load.  Else the two
+// 16-byte words that the codes touch, as far as these lie within the operand's memory (`from` to `end`),
+// shifted into place; at its very ends code by code.
+template <bool VEC> struct Codes;
+template <> struct Codes<true> {
+  uint4 w;
+  __device__ __forceinline__ void ask(const int8_t* row, int k, bool in, const int8_t*, uintptr_t) {
+    w = make_uint4(0u, 0u, 0u, 0u);
+    if (in) w = *reinterpret_cast<const uint4*>(row + k);
+  }
+  __device__ __forceinline__ uint4 get(const int8_t*, int, int, bool, const int8_t*, uintptr_t) const { return w; }
+};
+template <> struct Codes<false> {
+  uint4 a, b;
+  __device__ __forceinline__ void ask(const int8_t* row, int k, bool in, const int8_t* from, uintptr_t end) {
+    const uintptr_t word = reinterpret_cast<uintptr_t>(row + k) & ~(uintptr_t)15;
+    a = b = make_uint4(0u, 0u, 0u, 0u);
+    if (in && word >= reinterpret_cast<uintptr_t>(from) && word + 16 <= end) a = *reinterpret_cast<const uint4*>(word);
+    if (in && word + 32 <= end) b = *reinterpret_cast<const uint4*>(word + 16);
+  }
+  __device__ __forceinline__ uint4 get(const int8_t* row, int k, int K, bool in, const int8_t* from, uintptr_t end) const {
+    if (!in) return make_uint4(0u, 0u, 0u, 0u);
+    const uintptr_t at = reinterpret_cast<uintptr_t>(row + k), word = at & ~(uintptr_t)15;
+    const int n = K - k;
+    uint32_t r[4];
+    if (word >= reinterpret_cast<uintptr_t>(from) && word + 32 <= end) {
+      const uint4 q = bytes_from(a, b, (int)(at & 15));
+      r[0] = q.x; r[1] = q.y; r[2] = q.z; r[3] = q.w;
+    } else {
+      r[0] = r[1] = r[2] = r[3] = 0u;
+      for (int j = 0; j < 16 && j < n; ++j) {
+        const uint32_t c = (uint32_t)(uint8_t)row[k + j] << (8 * (j & 3));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) r[i] |= j >> 2 == i ? c : 0u;
+      }
+    }
+    if (n < 16) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int left = n - 4 * i;
+        if (left < 4) r[i] = left <= 0 ? 0u : r[i] & ((1u << (8 * left)) - 1u);
+      }
+    }
+    return make_uint4(r[0], r[1], r[2], r[3]);
+  }
+};
+
 __device__ __forceinline__ int dot16(const uint4& a, const uint4& b, int acc) {
   acc = __dp4a((int)a.x, (int)b.x, acc);
   acc = __dp4a((int)a.y, (int)b.y, acc);
@@ -71,41 +135,74 @@ __device__ __forceinline__ int dot16(const uint4& a, const uint4& b, int acc) {
   return __dp4a((int)a.w, (int)b.w, acc);
 }
 
-// One token, or a few: a warp takes MT rows by NT columns, its lanes 16 codes of K each in turn,
-// and adds the lanes' sums up.  Bound by reading B once.
-template <int MT, int NT>
+// One token, or a few: MT rows by NT columns for a warp, its lanes 16 codes of K each in turn, or for the
+// four warps of a CTA (SHARED), which share out K.  Bound by reading B once, and by how many of its bytes
+// are asked for at a time: 1 x 5760 x 1920 in 3.1 us shared, 3.6 by warps.
+template <int MT, int NT, bool VEC, bool SHARED>
 __global__ void __launch_bounds__(128)
 int8_dot_kernel(const Int8Params p) {
-  const int lane = threadIdx.x & 31;
-  const int64_t n0 = ((int64_t)blockIdx.x * 4 + (threadIdx.x >> 5)) * NT;
+  __shared__ int part[SHARED ? 4 : 1][MT * NT];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t n0 = (SHARED ? (int64_t)blockIdx.x : (int64_t)blockIdx.x * 4 + warp) * NT;
   if (n0 >= p.N) return;
   for (int64_t m0 = 0; m0 < p.M; m0 += MT) {
     int acc[MT][NT] = {};
-    for (int k = lane * 16; k < p.K; k += 512) {
-      uint4 b[NT];
+    for (int k = (SHARED ? (int)threadIdx.x : lane) * 16; k < p.K; k += SHARED ? 2048 : 512) {
+      Codes<VEC> a[MT], b[NT];
+      const int8_t *row_a[MT], *row_b[NT];
 #pragma unroll
-      for (int j = 0; j < NT; ++j)
-        b[j] = *reinterpret_cast<const uint4*>(p.b + (n0 + j < p.N ? n0 + j : p.N - 1) * p.ldb + k);
+      for (int j = 0; j < NT; ++j) {
+        row_b[j] = p.b + (n0 + j < p.N ? n0 + j : p.N - 1) * p.ldb;
+        b[j].ask(row_b[j], k, true, p.b, p.b_end);
+      }
 #pragma unroll
       for (int i = 0; i < MT; ++i) {
-        const uint4 a = *reinterpret_cast<const uint4*>(p.a + (m0 + i < p.M ? m0 + i : p.M - 1) * p.lda + k);
+        row_a[i] = p.a + (m0 + i < p.M ? m0 + i : p.M - 1) * p.lda;
+        a[i].ask(row_a[i], k, true, p.a, p.a_end);
+      }
+      uint4 cb[NT];
 #pragma unroll
-        for (int j = 0; j < NT; ++j) acc[i][j] = dot16(a, b[j], acc[i][j]);
+      for (int j = 0; j < NT; ++j) cb[j] = b[j].get(row_b[j], k, p.K, true, p.b, p.b_end);
+#pragma unroll
+      for (int i = 0; i < MT; ++i) {
+        const uint4 ca = a[i].get(row_a[i], k, p.K, true, p.a, p.a_end);
+#pragma unroll
+        for (int j = 0; j < NT; ++j) acc[i][j] = dot16(ca, cb[j], acc[i][j]);
       }
     }
+    const int mine = lane;                                // lane i NT + j: output (m0 + i, n0 + j)
+    const int64_t m = m0 + mine / NT, n = n0 + mine % NT;
+    const bool out = (!SHARED || warp == 0) && mine < MT * NT && m < p.M && n < p.N;
+    const float sa = out ? scale_a(p, m) : 0.0f, sb = out ? scale_b(p, n) : 0.0f;
+    int s = 0;
 #pragma unroll
     for (int i = 0; i < MT; ++i)
 #pragma unroll
       for (int j = 0; j < NT; ++j) {
-        const int s = __reduce_add_sync(0xFFFFFFFFu, acc[i][j]);
-        if (lane == (i * NT + j) % 32 && m0 + i < p.M && n0 + j < p.N) store_out(p, m0 + i, n0 + j, s, scale_a(p, m0 + i), scale_b(p, n0 + j));
+        const int all = __reduce_add_sync(0xFFFFFFFFu, acc[i][j]);
+        if (lane == i * NT + j) s = all;
       }
+    if constexpr (SHARED) {
+      if (mine < MT * NT) part[warp][mine] = s;
+      __syncthreads();
+      if (out) s = part[0][mine] + part[1][mine] + part[2][mine] + part[3][mine];
+      if (m0 + MT < p.M) __syncthreads();
+    }
+    if (out) store_out(p, m, n, s, sa, sb);
   }
 }
 
-template <int MT> int launch_dot(const Int8Params& p, cudaStream_t st) {
+template <int MT> int launch_dot(const Int8Params& p, bool vec, cudaStream_t st) {
   constexpr int NT = 4;
-  int8_dot_kernel<MT, NT><<<(unsigned)((p.N + 4 * NT - 1) / (4 * NT)), 128, 0, st>>>(p);
+  static_assert(MT * NT <= 32, "an output a lane");
+  const int64_t groups = (p.N + NT - 1) / NT;
+  // Shared where there is something to share, K > 512; but 16 sums of four unaligned tokens, with their
+  // registers, only where there are few columns (4 x 60 x 20000 5.8 us, 18.4 by warps, and unaligned 4 x 5760 x
+  // 1921 13.2, 9.0 by warps).
+  const bool shared = p.K > 512 && (MT == 1 || vec || groups <= 2 * emu_ops_sm_count());
+  auto kernel = vec ? shared ? int8_dot_kernel<MT, NT, true, true> : int8_dot_kernel<MT, NT, true, false>
+                    : shared ? int8_dot_kernel<MT, NT, false, true> : int8_dot_kernel<MT, NT, false, false>;
+  kernel<<<(unsigned)(shared ? groups : (groups + 3) / 4), 128, 0, st>>>(p);
   return EMU_OK;
 }
 
@@ -118,36 +215,6 @@ __device__ __forceinline__ void codes_to_f16(uint32_t w, uint32_t& lo, uint32_t&
   const __half2 x = __hsub2(*reinterpret_cast<__half2*>(&a), bias), y = __hsub2(*reinterpret_cast<__half2*>(&b), bias);
   lo = *reinterpret_cast<const uint32_t*>(&x);
   hi = *reinterpret_cast<const uint32_t*>(&y);
-}
-
-// ---------------------------------------------------------------------------------------
-// Rows of A, then of B, copied to 16-byte aligned rows of `ldo` codes, zeros after the K-th: for operands
-// whose rows the vector kernels cannot read as they are.  A thread takes 16 codes.
-__global__ void __launch_bounds__(256)
-int8_align_kernel(const int8_t* a, int64_t lda, int64_t rows_a, const int8_t* b, int64_t ldb, int64_t rows_b, int K,
-                  int8_t* out_a, int8_t* out_b, int ldo) {
-  const uint32_t chunks = (uint32_t)ldo / 16;
-  const int64_t rows = rows_a + rows_b, total = rows * chunks;
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
-    int64_t row;
-    uint32_t c;
-    if (total <= 0xFFFFFFFFll) {
-      const uint32_t q = (uint32_t)i / chunks;
-      row = q;
-      c = (uint32_t)i - q * chunks;
-    } else {
-      row = i / chunks;
-      c = (uint32_t)(i - row * chunks);
-    }
-    const bool is_a = row < rows_a;
-    const int64_t r = is_a ? row : row - rows_a;
-    const int8_t* src = (is_a ? a + r * lda : b + r * ldb) + c * 16;
-    uint32_t w[4] = {0u, 0u, 0u, 0u};
-#pragma unroll
-    for (int j = 0; j < 16; ++j)
-      if ((int)c * 16 + j < K) w[j >> 2] |= (uint32_t)(uint8_t)src[j] << (8 * (j & 3));
-    *reinterpret_cast<uint4*>((is_a ? out_a : out_b) + r * ldo + c * 16) = make_uint4(w[0], w[1], w[2], w[3]);
-  }
 }
 
 }  // namespace emu_ops
@@ -188,19 +255,40 @@ inline int64_t round_up(int64_t v, int64_t to) { return (v + to - 1) / to * to; 
 enum class Int8Kind { dot, few, tensor };
 struct Plan {
   Int8Kind kind;
-  int64_t Kp;                    // operands laid out in rows of Kp values (others: only where not aligned)
-  int64_t rows_a, rows_b;        // tensor: the rows laid out at a time
-  size_t a_bytes, b_bytes;       // workspace: A's part, then B's
+  int64_t Kp;                    // tensor: operands laid out in rows of Kp values,
+  int64_t rows_a, rows_b;        // so many rows at a time,
+  size_t a_bytes, b_bytes;       // in the workspace: A's part, then B's
 };
+constexpr int64_t kSms = 152;                      // of the GPU that the rule was measured on
 constexpr size_t kSlabBytes = (size_t)128 << 20;   // fp16 rows at a time, so that the workspace stays small
 
-Plan plan_for(int64_t M, int64_t N, int64_t K, bool aligned16) {
+// The few-token kernel's slices of K: the rounds of CTAs (`room` of them live at once) times the stages of a
+// slice and, in stages, a CTA's fixed time are to be few.
+struct Slices { int S; int64_t rounds, stages; };
+Slices few_slices(int64_t tiles, int64_t room, int stages) {
+  Slices best = {1, (tiles + room - 1) / room, stages};
+  for (int n = 2; n <= kMaxSlices && n <= stages; ++n) {
+    const Slices s = {n, (tiles * n + room - 1) / room, (stages + n - 1) / n};
+    if (s.rounds * (s.stages + kFixedStages) < best.rounds * (best.stages + kFixedStages)) best = s;
+  }
+  return best;
+}
+
+Plan plan_for(int64_t M, int64_t N, int64_t K) {
   Plan pl = {};
-  // Laying the operands out and filling 128 x 256 tiles pays for many tokens and from about ten stages of
-  // 128 x 128 x 128 an SM on (200 x 5760 x 1920, 8.9 of them: 20.8 us as few, 22.9 as many;
-  // 400 x 5760 x 1920, 17.8: 35.9 and 24.5); few tokens never repay the laying out of B.
-  const int64_t stages = ((M + 127) / 128) * ((N + 127) / 128) * ((K + 127) / 128);
-  pl.kind = M <= 4 || K == 0 ? Int8Kind::dot : M > 128 && stages > 10 * 152 ? Int8Kind::tensor : Int8Kind::few;
+  pl.kind = M <= 4 || K == 0 ? Int8Kind::dot : Int8Kind::few;
+  if (pl.kind == Int8Kind::few && M > 128) {
+    // For many tokens both are open.  Measured, in us: the few-token kernel takes 3, and a round 4.5 and 0.8 a
+    // stage, 2.1 where rows are not 16-byte aligned; laying out 5.5 and 0.43 a million codes, and then a round
+    // of 128 x 256 tiles 2 and 0.27 for 64 of K.  As few and laid out: 1637 x 188 x 32 8.4 and 8.9, 300 x 5760
+    // x 301 13.9 and 9.6, 2000 x 1000 x 1000 23.1 and 13.0, 400 x 5760 x 1920 35.4 and 21.0, 130 x 2000 x
+    // 8000 20.5 and 48.7.
+    const Slices f = few_slices(((M + 127) / 128) * ((N + 127) / 128), kSms, (int)((K + 127) / 128));
+    const double few = 3.0 + (double)f.rounds * (4.5 + (K % 16 == 0 ? 0.8 : 2.1) * (double)f.stages);
+    const double rounds = (double)((((M + 127) / 128) * ((N + 255) / 256) + kSms - 1) / kSms);
+    const double laid_out = 5.5 + (double)(M + N) * (double)K * 0.43e-6 + rounds * (2.0 + 0.27 * (double)((K + 63) / 64));
+    if (laid_out < few) pl.kind = Int8Kind::tensor;
+  }
   if (pl.kind == Int8Kind::tensor) {
     pl.Kp = round_up(K, kTcBK);
     const int64_t most = (int64_t)(kSlabBytes / (2 * (size_t)pl.Kp)) / kTcBN * kTcBN;   // K < 2^17: 512 rows at least
@@ -208,10 +296,6 @@ Plan plan_for(int64_t M, int64_t N, int64_t K, bool aligned16) {
     pl.rows_b = N < most ? N : most;
     pl.a_bytes = round256((size_t)pl.rows_a * (size_t)pl.Kp * 2);
     pl.b_bytes = round256((size_t)pl.rows_b * (size_t)pl.Kp * 2);
-  } else if (!aligned16) {
-    pl.Kp = round_up(K, 16);
-    pl.a_bytes = round256((size_t)M * (size_t)pl.Kp);
-    pl.b_bytes = round256((size_t)N * (size_t)pl.Kp);
   }
   return pl;
 }
@@ -233,8 +317,9 @@ int launch_tc(const Int8Params& p, const Plan& pl, bool vec, unsigned char* ws, 
       const uint64_t work = ((uint64_t)lay_a + (lay_b ? (uint64_t)rows_b : 0u)) * chunks;
       if (work > 0) {
         const uint64_t blocks = (work + 255) / 256;
-        int8_to_f16_kernel<<<(unsigned)(blocks < 16384 ? blocks : 16384), 256, 0, st>>>(
-            p.a + m * p.lda, p.lda, lay_a, a16, p.b + n * p.ldb, p.ldb, lay_b ? (uint32_t)rows_b : 0u, b16, p.K, chunks, vec);
+        auto lay_out = vec ? int8_to_f16_kernel<true> : int8_to_f16_kernel<false>;
+        lay_out<<<(unsigned)(blocks < 16384 ? blocks : 16384), 256, 0, st>>>(
+            p, m, lay_a, a16, n, lay_b ? (uint32_t)rows_b : 0u, b16, chunks);
       }
       CUtensorMap map_a, map_b;
       int rc = f16_map(&map_a, a16, rows_a, pl.Kp, kTcBM);
@@ -266,24 +351,16 @@ int launch_tc(const Int8Params& p, const Plan& pl, bool vec, unsigned char* ws, 
   return EMU_OK;
 }
 
-template <int BT> int launch_few(const Int8Params& p, cudaStream_t st) {
+template <int BT> int launch_few(const Int8Params& p, bool vec, cudaStream_t st) {
   using SH = FewShape<BT>;
-  // slices of K: rounds of CTAs (`resident` an SM) times the stages of a slice and, in stages, a CTA's fixed time
   const int64_t tn = (p.N + 127) / 128, tiles = tn * ((p.M + BT - 1) / BT), room = (int64_t)emu_ops_sm_count() * SH::RESIDENT;
   const int stages = (p.K + 127) / 128;
-  int S = 1;
-  int64_t best = 0;
-  for (int n = 1; n <= kMaxSlices && n <= stages; ++n) {
-    const int64_t cost = (tiles * n + room - 1) / room * ((stages + n - 1) / n + kFixedStages);
-    if (n == 1 || cost < best) {
-      best = cost;
-      S = n;
-    }
-  }
+  const int S = few_slices(tiles, room, stages).S;
   const bool is_long = (stages + S - 1) / S > 8;
-  auto kernel = is_long ? int8_few_kernel<BT, true> : int8_few_kernel<BT, false>;
-  static std::atomic<bool> done[2][64];
-  if (!emu_ops_allow_smem(reinterpret_cast<const void*>(kernel), SH::SMEM, done[is_long]))
+  auto kernel = vec ? is_long ? int8_few_kernel<BT, true, true> : int8_few_kernel<BT, false, true>
+                    : is_long ? int8_few_kernel<BT, true, false> : int8_few_kernel<BT, false, false>;
+  static std::atomic<bool> done[4][64];
+  if (!emu_ops_allow_smem(reinterpret_cast<const void*>(kernel), SH::SMEM, done[2 * vec + is_long]))
     return emu_ops_launched("cudaFuncSetAttribute");
   // rows of tiles on grid.y, at most 65535 a launch
   for (int64_t m = 0; m < p.M; m += (int64_t)65535 * BT) {
@@ -309,30 +386,14 @@ template <int BT> int launch_few(const Int8Params& p, cudaStream_t st) {
 }
 
 int run_plan(const Int8Params& p, bool vec, void* workspace, cudaStream_t st) {
-  const Plan pl = plan_for(p.M, p.N, p.K, vec);
-  unsigned char* ws = static_cast<unsigned char*>(workspace);
-  if (pl.kind == Int8Kind::tensor) {
-    const int rc = launch_tc(p, pl, vec, ws, st);
-    return rc == EMU_OK ? emu_ops_launched("emu_int8_scaled_mm") : rc;
-  }
-  Int8Params q = p;
-  if (!vec && p.K > 0) {
-    int8_t* a = reinterpret_cast<int8_t*>(ws);
-    int8_t* b = reinterpret_cast<int8_t*>(ws + pl.a_bytes);
-    const int64_t work = (p.M + p.N) * (pl.Kp / 16), blocks = (work + 255) / 256;
-    int8_align_kernel<<<(unsigned)(blocks < 16384 ? blocks : 16384), 256, 0, st>>>(p.a, p.lda, p.M, p.b, p.ldb, p.N, p.K, a, b,
-                                                                                  (int)pl.Kp);
-    q.a = a;
-    q.b = b;
-    q.lda = q.ldb = pl.Kp;
-    q.K = (int)pl.Kp;
-  }
+  const Plan pl = plan_for(p.M, p.N, p.K);
   int rc;
-  if (pl.kind == Int8Kind::dot) rc = q.M == 1 ? launch_dot<1>(q, st) : launch_dot<4>(q, st);
-  else if (q.M <= 16) rc = launch_few<16>(q, st);
-  else if (q.M <= 32) rc = launch_few<32>(q, st);
-  else if (q.M <= 64) rc = launch_few<64>(q, st);
-  else rc = launch_few<128>(q, st);
+  if (pl.kind == Int8Kind::tensor) rc = launch_tc(p, pl, vec, static_cast<unsigned char*>(workspace), st);
+  else if (pl.kind == Int8Kind::dot) rc = p.M == 1 ? launch_dot<1>(p, vec, st) : launch_dot<4>(p, vec, st);
+  else if (p.M <= 16) rc = launch_few<16>(p, vec, st);
+  else if (p.M <= 32) rc = launch_few<32>(p, vec, st);
+  else if (p.M <= 64) rc = launch_few<64>(p, vec, st);
+  else rc = launch_few<128>(p, vec, st);
   return rc == EMU_OK ? emu_ops_launched("emu_int8_scaled_mm") : rc;
 }
 
@@ -355,9 +416,9 @@ int emu_ops_int8_status(int* status, bool reset) {
 
 extern "C" {
 
-size_t emu_int8_workspace_bytes(int64_t M, int64_t N, int64_t K, int32_t aligned16) {
+size_t emu_int8_workspace_bytes(int64_t M, int64_t N, int64_t K) {
   if (M < 1 || N < 1 || K < 1 || K > kInt8MaxK || M >= ((int64_t)1 << 31) || N >= ((int64_t)1 << 31)) return 0;
-  const Plan plan = plan_for(M, N, K, aligned16 != 0);
+  const Plan plan = plan_for(M, N, K);
   return plan.a_bytes + plan.b_bytes;
 }
 
@@ -381,11 +442,14 @@ int emu_int8_scaled_mm(const int8_t* A, int64_t lda, const int8_t* B, int64_t ld
   if (!aligned(out, es) || !aligned(scale_a, 4) || !aligned(scale_b, 4))
     return emu_ops_fail(EMU_EINVAL, "a tensor is not aligned to its elements");
   const bool vec = K % 16 == 0 && lda % 16 == 0 && ldb % 16 == 0 && aligned(A, 16) && aligned(B, 16);
-  const size_t need = emu_int8_workspace_bytes(M, N, K, vec);
+  const size_t need = emu_int8_workspace_bytes(M, N, K);
   if (need > 0 && (!workspace || workspace_bytes < need || !aligned(workspace, 256)))
     return emu_ops_fail(EMU_EINVAL, "workspace of %zu bytes needed, 256-byte aligned (got %zu)", need, workspace_bytes);
   Int8Params p;
-  p.a = A; p.lda = lda; p.b = B; p.ldb = ldb; p.M = M; p.N = N; p.cols = N; p.K = (int)K;
+  p.a = A; p.lda = lda; p.b = B; p.ldb = ldb;
+  p.a_end = reinterpret_cast<uintptr_t>(A) + (size_t)(M - 1) * (size_t)lda + (size_t)K;
+  p.b_end = reinterpret_cast<uintptr_t>(B) + (size_t)(N - 1) * (size_t)ldb + (size_t)K;
+  p.M = M; p.N = N; p.cols = N; p.K = (int)K;
   p.scale_a = scale_a; p.sa_step = scale_a_count == 1 ? 0 : 1;
   p.scale_b = scale_b; p.sb_step = scale_b_count == 1 ? 0 : 1;
   p.out = out; p.out_type = (int)out_dtype;

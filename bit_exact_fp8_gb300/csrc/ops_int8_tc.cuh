@@ -121,11 +121,11 @@ template <int N> __device__ __forceinline__ void tc_read(uint32_t addr, float (&
 
 // LONG: slices of more than eight stages, whose sums are taken out of the tensor memory every 1024 of K
 constexpr int kFewThreads = 288;
-template <int BT, bool LONG>
+template <int BT, bool LONG, bool VEC>
 __global__ void __launch_bounds__(kFewThreads, FewShape<BT>::RESIDENT)
 int8_few_kernel(const Int8Params p, int S) {
   using SH = FewShape<BT>;
-  constexpr int PP = SH::PIECES, AHEAD = SH::AHEAD, STEP = SH::OWN < 32 ? 16 : 32;
+  constexpr int PP = SH::PIECES, AHEAD = VEC ? SH::AHEAD : 1, STEP = SH::OWN < 32 ? 16 : 32;
   extern __shared__ unsigned char raw_smem[];
   __shared__ __align__(8) uint64_t bars[5];                 // full[2], empty[2], read (sums taken)
   __shared__ uint32_t slot;
@@ -141,15 +141,13 @@ int8_few_kernel(const Int8Params p, int S) {
   // piece i of a thread: codes 16 c8 to 16 c8 + 15 of a stage, of row r8 + 32 i (B's 128 rows, then tokens)
   const int c8 = tid & 7, r8 = (tid & 255) >> 3;
   const int8_t* at[PP];
-  uint4 w[AHEAD][PP];
-  auto load = [&](int st, uint4 (&v)[PP]) {
-    const int k = (int)(first + st) * 128 + c8 * 16;
+  Codes<VEC> w[AHEAD][PP];
+  auto first_of = [&](int st) { return (int)(first + st) * 128 + c8 * 16; };
+  auto load = [&](int st, Codes<VEC> (&v)[PP]) {
+    const int k = first_of(st);
     const bool in = st < count && k < p.K;
 #pragma unroll
-    for (int i = 0; i < PP; ++i) {
-      v[i] = make_uint4(0u, 0u, 0u, 0u);
-      if (in && at[i]) v[i] = *reinterpret_cast<const uint4*>(at[i] + k);
-    }
+    for (int i = 0; i < PP; ++i) v[i].ask(at[i], k, in && at[i], i < 4 ? p.b : p.a, i < 4 ? p.b_end : p.a_end);
   };
   if (warp < 8) {
 #pragma unroll
@@ -240,11 +238,13 @@ int8_few_kernel(const Int8Params p, int S) {
         for (int i = 0; i < PP; ++i) {
           const int row = r8 + 32 * i;
           if (PP * 32 != SH::ROWS && row >= SH::ROWS) break;
+          const uint4 q = w[u][i].get(at[i], first_of(st), p.K, first_of(st) < p.K && at[i], i < 4 ? p.b : p.a,
+                                      i < 4 ? p.b_end : p.a_end);
           uint32_t h[8];
-          codes_to_f16(w[u][i].x, h[0], h[1]);
-          codes_to_f16(w[u][i].y, h[2], h[3]);
-          codes_to_f16(w[u][i].z, h[4], h[5]);
-          codes_to_f16(w[u][i].w, h[6], h[7]);
+          codes_to_f16(q.x, h[0], h[1]);
+          codes_to_f16(q.y, h[2], h[3]);
+          codes_to_f16(q.z, h[4], h[5]);
+          codes_to_f16(q.w, h[6], h[7]);
           const uint4 lo = make_uint4(h[0], h[1], h[2], h[3]), hi = make_uint4(h[4], h[5], h[6], h[7]);
           // the two atoms' chunks share banks: their threads store odd and even chunks in turn
           const int odd = c8 >> 2, chunk = (c8 & 3) * 2;
@@ -269,14 +269,26 @@ int8_few_kernel(const Int8Params p, int S) {
   const int nl = quad * 32 + lane;
   if (S == 1) {
     const int64_t n = n0 + nl;
-    if (reads && n < p.N) {
-      const float sb = scale_b(p, n);
+    if (!reads) return;                                     // whole warps
+    const float sb = n < p.N ? scale_b(p, n) : 0.0f;
+    float sa[(SH::OWN + 31) / 32];                            // of token lane, lane + 32: asked for at once
+#pragma unroll
+    for (int i = 0; i < SH::OWN; i += 32) {
+      const int64_t m = m0 + t0 + i + lane;
+      sa[i / 32] = i + lane < SH::OWN && m < p.M ? scale_a(p, m) : 0.0f;
+    }
+    auto write = [&](auto* out) {
+      using T = std::remove_pointer_t<decltype(out)>;
 #pragma unroll
       for (int i = 0; i < SH::OWN; ++i) {
         const int64_t m = m0 + t0 + i;
-        if (m < p.M) store_out(p, m, n, sum[i], scale_a(p, m), sb);
+        const float v = ((float)sum[i] * __shfl_sync(0xFFFFFFFFu, sa[i / 32], i % 32)) * sb;
+        if (m < p.M && n < p.N) out[m * p.N + n] = from_f<T>(v);
       }
-    }
+    };
+    if (p.out_type == EMU_OUT_F32) write(static_cast<float*>(p.out));
+    else if (p.out_type == EMU_OUT_BF16) write(static_cast<__nv_bfloat16*>(p.out));
+    else write(static_cast<__half*>(p.out));
     return;
   }
   // slice s adds up the tokens s, s + S, ...: every slice writes its sums of them there, once that CTA is
@@ -288,6 +300,13 @@ int8_few_kernel(const Int8Params p, int S) {
   float sb[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j) sb[j] = n + j < p.N ? scale_b(p, n + j) : 0.0f;
+  float sa[BT < 64 ? 1 : 2];                                // of its lane-th token, its lane + 32-th
+#pragma unroll
+  for (int i = 0; i < (BT < 64 ? 1 : 2); ++i) {
+    const int q = i * 32 + lane;
+    const int64_t m = m0 + (int64_t)q * S + slice;
+    sa[i] = q < slots && m < p.M ? scale_a(p, m) : 0.0f;
+  }
   cluster_wait();
   if (reads) {
     int owner = t0 % S, slot_of = t0 / S;
@@ -305,7 +324,7 @@ int8_few_kernel(const Int8Params p, int S) {
   for (int q = tid / 32; tid < 256 && q * S + (int)slice < BT; q += 8) {
     const int64_t m = m0 + q * S + slice;
     if (m >= p.M) break;
-    const float sa = scale_a(p, m);
+    const float of_token = __shfl_sync(0xFFFFFFFFu, BT >= 64 && q >= 32 ? sa[BT >= 64] : sa[0], q % 32);
     int v[4] = {0, 0, 0, 0};
 #pragma unroll
     for (int r = 0; r < kMaxSlices; ++r)
@@ -316,46 +335,44 @@ int8_few_kernel(const Int8Params p, int S) {
         v[2] += x.z;
         v[3] += x.w;
       }
-    store_row<4>(p, m, n, v, sa, sb, together);
+    store_row<4>(p, m, n, v, of_token, sb, together);
   }
 }
 
 // ---------------------------------------------------------------------------------------
-// For many tokens.  Codes to fp16 rows of Kp values, zeros after the K-th: rows_a rows of A, then rows_b of B.  A
-// thread takes 16 codes.
+// For many tokens.  Codes to fp16 rows of 16 `chunks` values, zeros after the K-th: rows_a rows of A from row
+// m on, then rows_b of B from row n on.  A thread takes 16 codes.
+template <bool VEC>
 __global__ void __launch_bounds__(256)
-int8_to_f16_kernel(const int8_t* a, int64_t lda, uint32_t rows_a, uint16_t* a16, const int8_t* b, int64_t ldb,
-                   uint32_t rows_b, uint16_t* b16, int K, uint32_t chunks, bool vec) {
+int8_to_f16_kernel(const Int8Params p, int64_t m, uint32_t rows_a, uint16_t* a16, int64_t n, uint32_t rows_b, uint16_t* b16,
+                   uint32_t chunks) {
   const uint32_t total = (rows_a + rows_b) * chunks;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the product waits for this kernel's end
   for (uint32_t i = blockIdx.x * 256u + threadIdx.x; i < total; i += gridDim.x * 256u) {
     const uint32_t row = i / chunks, c = i - row * chunks;
     const bool is_a = row < rows_a;
     const uint32_t r = is_a ? row : row - rows_a;
-    const int8_t* src = is_a ? a + (int64_t)r * lda : b + (int64_t)r * ldb;
     const int k = (int)c * 16;
-    uint32_t w[4] = {0u, 0u, 0u, 0u};
-    if (vec) {
-      if (k < K) {
-        const uint4 q = *reinterpret_cast<const uint4*>(src + k);
-        w[0] = q.x; w[1] = q.y; w[2] = q.z; w[3] = q.w;
-      }
-    } else {
-#pragma unroll
-      for (int j = 0; j < 16; ++j)
-        if (k + j < K) w[j >> 2] |= (uint32_t)(uint8_t)src[k + j] << (8 * (j & 3));
-    }
+    const int8_t* const row_at = is_a ? p.a + (m + r) * p.lda : p.b + (n + r) * p.ldb;
+    const int8_t* const from = is_a ? p.a : p.b;
+    const uintptr_t end = is_a ? p.a_end : p.b_end;
+    Codes<VEC> codes;
+    codes.ask(row_at, k, k < p.K, from, end);
+    const uint4 q = codes.get(row_at, k, p.K, k < p.K, from, end);
     uint4* dst = reinterpret_cast<uint4*>((is_a ? a16 : b16) + (size_t)r * chunks * 16 + (size_t)c * 16);
     uint32_t h[8];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) codes_to_f16(w[j], h[2 * j], h[2 * j + 1]);
+    codes_to_f16(q.x, h[0], h[1]);
+    codes_to_f16(q.y, h[2], h[3]);
+    codes_to_f16(q.z, h[4], h[5]);
+    codes_to_f16(q.w, h[6], h[7]);
     dst[0] = make_uint4(h[0], h[1], h[2], h[3]);
     dst[1] = make_uint4(h[4], h[5], h[6], h[7]);
   }
 }
 
-// A warp's 32 rows x 128 columns of sums, a row a lane, scaled and written out: 128 bytes of each row at a time go through shared memory (16 bytes a lane, a row's chunks
-// permuted by its number: no two lanes of a phase meet in a bank), so that whole lines are stored.
+// A warp's 32 rows x 128 columns of sums, a row a lane, scaled and written out: 128 bytes of each row at a
+// time go through shared memory (16 bytes a lane, a row's chunks permuted by its number: no two lanes of a
+// phase meet in a bank), so that whole lines are stored, or, where rows are not 16-byte aligned, elements.
 // sb: scale_b of columns lane, lane + 32, ...
 template <class T>
 __device__ __forceinline__ void write_tile(const Int8Params& p, const int (&sum)[128], const float (&sb)[4], float sa,
@@ -391,12 +408,26 @@ __device__ __forceinline__ void write_tile(const Int8Params& p, const int (&sum)
         }
       }
     } else {
-      for (int r = 0; r < rows; ++r)
+      const unsigned char* from = stage + (lane % VEC) * sizeof(T);
+      const int chunk = lane / VEC * 16;
+      T* to = out + m0 * p.N + nc + lane;
+#pragma unroll 1
+      for (int r0 = 0; r0 < rows; r0 += 8, from += 8 * kTcStageRow) {
 #pragma unroll
-        for (int i = 0; i < COLS; i += 32)
-          if (nc + i + lane < p.cols)
-            out[(m0 + r) * p.N + nc + i + lane] =
-                reinterpret_cast<const T*>(stage + r * kTcStageRow + ((((i + lane) / VEC) ^ (r & 7)) * 16))[lane % VEC];
+        for (int h = 0; h < 8; h += 4) {                   // four rows' values asked for at once
+          T v[4][COLS / 32];
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+#pragma unroll
+            for (int i = 0; i < COLS / 32; ++i)
+              v[r][i] = *reinterpret_cast<const T*>(from + (h + r) * kTcStageRow + (chunk ^ ((i * 32 / VEC ^ (h + r)) * 16)));
+#pragma unroll
+          for (int r = 0; r < 4; ++r, to += p.N)
+#pragma unroll
+            for (int i = 0; i < COLS / 32; ++i)
+              if (r0 + h + r < rows && nc + i * 32 + lane < p.cols) to[i * 32] = v[r][i];
+        }
+      }
     }
   }
 }

@@ -254,8 +254,7 @@ PyObject* int8_mm(PyObject* const* a) {
   const at::Tensor out = a[5] == Py_None ? make({M, N}, ot, dev) : given(a[5], "out", M, N, ot, dev);
   const int8_t* A = m1.data_ptr<int8_t>();
   const int8_t* B = m2.data_ptr<int8_t>();
-  const bool aligned = ((uint64_t)(K | lda | ldb) | reinterpret_cast<uintptr_t>(A) | reinterpret_cast<uintptr_t>(B)) % 16 == 0;
-  const size_t need = emu_int8_workspace_bytes(M, N, K, aligned);
+  const size_t need = emu_int8_workspace_bytes(M, N, K);
   at::Tensor ws;
   if (a[6] != Py_None) {
     ws = tensor(a[6], "workspace");

@@ -78,9 +78,8 @@ def rms_norm_backward(grad_y: torch.Tensor, hidden: torch.Tensor, rstd: torch.Te
 
 
 def int8_workspace_bytes(M: int, N: int, K: int) -> int:
-    """Device workspace bytes ``int8_scaled_mm`` needs for these sizes, whatever the
-    operands' alignment."""
-    return int(_lib.load().emu_int8_workspace_bytes(M, N, K, 0))
+    """Device workspace bytes ``int8_scaled_mm`` needs for these sizes."""
+    return int(_lib.load().emu_int8_workspace_bytes(M, N, K))
 
 
 def int8_scaled_mm(mat1: torch.Tensor, mat2: torch.Tensor, scale_a: torch.Tensor, scale_b: torch.Tensor, *,

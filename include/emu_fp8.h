@@ -353,13 +353,12 @@ int emu_rms_norm_backward(const void* grad_y, int64_t ldy, const void* hidden, i
  *   A  [M,K] row-major, rows lda apart;  B  [K,N] column-major, columns ldb apart (the
  *      w.t() of a row-major [N,K] weight);  scale_a M values or one, scale_b N or one
  *   out [M,N] contiguous
- *   workspace: emu_int8_workspace_bytes bytes, 256-byte aligned (NULL where 0).  aligned16:
- *      nonzero where A and B are 16-byte aligned and K, lda and ldb multiples of 16; 0 gives
- *      what every alignment is content with
+ *   workspace: emu_int8_workspace_bytes(M, N, K) bytes, 256-byte aligned (NULL where 0);
+ *      at most 256 MiB and little more
  * Sizes: M, N < 2^31, K <= 131071 (EMU_EUNSUPPORTED above: the sums could overflow).
  * K == 0 gives zeros times the scales.
  */
-size_t emu_int8_workspace_bytes(int64_t M, int64_t N, int64_t K, int32_t aligned16);
+size_t emu_int8_workspace_bytes(int64_t M, int64_t N, int64_t K);
 int emu_int8_scaled_mm(const int8_t* A, int64_t lda, const int8_t* B, int64_t ldb,
                        int64_t M, int64_t N, int64_t K, const float* scale_a, int64_t scale_a_count,
                        const float* scale_b, int64_t scale_b_count, void* out, emu_out_t out_dtype,

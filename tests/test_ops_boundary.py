@@ -90,8 +90,8 @@ def test_int8_empty_and_workspace(lib):
     assert int8(lib, M=0, na=1, A=0, out=0, sa=0) == 0
     assert int8(lib, N=0, nb=1, B=0, out=0, sb=0) == 0
     L = lib.load()
-    assert L.emu_int8_workspace_bytes(-1, 8, 8, 0) == 0 and L.emu_int8_workspace_bytes(0, 8, 8, 0) == 0
-    need = L.emu_int8_workspace_bytes(8192, 5760, 1920, 1)
+    assert L.emu_int8_workspace_bytes(-1, 8, 8) == 0 and L.emu_int8_workspace_bytes(0, 8, 8) == 0
+    need = L.emu_int8_workspace_bytes(8192, 5760, 1920)
     if need:
         a = dict(M=8192, N=5760, K=1920, lda=1920, ldb=1920, na=8192, nb=5760)
         assert int8(lib, **a, wb=need - 1) == -1 and "workspace" in lib.emu_ops_last_error()
