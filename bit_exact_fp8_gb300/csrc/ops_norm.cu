@@ -506,14 +506,12 @@ template <class T> int pick_norm(const NormParams& p, bool alike, bool aligned16
 }
 
 // ------------------------------------------------------------------------- gradient
-// The parts of column sums that there can be: one of every two CTAs, of up to 608 CTAs, or of up to 2432
-// where rows are short and many CTAs live on an SM (2.5 MB in all).  A multiple of four, as CTAs
-// come by eights.
-int64_t parts_for(int64_t T, int64_t H) {
-  int64_t most = ((int64_t)1 << 20) * 10 / 16 / H;
-  most = most < 304 ? 304 : most > 1216 ? 1216 : most / 4 * 4;
+// The parts of column sums that there can be: one of every two CTAs, of up to 608 CTAs.  (With four times as
+// many, where rows are short and more CTAs would live on an SM, joining them took longer than they
+// saved.)  A multiple of four, as CTAs come by eights.
+int64_t parts_for(int64_t T) {
   const int64_t n = (T + 7) / 8 * 4;
-  return n < most ? n : most;
+  return n < 304 ? n : 304;
 }
 
 struct NormGradParams {
@@ -744,7 +742,7 @@ int launch_grad(const NormGradParams& p, int threads, bool aligned16, cudaStream
   const Ring ring = ring_for(p.H, sizeof(T), aligned16, inputs, MAXT * MINB / threads, &resident);
   const int64_t most = (int64_t)emu_ops_sm_count() * resident;
   int64_t ctas = ((p.T < most ? p.T : most) + 7) / 8 * 8;  // whole clusters, and a CTA's rows lie alike
-  if (ctas > parts_for(p.T, p.H) * kGradCluster) ctas = parts_for(p.T, p.H) * kGradCluster;
+  if (ctas > parts_for(p.T) * kGradCluster) ctas = parts_for(p.T) * kGradCluster;
   const size_t bytes = (size_t)ring.S * inputs * ring.pitch;   // two rows of two tensors at least: room for [H] fp32
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)ctas);
@@ -769,7 +767,7 @@ template <class T> int pick_norm_grad(const NormGradParams& p, bool alike, bool 
     if (nv <= 1024) return launch_grad<T, 4, 256, 2>(p, threads_for(nv, 4), aligned16, st);
     return launch_grad<T, 4, 512, 1>(p, threads_for(nv, 4), aligned16, st);
   }
-  const int parts = (int)parts_for(p.T, p.H);
+  const int parts = (int)parts_for(p.T);
   norm_grad_rows_kernel<T><<<(unsigned)p.T, 256, 0, st>>>(p);
   norm_grad_weight_kernel<T><<<dim3((unsigned)parts, (unsigned)((p.H + 255) / 256)), 256, 0, st>>>(p);
   return parts;
@@ -862,7 +860,7 @@ int emu_rms_norm_quant(const void* x, int64_t ldx, const void* residual, int64_t
 
 size_t emu_rms_norm_backward_workspace_bytes(int64_t T, int64_t H) {
   if (T < 1 || H < 1 || H > (1 << 22)) return 0;
-  return (size_t)parts_for(T, H) * (size_t)H * sizeof(float);
+  return (size_t)parts_for(T) * (size_t)H * sizeof(float);
 }
 
 int emu_rms_norm_backward(const void* grad_y, int64_t ldy, const void* hidden, int64_t ldh,
