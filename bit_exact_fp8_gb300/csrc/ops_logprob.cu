@@ -324,11 +324,11 @@ __device__ __forceinline__ float least_of(unsigned long long bound) {
 }
 
 // One warp a row: for short rows.
-constexpr int kWarpRows = 4, kWarpList = 256;
+constexpr int kWarpRows = 4, kWarpList = 512;
 template <class T>
 __global__ void __launch_bounds__(32 * kWarpRows)
 logprob_warp_kernel(const LogprobParams p) {
-  __shared__ unsigned long long list_all[kWarpRows][kWarpList];
+  __shared__ __align__(16) unsigned long long list_all[kWarpRows][kWarpList + 2];
   __shared__ int cand_all[kWarpRows][kMaxTop];
   __shared__ int count_all[kWarpRows];
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
@@ -371,12 +371,29 @@ logprob_warp_kernel(const LogprobParams p) {
   }
   __syncwarp();
   const int n = count;
-  if (n <= kWarpList) {
-    for (int i = lane; i < n; i += 32) {
-      const unsigned long long c = list[i];
-      int rank = 0;
-      for (int j = 0; j < n; ++j) rank += list[j] > c;
-      if (rank < p.k) put_top(p, r, rank, c, s);
+  if (n <= 32) {
+    const unsigned long long mine = lane < n ? list[lane] : 0ull;
+    int rank = 0;
+    for (int j = 0; j < n; ++j) rank += list[j] > mine;
+    if (lane < n && rank < p.k) put_top(p, r, rank, mine, s);
+    return;
+  }
+  if (n <= kWarpList) {                                // four entries a lane against two at a time
+    if (lane == 0 && n % 2) list[n] = 0ull;
+    __syncwarp();
+    for (int i0 = lane; i0 < n; i0 += 128) {
+      unsigned long long mine[4];
+      int rank[4] = {0, 0, 0, 0};
+#pragma unroll
+      for (int u = 0; u < 4; ++u) mine[u] = i0 + 32 * u < n ? list[i0 + 32 * u] : ~0ull;
+      for (int j = 0; j < n; j += 2) {
+        const ulonglong2 c = *reinterpret_cast<const ulonglong2*>(list + j);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) rank[u] += (c.x > mine[u]) + (c.y > mine[u]);
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        if (i0 + 32 * u < n && rank[u] < p.k) put_top(p, r, rank[u], mine[u], s);
     }
     return;
   }
@@ -400,18 +417,20 @@ logprob_warp_kernel(const LogprobParams p) {
 // A CTA, or the C CTAs of a cluster, a row: for long rows, and more CTAs a row the fewer rows there
 // are.  Each CTA takes a run of the row's vectors; the first one joins the sums and the k
 // largest of each through distributed shared memory.
-constexpr int kGroups = 128, kList = 1024, kMaxCluster = 8;
+constexpr int kGroups = 128, kMaxCluster = 8;
 template <class T, int NT>
 __global__ void __launch_bounds__(NT, NT == 512 ? 1 : 5)
 logprob_row_kernel(const LogprobParams p, int C) {
   constexpr int NW = NT / 32, GT = NT / kGroups;      // GT threads a group
   constexpr bool FEW = NT == 512;                      // the form for few rows
+  constexpr int kList = FEW ? 1024 : 768;              // a row of equal logits lists 8 k GT
   __shared__ Soft warp_soft[NW];
   __shared__ __align__(16) unsigned long long heads[kGroups];
   __shared__ int cand[kMaxTop];
   __shared__ unsigned long long bound;
   __shared__ int count, taken;
   __shared__ unsigned long long list[kList];
+  __shared__ unsigned long long kept[kMaxTop * (kList / kGroups)];       // of the list: k groups' at most
   __shared__ Soft parts[kMaxCluster];                                    // of the first CTA: all CTAs'
   __shared__ unsigned long long tops[kMaxCluster][kMaxTop];
   __shared__ unsigned long long best_of[NW];
@@ -446,7 +465,8 @@ logprob_row_kernel(const LogprobParams p, int C) {
   for (int i = 1; i < NW; ++i) s = soft_join(s, warp_soft[i]);
 
   if (p.k > 0) {
-    {                                                  // GT threads a head, each with its share of the others
+    // how many heads exceed each group's, GT threads a head, each with its share of the others; the k-th is the bound
+    auto rank_heads = [&](unsigned long long* at) {
       const unsigned long long head = heads[tid / GT];
       int above = 0;
 #pragma unroll 16
@@ -456,11 +476,13 @@ logprob_row_kernel(const LogprobParams p, int C) {
       }
 #pragma unroll
       for (int o = 1; o < GT; o <<= 1) above += __shfl_xor_sync(0xFFFFFFFFu, above, o);
-      if (tid % GT == 0 && head != 0ull && above < p.k) {
-        cand[above] = tid / GT;
-        atomicAdd(&taken, 1);
-        if (above == p.k - 1) bound = head;
-      }
+      if (tid % GT == 0 && head != 0ull && above == p.k - 1) *at = head;
+      return tid % GT == 0 && head != 0ull && above < p.k ? above : -1;
+    };
+    const int place = rank_heads(&bound);
+    if (place >= 0) {
+      cand[place] = tid / GT;
+      atomicAdd(&taken, 1);
     }
     __syncthreads();
     const float least = least_of(bound);
@@ -501,10 +523,31 @@ logprob_row_kernel(const LogprobParams p, int C) {
     if (tid < kMaxTop) tops[part][tid] = 0ull;         // fewer logits than k in this run
     __syncthreads();
     if (n <= kList) {
-      for (int i = tid; i < n; i += NT) {
-        const unsigned long long c = list[i];
+      const unsigned long long* from = list;
+      int m = n;
+      if (n > kGroups) {                               // equal logits, above all: the same bound once more, for the listed
+        unsigned long long head = 0ull;
+        for (int i = tid; i < n; i += NT) head = list[i] > head ? list[i] : head;
+#pragma unroll
+        for (int o = 1; o < GT; o <<= 1) {
+          const unsigned long long c = __shfl_xor_sync(0xFFFFFFFFu, head, o);
+          head = c > head ? c : head;
+        }
+        if (tid % GT == 0) heads[tid / GT] = head;
+        if (tid == 0) count = 0;
+        __syncthreads();
+        (void)rank_heads(&bound);
+        __syncthreads();
+        for (int i = tid; i < n; i += NT)
+          if (list[i] >= bound) kept[atomicAdd(&count, 1)] = list[i];
+        __syncthreads();
+        from = kept;
+        m = count;
+      }
+      for (int i = tid; i < m; i += NT) {
+        const unsigned long long c = from[i];
         int rank = 0;
-        for (int j = 0; j < n; ++j) rank += list[j] > c;
+        for (int j = 0; j < m; ++j) rank += from[j] > c;
         if (rank < p.k) tops[part][rank] = c;
       }
       __syncthreads();
@@ -586,13 +629,24 @@ template <class T, int NT> int launch_row(const LogprobParams& p, int C, cudaStr
 
 template <class T> int pick_logprob(const LogprobParams& p, cudaStream_t st) {
   const int nvec = (int)(((int64_t)p.V + Row<T>::VEC - 1) / Row<T>::VEC);
-  if (nvec <= 1024) {
+  // A warp for short rows, and for many longer ones with few alternatives (with many, too much of a long row
+  // reaches a bound that 32 lanes' maxima give): 6852 x 16658 fp16 with 5 alternatives 70 us by warps, 83 by
+  // CTAs of 128 threads, but 300 rows 19 and 7.
+  if (nvec <= 1024 || (nvec <= 2560 && p.k <= 8 && p.T >= 16 * emu_ops_sm_count())) {
     logprob_warp_kernel<T><<<(unsigned)((p.T + kWarpRows - 1) / kWarpRows), 32 * kWarpRows, 0, st>>>(p);
     return EMU_OK;
   }
-  int C = 1;                                            // until two CTAs an SM, four vectors a thread
-  while (C < kMaxCluster && p.T * C < 2 * emu_ops_sm_count() && nvec >= 2 * C * 512 * 4) C *= 2;
-  return C > 1 ? launch_row<T, 512>(p, C, st) : launch_row<T, 256>(p, 1, st);
+  // Small CTAs for many rows of middling length: 6852 x 16658 fp16 with 32 alternatives 128 us, 139 by 256
+  // threads; 2000 x 30000 bf16 with 5 38 and 42.
+  if (nvec <= 4096 && p.T >= 2 * emu_ops_sm_count()) return launch_row<T, 128>(p, 1, st);
+  // Few rows: CTAs of 512 threads with twice the loads in flight, one an SM, in clusters as long as they all
+  // run at once and have four vectors a thread: 150 x 131072 bf16 with 5 alternatives 15.6 us, 23.3 by 256
+  // threads, 38.6 in clusters of two, which take turns; 30 x 131072 with 20 9.6 us in clusters of four, 18.1 of
+  // eight.  Rows of 4096 vectors or less gain nothing by more than 256 threads.
+  const int sms = emu_ops_sm_count();
+  int C = 1;
+  while (C < kMaxCluster && 2 * p.T * C <= sms && nvec >= 2 * C * 512 * 4) C *= 2;
+  return p.T <= sms && nvec >= 4096 ? launch_row<T, 512>(p, C, st) : launch_row<T, 256>(p, 1, st);
 }
 
 struct LogprobGradParams {
