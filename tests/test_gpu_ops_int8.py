@@ -26,7 +26,7 @@ def codes(gen, rows, cols, low=-128, high=128):
 
 
 def expected(a, w, sa, sb, dt):
-    acc = a.double() @ w.double().t()
+    acc = a.double() @ w.double().t() + 0.0                  # a whole number's zero has no sign: 0.0 * -5.0 has
     return (acc.float() * sa.reshape(-1, 1) * sb.reshape(1, -1)).to(dt)
 
 
@@ -162,3 +162,28 @@ def test_refusals(fw):
         fw.int8_scaled_mm(big, big.t(), one, one)
     with pytest.raises(fw.UnsupportedFeatureError):
         fw.int8_scaled_mm(a, w.t(), sa, sb, out_dtype=torch.int32)
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 9, 513), (2, 4000, 512), (1, 60, 20000), (3, 61, 20001), (4, 700, 5001), (4, 3001, 2049),
+                                   (150, 333, 7001), (300, 5764, 301), (400, 1001, 2999), (700, 255, 4096), (1000, 258, 64),
+                                   (3000, 1602, 191)])
+def test_forms(fw, M, N, K):
+    """K shared by a CTA's warps or not, slices, tiles whose output rows start at any address."""
+    a, w, sa, sb = make(M, N, K, seed=M + N + K)
+    for dt in DT.values():
+        check(fw, a, w, sa, sb, dt)
+
+
+@pytest.mark.parametrize("M,N", [(1, 5), (3, 130), (20, 40), (150, 9), (600, 300)])
+@pytest.mark.parametrize("K", [1, 15, 17, 31, 47, 130, 1023])
+def test_codes_beside_the_operands_do_not_count(fw, M, N, K):
+    """Operands in the middle of other codes, at every address modulo 16 in turn."""
+    a, w, sa, sb = make(M, N, K, seed=K)
+    for off in range(0, 16, 3):
+        parts = []
+        for x in (a, w):
+            buf = torch.full((x.numel() + 64,), 127, dtype=torch.int8, device=DEV)
+            at = buf[off:off + x.numel()].view(x.shape)
+            at.copy_(x)
+            parts.append(at)
+        check(fw, parts[0], parts[1], sa, sb, torch.float32)

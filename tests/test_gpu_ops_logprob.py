@@ -311,3 +311,18 @@ def test_refusals(fw):
         fw.token_logprobs(x, tok, top_k=33)
     with pytest.raises(fw.UnsupportedFeatureError):
         fw.token_logprobs(x.clone().requires_grad_(), tok)
+
+
+@pytest.mark.parametrize("T,V,dt,k", [(2500, 16658, "f16", 5), (2500, 16658, "f16", 9), (310, 16658, "bf16", 32), (160, 33000, "bf16", 20),
+                                      (140, 33000, "bf16", 20), (140, 131072, "bf16", 5), (76, 70001, "f32", 32), (77, 70001, "f32", 32),
+                                      (6, 33000, "bf16", 32), (12, 228, "bf16", 32)])
+def test_forms(fw, T, V, dt, k):
+    """Many rows and few, a CTA or a cluster a row, among them rows of equal and of few different logits, whose
+    alternatives are the lowest ids."""
+    x, tok = make(T, V, DT[dt], seed=T + V)
+    x[1] = -math.inf
+    x[2] = 1.5
+    x[3] = (torch.arange(V, device=DEV) % 3).to(x.dtype)
+    x[4, : V // 2] = -math.inf
+    x[5, 40:] = -math.inf
+    check(fw, x, tok, k)
