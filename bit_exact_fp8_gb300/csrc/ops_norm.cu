@@ -523,7 +523,72 @@ struct NormGradParams {
   int64_t T; int H;
   void* gx;                                       // [T, H] contiguous
   float* part;                                    // [gridDim.x, H]
+  uint32_t row_ctas;                              // CTAs that take rows; those after them take columns (few rows)
+  float* gw;                                      // of the latter
 };
+
+// Few rows: gw needs nothing that the rows' pass finds, so CTAs of the same launch sum the columns, from the
+// inputs (the second reading of few rows costs less than parts in memory and a kernel that joins them).  A CTA
+// takes 8 vectors of columns, a lane one of them of every 4th of the warps' rows, or, where rows are not
+// aligned, every 32nd column of the warp's rows.  red: a warp's sums of all the CTA's columns.
+template <class T> constexpr int kColumns = 128 / sizeof(T);
+template <class T, bool EDGES>
+__device__ __forceinline__ void sum_columns(const NormGradParams& p, int block, float* red) {
+  constexpr int VEC = 16 / sizeof(T), COLS = kColumns<T>, N = EDGES ? COLS / 32 : VEC, U = EDGES ? 8 : 4;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  const int64_t c0 = (int64_t)block * COLS;
+  const int64_t first = c0 + (EDGES ? lane : (lane & 7) * VEC);       // this lane's columns: VEC together, or 32 apart
+  const int row0 = EDGES ? warp : warp * 4 + (lane >> 3), step = EDGES ? warps : 4 * warps, rows = (int)p.T;
+  const T *gy = static_cast<const T*>(p.gy) + first, *h = static_cast<const T*>(p.h) + first;
+  float acc[N], odd[N];                                               // two sums a column: shorter chains
+#pragma unroll
+  for (int j = 0; j < N; ++j) acc[j] = odd[j] = 0.0f;
+  for (int r0 = row0; r0 < rows; r0 += U * step) {                    // U rows asked for at once
+    alignas(16) T y[U][N], x[U][N];
+    float rstd[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t r = r0 + u * step;
+      const bool in = r < rows;
+      rstd[u] = in ? p.rstd[r] : 0.0f;
+      if constexpr (EDGES) {
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+          const bool at = in && first + 32 * j < p.H;
+          y[u][j] = at ? gy[r * p.ldy + 32 * j] : from_f<T>(0.0f);
+          x[u][j] = at ? h[r * p.ldh + 32 * j] : from_f<T>(0.0f);
+        }
+      } else {
+        const bool at = in && first < p.H;
+        const uint4 none = make_uint4(0u, 0u, 0u, 0u);
+        *reinterpret_cast<uint4*>(y[u]) = at ? *reinterpret_cast<const uint4*>(gy + r * p.ldy) : none;
+        *reinterpret_cast<uint4*>(x[u]) = at ? *reinterpret_cast<const uint4*>(h + r * p.ldh) : none;
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int j = 0; j < N; ++j) {
+        float& sum = u % 2 ? odd[j] : acc[j];
+        sum = fmaf(to_f(y[u][j]) * rstd[u], to_f(x[u][j]), sum);
+      }
+  }
+#pragma unroll
+  for (int j = 0; j < N; ++j) {
+    acc[j] += odd[j];
+    if (!EDGES) {
+      acc[j] += __shfl_xor_sync(0xFFFFFFFFu, acc[j], 8);
+      acc[j] += __shfl_xor_sync(0xFFFFFFFFu, acc[j], 16);
+    }
+    if (EDGES || lane < 8) red[warp * COLS + (EDGES ? lane + 32 * j : lane * VEC + j)] = acc[j];
+  }
+  __syncthreads();
+  for (int c = threadIdx.x; c < COLS && c0 + c < p.H; c += blockDim.x) {
+    float a = 0.0f;
+    for (int i = 0; i < warps; ++i) a += red[i * COLS + c];
+    p.gw[c0 + c] = a;
+  }
+}
 
 // The gradient in one pass.  As in the forward kernel, a CTA takes rows a grid apart through a ring in
 // shared memory.  A row's sum of g h (g = gy w) has to be known before its first output, so each
@@ -543,17 +608,22 @@ norm_grad_kernel(const NormGradParams p, const Ring ring) {
   const int t = threadIdx.x, nt = blockDim.x, lane = t & 31, warp = t >> 5;
   const int inputs = p.gh ? 3 : 2;
   const uint32_t stage_bytes = (uint32_t)inputs * ring.pitch;
-  const int rows = (int)(p.T > blockIdx.x ? (p.T - blockIdx.x + gridDim.x - 1) / gridDim.x : 0);
+  const int ctas = (int)p.row_ctas;
+  const int rows = (int)(p.T > blockIdx.x ? (p.T - blockIdx.x + ctas - 1) / ctas : 0);
   const int apart = nt > 64 ? 32 : 1;                       // threads 0, 1, 2 of these fetch a tensor each
   const bool fetches = t % apart == 0 && t / apart < inputs;
   auto fill = [&](int i, int s) {
-    const int64_t row = blockIdx.x + (int64_t)i * gridDim.x;
+    const int64_t row = blockIdx.x + (int64_t)i * ctas;
     const int which = t / apart;
     const T* base = static_cast<const T*>(which == 0 ? p.gy : which == 1 ? p.h : p.gh);
     fill_row(dyn + s * stage_bytes + which * ring.pitch, base, which == 0 ? p.ldy : which == 1 ? p.ldh : p.ldg, row, p.T,
              p.H, smem_addr(&full[s]));
   };
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the joining kernel waits for this one's end
+  if (p.gw && blockIdx.x >= p.row_ctas) {                   // whole clusters
+    sum_columns<T, EDGES>(p, (int)(blockIdx.x - p.row_ctas), reinterpret_cast<float*>(dyn));
+    return;
+  }
   if (t < 16) sums[0][t] = sums[1][t] = 0.0f;
   if (t == 0) {
     for (int i = 0; i < ring.S; ++i) bar_init(smem_addr(&full[i]), inputs);
@@ -575,7 +645,7 @@ norm_grad_kernel(const NormGradParams p, const Ring ring) {
   int s = 0, before = ring.S - 1;                           // row k's stage and row k - 1's
   uint32_t phase = 0;
   for (int k = 0; k < rows; ++k) {
-    const int64_t row = blockIdx.x + (int64_t)k * gridDim.x;
+    const int64_t row = blockIdx.x + (int64_t)k * ctas;
     const float rstd = p.rstd[row];
     ok = bar_wait(smem_addr(&full[s]), phase);
     const unsigned char* in = dyn + s * stage_bytes;
@@ -637,6 +707,7 @@ norm_grad_kernel(const NormGradParams p, const Ring ring) {
       (void)bar_wait(smem_addr(&full[i]), 1);
     }
   }
+  if (p.gw) return;                                         // its columns are summed by others
   __syncthreads();
   float* const column_sums = reinterpret_cast<float*>(dyn);
 #pragma unroll
@@ -730,20 +801,36 @@ norm_grad_join_kernel(const float* part, int parts, int H, float* gw) {
   }
 }
 
-// Launches the kernel; the parts that it leaves for the joining kernel, 0 if it failed.
+// Launches the kernel; the parts that it leaves for the joining kernel: none (0) where it sums the columns
+// itself, and -1 if it failed.
 template <class T, int IT, int MAXT, int MINB>
-int launch_grad(const NormGradParams& p, int threads, bool aligned16, cudaStream_t st) {
+int launch_grad(const NormGradParams& given, int threads, bool aligned16, cudaStream_t st) {
+  NormGradParams p = given;
   auto kernel = aligned16 ? norm_grad_kernel<T, IT, MAXT, MINB, false> : norm_grad_kernel<T, IT, MAXT, MINB, true>;
   static std::atomic<bool> flags[2][64];
   std::atomic<bool>* done = flags[aligned16];
-  if (!emu_ops_allow_smem(reinterpret_cast<const void*>(kernel), kMaxSmem - 1024, done)) return 0;
+  if (!emu_ops_allow_smem(reinterpret_cast<const void*>(kernel), kMaxSmem - 1024, done)) return -1;
   int resident;
   const int inputs = p.gh ? 3 : 2;
   const Ring ring = ring_for(p.H, sizeof(T), aligned16, inputs, MAXT * MINB / threads, &resident);
   const int64_t most = (int64_t)emu_ops_sm_count() * resident;
   int64_t ctas = ((p.T < most ? p.T : most) + 7) / 8 * 8;  // whole clusters, and a CTA's rows lie alike
   if (ctas > parts_for(p.T) * kGradCluster) ctas = parts_for(p.T) * kGradCluster;
-  const size_t bytes = (size_t)ring.S * inputs * ring.pitch;   // two rows of two tensors at least: room for [H] fp32
+  size_t bytes = (size_t)ring.S * inputs * ring.pitch;      // two rows of two tensors at least: room for [H] fp32
+  p.row_ctas = (uint32_t)ctas;
+  // As few rows as a warp sums up soon, of tensors of 16 MiB at most.  So, and with parts and a joining kernel:
+  // 1 x 1920 bf16 2.8 us and 5.6, 256 x 1920 3.8 and 6.9, 512 x 1920 6.0 and 7.9, 500 x 16384 20.7 and 23.7;
+  // but 256 x 96 (64 rows a thread) 8.7 and 5.4, 1000 x 16384 40.0 and 34.8; not aligned 128 x 1921 3.7 and 7.2,
+  // 200 x 2505 5.7 and 10.2, but 128 x 197 (128 rows) 8.0 and 6.1.
+  const bool sums_columns = p.T <= (aligned16 ? 4 * 32 : 80) * (threads / 32) && p.T * p.H * (int64_t)sizeof(T) <= 16 << 20;
+  if (sums_columns) {
+    const size_t need = (size_t)(threads / 32) * 4 * kColumns<T>;
+    bytes = bytes < need ? need : bytes;
+    const int64_t blocks = (p.H + kColumns<T> - 1) / kColumns<T>;
+    ctas += (blocks + kGradCluster - 1) / kGradCluster * kGradCluster;
+  } else {
+    p.gw = nullptr;
+  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)ctas);
   cfg.blockDim = dim3((unsigned)threads);
@@ -755,10 +842,11 @@ int launch_grad(const NormGradParams& p, int threads, bool aligned16, cudaStream
   at.val.clusterDim.y = at.val.clusterDim.z = 1;
   cfg.attrs = &at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, p, ring) == cudaSuccess ? (int)(ctas / kGradCluster) : 0;
+  if (cudaLaunchKernelEx(&cfg, kernel, p, ring) != cudaSuccess) return -1;
+  return sums_columns ? 0 : (int)(p.row_ctas / kGradCluster);
 }
 
-// The fewest vectors a thread that leave a CTA within its threads; 0: a launch failed.
+// The fewest vectors a thread that leave a CTA within its threads; as launch_grad.
 template <class T> int pick_norm_grad(const NormGradParams& p, bool alike, bool aligned16, cudaStream_t st) {
   constexpr int V = 16 / sizeof(T);
   const int nv = aligned16 ? p.H / V : (p.H + 2 * V - 2) / V;       // vectors that a row can touch
@@ -898,6 +986,7 @@ int emu_rms_norm_backward(const void* grad_y, int64_t ldy, const void* hidden, i
   p.gy = grad_y; p.ldy = ldy; p.h = hidden; p.ldh = ldh; p.gh = grad_residual; p.ldg = ldg;
   p.weight = weight; p.weight_f32 = weight_type == EMU_OUT_F32; p.rstd = rstd;
   p.T = T; p.H = (int)H; p.gx = grad_x; p.part = static_cast<float*>(workspace);
+  p.row_ctas = 0; p.gw = grad_weight;
   // do all rows start on 16 bytes, or at least all tensors' alike
   auto at = [](const void* t) { return reinterpret_cast<uintptr_t>(t); };
   const uintptr_t bases = (at(grad_y) ^ at(hidden)) | (at(grad_y) ^ at(grad_x)) |
@@ -909,7 +998,7 @@ int emu_rms_norm_backward(const void* grad_y, int64_t ldy, const void* hidden, i
   const int parts = type == EMU_OUT_F32    ? pick_norm_grad<float>(p, alike, aligned16, st)
                     : type == EMU_OUT_BF16 ? pick_norm_grad<__nv_bfloat16>(p, alike, aligned16, st)
                                            : pick_norm_grad<__half>(p, alike, aligned16, st);
-  if (parts == 0) return emu_ops_launched("emu_rms_norm_backward");
+  if (parts <= 0) return emu_ops_launched("emu_rms_norm_backward");
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)((H + 31) / 32));
   cfg.blockDim = dim3(512);

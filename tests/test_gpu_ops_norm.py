@@ -312,3 +312,19 @@ def test_refusals(fw):
         fw.rms_norm_quant(x, w, out_dtype=torch.uint8)
     with pytest.raises(fw.UnsupportedFeatureError):
         fw.rms_norm_quant(x, w.clone().requires_grad_())
+
+
+@pytest.mark.parametrize("dt", DT)
+@pytest.mark.parametrize("T,H", [(1, 8), (2, 16), (4, 96), (128, 96), (129, 96), (80, 197), (81, 197), (256, 1920), (512, 1920),
+                                 (513, 1920), (128, 1921), (400, 1921), (64, 5761), (40, 16384), (17, 16383), (65, 8200)])
+def test_grad_of_few_rows(fw, T, H, dt):
+    """Columns summed beside the rows, up to as many rows as that takes, and just above."""
+    check_grad(fw, *make_grad(T, H, DT[dt], seed=T + H))
+    check_grad(fw, *make_grad(T, H, DT[dt], seed=T + H, residual=False, wdt=torch.float32))
+
+
+def test_grad_rows_do_not_depend_on_how_columns_are_summed(fw):
+    for H in (1920, 1921):
+        gy, h, rstd, w, gr = make_grad(2000, H, torch.bfloat16)
+        all_rows = fw.rms_norm_backward(gy, h, rstd, w, gr)[0]
+        assert torch.equal(fw.rms_norm_backward(gy[:64], h[:64], rstd[:64], w, gr[:64])[0], all_rows[:64])
