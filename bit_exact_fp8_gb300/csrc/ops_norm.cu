@@ -6,6 +6,7 @@
 #include <cstdarg>
 #include <cstdio>
 #include <string>
+#include <type_traits>
 
 namespace {
 thread_local std::string g_ops_error;
@@ -494,13 +495,27 @@ int launch_norm_ring(const NormParams& p, int threads, bool aligned16, bool q_ve
 template <class T> int pick_norm(const NormParams& p, bool alike, bool aligned16, bool q_vec, cudaStream_t st) {
   constexpr int V = 16 / sizeof(T);
   const int nv = aligned16 ? p.H / V : (p.H + 2 * V - 2) / V;       // vectors that a row can touch
+  // Short rows: a warp a row, straight from memory, by vectors or by elements; a ring's barriers and copies
+  // would cost more than such a row.  So, and by the ring, bf16 with a residual: 100000 x 64 31 us and 62,
+  // 100000 x 512 64 and 78, 50000 x 768 49 and 59, but 50000 x 1024 63 and 60; 100000 x 91 30 and 90,
+  // 100000 x 255 50 and 108.
+  if (aligned16 && nv <= 96) {
+    if (nv <= 32) launch_norm<T, V, 32, 1>(p, st);
+    else if (nv <= 64) launch_norm<T, V, 32, 2>(p, st);
+    else launch_norm<T, V, 32, 3>(p, st);
+    return EMU_OK;
+  }
+  if (!aligned16 && p.H <= 256) {
+    if (p.H <= 128) launch_norm<T, 1, 32, 4>(p, st);
+    else launch_norm<T, 1, 32, 8>(p, st);
+    return EMU_OK;
+  }
   if (alike && nv <= 2048) {
     if (nv <= 256) return launch_norm_ring<T, 2, 128, 8>(p, threads_for(nv, 2), aligned16, q_vec, st);
     if (nv <= 1024) return launch_norm_ring<T, 4, 256, 2>(p, threads_for(nv, 4), aligned16, q_vec, st);
     return launch_norm_ring<T, 4, 512, 1>(p, threads_for(nv, 4), aligned16, q_vec, st);
   }
   if (aligned16 && alike) launch_norm<T, V, 512, 0>(p, st);
-  else if (p.H <= 256) launch_norm<T, 1, 32, 8>(p, st);
   else launch_norm<T, 1, 512, 0>(p, st);
   return EMU_OK;
 }
@@ -540,7 +555,7 @@ __device__ __forceinline__ void sum_columns(const NormGradParams& p, int block, 
   const int64_t first = c0 + (EDGES ? lane : (lane & 7) * VEC);       // this lane's columns: VEC together, or 32 apart
   const int row0 = EDGES ? warp : warp * 4 + (lane >> 3), step = EDGES ? warps : 4 * warps, rows = (int)p.T;
   const T *gy = static_cast<const T*>(p.gy) + first, *h = static_cast<const T*>(p.h) + first;
-  float acc[N], odd[N];                                               // two sums a column: shorter chains
+  float acc[N], odd[N];                                               // of many rows two sums: shorter chains
 #pragma unroll
   for (int j = 0; j < N; ++j) acc[j] = odd[j] = 0.0f;
   for (int r0 = row0; r0 < rows; r0 += U * step) {                    // U rows asked for at once
@@ -569,13 +584,13 @@ __device__ __forceinline__ void sum_columns(const NormGradParams& p, int block, 
     for (int u = 0; u < U; ++u)
 #pragma unroll
       for (int j = 0; j < N; ++j) {
-        float& sum = u % 2 ? odd[j] : acc[j];
+        float& sum = EDGES && u % 2 ? odd[j] : acc[j];
         sum = fmaf(to_f(y[u][j]) * rstd[u], to_f(x[u][j]), sum);
       }
   }
 #pragma unroll
   for (int j = 0; j < N; ++j) {
-    acc[j] += odd[j];
+    if (EDGES) acc[j] += odd[j];
     if (!EDGES) {
       acc[j] += __shfl_xor_sync(0xFFFFFFFFu, acc[j], 8);
       acc[j] += __shfl_xor_sync(0xFFFFFFFFu, acc[j], 16);
@@ -736,6 +751,93 @@ norm_grad_kernel(const NormGradParams p, const Ring ring) {
   cluster_sync();
 }
 
+// Short rows: a warp a row, as above but straight from memory, by vectors or, where rows are not aligned, by
+// elements, the next row's values asked for before this one's are used, and with the sums of a CTA's warps
+// for one part.  By the ring a row's copies, barriers and waits cost more than its values; so, and by the
+// ring, bf16: 8192 x 512 10.3 us and 20.3, 100000 x 512 67 (6.1 TB/s) and 161, 100000 x 64 37 and 135, not
+// aligned 100000 x 255 47 and 232, 1169 x 91 4.7 and 8.2.
+constexpr int kShortWarps = 8;
+template <class T, int VEC, int IT>
+__global__ void __launch_bounds__(32 * kShortWarps, 2)
+norm_grad_short_kernel(const NormGradParams p) {
+  constexpr int COLS = 32 * VEC * IT;
+  constexpr bool EDGES = VEC == 1;
+  __shared__ __align__(16) float red[kShortWarps * (COLS > kColumns<T> ? COLS : kColumns<T>)];
+  if (p.gw && blockIdx.x >= p.row_ctas) {
+    sum_columns<T, EDGES>(p, (int)(blockIdx.x - p.row_ctas), red);
+    return;
+  }
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  float w[IT][VEC], dw[IT][VEC];
+#pragma unroll
+  for (int i = 0; i < IT; ++i)
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) {
+      const int c = (i * 32 + lane) * VEC + j;
+      w[i][j] = c >= p.H ? 0.0f : p.weight_f32 ? static_cast<const float*>(p.weight)[c] : to_f(static_cast<const T*>(p.weight)[c]);
+      dw[i][j] = 0.0f;
+    }
+  const float inv_h = __fdiv_rn(1.0f, (float)p.H);
+  const int64_t step = (int64_t)p.row_ctas * kShortWarps;
+  using Raw = std::conditional_t<(VEC > 1), uint4, T>;     // a vector as words, not as elements a register each
+  Raw raw[3][IT];
+  float rstd = 0.0f;
+  auto load = [&](int64_t row) {
+    const bool in = row < p.T;
+    rstd = in ? p.rstd[row] : 0.0f;
+#pragma unroll
+    for (int i = 0; i < IT; ++i) {
+      const int c = (i * 32 + lane) * VEC;
+      if (!in || c >= p.H) continue;
+      raw[0][i] = *reinterpret_cast<const Raw*>(static_cast<const T*>(p.gy) + row * p.ldy + c);
+      raw[1][i] = *reinterpret_cast<const Raw*>(static_cast<const T*>(p.h) + row * p.ldh + c);
+      if (p.gh) raw[2][i] = *reinterpret_cast<const Raw*>(static_cast<const T*>(p.gh) + row * p.ldg + c);
+    }
+  };
+#pragma unroll
+  for (int i = 0; i < IT; ++i) raw[0][i] = raw[1][i] = raw[2][i] = Raw{};   // what no load writes counts as zeros
+  int64_t row = (int64_t)blockIdx.x * kShortWarps + warp;
+  load(row);
+  for (; row < p.T; row += step) {
+    float y[IT][VEC], x[IT][VEC], g[IT][VEC], sum = 0.0f;
+    const float r = rstd;
+#pragma unroll
+    for (int i = 0; i < IT; ++i) {
+      load_f<T, VEC>(reinterpret_cast<const T*>(&raw[0][i]), y[i]);
+      load_f<T, VEC>(reinterpret_cast<const T*>(&raw[1][i]), x[i]);
+      load_f<T, VEC>(reinterpret_cast<const T*>(&raw[2][i]), g[i]);
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) sum = fmaf(y[i][j] * w[i][j], x[i][j], sum);
+    }
+    load(row + step);
+    const float coef = warp_sum(sum) * inv_h * r * r * r;
+#pragma unroll
+    for (int i = 0; i < IT; ++i) {
+      const int c = (i * 32 + lane) * VEC;
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) {
+        const float yr = y[i][j] * r;
+        dw[i][j] = fmaf(yr, x[i][j], dw[i][j]);
+        g[i][j] = fmaf(yr, w[i][j], fmaf(x[i][j], -coef, g[i][j]));
+      }
+      if (c < p.H) store_f<T, VEC>(static_cast<T*>(p.gx) + row * p.H + c, g[i]);
+    }
+  }
+  if (p.gw) return;
+#pragma unroll
+  for (int i = 0; i < IT; ++i)
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) red[warp * COLS + (i * 32 + lane) * VEC + j] = dw[i][j];
+  __syncthreads();
+  for (int c = threadIdx.x; c < p.H; c += 32 * kShortWarps) {
+    float a = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kShortWarps; ++i) a += red[i * COLS + c];
+    p.part[(int64_t)blockIdx.x * p.H + c] = a;
+  }
+}
+
 // Rows too long for a CTA's registers, in two passes over them.
 //
 // Row t: g = gy w, c = rstd^2 mean(g h), gx = rstd (g - h c) + gh.  One element a thread and
@@ -820,8 +922,8 @@ int launch_grad(const NormGradParams& given, int threads, bool aligned16, cudaSt
   p.row_ctas = (uint32_t)ctas;
   // As few rows as a warp sums up soon, of tensors of 16 MiB at most.  So, and with parts and a joining kernel:
   // 1 x 1920 bf16 2.8 us and 5.6, 256 x 1920 3.8 and 6.9, 512 x 1920 6.0 and 7.9, 500 x 16384 20.7 and 23.7;
-  // but 256 x 96 (64 rows a thread) 8.7 and 5.4, 1000 x 16384 40.0 and 34.8; not aligned 128 x 1921 3.7 and 7.2,
-  // 200 x 2505 5.7 and 10.2, but 128 x 197 (128 rows) 8.0 and 6.1.
+  // but 1000 x 16384 40.0 and 34.8; not aligned 128 x 1921 3.7 and 7.2, 200 x 2505 5.7 and 10.2, but 256 x
+  // 953 (128 rows a warp) 8.5 and 7.9.
   const bool sums_columns = p.T <= (aligned16 ? 4 * 32 : 80) * (threads / 32) && p.T * p.H * (int64_t)sizeof(T) <= 16 << 20;
   if (sums_columns) {
     const size_t need = (size_t)(threads / 32) * 4 * kColumns<T>;
@@ -846,10 +948,24 @@ int launch_grad(const NormGradParams& given, int threads, bool aligned16, cudaSt
   return sums_columns ? 0 : (int)(p.row_ctas / kGradCluster);
 }
 
+template <class T, int VEC, int IT> int launch_grad_short(const NormGradParams& given, cudaStream_t st) {
+  NormGradParams p = given;
+  const int64_t ctas = (p.T + kShortWarps - 1) / kShortWarps, most = parts_for(p.T);
+  p.row_ctas = (uint32_t)(ctas < most ? ctas : most);
+  // so, and with parts: 256 x 96 bf16 3.1 us and 3.6, 1000 x 96 7.3 and 4.3; not aligned 400 x 197 5.5 and 4.2
+  const bool sums_columns = p.T <= (VEC > 1 ? 64 : 32) * kShortWarps;
+  if (!sums_columns) p.gw = nullptr;
+  const int64_t columns = sums_columns ? (p.H + kColumns<T> - 1) / kColumns<T> : 0;
+  norm_grad_short_kernel<T, VEC, IT><<<(unsigned)(p.row_ctas + columns), 32 * kShortWarps, 0, st>>>(p);
+  return sums_columns ? 0 : (int)p.row_ctas;
+}
+
 // The fewest vectors a thread that leave a CTA within its threads; as launch_grad.
 template <class T> int pick_norm_grad(const NormGradParams& p, bool alike, bool aligned16, cudaStream_t st) {
   constexpr int V = 16 / sizeof(T);
   const int nv = aligned16 ? p.H / V : (p.H + 2 * V - 2) / V;       // vectors that a row can touch
+  if (aligned16 && nv <= 64) return nv <= 32 ? launch_grad_short<T, V, 1>(p, st) : launch_grad_short<T, V, 2>(p, st);
+  if (!aligned16 && p.H <= 256) return p.H <= 128 ? launch_grad_short<T, 1, 4>(p, st) : launch_grad_short<T, 1, 8>(p, st);
   if (alike && nv <= 2048) {
     if (nv <= 256) return launch_grad<T, 2, 128, 6>(p, threads_for(nv, 2), aligned16, st);
     if (nv <= 1024) return launch_grad<T, 4, 256, 2>(p, threads_for(nv, 4), aligned16, st);

@@ -328,3 +328,26 @@ def test_grad_rows_do_not_depend_on_how_columns_are_summed(fw):
         gy, h, rstd, w, gr = make_grad(2000, H, torch.bfloat16)
         all_rows = fw.rms_norm_backward(gy, h, rstd, w, gr)[0]
         assert torch.equal(fw.rms_norm_backward(gy[:64], h[:64], rstd[:64], w, gr[:64])[0], all_rows[:64])
+
+
+@pytest.mark.parametrize("dt", DT)
+@pytest.mark.parametrize("T,H", [(300, 96), (3000, 96), (2600, 512), (2500, 255), (2500, 256), (600, 129), (513, 200), (257, 91),
+                                 (40, 768), (40, 776), (1100, 384), (1, 255), (9, 33)])
+def test_short_rows(fw, T, H, dt):
+    """A warp a row, by vectors and by elements, and just longer rows."""
+    x, w, r = make(T, H, DT[dt], seed=T + H)
+    check_norm(fw, x, w, r, "e4m3", None)
+    check_norm(fw, x, w, None, "int8", torch.full((1,), 8.0 / QMAX["int8"], device=DEV))
+    check_grad(fw, *make_grad(T, H, DT[dt], seed=T + H))
+    check_grad(fw, *make_grad(T, H, DT[dt], seed=T + H, residual=False, wdt=torch.float32))
+
+
+@pytest.mark.parametrize("skip", [0, 1, 8])
+def test_short_rows_of_wider_ones(fw, skip):
+    x, w, r = make(700, 272, torch.bfloat16)
+    gy, h, rstd, _, gr = make_grad(700, 272, torch.bfloat16)
+    for H in (91, 96, 256):
+        c = slice(skip, skip + H)
+        check_norm(fw, x[:, c], w[:H].contiguous(), r[:, c], "e4m3", None)
+        part = h[:, c].float()
+        check_grad(fw, gy[:, c], h[:, c], (part.square().mean(-1) + 1e-6).rsqrt(), w[:H].contiguous(), gr[:, c])
