@@ -285,9 +285,15 @@ __device__ __forceinline__ void finish_row(const LogprobParams& p, int64_t row, 
 }
 // alternative `rank` of the row: logit of this key at this id
 __device__ __forceinline__ void put_top(const LogprobParams& p, int64_t row, int rank, unsigned long long c, const Soft& s) {
-  const bool bad = s.z != s.z;
-  p.top_val[row * p.k + rank] = bad ? NAN : s.z == 0.0f ? -INFINITY : key_value((uint32_t)(c >> 32)) - s.m - logf(s.z);
-  p.top_id[row * p.k + rank] = bad ? -1 : (int64_t)(0xFFFFFFFFu - (uint32_t)c);
+  p.top_val[row * p.k + rank] = s.z == 0.0f ? -INFINITY : key_value((uint32_t)(c >> 32)) - s.m - logf(s.z);
+  p.top_id[row * p.k + rank] = (int64_t)(0xFFFFFFFFu - (uint32_t)c);
+}
+// The alternatives of a row that holds NaN or +inf, whose z is NaN.  They are written without ranking: NaN
+// has no place in the order of keys, and a vector of nothing else has no largest logit to be listed by.
+__device__ __forceinline__ bool is_bad(const Soft& s) { return s.z != s.z; }
+__device__ __forceinline__ void put_bad(const LogprobParams& p, int64_t row, int rank) {
+  p.top_val[row * p.k + rank] = NAN;
+  p.top_id[row * p.k + rank] = -1;
 }
 
 // The top k of a row in one more look at a few of its logits.  The pass above leaves each group of
@@ -341,6 +347,10 @@ logprob_warp_kernel(const LogprobParams p) {
   const Soft s = soft_warp(mine.sums());
   if (lane == 0) finish_row(p, r, s, logit, ignored);
   if (p.k == 0) return;
+  if (is_bad(s)) {                                     // in every lane alike
+    if (lane < p.k) put_bad(p, r, lane);
+    return;
+  }
   unsigned long long* list = list_all[w];
   int& count = count_all[w];
   if (lane == 0) count = 0;
@@ -464,7 +474,7 @@ logprob_row_kernel(const LogprobParams p, int C) {
 #pragma unroll
   for (int i = 1; i < NW; ++i) s = soft_join(s, warp_soft[i]);
 
-  if (p.k > 0) {
+  if (p.k > 0 && !is_bad(s)) {                         // in every thread alike; a bad part makes the row bad
     // how many heads exceed each group's, GT threads a head, each with its share of the others; the k-th is the bound
     auto rank_heads = [&](unsigned long long* at) {
       const unsigned long long head = heads[tid / GT];
@@ -594,6 +604,10 @@ logprob_row_kernel(const LogprobParams p, int C) {
     for (int i = 1; i < C; ++i) s = soft_join(s, parts[i]);
   }
   if (tid == NT - 1) finish_row(p, r, s, logit, ignored);
+  if (is_bad(s)) {
+    if (tid < p.k) put_bad(p, r, tid);
+    return;
+  }
   for (int i = tid; i < C * kMaxTop; i += NT) {
     const int q = i / kMaxTop, j = i % kMaxTop;
     const unsigned long long c = j < p.k ? tops[q][j] : 0ull;
