@@ -318,7 +318,9 @@ typedef enum { EMU_Q_E4M3FN = 0, EMU_Q_E5M2 = 1, EMU_Q_INT8 = 2 } emu_q_t;
  *   residual_out  [T,H] of `type`, rows ldo apart: h rounded once; NULL: not wanted.  May
  *                 be x or residual itself, and may not overlap them otherwise
  *   rstd          [T] fp32, for the gradient
- * Sums are fp32.  |h * weight| has to stay within fp32's normal range (or be 0), and so has
+ * Sums are fp32; y / scale is computed as (h * weight) * (rstd / scale), or with a row's own scale
+ * (h * weight) * (qmax / max|h * weight|), and is within 2^-21 of its value before the rounding to
+ * 8 bits.  |h * weight| has to stay within fp32's normal range (or be 0), and so has
  * a given scale.  A row holding NaN or Inf
  * gives NaN for its own scale and codes of NaN or 0 (a NaN becomes FP8's NaN, int8's 0),
  * and touches no other row.  Sizes: T < 2^31, 1 <= H <= 2^22.
