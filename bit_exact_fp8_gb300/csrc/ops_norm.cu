@@ -269,55 +269,158 @@ __device__ __forceinline__ void row_reduce(float& sum, float& mx, float (*sm)[2]
   }
 }
 
-// One row for each TPR threads (a warp's rows: four to a CTA).  With h = x + residual in
-// fp32, both the sum of squares and amax |h w| come from one pass over the row, so a row
-// needs one reduction and one barrier: rstd = 1 / sqrt(mean h^2 + eps), and since rstd > 0
-// is common to the row, amax |y| = rstd amax |h w|.  IT > 0: the products h w of the row
-// stay in registers (IT vectors a thread) and memory is read once.  IT == 0, rows too long
-// for that: the row is read again (residual_out is written in that second pass, by the
-// thread that read the element, so it may be x or residual itself).
-template <class T, int VEC, int TPR, int IT>
+// ---- the order of a row's sum of squares, the same in every kernel and at every address, so that a row's
+// rstd, scale and codes are its own wherever it stands.  The columns are taken in blocks of VEC, and block b
+// belongs to thread b % N (N: split_of() below, by the row's length alone).  A block's squares are added from its
+// last column to its first, even and odd columns apart (the halves of a pair), a thread's blocks in rising
+// order, then the halves, the lanes by shuffles and the warps by sum16.
+template <int NP> __device__ __forceinline__ f2 add_squares(const f2 (&q)[NP], f2 s) {
+#pragma unroll
+  for (int j = NP - 1; j >= 0; --j) s = fma2(q[j], q[j], s);
+  return s;
+}
+struct Split {
+  int it, threads;              // blocks a thread (0: as many as it takes) and threads a row
+};
+int threads_for(int n, int it) { return ((n + it - 1) / it + 31) / 32 * 32; }
+template <class T> Split split_of(int H) {
+  const int V = 16 / (int)sizeof(T), n = (H + V - 1) / V;
+  return n <= 256 ? Split{2, threads_for(n, 2)} : n <= 2048 ? Split{4, threads_for(n, 4)} : Split{0, 512};
+}
+
+// A row a warp (TPR 32, four rows to a CTA) or a CTA of up to TPR threads, straight from memory.  With
+// h = x + residual in fp32, both the sum of squares and max|h w| come from one pass over the row, so a row needs
+// one reduction and one barrier.  IT > 0: the products h w of the row stay in registers (IT blocks a thread) and
+// memory is read once.  IT == 0, rows too long for that: the row is read again (residual_out is written in that
+// second pass, by the thread that read the element, so it may be x or residual itself).  VECS: a thread
+// loads its blocks as vectors.  Else, where rows are not aligned, a warp loads its 32 blocks element by
+// element, 32 neighbours at a time, and turns them round in shared memory for the sum.
+template <class T, bool VECS, int TPR, int IT, int J>
 __global__ void __launch_bounds__(TPR == 32 ? 128 : TPR)
 norm_quant_kernel(const NormParams p) {
-  __shared__ float sm[TPR / 32][2];
-  const int t = TPR == 32 ? (threadIdx.x & 31) : threadIdx.x;
-  const int64_t row = TPR == 32 ? (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5) : (int64_t)blockIdx.x;
+  constexpr int VEC = 16 / sizeof(T), NP = VEC / 2, WARPS = TPR == 32 ? 4 : TPR / 32;
+  __shared__ __align__(16) float sums[16], tops[16];
+  __shared__ __align__(16) float turn_all[VECS ? 1 : WARPS][VECS ? 4 : 32 * VEC];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int t = TPR == 32 ? lane : threadIdx.x, n = TPR == 32 ? 32 : IT == 0 ? TPR : blockDim.x;
+  const int64_t row = TPR == 32 ? (int64_t)blockIdx.x * 4 + warp : (int64_t)blockIdx.x;
   if (TPR == 32 && row >= p.T) return;
   const T* x = static_cast<const T*>(p.x) + row * p.ldx;
   const T* r = p.residual ? static_cast<const T*>(p.residual) + row * p.ldr : nullptr;
   T* ho = p.residual_out ? static_cast<T*>(p.residual_out) + row * p.ldo : nullptr;
   uint8_t* q = p.q + row * p.H;
+  float* turn = turn_all[VECS ? 0 : warp];
+  // slot i: this thread's first column, and how far apart its J columns are (J < VEC: rows that end within so many)
+  auto first_of = [&](int i) { return VECS ? (i * n + t) * VEC : (i * n + (t & ~31)) * VEC + lane; };
+  constexpr int APART = VECS ? 1 : 32;
   constexpr int N = IT > 0 ? IT : 1;
-  float hw[N][VEC];
-  float sum = 0.0f, mx = 0.0f;
-  auto take = [&](int col, float (&v)[VEC], bool store) {
-    load_f<T, VEC>(x + col, v);
-    if (r) {
-      float a[VEC];
-      load_f<T, VEC>(r + col, a);
+  float hw[N][J];
+  float mx = 0.0f;
+  f2 sq[2] = {0ull, 0ull};                                  // [1]: a warp's rows of 64 threads' blocks, the second 32's
+  // slot i of h into v (columns past the row: 0)
+  auto load = [&](int i, float (&v)[J]) {
+    const int col = first_of(i);
+    if constexpr (VECS) {
+      if (col >= p.H) return;
+      load_f<T, VEC>(x + col, v);
+      if (r) {
+        float a[VEC];
+        load_f<T, VEC>(r + col, a);
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) v[j] += a[j];
-    }
-    if (store && ho) store_f<T, VEC>(ho + col, v);
-    float w[VEC];
-    load_weight<T, VEC>(p, col, w);
+        for (int j = 0; j < J; ++j) v[j] += a[j];
+      }
+    } else {
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) {
-      if (IT > 0 || !store) sum = fmaf(v[j], v[j], sum);
-      v[j] *= w[j];
-      if (IT > 0 || !store) mx = max_nan(mx, fabsf(v[j]));
+      for (int j = 0; j < J; ++j) {
+        const int c = col + j * APART;
+        v[j] = c < p.H ? to_f(x[c]) : 0.0f;
+        if (r && c < p.H) v[j] += to_f(r[c]);
+      }
     }
   };
+  auto keep = [&](int i, const float (&v)[J]) {           // to residual_out
+    const int col = first_of(i);
+    if constexpr (VECS) {
+      if (col < p.H) store_f<T, VEC>(ho + col, v);
+    } else {
+#pragma unroll
+      for (int j = 0; j < J; ++j)
+        if (col + j * APART < p.H) ho[col + j * APART] = from_f<T>(v[j]);
+    }
+  };
+  // h w in the place of h; in the summing pass h counts in the sum, and h w in the maximum
+  auto weigh = [&](int i, float (&v)[J], bool sum) {
+    const int col = first_of(i);
+    if (VECS && col >= p.H) return;
+    if (sum) {
+      f2 h[NP];
+      if constexpr (!VECS) {
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < J; ++j) turn[j * 32 + lane] = v[j];
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < VEC; j += 2)
+          h[j / 2] = lane * VEC < J * 32 ? pair(turn[lane * VEC + j], turn[lane * VEC + j + 1]) : 0ull;
+      } else {
+#pragma unroll
+        for (int j = 0; j < VEC; j += 2) h[j / 2] = pair(v[j], v[j + 1]);
+      }
+      sq[IT == 3 ? i & 1 : 0] = add2(sq[IT == 3 ? i & 1 : 0], add_squares(h, 0ull));
+    }
+    float w[J];
+    if constexpr (VECS) {
+      load_weight<T, VEC>(p, col, w);
+    } else {
+#pragma unroll
+      for (int j = 0; j < J; ++j) {
+        const int c = col + j * APART;
+        w[j] = c >= p.H ? 0.0f : p.weight_f32 ? static_cast<const float*>(p.weight)[c] : to_f(static_cast<const T*>(p.weight)[c]);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+      v[j] *= w[j];
+      if (sum) mx = max_nan(mx, fabsf(v[j]));
+    }
+  };
+  auto live = [&](int i) { return (VECS ? first_of(i) : (i * n + (t & ~31)) * VEC) < p.H; };   // by elements: the warp's
   if constexpr (IT > 0) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const int col = (i * TPR + t) * VEC;
-      if (col < p.H) take(col, hw[i], true);
-    }
+    for (int i = 0; i < N; ++i)
+      if (live(i)) load(i, hw[i]);
+    if (ho)
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        if (live(i)) keep(i, hw[i]);
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (live(i)) weigh(i, hw[i], true);
   } else {
-    for (int col = t * VEC; col < p.H; col += TPR * VEC) take(col, hw[0], false);
+#pragma unroll 4
+    for (int i = 0; live(i); ++i) {
+      load(i, hw[0]);
+      weigh(i, hw[0], true);
+    }
   }
-  row_reduce<TPR>(sum, mx, sm);
+  float s0, s1;
+  halves(sq[0], s0, s1);
+  float sum = warp_sum(s0 + s1);
+  if constexpr (IT == 3) {
+    halves(sq[1], s0, s1);
+    sum += warp_sum(s0 + s1);
+  }
+  mx = warp_max_nan(mx);
+  if constexpr (TPR > 32) {
+    if (lane == 0) {
+      sums[warp] = sum;
+      tops[warp] = mx;
+    }
+    if (t < 16 && t >= n / 32) sums[t] = tops[t] = 0.0f;
+    __syncthreads();
+    sum = sum16(sums);
+    mx = max16(tops);
+  }
   const RowRule rule = rule_of(p);
   const float rstd = rule.rstd(sum);
   const float scale = p.scale ? __ldg(p.scale) : rule.scale(mx, rstd);
@@ -325,29 +428,35 @@ norm_quant_kernel(const NormParams p) {
   float fa, fb;
   rule.factors(mx, rstd, scale, p.scale != nullptr, fa, fb);
   if (t == 0) p.rstd[row] = rstd;
+  auto put = [&](int i, float (&v)[J]) {
+    const int col = first_of(i);
+#pragma unroll
+    for (int j = 0; j < J; ++j) v[j] = v[j] * fa * fb;
+    if constexpr (VECS) {
+      if (col < p.H) store_codes<VEC>(q + col, v, p.q_format);
+    } else {
+#pragma unroll
+      for (int j = 0; j < J; ++j)
+        if (col + j * APART < p.H) q[col + j * APART] = (uint8_t)code_pair(v[j], 0.0f, p.q_format);
+    }
+  };
   if constexpr (IT > 0) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const int col = (i * TPR + t) * VEC;
-      if (col < p.H) {
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) hw[i][j] = hw[i][j] * fa * fb;
-        store_codes<VEC>(q + col, hw[i], p.q_format);
-      }
-    }
+    for (int i = 0; i < N; ++i)
+      if (live(i)) put(i, hw[i]);
   } else {
-    for (int col = t * VEC; col < p.H; col += TPR * VEC) {
-      take(col, hw[0], true);
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) hw[0][j] = hw[0][j] * fa * fb;
-      store_codes<VEC>(q + col, hw[0], p.q_format);
+    for (int i = 0; live(i); ++i) {
+      load(i, hw[0]);
+      if (ho) keep(i, hw[0]);
+      weigh(i, hw[0], false);
+      put(i, hw[0]);
     }
   }
 }
 
-template <class T, int VEC, int TPR, int IT> void launch_norm(const NormParams& p, cudaStream_t st) {
+template <class T, bool VECS, int TPR, int IT, int J = 16 / (int)sizeof(T)> void launch_norm(const NormParams& p, cudaStream_t st) {
   const int64_t blocks = TPR == 32 ? (p.T + 3) / 4 : p.T;
-  norm_quant_kernel<T, VEC, TPR, IT><<<(unsigned)blocks, TPR == 32 ? 128 : TPR, 0, st>>>(p);
+  norm_quant_kernel<T, VECS, TPR, IT, J><<<(unsigned)blocks, TPR == 32 ? 128 : split_of<T>(p.H).threads, 0, st>>>(p);
 }
 
 // Many rows: a CTA takes rows blockIdx.x, + gridDim.x, ..., staged ahead in a ring in shared memory by
@@ -384,6 +493,14 @@ norm_quant_ring_kernel(const NormParams p, const Ring ring) {
   f2 w[IT][NP];
 #pragma unroll
   for (int i = 0; i < IT; ++i) weight_pairs(p, Columns<T, EDGES>(i * nt + t, off, p.H), w[i]);
+  f2 tail[NP];                                              // 1 for a vector's first off values, else 0
+#pragma unroll
+  for (int j = 0; j < NP; ++j) tail[j] = pair(2 * j < off ? 1.0f : 0.0f, 2 * j + 1 < off ? 1.0f : 0.0f);
+  // a row that begins inside its first vector may end in one past the threads': its few columns, one a thread
+  const int late = IT * nt * VEC - off + t;
+  const bool has_late = EDGES && late < p.H;
+  const float late_w = !has_late ? 0.0f : p.weight_f32 ? static_cast<const float*>(p.weight)[late]
+                                                      : to_f(static_cast<const T*>(p.weight)[late]);
   const RowRule rule = rule_of(p);
   const float given = p.scale ? __ldg(p.scale) : 0.0f;
   bool ok = true;
@@ -395,27 +512,83 @@ norm_quant_ring_kernel(const NormParams p, const Ring ring) {
     const unsigned char* in = dyn + s * stage_bytes;
     T* ho = p.residual_out ? static_cast<T*>(p.residual_out) + row * p.ldo : nullptr;
     f2 hw[IT][NP], sq = 0ull;
-    float mx = 0.0f;
-#pragma unroll
-    for (int i = 0; i < IT; ++i) {
-      const Columns<T, EDGES> c(i * nt + t, off, p.H);
-      if (!c.any()) continue;
-      read_pairs(in + (i * nt + t) * 16, c, hw[i]);
+    float mx = 0.0f, late_hw = 0.0f;
+    // vector v of the row as h = x + residual
+    auto read_h = [&](int v, const Columns<T, EDGES>& c, f2 (&h)[NP]) {
+      read_pairs(in + v * 16, c, h);
       if (inputs == 2) {
         f2 r[NP];
-        read_pairs(in + ring.pitch + (i * nt + t) * 16, c, r);
+        read_pairs(in + ring.pitch + v * 16, c, r);
 #pragma unroll
-        for (int j = 0; j < NP; ++j) hw[i][j] = add2(hw[i][j], r[j]);
+        for (int j = 0; j < NP; ++j) h[j] = add2(h[j], r[j]);
       }
-      if (ho) write_pairs(ho, c, hw[i]);
+    };
+    // of the vectors after the warp's last ones, a slot a lane: the sums of the columns of the blocks before them
+    f2 next = 0ull;
+    if (EDGES && off != 0 && lane < IT) {
+      const int v = lane * nt + (t & ~31) + 32;
+      const Columns<T, EDGES> c(v, off, p.H);
+      if (c.any()) {
+        const int most = off < c.hi ? off : c.hi;
+        float x[VEC], r[VEC];
+        load_f<T, VEC>(reinterpret_cast<const T*>(in + v * 16), x);
+        if (inputs == 2) load_f<T, VEC>(reinterpret_cast<const T*>(in + ring.pitch + v * 16), r);
+        f2 h[NP];
+#pragma unroll
+        for (int j = 0; j < VEC; j += 2) {
+          if (inputs == 2) {
+            x[j] += r[j];
+            x[j + 1] += r[j + 1];
+          }
+          h[j / 2] = pair(j < most ? x[j] : 0.0f, j + 1 < most ? x[j + 1] : 0.0f);
+        }
+        next = add_squares(h, 0ull);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < IT; ++i) {
+      const int v = i * nt + t;
+      const Columns<T, EDGES> c(v, off, p.H);
+      if (!EDGES && !c.any()) continue;
+      if (c.any()) read_h(v, c, hw[i]);
+      if constexpr (EDGES) {
+        if (!c.any()) {
+#pragma unroll
+          for (int j = 0; j < NP; ++j) hw[i][j] = 0ull;
+        }
+      }
+      if (!EDGES || off == 0) {
+        sq = add2(sq, add_squares(hw[i], 0ull));
+      } else {
+        // This vector holds the last off columns of the block before and the first ones of its own: the former's
+        // sum goes to the lane before, which goes on with it.
+        f2 mine[NP];
+#pragma unroll
+        for (int j = 0; j < NP; ++j) mine[j] = mul2(hw[i][j], tail[j]);
+        f2 after = __shfl_down_sync(0xFFFFFFFFu, add_squares(mine, 0ull), 1);
+        const f2 from_next = __shfl_sync(0xFFFFFFFFu, next, i);
+        if (lane == 31) after = from_next;
+#pragma unroll
+        for (int j = 0; j < NP; ++j) mine[j] = fma2(mine[j], pair(-1.0f, -1.0f), hw[i][j]);
+        sq = add2(sq, add_squares(mine, after));
+        if (!c.any()) continue;
+      }
+      if (ho && c.any()) write_pairs(ho, c, hw[i]);
 #pragma unroll
       for (int j = 0; j < NP; ++j) {
-        sq = fma2(hw[i][j], hw[i][j], sq);
         hw[i][j] = mul2(hw[i][j], w[i][j]);
         float a, b;
         halves(hw[i][j], a, b);
         mx = max_nan(mx, max_nan(fabsf(a), fabsf(b)));
       }
+    }
+    if (has_late) {
+      const T* from = reinterpret_cast<const T*>(in + IT * nt * 16) + t;
+      float h = to_f(*from);
+      if (inputs == 2) h += to_f(*reinterpret_cast<const T*>(reinterpret_cast<const unsigned char*>(from) + ring.pitch));
+      if (ho) ho[late] = from_f<T>(h);
+      late_hw = h * late_w;
+      mx = max_nan(mx, fabsf(late_hw));
     }
     float s0, s1;
     halves(sq, s0, s1);
@@ -462,6 +635,7 @@ norm_quant_ring_kernel(const NormParams p, const Ring ring) {
           if (j >= c.lo && j < c.hi) q[c.first + j] = (uint8_t)code_pair(v[j], 0.0f, p.q_format);
       }
     }
+    if (has_late) q[late] = (uint8_t)code_pair(late_hw * fa * fb, 0.0f, p.q_format);
   }
   if (!ok && t == 0) {                                      // a copy that never came: wait for the others, then end
     atomicExch(&g_norm_status, 1);
@@ -486,17 +660,17 @@ Ring ring_for(int64_t H, size_t es, bool aligned16, int inputs, int most, int* r
   *resident = n;
   return r;
 }
-int threads_for(int n, int it) { return ((n + it - 1) / it + 31) / 32 * 32; }
 
-template <class T, int IT, int MAXT, int MINB>
+// MINB and EDGEB: the CTAs of MAXT threads that registers let live on an SM, of aligned rows and of others
+template <class T, int IT, int MAXT, int MINB, int EDGEB>
 int launch_norm_ring(const NormParams& p, int threads, bool aligned16, bool q_vec, cudaStream_t st) {
-  auto kernel = aligned16 ? norm_quant_ring_kernel<T, IT, MAXT, MINB, false> : norm_quant_ring_kernel<T, IT, MAXT, MINB, true>;
+  auto kernel = aligned16 ? norm_quant_ring_kernel<T, IT, MAXT, MINB, false> : norm_quant_ring_kernel<T, IT, MAXT, EDGEB, true>;
   static std::atomic<bool> flags[2][64];
   std::atomic<bool>* done = flags[aligned16];
   if (!emu_ops_allow_smem(reinterpret_cast<const void*>(kernel), kMaxSmem - 1024, done))
     return emu_ops_launched("cudaFuncSetAttribute");
   int resident;
-  Ring ring = ring_for(p.H, sizeof(T), aligned16, p.residual ? 2 : 1, MAXT * MINB / threads, &resident);
+  Ring ring = ring_for(p.H, sizeof(T), aligned16, p.residual ? 2 : 1, MAXT * (aligned16 ? MINB : EDGEB) / threads, &resident);
   ring.q_vec = q_vec;
   const int64_t most = (int64_t)emu_ops_sm_count() * resident;
   int64_t ctas = p.T < most ? p.T : most;
@@ -508,32 +682,36 @@ int launch_norm_ring(const NormParams& p, int threads, bool aligned16, bool q_ve
 // A row's step has a fixed part for each warp (reduction, barrier, scale), so rows take few threads of
 // many vectors: 8192 x 5760 bf16 in 52.7 us with four vectors a thread, 54.5 with two.  (Few rows would be
 // done a little sooner by more threads, 64 x 5760 in 3.6 us with two vectors, 4.0 with four; but the
-// choice goes by the row's length alone, so that a row's codes do not depend on the rows beside it.)
+// split goes by the row's length alone, so that a row's codes do not depend on the rows beside it.)
 template <class T> int pick_norm(const NormParams& p, bool alike, bool aligned16, bool q_vec, cudaStream_t st) {
   constexpr int V = 16 / sizeof(T);
-  const int nv = aligned16 ? p.H / V : (p.H + 2 * V - 2) / V;       // vectors that a row can touch
+  const int nv = (p.H + V - 1) / V;
+  const Split sp = split_of<T>(p.H);
   // Short rows: a warp a row, straight from memory, by vectors or by elements; a ring's barriers and copies
-  // would cost more than such a row.  So, and by the ring, bf16 with a residual: 100000 x 64 31 us and 62,
-  // 100000 x 512 64 and 78, 50000 x 768 49 and 59, but 50000 x 1024 63 and 60; 100000 x 91 30 and 90,
-  // 100000 x 255 50 and 108.
+  // would cost more than such a row.  So, and by the ring, bf16 with a residual: 100000 x 64 32 us and 62,
+  // 100000 x 512 61 and 78, 50000 x 768 47 and 59, but 50000 x 1024 63 and 61; 100000 x 91 28 and 90,
+  // 100000 x 255 50 and 108 (the ring's when it added unaligned rows by address, which was faster than now).
   if (aligned16 && nv <= 96) {
-    if (nv <= 32) launch_norm<T, V, 32, 1>(p, st);
-    else if (nv <= 64) launch_norm<T, V, 32, 2>(p, st);
-    else launch_norm<T, V, 32, 3>(p, st);
+    if (nv <= 32) launch_norm<T, true, 32, 1>(p, st);
+    else if (nv <= 64) launch_norm<T, true, 32, 2>(p, st);
+    else launch_norm<T, true, 32, 3>(p, st);                // split_of: 64 threads of two blocks; see sq above
     return EMU_OK;
   }
   if (!aligned16 && p.H <= 256) {
-    if (p.H <= 128) launch_norm<T, 1, 32, 4>(p, st);
-    else launch_norm<T, 1, 32, 8>(p, st);
+    if (p.H <= 128) launch_norm<T, false, 32, 1, 4>(p, st);
+    else launch_norm<T, false, 32, (V < 8 ? 2 : 1)>(p, st);
     return EMU_OK;
   }
-  if (alike && nv <= 2048) {
-    if (nv <= 256) return launch_norm_ring<T, 2, 128, 8>(p, threads_for(nv, 2), aligned16, q_vec, st);
-    if (nv <= 1024) return launch_norm_ring<T, 4, 256, 2>(p, threads_for(nv, 4), aligned16, q_vec, st);
-    return launch_norm_ring<T, 4, 512, 1>(p, threads_for(nv, 4), aligned16, q_vec, st);
+  // By columns' blocks instead of by address, unaligned rows take longer: 8192 x 1111 bf16 24.4 us and 22.0,
+  // 8192 x 5761 81.6 and 65.8 (aligned 5760 52.9).
+  if (alike && sp.it > 0) {
+    if (nv <= 256) return launch_norm_ring<T, 2, 128, 8, 6>(p, sp.threads, aligned16, q_vec, st);
+    if (nv <= 1024) return launch_norm_ring<T, 4, 256, 2, 2>(p, sp.threads, aligned16, q_vec, st);
+    return launch_norm_ring<T, 4, 512, 1, 1>(p, sp.threads, aligned16, q_vec, st);
   }
-  if (aligned16 && alike) launch_norm<T, V, 512, 0>(p, st);
-  else launch_norm<T, 1, 512, 0>(p, st);
+  if (sp.it > 0) launch_norm<T, false, 512, 4>(p, st);
+  else if (aligned16) launch_norm<T, true, 512, 0>(p, st);
+  else launch_norm<T, false, 512, 0>(p, st);
   return EMU_OK;
 }
 

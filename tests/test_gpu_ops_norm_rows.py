@@ -77,3 +77,39 @@ def test_codes_are_nearer_than_step_by_step(fw):
             off["steps"] += int((codes_step_by_step(x, r, w, q, top, torch.float32) != want).sum())
             off["kernel"] += int((fw.rms_norm_quant(x, w, r, out_dtype=q).q.float() != want).sum())
     assert off["kernel"] <= 0.9 * off["steps"], off
+
+
+# short rows by vectors and by elements, the ring at each of its sizes (with rows that fill its threads to the last
+# column), and rows too long for it
+WIDTHS = [33, 91, 255, 256, 512, 640, 700, 768, 1111, 1920, 2047, 2048, 2049, 4096, 4099, 5761, 8192, 16384, 16385, 20481]
+
+
+@pytest.mark.parametrize("dt", DT)
+@pytest.mark.parametrize("H", WIDTHS)
+def test_a_row_is_the_same_wherever_it_stands(fw, H, dt):
+    g = torch.Generator(device=DEV).manual_seed(H)
+    T = 16
+    x, r = (torch.randn(T, H, generator=g, device=DEV).to(DT[dt]) for _ in range(2))
+    w = (1 + 0.3 * torch.randn(H, generator=g, device=DEV)).to(DT[dt])
+    want = fw.rms_norm_quant(x, w, r, out_dtype=torch.int8)
+    for turn in range(1, 9):                                 # every row at other places, eight apart and less
+        got = fw.rms_norm_quant(x.roll(turn, 0), w, r.roll(turn, 0), out_dtype=torch.int8)
+        assert torch.equal(got.q.roll(-turn, 0), want.q) and torch.equal(got.rstd.roll(-turn, 0), want.rstd)
+        assert torch.equal(got.scale.roll(-turn, 0), want.scale) and torch.equal(got.residual.roll(-turn, 0), want.residual)
+    for i in range(T):                                       # alone: a view into the batch, and a tensor of its own
+        assert same(want, fw.rms_norm_quant(x[i:i + 1], w, r[i:i + 1], out_dtype=torch.int8), slice(i, i + 1))
+        assert same(want, fw.rms_norm_quant(x[i:i + 1].clone(), w, r[i:i + 1].clone(), out_dtype=torch.int8), slice(i, i + 1))
+    ww = placed(w[None], 3, 1)[0]                            # the weight beside 16 bytes
+    for a, b in layouts((x, r)):
+        for wt in (w, ww):
+            got = fw.rms_norm_quant(a, wt, b, out_dtype=torch.int8)
+            assert same(got, want) and torch.equal(got.residual, want.residual)
+            got = fw.rms_norm_quant(a[3:4], wt, b[3:4], out_dtype=torch.int8)
+            assert same(want, got, slice(3, 4))
+    q = torch.empty(T * H + 5, dtype=torch.int8, device=DEV)[5:].view(T, H)      # codes beside 16 bytes
+    assert same(fw.rms_norm_quant(x, w, r, out_dtype=torch.int8, out=q), want)
+    alone = fw.rms_norm_quant(x, w, out_dtype=torch.float8_e4m3fn)               # without a residual
+    for a, _ in layouts((x, r)):
+        assert same(fw.rms_norm_quant(a, w, out_dtype=torch.float8_e4m3fn), alone)
+    big = x.repeat(60, 1)                                    # many rows
+    assert torch.equal(fw.rms_norm_quant(big, w, out_dtype=torch.float8_e4m3fn).q.view(torch.uint8)[-T:], alone.q.view(torch.uint8))
