@@ -100,7 +100,8 @@ __device__ __forceinline__ void load_weight(const P& p, int col, float (&w)[VEC]
 // fp32's only where y / scale is far above every code, or far below).
 struct RowRule {
   float inv_h, inv_qmax, qmax, eps;
-  __device__ __forceinline__ float rstd(float sum) const { return rsqrtf(fmaf(sum, inv_h, eps)); }
+  // NaN where the sum is none: rstd = 0 would make a row past fp32's range look like one of zeros
+  __device__ __forceinline__ float rstd(float sum) const { return sum < INFINITY ? rsqrtf(fmaf(sum, inv_h, eps)) : NAN; }
   __device__ __forceinline__ float scale(float mx, float rstd) const { return max_nan(mx * rstd * inv_qmax, kScaleMin); }
   __device__ __forceinline__ void factors(float mx, float rstd, float scale, bool given, float& a, float& b) const {
     const bool own = !given && scale > kScaleMin;            // not at its least, nor NaN

@@ -62,7 +62,10 @@ def rms_norm_quant(x: torch.Tensor, weight: torch.Tensor, residual: Optional[tor
     ``scaled_mm`` takes as scale_a); without it each row has its own, ``max|y| / qmax``
     but at least 2^-126 (what ``int8_scaled_mm`` takes as scale_a).  The returned
     ``residual`` is h rounded to x's dtype, in ``residual_out`` if given (it may be
-    ``residual`` or ``x``: updated in place); ``rstd`` is for ``rms_norm_backward``."""
+    ``residual`` or ``x``: updated in place); ``rstd`` is for ``rms_norm_backward``.
+
+    A row holding NaN or Inf, or whose sum of squares passes fp32's range (values of about
+    1e18 and more), has NaN for its rstd and its own scale, and codes of NaN (int8: 0)."""
     return RmsNormQuant._make(_calls().rms_norm_quant(x, weight, residual, eps, out_dtype, scale, out,
                                                        residual_out))
 

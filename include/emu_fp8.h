@@ -320,10 +320,10 @@ typedef enum { EMU_Q_E4M3FN = 0, EMU_Q_E5M2 = 1, EMU_Q_INT8 = 2 } emu_q_t;
  *   rstd          [T] fp32, for the gradient
  * Sums are fp32; y / scale is computed as (h * weight) * (rstd / scale), or with a row's own scale
  * (h * weight) * (qmax / max|h * weight|), and is within 2^-21 of its value before the rounding to
- * 8 bits.  |h * weight| has to stay within fp32's normal range (or be 0), and so has
- * a given scale.  A row holding NaN or Inf
- * gives NaN for its own scale and codes of NaN or 0 (a NaN becomes FP8's NaN, int8's 0),
- * and touches no other row.  Sizes: T < 2^31, 1 <= H <= 2^22.
+ * 8 bits.  |h * weight| has to stay within fp32's normal range (or be 0), and so has a given
+ * scale.  A row holding NaN or Inf, or whose sum of h^2 passes fp32's range (values of about 1e18
+ * and more), gives NaN for its rstd and its own scale and codes of NaN (FP8's NaN, int8's 0), and
+ * touches no other row.  Sizes: T < 2^31, 1 <= H <= 2^22.
  */
 int emu_rms_norm_quant(const void* x, int64_t ldx, const void* residual, int64_t ldr,
                        const void* weight, emu_out_t weight_type, emu_out_t type,

@@ -113,3 +113,28 @@ def test_a_row_is_the_same_wherever_it_stands(fw, H, dt):
         assert same(fw.rms_norm_quant(a, w, out_dtype=torch.float8_e4m3fn), alone)
     big = x.repeat(60, 1)                                    # many rows
     assert torch.equal(fw.rms_norm_quant(big, w, out_dtype=torch.float8_e4m3fn).q.view(torch.uint8)[-T:], alone.q.view(torch.uint8))
+
+
+@pytest.mark.parametrize("q", [torch.float8_e4m3fn, torch.float8_e5m2, torch.int8])
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("H", [64, 91, 255, 700, 1111, 1920, 4096, 20480, 20481])
+def test_rows_past_the_range_do_not_look_like_zeros(fw, H, dt, q):
+    """Finite values whose squares add up to more than fp32 holds, or rows with an infinity: NaN, not codes of 0."""
+    g = torch.Generator(device=DEV).manual_seed(H)
+    x = torch.randn(9, H, generator=g, device=DEV).to(DT[dt])
+    w = (1 + 0.3 * torch.randn(H, generator=g, device=DEV)).to(DT[dt])
+    clean = {s: fw.rms_norm_quant(x, w, out_dtype=q, scale=s) for s in (None, torch.full((1,), 0.03, device=DEV))}
+    x[2] *= 1e20
+    x[5, H // 2] = 3e19
+    x[7, H - 1] = float("inf")
+    x[8] *= 1e15                                             # large, but within the range
+    for a in (x, placed(x, 8, 3), placed(x, 5, 1)):
+        for scale, want in clean.items():
+            got = fw.rms_norm_quant(a, w, out_dtype=q, scale=scale)
+            codes = got.q.float()
+            for i in (2, 5, 7):
+                assert bool(got.rstd[i].isnan()) and bool((codes[i] == 0).all() if q == torch.int8 else codes[i].isnan().all())
+                assert scale is not None or bool(got.scale[i].isnan())
+            for i in (0, 1, 3, 4, 6):
+                assert torch.equal(got.q.view(torch.uint8)[i], want.q.view(torch.uint8)[i]) and got.rstd[i] == want.rstd[i]
+            assert bool(torch.isfinite(got.rstd[8])) and bool(codes[8].any()) and bool(torch.isfinite(codes[8]).all())
