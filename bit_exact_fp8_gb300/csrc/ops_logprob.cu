@@ -695,7 +695,8 @@ logprob_grad_kernel(const LogprobGradParams p, uint32_t parts, bool same) {
   const float m = p.stats[r * 3], logz = p.stats[r * 3 + 1], H = p.stats[r * 3 + 2];
   const int64_t tok = p.tokens[r];
   const bool out_of_range = tok != p.ignore && (tok < 0 || tok >= p.V);
-  const float gl = tok == p.ignore || !p.g_logprob ? 0.0f : out_of_range ? NAN : p.g_logprob[r];
+  // out of range is an error of the caller's: NaN, even where nothing of the logprob's gradient is asked for
+  const float gl = out_of_range ? NAN : tok == p.ignore || !p.g_logprob ? 0.0f : p.g_logprob[r];
   const float ge = p.g_entropy ? p.g_entropy[r] : 0.0f;
   const bool empty = m == -INFINITY && logz == -INFINITY;
   const int hot = !empty && tok >= 0 && tok < p.V ? (int)tok : -1;
@@ -722,7 +723,7 @@ logprob_grad_kernel(const LogprobGradParams p, uint32_t parts, bool same) {
     if (empty) {
       asm volatile("");                                  // branches: few rows and vectors take them
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) f[j] = 0.0f;
+      for (int j = 0; j < VEC; ++j) f[j] = out_of_range ? NAN : 0.0f;
     }
     if ((uint32_t)(hot - id0) < (uint32_t)VEC && hot >= 0) {
       asm volatile("");

@@ -105,7 +105,8 @@ def token_logprobs(logits: torch.Tensor, tokens: torch.Tensor, *, top_k: int = 0
 
     A token equal to ignore_index has logprob 0; any other token outside [0, V) has NaN.
     -inf logits have probability 0.  A row of nothing but -inf has entropy 0 and -inf
-    otherwise; a row holding NaN or +inf has NaN, and ids of -1."""
+    otherwise; a row holding NaN or +inf has NaN, and ids of -1 (an ignored token's logprob
+    is 0 there too)."""
     return TokenLogprobs._make(_calls().token_logprobs(logits, tokens, top_k, ignore_index))
 
 
@@ -113,6 +114,7 @@ def token_logprobs_backward(logits: torch.Tensor, tokens: torch.Tensor, stats: t
                             grad_logprob: Optional[torch.Tensor], grad_entropy: Optional[torch.Tensor] = None, *,
                             ignore_index: int = -100, out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """Gradient of ``token_logprobs``' logprob and entropy by the logits, of their dtype;
-    ``stats`` is what it returned.  ``out`` may be the logits themselves: the gradient then
+    ``stats`` is what it returned.  Rows of tokens outside [0, V) that are not ignored get NaN,
+    whatever else holds of them; rows of nothing but -inf zeros.  ``out`` may be the logits themselves: the gradient then
     takes their place."""
     return _calls().token_logprobs_backward(logits, tokens, stats, grad_logprob, grad_entropy, ignore_index, out)

@@ -376,7 +376,8 @@ int emu_int8_scaled_mm(const int8_t* A, int64_t lda, const int8_t* B, int64_t ld
  * all fp32, ids int64; 0 <= top_k <= 32 (and <= V).  tokens: int64; a token equal to
  * ignore_index has logprob 0, any other one outside [0, V) has NaN.  -inf logits have
  * probability 0.  A row of nothing but -inf has lse, logprob and top_logprobs -inf and
- * entropy 0; a row holding NaN or +inf has NaN for all of them and -1 for its ids.
+ * entropy 0; a row holding NaN or +inf has NaN for all of them (an ignored token's logprob is 0
+ * there too) and -1 for its ids.
  */
 int emu_token_logprobs(const void* logits, int64_t ldx, emu_out_t type, const int64_t* tokens,
                        int64_t T, int64_t V, int32_t top_k, int64_t ignore_index, float* logprob,
@@ -387,8 +388,8 @@ int emu_token_logprobs(const void* logits, int64_t ldx, emu_out_t type, const in
  * Gradient of the above by the logits, of their type, rows ldo apart:
  *   grad_logits = grad_logprob ([v = token] - p) - grad_entropy p (log p + entropy)
  * grad_logprob and grad_entropy [T] fp32 (either may be NULL: zero); stats as the forward
- * call gave them.  Rows of ignored tokens get
- * the entropy's part alone, empty rows zeros, rows of tokens outside [0, V) NaN.
+ * call gave them.  Rows of tokens outside [0, V) that are not ignored get NaN (empty rows, and
+ * without a grad_logprob, too), rows of ignored tokens the entropy's part alone, empty rows zeros.
  * grad_logits may be the logits themselves, and may not overlap them otherwise.
  */
 int emu_token_logprobs_backward(const void* logits, int64_t ldx, emu_out_t type,
