@@ -6,6 +6,7 @@
 
 #include <ATen/ATen.h>
 #include <ATen/cuda/EmptyTensor.h>
+#include <c10/core/AutogradState.h>
 #include <c10/core/GradMode.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
@@ -63,9 +64,16 @@ emu_out_t float_type(c10::ScalarType t, const char* name) {
   if (t == at::kHalf) return EMU_OUT_F16;
   bad(std::string(name) + ": fp32, bf16 or fp16 expected, got " + text(t));
 }
+// No floating input takes part in autograd: neither one that it records the calls of, nor one with a tangent
 void no_grad(const at::Tensor& t) {
   if (c10::GradMode::is_enabled() && t.requires_grad())
     unsupported("not differentiable by autograd: an input requires grad under grad mode (call the _backward function)");
+  if (c10::AutogradState::get_tls_state().get_fw_grad_mode() && t._fw_grad(0).defined())
+    unsupported("not differentiable by autograd: an input carries a forward-mode tangent");
+}
+// An output of the caller's: autograd learns that its values are others now, as of any write in place.
+void written(const at::Tensor& t) {
+  if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
 }
 // the row stride of [rows, cols] values whose rows are contiguous
 int64_t rows_of(const at::Tensor& t, const char* name, int64_t rows, int64_t cols, c10::ScalarType type, c10::Device dev) {
@@ -90,6 +98,7 @@ at::Tensor make(at::IntArrayRef sizes, c10::ScalarType type, c10::Device dev) {
 }
 at::Tensor given(PyObject* o, const char* name, int64_t rows, int64_t cols, c10::ScalarType type, c10::Device dev) {
   const at::Tensor& t = tensor(o, name);
+  no_grad(t);
   if (t.dim() != 2 || t.size(0) != rows || t.size(1) != cols || t.scalar_type() != type || !t.is_contiguous() ||
       t.device() != dev)
     bad(std::string(name) + " must be a contiguous " + text(type) + " (" + std::to_string(rows) + ", " +
@@ -153,10 +162,12 @@ PyObject* norm_quant(PyObject* const* a) {
   const void* rp = nullptr;
   void* op = nullptr;
   int64_t ldr = 0, ldo = 0;
-  at::Tensor made;
+  at::Tensor made, place;
   PyObject* h = a[0];
   if (a[7] != Py_None) {
-    const at::Tensor& o = tensor(a[7], "residual_out");
+    place = tensor(a[7], "residual_out");
+    const at::Tensor& o = place;
+    no_grad(o);
     ldo = rows_of(o, "residual_out", T, H, type, dev);
     op = o.data_ptr();
     h = a[7];
@@ -178,13 +189,17 @@ PyObject* norm_quant(PyObject* const* a) {
   const float* sp = nullptr;
   float* so = nullptr;
   if (a[5] != Py_None) {
-    sp = static_cast<const float*>(vector_of(tensor(a[5], "scale"), "scale", 1, at::kFloat, dev));
+    const at::Tensor& scale = tensor(a[5], "scale");
+    no_grad(scale);
+    sp = static_cast<const float*>(vector_of(scale, "scale", 1, at::kFloat, dev));
   } else {
     scales = make({T}, at::kFloat, dev);
     so = scales.data_ptr<float>();
   }
   check(emu_rms_norm_quant(x.data_ptr(), ldx, rp, ldr, wp, wt == at::kFloat ? EMU_OUT_F32 : ct, ct, T, H, (float)eps, sp,
                            fmt, q.data_ptr(), so, op, ldo, rstd.data_ptr<float>(), on.stream), "rms_norm_quant");
+  if (place.defined()) written(place);
+  if (a[6] != Py_None) written(q);
   return tuple_of({a[6] == Py_None ? THPVariable_Wrap(q) : same(a[6]), sp ? same(a[5]) : THPVariable_Wrap(scales),
                    made.defined() ? THPVariable_Wrap(made) : same(h), THPVariable_Wrap(rstd)});
 }
@@ -204,7 +219,9 @@ PyObject* norm_backward(PyObject* const* a) {
   const int64_t ldh = rows_of(h, "hidden", T, H, type, dev), ldy = rows_of(gy, "grad_y", T, H, type, dev);
   if (wt != type && wt != at::kFloat) bad("weight: hidden's dtype or fp32 expected, got " + text(wt));
   void* wp = vector_of(weight, "weight", H, wt, dev);
-  const float* rp = static_cast<const float*>(vector_of(tensor(a[2], "rstd"), "rstd", T, at::kFloat, dev));
+  const at::Tensor& rstd = tensor(a[2], "rstd");
+  no_grad(rstd);
+  const float* rp = static_cast<const float*>(vector_of(rstd, "rstd", T, at::kFloat, dev));
   const void* gp = nullptr;
   int64_t ldg = 0;
   if (a[4] != Py_None) {
@@ -245,6 +262,8 @@ PyObject* int8_mm(PyObject* const* a) {
   if (ot != at::kFloat && ot != at::kBFloat16 && ot != at::kHalf) unsupported("out_dtype " + text(ot) + " is not supported");
   const at::Tensor& sa = tensor(a[2], "scale_a");
   const at::Tensor& sb = tensor(a[3], "scale_b");
+  no_grad(sa);
+  no_grad(sb);
   const int64_t na = sa.numel(), nb = sb.numel();
   if (na != 1 && na != M) bad("scale_a: one value or " + std::to_string(M) + " expected, got " + std::to_string(na));
   if (nb != 1 && nb != N) bad("scale_b: one value or " + std::to_string(N) + " expected, got " + std::to_string(nb));
@@ -265,6 +284,7 @@ PyObject* int8_mm(PyObject* const* a) {
   check(emu_int8_scaled_mm(A, lda, B, ldb, M, N, K, pa, na, pb, nb, out.data_ptr(),
                            ot == at::kFloat ? EMU_OUT_F32 : ot == at::kBFloat16 ? EMU_OUT_BF16 : EMU_OUT_F16,
                            need ? ws.data_ptr() : nullptr, need, on.stream), "int8_scaled_mm");
+  if (a[5] != Py_None) written(out);
   return a[5] == Py_None ? THPVariable_Wrap(out) : same(a[5]);
 }
 
@@ -299,15 +319,21 @@ PyObject* logprobs_backward(PyObject* const* a) {
   const emu_out_t ct = float_type(type, "logits");
   const int64_t ldx = rows_of(x, "logits", T, V, type, dev);
   const int64_t* tok = static_cast<const int64_t*>(vector_of(tensor(a[1], "tokens"), "tokens", T, at::kLong, dev));
-  const float* st = static_cast<const float*>(vector_of(tensor(a[2], "stats"), "stats", 3 * T, at::kFloat, dev));
-  const float *gl = nullptr, *ge = nullptr;
-  if (a[3] != Py_None) gl = static_cast<const float*>(vector_of(tensor(a[3], "grad_logprob"), "grad_logprob", T, at::kFloat, dev));
-  if (a[4] != Py_None) ge = static_cast<const float*>(vector_of(tensor(a[4], "grad_entropy"), "grad_entropy", T, at::kFloat, dev));
+  auto values = [&](PyObject* o, const char* name, int64_t count) -> const float* {
+    const at::Tensor& t = tensor(o, name);
+    no_grad(t);
+    return static_cast<const float*>(vector_of(t, name, count, at::kFloat, dev));
+  };
+  const float* st = values(a[2], "stats", 3 * T);
+  const float* gl = a[3] == Py_None ? nullptr : values(a[3], "grad_logprob", T);
+  const float* ge = a[4] == Py_None ? nullptr : values(a[4], "grad_entropy", T);
   On on(dev);
   const at::Tensor gx = a[6] == Py_None ? make({T, V}, type, dev) : tensor(a[6], "out");
+  no_grad(gx);
   const int64_t ldo = rows_of(gx, "out", T, V, type, dev);
   check(emu_token_logprobs_backward(x.data_ptr(), ldx, ct, tok, T, V, ignore, st, gl, ge, gx.data_ptr(), ldo, on.stream),
         "token_logprobs_backward");
+  if (a[6] != Py_None) written(gx);
   return a[6] == Py_None ? THPVariable_Wrap(gx) : same(a[6]);
 }
 

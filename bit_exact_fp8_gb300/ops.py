@@ -4,7 +4,9 @@ and an 8-bit output (``rms_norm_quant``), the product of 8-bit integers
 with the gradients that training needs.  They follow ``scaled_mm``: PyTorch provides
 device memory and the stream, the work runs in libemufp8's CUDA kernels on the current
 stream, and there is no CPU path.  They take no part in autograd: a training step calls
-the ``_backward`` functions itself.
+the ``_backward`` functions itself, and an input or output that requires grad under grad mode,
+or carries a forward-mode tangent, is refused.  Writing into a tensor that was given
+counts as a write in place.
 """
 from __future__ import annotations
 
