@@ -10,6 +10,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
+#include <initializer_list>
 
 // host side (ops_norm.cu): records the message emu_ops_last_error returns; gives `code`
 int emu_ops_fail(int code, const char* fmt, ...) __attribute__((format(printf, 2, 3)));
@@ -33,8 +34,18 @@ struct Span {
       : lo(reinterpret_cast<uintptr_t>(p)), hi(lo) {
     if (p && rows > 0 && cols > 0) hi = lo + ((size_t)(rows - 1) * (size_t)ld + (size_t)cols) * esz;
   }
-  bool meets(const Span& o) const { return lo < o.hi && o.lo < hi; }
+  bool meets(const Span& o) const { return lo < hi && o.lo < o.hi && lo < o.hi && o.lo < hi; }
 };
+// do all of `outs` lie apart, from each other and from all of `ins`
+inline bool apart(std::initializer_list<Span> outs, std::initializer_list<Span> ins) {
+  for (const Span* o = outs.begin(); o != outs.end(); ++o) {
+    for (const Span* p = o + 1; p != outs.end(); ++p)
+      if (o->meets(*p)) return false;
+    for (const Span& i : ins)
+      if (o->meets(i)) return false;
+  }
+  return true;
+}
 
 __device__ __forceinline__ float to_f(float v) { return v; }
 __device__ __forceinline__ float to_f(__nv_bfloat16 v) { return __bfloat162float(v); }

@@ -445,6 +445,10 @@ int emu_int8_scaled_mm(const int8_t* A, int64_t lda, const int8_t* B, int64_t ld
   const size_t need = emu_int8_workspace_bytes(M, N, K);
   if (need > 0 && (!workspace || workspace_bytes < need || !aligned(workspace, 256)))
     return emu_ops_fail(EMU_EINVAL, "workspace of %zu bytes needed, 256-byte aligned (got %zu)", need, workspace_bytes);
+  if (!apart({Span(out, M, N, N, es), Span(need ? workspace : nullptr, 1, 1, 1, need)},
+             {Span(A, M, lda, K, 1), Span(B, N, ldb, K, 1), Span(scale_a, 1, scale_a_count, scale_a_count, 4),
+              Span(scale_b, 1, scale_b_count, scale_b_count, 4)}))
+    return emu_ops_fail(EMU_EINVAL, "the output or the workspace overlaps an input, or the other");
   Int8Params p;
   p.a = A; p.lda = lda; p.b = B; p.ldb = ldb;
   p.a_end = reinterpret_cast<uintptr_t>(A) + (size_t)(M - 1) * (size_t)lda + (size_t)K;

@@ -798,6 +798,10 @@ int emu_token_logprobs(const void* logits, int64_t ldx, emu_out_t type, const in
       !aligned(top_logprobs, 4) ||
       !aligned(top_ids, 8))
     return emu_ops_fail(EMU_EINVAL, "an output is not aligned to its elements");
+  if (!apart({Span(logprob, 1, T, T, 4), Span(entropy, 1, T, T, 4), Span(lse, 1, T, T, 4), Span(stats, T, 3, 3, 4),
+              Span(top_logprobs, T, top_k, top_k, 4), Span(top_ids, T, top_k, top_k, 8)},
+             {Span(logits, T, ldx, V, elem_bytes(type)), Span(tokens, 1, T, T, 8)}))
+    return emu_ops_fail(EMU_EINVAL, "an output overlaps an input or another output");
   LogprobParams p;
   p.x = logits; p.ldx = ldx; p.tokens = tokens; p.ignore = ignore_index;
   p.T = T; p.V = (int)V; p.k = top_k;
@@ -821,8 +825,12 @@ int emu_token_logprobs_backward(const void* logits, int64_t ldx, emu_out_t type,
   const size_t es = elem_bytes(type);
   if (!aligned(grad_logits, es) || !aligned(stats, 4) || !aligned(grad_logprob, 4) || !aligned(grad_entropy, 4))
     return emu_ops_fail(EMU_EINVAL, "a tensor is not aligned to its elements");
-  if (Span(grad_logits, T, ldo, V, es).meets(Span(logits, T, ldx, V, es)) && !(grad_logits == logits && ldo == ldx))
+  const Span g(grad_logits, T, ldo, V, es);
+  if (g.meets(Span(logits, T, ldx, V, es)) && !(grad_logits == logits && ldo == ldx))
     return emu_ops_fail(EMU_EINVAL, "grad_logits overlaps the logits without being them");
+  if (!apart({g}, {Span(tokens, 1, T, T, 8), Span(stats, T, 3, 3, 4), Span(grad_logprob, 1, T, T, 4),
+                   Span(grad_entropy, 1, T, T, 4)}))
+    return emu_ops_fail(EMU_EINVAL, "grad_logits overlaps another input");
   LogprobGradParams p;
   p.x = logits; p.ldx = ldx; p.tokens = tokens; p.ignore = ignore_index; p.T = T; p.V = (int)V;
   p.stats = stats; p.g_logprob = grad_logprob; p.g_entropy = grad_entropy;

@@ -1226,13 +1226,14 @@ int emu_rms_norm_quant(const void* x, int64_t ldx, const void* residual, int64_t
     if (!aligned(b, es)) return emu_ops_fail(EMU_EINVAL, "a tensor is not aligned to its elements");
   if (!aligned(weight, elem_bytes(weight_type)) || !aligned(rstd, 4) || !aligned(scale, 4) || !aligned(scale_out, 4))
     return emu_ops_fail(EMU_EINVAL, "a tensor is not aligned to its elements");
-  if (residual_out) {
-    // an output row may replace its input row, and may not meet any other
-    const Span o(residual_out, T, ldo, H, es);
-    if ((o.meets(Span(x, T, ldx, H, es)) && !(residual_out == x && ldo == ldx)) ||
-        (residual && o.meets(Span(residual, T, ldr, H, es)) && !(residual_out == residual && ldo == ldr)))
-      return emu_ops_fail(EMU_EINVAL, "residual_out overlaps an input without being that input");
-  }
+  const Span sx(x, T, ldx, H, es), sr(residual, T, ldr, H, es), so(residual_out, T, ldo, H, es);
+  const Span sw(weight, 1, H, H, elem_bytes(weight_type)), ss(scale, 1, 1, 1, 4);
+  // an output row may replace its input row, and may not meet any other
+  if ((so.meets(sx) && !(residual_out == x && ldo == ldx)) || (so.meets(sr) && !(residual_out == residual && ldo == ldr)))
+    return emu_ops_fail(EMU_EINVAL, "residual_out overlaps an input without being that input");
+  if (!apart({so}, {sw, ss}) ||
+      !apart({Span(q, T, H, H, 1), Span(rstd, 1, T, T, 4), Span(scale ? nullptr : scale_out, 1, T, T, 4)}, {sx, sr, so, sw, ss}))
+    return emu_ops_fail(EMU_EINVAL, "an output overlaps an input or another output");
   NormParams p;
   p.x = x; p.ldx = ldx;
   p.residual = residual; p.ldr = ldr;
@@ -1287,13 +1288,13 @@ int emu_rms_norm_backward(const void* grad_y, int64_t ldy, const void* hidden, i
   if (!aligned(grad_y, es) || !aligned(hidden, es) || !aligned(grad_residual, es) || !aligned(grad_x, es) ||
       !aligned(weight, elem_bytes(weight_type)) || !aligned(rstd, 4))
     return emu_ops_fail(EMU_EINVAL, "a tensor is not aligned to its elements");
-  const Span o(grad_x, T, H, H, es);
-  if (o.meets(Span(grad_y, T, ldy, H, es)) || o.meets(Span(hidden, T, ldh, H, es)) ||
-      (grad_residual && o.meets(Span(grad_residual, T, ldg, H, es))))
-    return emu_ops_fail(EMU_EINVAL, "grad_x overlaps an input");
   const size_t need = emu_rms_norm_backward_workspace_bytes(T, H);
   if (!workspace || workspace_bytes < need || !aligned(workspace, 16))
     return emu_ops_fail(EMU_EINVAL, "workspace of %zu bytes needed, 16-byte aligned (got %zu)", need, workspace_bytes);
+  if (!apart({Span(grad_x, T, H, H, es), Span(grad_weight, 1, H, H, 4), Span(workspace, 1, 1, 1, need)},
+             {Span(grad_y, T, ldy, H, es), Span(hidden, T, ldh, H, es), Span(grad_residual, T, ldg, H, es),
+              Span(rstd, 1, T, T, 4), Span(weight, 1, H, H, elem_bytes(weight_type))}))
+    return emu_ops_fail(EMU_EINVAL, "an output or the workspace overlaps an input, or another of them");
   NormGradParams p;
   p.gy = grad_y; p.ldy = ldy; p.h = hidden; p.ldh = ldh; p.gh = grad_residual; p.ldg = ldg;
   p.weight = weight; p.weight_f32 = weight_type == EMU_OUT_F32; p.rstd = rstd;

@@ -298,7 +298,8 @@ int emu_tc_selftest(uint32_t* mismatches);
  * depend on what outputs and workspaces held before, and a call may be captured in a CUDA
  * graph.  All results are the same from run to run.  Errors leave their message in
  * emu_ops_last_error.  Tensors are row-major with the given row strides (in elements);
- * any alignment of whole elements is accepted, 16-byte alignment of rows is faster.
+ * any alignment of whole elements is accepted, 16-byte alignment of rows is faster.  Outputs
+ * and workspaces may not overlap inputs or one another (EMU_EINVAL), but where a call says so.
  */
 
 /* 8-bit formats of a quantised output: the two FP8 formats, and signed integers. */
