@@ -75,15 +75,9 @@ def ops_commands(out: str) -> "tuple[list, list]":
 
 def build(force: bool = False, verbose: bool = False) -> str:
     """Compile whichever of the two libraries and the operators' extension is stale; returns the
-    GEMM library's path."""
+    GEMM library's path.  Each is put in place as soon as it is made, whatever becomes of the
+    others (the libraries need nvcc alone); what could not be made is raised at the end."""
     jobs = []
-    ops_tmp = OPS_LIB + f".tmp{os.getpid()}"
-    ops_stale = force or not _up_to_date(OPS_LIB, OPS_DEPS)
-    if ops_stale:
-        ops_compile, ops_link = ops_commands(ops_tmp)
-        if verbose:
-            print(" ".join(ops_compile), file=sys.stderr)
-        ops_proc = subprocess.Popen(ops_compile)
     for lib, srcs, deps in ((LIB, SOURCES, DEPS), (PEAKS_LIB, PEAKS_SOURCES, PEAKS_DEPS)):
         if force or not _up_to_date(lib, deps):
             tmp = lib + f".tmp{os.getpid()}"
@@ -91,17 +85,30 @@ def build(force: bool = False, verbose: bool = False) -> str:
             if verbose:
                 print(" ".join(cmd), file=sys.stderr)
             jobs.append((lib, tmp, subprocess.Popen(cmd)))
-    failed = [lib for lib, _, proc in jobs if proc.wait() != 0]
-    if ops_stale and ops_proc.wait() != 0:
-        failed.append(OPS_LIB)
+    failed, ops_proc = [], None
+    ops_tmp = OPS_LIB + f".tmp{os.getpid()}"
+    if force or not _up_to_date(OPS_LIB, OPS_DEPS):
+        try:
+            ops_compile, ops_link = ops_commands(ops_tmp)
+            if verbose:
+                print(" ".join(ops_compile), file=sys.stderr)
+            ops_proc = subprocess.Popen(ops_compile)
+        except (ImportError, OSError) as e:                  # no torch, or no host compiler
+            failed.append(f"{OPS_LIB}: {e}")
+    for lib, tmp, proc in jobs:
+        if proc.wait() == 0:
+            os.replace(tmp, lib)
+        else:
+            failed.append(lib)
+    if ops_proc is not None:
+        if ops_proc.wait() == 0 and os.path.exists(LIB) and subprocess.run(ops_link).returncode == 0:
+            os.replace(ops_tmp, OPS_LIB)
+        else:
+            failed.append(OPS_LIB)
+        if os.path.exists(ops_tmp + ".o"):
+            os.remove(ops_tmp + ".o")
     if failed:
         raise subprocess.CalledProcessError(1, f"nvcc or g++ ({', '.join(failed)})")
-    for lib, tmp, _ in jobs:
-        os.replace(tmp, lib)
-    if ops_stale:
-        subprocess.run(ops_link, check=True)
-        os.replace(ops_tmp, OPS_LIB)
-        os.remove(ops_tmp + ".o")
     return LIB
 
 
