@@ -9,7 +9,7 @@ import importlib.machinery
 import importlib.util
 import os
 
-from .build import LIB, OPS_LIB
+from .build import LIB, OPS_LIB, built_for, ops_built_for
 
 EMU_OK = 0
 EMU_EINVAL = -1
@@ -132,11 +132,16 @@ def load(path: str = LIB) -> ctypes.CDLL:
 
 def load_ops(path: str = OPS_LIB):
     """The extension module of the operators' torch-facing calls (ops_torch.cpp), beside the
-    libemufp8 it is linked to; raises OSError if it has not been built."""
+    libemufp8 it is linked to; raises OSError if it has not been built, or for another torch or
+    Python than this."""
     load()
     if not os.path.exists(path):
         raise OSError(f"the operators' extension is not built ({path} missing): run "
                       "python -m bit_exact_fp8_gb300.build")
+    made, here = ops_built_for(path), built_for()
+    if made != here:
+        raise OSError(f"the operators' extension ({path}) was built for {made or 'something else'}, this is "
+                      f"{here}: run python -m bit_exact_fp8_gb300.build")
     loader = importlib.machinery.ExtensionFileLoader("_ops_torch", path)
     spec = importlib.util.spec_from_file_location("_ops_torch", path, loader=loader)
     module = importlib.util.module_from_spec(spec)

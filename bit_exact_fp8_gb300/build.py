@@ -10,6 +10,7 @@ headers is newer.
 """
 from __future__ import annotations
 
+import importlib.metadata
 import os
 import shutil
 import subprocess
@@ -30,6 +31,8 @@ PEAKS_DEPS = PEAKS_SOURCES + [os.path.join(INCLUDE, "emu_peaks.h")]
 DEPS = SOURCES + [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cuh", ".h"))] \
     + [os.path.join(INCLUDE, "emu_fp8.h")]
 
+#: what stands before built_for() in the operators' extension
+OPS_MARK = "emu operators built for "
 OPS_SOURCES = [os.path.join(CSRC, "ops_torch.cpp")]
 OPS_DEPS = OPS_SOURCES + [os.path.join(INCLUDE, "emu_fp8.h")]
 
@@ -54,8 +57,28 @@ def _up_to_date(lib: str, deps) -> bool:
     return all(os.path.getmtime(d) <= t for d in deps)
 
 
+def built_for() -> str:
+    """What the operators' extension is tied to, and is made anew for: torch and Python (and with
+    Python's tag the machine)."""
+    return f"torch {importlib.metadata.version('torch')}, {sysconfig.get_config_var('SOABI')}"
+
+
+def ops_built_for(lib: str) -> str:
+    """What the extension at this path was built for, "" if it does not say: read from the file, as
+    an extension of another torch may not survive its loading."""
+    mark = OPS_MARK.encode()
+    with open(lib, "rb") as f:
+        data = f.read()
+    at = data.find(mark)
+    return data[at + len(mark):data.index(b"\0", at)].decode(errors="replace") if at >= 0 else ""
+
+
+def _ops_up_to_date() -> bool:
+    return _up_to_date(OPS_LIB, OPS_DEPS) and ops_built_for(OPS_LIB) == built_for()
+
+
 def up_to_date() -> bool:
-    return _up_to_date(LIB, DEPS) and _up_to_date(PEAKS_LIB, PEAKS_DEPS) and _up_to_date(OPS_LIB, OPS_DEPS)
+    return _up_to_date(LIB, DEPS) and _up_to_date(PEAKS_LIB, PEAKS_DEPS) and _ops_up_to_date()
 
 
 def ops_commands(out: str) -> "tuple[list, list]":
@@ -67,6 +90,7 @@ def ops_commands(out: str) -> "tuple[list, list]":
     obj = out + ".o"
     includes = [INCLUDE] + include_paths() + [os.path.join(cuda, "include"), sysconfig.get_paths()["include"]]
     compile_ = ["g++", "-O2", "-std=c++17", "-fPIC", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"]
+    compile_ += [f'-DEMU_OPS_BUILT_FOR="{OPS_MARK}{built_for()}"']
     compile_ += [f"-I{d}" for d in includes] + ["-c"] + OPS_SOURCES + ["-o", obj]
     link = ["g++", "-shared", obj, "-o", out, f"-L{PKG}", "-l:" + os.path.basename(LIB), "-Wl,-rpath,$ORIGIN"]
     link += [f"-L{d}" for d in library_paths()] + ["-ltorch_python", "-ltorch_cuda", "-ltorch_cpu", "-lc10_cuda", "-lc10"]
@@ -87,7 +111,11 @@ def build(force: bool = False, verbose: bool = False) -> str:
             jobs.append((lib, tmp, subprocess.Popen(cmd)))
     failed, ops_proc = [], None
     ops_tmp = OPS_LIB + f".tmp{os.getpid()}"
-    if force or not _up_to_date(OPS_LIB, OPS_DEPS):
+    try:
+        ops_stale = force or not _ops_up_to_date()
+    except ImportError:                                      # no torch: said below
+        ops_stale = True
+    if ops_stale:
         try:
             ops_compile, ops_link = ops_commands(ops_tmp)
             if verbose:

@@ -376,4 +376,12 @@ PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_ops_torch", nullptr, -1, g_meth
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__ops_torch(void) { return PyModule_Create(&g_module); }
+PyMODINIT_FUNC PyInit__ops_torch(void) {
+  PyObject* m = PyModule_Create(&g_module);
+  // the build and the loader look for this text in the file, to tell an extension of another torch
+  if (m && PyModule_AddStringConstant(m, "built_for", EMU_OPS_BUILT_FOR) < 0) {
+    Py_DECREF(m);
+    return nullptr;
+  }
+  return m;
+}

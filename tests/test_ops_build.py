@@ -40,3 +40,15 @@ def test_the_extension_does_not_hide_a_failed_library(small, monkeypatch):
     with pytest.raises(subprocess.CalledProcessError, match="lib.so"):
         build.build()
     assert not os.path.exists(build.LIB) and not os.path.exists(build.OPS_LIB)
+
+
+def test_an_extension_of_another_torch_is_made_anew(monkeypatch):
+    from bit_exact_fp8_gb300 import _lib
+    build.build()
+    assert build.up_to_date() and build.ops_built_for(build.OPS_LIB) == build.built_for()
+    assert _lib.load_ops().built_for == build.OPS_MARK + build.built_for()
+    for module in (build, _lib):
+        monkeypatch.setattr(module, "built_for", lambda: "torch 0.0, another")
+    assert not build.up_to_date()
+    with pytest.raises(OSError, match="another torch|built for"):
+        _lib.load_ops()
