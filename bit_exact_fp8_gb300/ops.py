@@ -6,7 +6,9 @@ device memory and the stream, the work runs in libemufp8's CUDA kernels on the c
 stream, and there is no CPU path.  They take no part in autograd: a training step calls
 the ``_backward`` functions itself, and an input or output that requires grad under grad mode,
 or carries a forward-mode tangent, is refused.  Writing into a tensor that was given
-counts as a write in place.
+counts as a write in place.  No call reads back the device status: a kernel whose bounded
+wait gave up leaves outputs unwritten and sets ``_lib.emu_ops_device_status``, which is the
+caller's to check where it synchronises.
 """
 from __future__ import annotations
 
@@ -62,7 +64,9 @@ def rms_norm_quant(x: torch.Tensor, weight: torch.Tensor, residual: Optional[tor
     weight``; ``q = y / scale`` rounded to nearest even and saturated to out_dtype
     (float8_e4m3fn, float8_e5m2 or int8).  ``scale`` is a one-element fp32 tensor (what
     ``scaled_mm`` takes as scale_a); without it each row has its own, ``max|y| / qmax``
-    but at least 2^-126 (what ``int8_scaled_mm`` takes as scale_a).  The returned
+    but at least 2^-126: with int8 codes what ``int8_scaled_mm`` takes as scale_a.  FP8 codes
+    with a scale for each row are for products outside this package (``scaled_mm`` takes one
+    scale for all rows).  The returned
     ``residual`` is h rounded to x's dtype, in ``residual_out`` if given (it may be
     ``residual`` or ``x``: updated in place); ``rstd`` is for ``rms_norm_backward``.
 
