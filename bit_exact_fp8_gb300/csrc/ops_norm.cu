@@ -551,6 +551,9 @@ norm_quant_ring_kernel(const NormParams p, const Ring ring) {
       const int v = i * nt + t;
       const Columns<T, EDGES> c(v, off, p.H);
       if (!EDGES && !c.any()) continue;
+      // none of the warp's (asked in the last slot of four, which is often so: 8192 x 4097 bf16 64 us, 74 without;
+      // asked in each slot it costs more than it spares where there are columns)
+      if (EDGES && IT > 2 && i == IT - 1 && (v - lane) * VEC - off >= p.H) continue;
       if (c.any()) read_h(v, c, hw[i]);
       if constexpr (EDGES) {
         if (!c.any()) {
@@ -703,8 +706,8 @@ template <class T> int pick_norm(const NormParams& p, bool alike, bool aligned16
     else launch_norm<T, false, 32, (V < 8 ? 2 : 1)>(p, st);
     return EMU_OK;
   }
-  // By columns' blocks instead of by address, unaligned rows take longer: 8192 x 1111 bf16 24.4 us and 22.0,
-  // 8192 x 5761 81.6 and 65.8 (aligned 5760 52.9).
+  // By columns' blocks instead of by address, unaligned rows take longer: 8192 x 1111 bf16 24 us and 22,
+  // 8192 x 3001 44 and 36, 8192 x 5761 84 and 66 (aligned 5760 53).
   if (alike && sp.it > 0) {
     if (nv <= 256) return launch_norm_ring<T, 2, 128, 8, 6>(p, sp.threads, aligned16, q_vec, st);
     if (nv <= 1024) return launch_norm_ring<T, 4, 256, 2, 2>(p, sp.threads, aligned16, q_vec, st);
