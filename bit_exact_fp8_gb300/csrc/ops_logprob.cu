@@ -694,11 +694,12 @@ logprob_grad_kernel(const LogprobGradParams p, uint32_t parts, bool same) {
     if (v0 + i * TPR < row.nvec) raw[i] = row.load_raw(v0 + i * TPR);
   const float m = p.stats[r * 3], logz = p.stats[r * 3 + 1], H = p.stats[r * 3 + 2];
   const int64_t tok = p.tokens[r];
+  const float given = p.g_logprob ? p.g_logprob[r] : 0.0f;     // asked for beside the token, not after it
   const bool out_of_range = tok != p.ignore && (tok < 0 || tok >= p.V);
   // out of range is an error of the caller's: NaN, even where nothing of the logprob's gradient is asked for
-  const float gl = out_of_range ? NAN : tok == p.ignore || !p.g_logprob ? 0.0f : p.g_logprob[r];
+  const float gl = out_of_range ? NAN : tok == p.ignore ? 0.0f : given;
   const float ge = p.g_entropy ? p.g_entropy[r] : 0.0f;
-  const bool empty = m == -INFINITY && logz == -INFINITY;
+  const bool empty = m == -INFINITY && logz == -INFINITY && !out_of_range;   // out of range: NaN below by gl
   const int hot = !empty && tok >= 0 && tok < p.V ? (int)tok : -1;
   const f2 m2 = pair(-m, -m), z2 = pair(-logz, -logz), L2 = pair(kLog2e, kLog2e), e2 = pair(-ge, -ge);
   const float rest = -fmaf(ge, H, gl);
@@ -723,7 +724,7 @@ logprob_grad_kernel(const LogprobGradParams p, uint32_t parts, bool same) {
     if (empty) {
       asm volatile("");                                  // branches: few rows and vectors take them
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) f[j] = out_of_range ? NAN : 0.0f;
+      for (int j = 0; j < VEC; ++j) f[j] = 0.0f;
     }
     if ((uint32_t)(hot - id0) < (uint32_t)VEC && hot >= 0) {
       asm volatile("");
