@@ -29,6 +29,10 @@ EMU_Q_E4M3FN = 0
 EMU_Q_E5M2 = 1
 EMU_Q_INT8 = 2
 
+EMU_BLOCK_ROWS = 0
+EMU_BLOCK_COLUMNS = 1
+EMU_BLOCK_SQUARES = 2
+
 #: every symbol include/emu_fp8.h declares
 EXPORTED = ("emu_preset_get", "emu_workspace_bytes", "emu_scaled_mm", "emu_last_error",
             "emu_abi_version", "emu_scaled_mm_noalloc", "emu_device_status",
@@ -36,7 +40,11 @@ EXPORTED = ("emu_preset_get", "emu_workspace_bytes", "emu_scaled_mm", "emu_last_
             "emu_scaled_mm_host", "emu_tile_for", "emu_tc_selftest", "emu_rms_norm_quant",
             "emu_rms_norm_backward_workspace_bytes", "emu_rms_norm_backward",
             "emu_int8_workspace_bytes", "emu_int8_scaled_mm", "emu_token_logprobs",
-            "emu_token_logprobs_backward", "emu_ops_last_error", "emu_ops_device_status")
+            "emu_token_logprobs_backward", "emu_ops_last_error", "emu_ops_device_status",
+            "emu_block_quant", "emu_swiglu_quant", "emu_swiglu_backward",
+            "emu_block_mm_workspace_bytes", "emu_block_scaled_mm",
+            "emu_grouped_block_mm_workspace_bytes", "emu_grouped_block_scaled_mm",
+            "emu_grouped_block_wgrad_workspace_bytes", "emu_grouped_block_scaled_wgrad")
 
 #: size of the static scratch of emu_scaled_mm_noalloc (EMU_NOALLOC_SCRATCH_BYTES)
 EMU_NOALLOC_SCRATCH_BYTES = 4 << 20
@@ -50,6 +58,13 @@ class emu_preset_t(ctypes.Structure):
 
     def as_dict(self):
         return {name: getattr(self, name) for name, _ in self._fields_}
+
+
+class emu_block_operand_t(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("format", ctypes.c_int), ("row_stride", ctypes.c_int64),
+                ("k_stride", ctypes.c_int64), ("group_stride", ctypes.c_int64), ("scale", ctypes.c_void_p),
+                ("scale_rows", ctypes.c_int32), ("scale_row_stride", ctypes.c_int64),
+                ("scale_k_stride", ctypes.c_int64), ("scale_group_stride", ctypes.c_int64)]
 
 
 _handle = None
@@ -118,6 +133,25 @@ def load(path: str = LIB) -> ctypes.CDLL:
     L.emu_token_logprobs.restype = I
     L.emu_token_logprobs_backward.argtypes = [P, I64, I, P, I64, I64, I64, P, P, P, P, I64, P]
     L.emu_token_logprobs_backward.restype = I
+    L.emu_block_quant.argtypes = [P, I64, I, I64, I64, I, I, P, P, P]
+    L.emu_block_quant.restype = I
+    L.emu_swiglu_quant.argtypes = [P, I64, I, I64, I64, I, I, P, P, P, P, P]
+    L.emu_swiglu_quant.restype = I
+    L.emu_swiglu_backward.argtypes = [P, I64, I, I64, I64, P, P, P, P]
+    L.emu_swiglu_backward.restype = I
+    O = ctypes.POINTER(emu_block_operand_t)                  # noqa: E741
+    L.emu_block_mm_workspace_bytes.argtypes = [O, O, I64, I64, I64]
+    L.emu_block_mm_workspace_bytes.restype = Z
+    L.emu_block_scaled_mm.argtypes = [O, O, I64, I64, I64, P, I, P, Z, P]
+    L.emu_block_scaled_mm.restype = I
+    L.emu_grouped_block_mm_workspace_bytes.argtypes = [O, O, I64, I64, I64, I64]
+    L.emu_grouped_block_mm_workspace_bytes.restype = Z
+    L.emu_grouped_block_scaled_mm.argtypes = [O, O, P, I64, I64, I64, I64, P, I, ctypes.c_int32, P, Z, P]
+    L.emu_grouped_block_scaled_mm.restype = I
+    L.emu_grouped_block_wgrad_workspace_bytes.argtypes = [O, O, I64, I64, I64]
+    L.emu_grouped_block_wgrad_workspace_bytes.restype = Z
+    L.emu_grouped_block_scaled_wgrad.argtypes = [O, O, P, I64, I64, I64, I64, P, I, P, Z, P]
+    L.emu_grouped_block_scaled_wgrad.restype = I
     L.emu_ops_last_error.argtypes = []
     L.emu_ops_last_error.restype = ctypes.c_char_p
     L.emu_ops_device_status.argtypes = [ctypes.POINTER(ctypes.c_int32), ctypes.c_int32]

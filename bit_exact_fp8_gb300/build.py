@@ -25,7 +25,7 @@ LIB = os.path.join(PKG, "libemufp8.so")
 PEAKS_LIB = os.path.join(PKG, "libemupeaks.so")
 OPS_LIB = os.path.join(PKG, "_ops_torch.so")
 SOURCES = [os.path.join(CSRC, f) for f in ("emu_api.cu", "ops_norm.cu", "ops_int8.cu",
-                                           "ops_logprob.cu")]
+                                           "ops_logprob.cu", "ops_block_quant.cu", "ops_block_mm.cu")]
 PEAKS_SOURCES = [os.path.join(CSRC, "emu_peaks.cu")]
 PEAKS_DEPS = PEAKS_SOURCES + [os.path.join(INCLUDE, "emu_peaks.h")]
 DEPS = SOURCES + [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cuh", ".h"))] \
@@ -34,7 +34,7 @@ DEPS = SOURCES + [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith(
 #: what stands before built_for() in the operators' extension
 OPS_MARK = "emu operators built for "
 OPS_SOURCES = [os.path.join(CSRC, "ops_torch.cpp")]
-OPS_DEPS = OPS_SOURCES + [os.path.join(INCLUDE, "emu_fp8.h")]
+OPS_DEPS = OPS_SOURCES + [os.path.join(CSRC, "ops_torch_block.h"), os.path.join(INCLUDE, "emu_fp8.h")]
 
 NVCC_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a", "-O3", "-lineinfo", "-std=c++17",
               "-Xcompiler", "-fPIC", "-shared", "--threads", "0", "-I" + INCLUDE, "-I" + CSRC]

@@ -337,6 +337,8 @@ PyObject* logprobs_backward(PyObject* const* a) {
   return a[6] == Py_None ? THPVariable_Wrap(gx) : same(a[6]);
 }
 
+#include "ops_torch_block.h"
+
 template <PyObject* (*F)(PyObject* const*), Py_ssize_t COUNT>
 PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
   HANDLE_TH_ERRORS
@@ -370,6 +372,14 @@ PyMethodDef g_methods[] = {EMU_METHOD("rms_norm_quant", (entry<norm_quant, 8>)),
                            EMU_METHOD("int8_scaled_mm", (entry<int8_mm, 7>)),
                            EMU_METHOD("token_logprobs", (entry<logprobs, 4>)),
                            EMU_METHOD("token_logprobs_backward", (entry<logprobs_backward, 7>)),
+                           EMU_METHOD("block_quant", (entry<block_quant, 4>)),
+                           EMU_METHOD("swiglu_quant", (entry<swiglu_quant, 5>)),
+                           EMU_METHOD("swiglu_backward", (entry<swiglu_backward, 3>)),
+                           EMU_METHOD("block_scaled_mm", (entry<block_mm, 7>)),
+                           EMU_METHOD("grouped_block_scaled_mm", (entry<grouped_mm, 8>)),
+                           EMU_METHOD("grouped_block_scaled_wgrad", (entry<grouped_wgrad, 8>)),
+                           EMU_METHOD("block_mm_workspace_bytes", (entry<block_mm_bytes, 2>)),
+                           EMU_METHOD("block_wgrad_workspace_bytes", (entry<block_wgrad_bytes, 2>)),
                            EMU_METHOD("set_errors", set_errors),
                            {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_ops_torch", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};

@@ -1,7 +1,10 @@
 """torch-facing operators around an 8-bit product: RMS norm with the residual's addition
 and an 8-bit output (``rms_norm_quant``), the product of 8-bit integers
 (``int8_scaled_mm``), and the log probabilities of given tokens (``token_logprobs``),
-with the gradients that training needs.  They follow ``scaled_mm``: PyTorch provides
+with the gradients that training needs; and 8-bit layers with a scale for each block of 128
+codes: quantisation (``block_quant``), the FP8 product, dense and by expert
+(``block_scaled_mm``, ``grouped_block_scaled_mm``), and SwiGLU between two of them
+(``swiglu_quant``).  They follow ``scaled_mm``: PyTorch provides
 device memory and the stream, the work runs in libemufp8's CUDA kernels on the current
 stream, and there is no CPU path.  They take no part in autograd: a training step calls
 the ``_backward`` functions itself, and an input or output that requires grad under grad mode,
@@ -37,6 +40,18 @@ class TokenLogprobs(NamedTuple):
     stats: torch.Tensor                    # [T, 3] fp32, for the gradient
     top_logprobs: torch.Tensor             # [T, top_k] fp32
     top_ids: torch.Tensor                  # [T, top_k] int64
+
+
+class BlockQuant(NamedTuple):
+    q: torch.Tensor                        # [T, H] FP8
+    scale: torch.Tensor                    # fp32, one for each block
+
+
+class SwigluQuant(NamedTuple):
+    q: torch.Tensor                        # [T, H] FP8
+    scale: torch.Tensor                    # fp32, one for each block
+    checkpoint: Optional[torch.Tensor]     # [T, 2 H] E4M3: the inputs, for the gradient
+    checkpoint_scale: Optional[torch.Tensor]   # [T, 2 ceil(H / 128)] fp32
 
 
 _ext = None
@@ -124,3 +139,87 @@ def token_logprobs_backward(logits: torch.Tensor, tokens: torch.Tensor, stats: t
     whatever else holds of them; rows of nothing but -inf zeros.  ``out`` may be the logits themselves: the gradient then
     takes their place."""
     return _calls().token_logprobs_backward(logits, tokens, stats, grad_logprob, grad_entropy, ignore_index, out)
+
+
+def block_quant(x: torch.Tensor, *, block: Tuple[int, int] = (1, 128),
+                out_dtype: torch.dtype = torch.float8_e4m3fn, out: Optional[torch.Tensor] = None) -> BlockQuant:
+    """``x`` [T, H] (fp32, bf16 or fp16, rows contiguous, any row stride) as FP8 codes
+    (float8_e4m3fn or float8_e5m2) with an fp32 scale for each block, ``max|x| / qmax`` but at
+    least 2^-126.
+
+    block (1, 128): for products over H, scales [T, ceil(H / 128)].  (128, 1): for products over T (a
+    weight's gradient), scales [ceil(T / 128), H].  (128, 128): for both, scales [ceil(T / 128),
+    ceil(H / 128)]: a weight, or activations that the forward product reads and the backward
+    pass reads again.  A block holding NaN or Inf has NaN for its scale and codes."""
+    return BlockQuant._make(_calls().block_quant(x, block, out_dtype, out))
+
+
+def block_mm_workspace_bytes(mat1: torch.Tensor, mat2: torch.Tensor) -> int:
+    """Device workspace bytes ``block_scaled_mm`` (mat2 [K, N]) or ``grouped_block_scaled_mm``
+    (mat2 [E, K, N]) needs for these operands."""
+    return _calls().block_mm_workspace_bytes(mat1, mat2)
+
+
+def block_scaled_mm(mat1: torch.Tensor, mat2: torch.Tensor, scale_a: torch.Tensor, scale_b: torch.Tensor, *,
+                    out_dtype: torch.dtype = torch.bfloat16, out: Optional[torch.Tensor] = None,
+                    workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """``mat1 @ mat2`` of FP8 codes (either format on either side) with a scale for each block
+    of 128 of K, each block's products summed in fp32 and scaled by ``scale_a * scale_b``.
+
+    mat1 [M, K] and mat2 [K, N], either dimension of each contiguous; scale_a [M, ceil(K / 128)] or
+    [ceil(M / 128), ceil(K / 128)], scale_b [ceil(K / 128), N] or [ceil(K / 128), ceil(N / 128)],
+    fp32, of any strides.  With activations x and a weight w [N, K] quantised by ``block_quant``:
+
+        y      = block_scaled_mm(x.q, w.q.t(), x.scale, w.scale.t())
+        grad_x = block_scaled_mm(g.q, w.q, g.scale, w.scale)            # g: grad_y in (1, 128) or (128, 128)
+        grad_w = block_scaled_mm(g.q.t(), x.q, g.scale.t(), x.scale)    # both in (128, 1) or (128, 128)
+
+    Returns [M, N] in out_dtype (fp32, bf16 or fp16)."""
+    return _calls().block_scaled_mm(mat1, mat2, scale_a, scale_b, out_dtype, out, workspace)
+
+
+def grouped_block_scaled_mm(mat1: torch.Tensor, mat2: torch.Tensor, offsets: torch.Tensor, scale_a: torch.Tensor,
+                            scale_b: torch.Tensor, *, out_dtype: torch.dtype = torch.bfloat16,
+                            out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """``block_scaled_mm`` by expert: rows offsets[e] to offsets[e + 1] of mat1 [T, K] (rows
+    contiguous) times mat2[e], mat2 [E, K, N] with either of its last dimensions contiguous
+    (``w.transpose(1, 2)`` of weights [E, N, K]), E up to 1024.
+
+    offsets [E + 1] int32 on the device, rising; read there alone, so no call waits for the router.
+    (They are taken within [0, T] and none below the one before it.)  scale_a as for
+    ``block_scaled_mm``, scale_b [E, ceil(K / 128), N or ceil(N / 128)].  Returns [T, N]; rows of
+    no expert are 0, or as they were in a given ``out``."""
+    return _calls().grouped_block_scaled_mm(mat1, mat2, offsets, scale_a, scale_b, out_dtype, out, workspace)
+
+
+def block_wgrad_workspace_bytes(grad: torch.Tensor, x: torch.Tensor) -> int:
+    """Device workspace bytes ``grouped_block_scaled_wgrad`` needs for these operands."""
+    return _calls().block_wgrad_workspace_bytes(grad, x)
+
+
+def grouped_block_scaled_wgrad(grad: torch.Tensor, x: torch.Tensor, offsets: torch.Tensor, scale_grad: torch.Tensor,
+                               scale_x: torch.Tensor, *, out_dtype: torch.dtype = torch.float32,
+                               out: Optional[torch.Tensor] = None,
+                               workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Gradients of the experts' weights: ``grad[rows of e].t() @ x[rows of e]`` for each expert,
+    [E, N, K] in out_dtype.  grad [T, N] and x [T, K] are the FP8 codes of the outputs' gradients and of
+    the inputs (rows contiguous) as ``block_quant`` makes them of all T rows in blocks (128, 1) or
+    (128, 128), whatever the groups are; offsets as for ``grouped_block_scaled_mm``.  An expert
+    without rows gets zeros."""
+    return _calls().grouped_block_scaled_wgrad(grad, x, offsets, scale_grad, scale_x, out_dtype, out, workspace)
+
+
+def swiglu_quant(gate_up: torch.Tensor, *, block: Tuple[int, int] = (1, 128),
+                 out_dtype: torch.dtype = torch.float8_e4m3fn, checkpoint: bool = False,
+                 out: Optional[torch.Tensor] = None) -> SwigluQuant:
+    """``silu(gate) * up`` as FP8 codes with block scales, (1, 128) or (128, 128), as
+    ``block_quant`` would make them of the fp32 values; gate_up [T, 2 H] (fp32, bf16 or fp16) holds
+    gate in its first H columns.  With ``checkpoint`` the inputs are kept too, as E4M3 codes with a scale
+    for each (1, 128) block of either half: half the bytes of 16-bit ones, for ``swiglu_backward``."""
+    return SwigluQuant._make(_calls().swiglu_quant(gate_up, block, out_dtype, checkpoint, out))
+
+
+def swiglu_backward(grad_y: torch.Tensor, checkpoint: torch.Tensor, checkpoint_scale: torch.Tensor) -> torch.Tensor:
+    """Gradient of ``swiglu_quant`` by gate_up, [T, 2 H] of grad_y's dtype, straight through the
+    8-bit roundings, at the inputs that the checkpoint holds; grad_y [T, H] is the gradient of its output."""
+    return _calls().swiglu_backward(grad_y, checkpoint, checkpoint_scale)

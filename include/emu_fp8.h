@@ -399,6 +399,110 @@ int emu_token_logprobs_backward(const void* logits, int64_t ldx, emu_out_t type,
                                 const float* grad_entropy, void* grad_logits, int64_t ldo,
                                 void* stream);
 
+/*
+ * ---- 8-bit layers with block scales.  FP8 codes with an fp32 scale for each block of 128:
+ * 128 values of a row, 128 of a column, or a square of both.  Blocks count from the first row
+ * and column; the last ones of a row or column may be shorter.
+ */
+
+/* What shares a scale: EMU_BLOCK_ROWS 1 x 128, EMU_BLOCK_COLUMNS 128 x 1, EMU_BLOCK_SQUARES 128 x 128. */
+typedef enum { EMU_BLOCK_ROWS = 0, EMU_BLOCK_COLUMNS = 1, EMU_BLOCK_SQUARES = 2 } emu_block_t;
+
+/*
+ * Quantisation of x [T,H] (type fp32, bf16 or fp16, rows ldx elements apart) in blocks:
+ *   scale = max|x| / qmax over the block, but at least 2^-126    (qmax: 448 or 57344)
+ *   q = x / scale rounded to nearest even                         (FP8, [T,H] contiguous)
+ *   scale  fp32, contiguous: [T, ceil(H/128)], [ceil(T/128), H] or [ceil(T/128), ceil(H/128)]
+ * x / scale is computed as x * (qmax / max|x|) and is within 2^-23 of its value before the
+ * rounding to 8 bits.  A block that holds NaN or Inf has NaN for its scale and all its codes,
+ * and touches no other block.  Sizes: T, H < 2^31.
+ */
+int emu_block_quant(const void* x, int64_t ldx, emu_out_t type, int64_t T, int64_t H, emu_block_t block,
+                    emu_fp8_t q_format, void* q, float* scale, void* stream);
+
+/*
+ * SwiGLU with an 8-bit output: gate_up [T, 2H] holds g in its first H columns and u in the others,
+ *   y = g / (1 + e^-g) * u    (fp32)
+ * quantised as by emu_block_quant in rows or squares (q [T,H], scale).  checkpoint [T, 2H] and
+ * checkpoint_scale [T, 2 ceil(H/128)] (both NULL: not wanted): g and u themselves as E4M3 codes
+ * with a scale for each 1 x 128 block of either half, for the backward pass.
+ */
+int emu_swiglu_quant(const void* gate_up, int64_t ldx, emu_out_t type, int64_t T, int64_t H,
+                     emu_block_t block, emu_fp8_t q_format, void* q, float* scale, void* checkpoint,
+                     float* checkpoint_scale, void* stream);
+
+/*
+ * Gradient of y = g / (1 + e^-g) * u by g and u, straight through y's 8-bit rounding, at the g
+ * and u that the checkpoint holds (its code times its scale, in fp32), s = 1 / (1 + e^-g):
+ *   grad_gate_up [T, 2H] = [ grad_y u s (1 + g (1 - s)),  grad_y g s ]
+ * of grad_y's type (fp32, bf16 or fp16), contiguous; grad_y [T,H] has rows ldy apart.
+ */
+int emu_swiglu_backward(const void* grad_y, int64_t ldy, emu_out_t type, int64_t T, int64_t H,
+                        const void* checkpoint, const float* checkpoint_scale, void* grad_gate_up,
+                        void* stream);
+
+/*
+ * One side of an FP8 product: `rows` vectors of K codes each, of which either the codes of a row
+ * (k_stride 1) or those of a K position (row_stride 1) are contiguous, and a scale for each
+ * block of 128 of K of a row (scale_rows 1) or of 128 rows (scale_rows 128), at
+ * scale[(row / scale_rows) * scale_row_stride + (k / 128) * scale_k_stride].  The group strides
+ * are those of the experts' weights; other operands leave them 0.  Strides are in elements.
+ */
+typedef struct {
+  const void* codes;
+  emu_fp8_t format;
+  int64_t row_stride, k_stride, group_stride;
+  const float* scale;
+  int32_t scale_rows;
+  int64_t scale_row_stride, scale_k_stride, scale_group_stride;
+} emu_block_operand_t;
+
+/*
+ * out[M,N] = sum over the blocks of K of (sum of the block's products) * (scale_a * scale_b),
+ * contiguous, rounded once to out_dtype (fp32, bf16 or fp16).  a has M rows, b has N: b's rows
+ * are the columns of the product's right-hand side.  A block's products are added up in fp32
+ * within 2^-20 of the sum of their magnitudes, the blocks in fp32.  Any mixture of the two
+ * formats and of the strides above, so that a layer's forward product and both its gradients
+ * read the same codes.  A NaN among a row's codes or scales gives NaN in that row's (column's)
+ * outputs alone.  K == 0 gives zeros.  Sizes: M, N, K < 2^31.
+ *   workspace: emu_block_mm_workspace_bytes of the same operands (0 where both are 16-byte
+ *   aligned with strides that are multiples of 16), 256-byte aligned
+ */
+size_t emu_block_mm_workspace_bytes(const emu_block_operand_t* a, const emu_block_operand_t* b,
+                                    int64_t M, int64_t N, int64_t K);
+int emu_block_scaled_mm(const emu_block_operand_t* a, const emu_block_operand_t* b, int64_t M, int64_t N,
+                        int64_t K, void* out, emu_out_t out_dtype, void* workspace, size_t workspace_bytes,
+                        void* stream);
+
+/*
+ * The same by expert: rows offsets[e] to offsets[e+1] of a [T,K] times expert e's weights (b: N
+ * rows for each of E experts, group strides apart), out [T,N] contiguous.  offsets: E + 1 int32 on
+ * the device, rising; they are read there alone, so that a router's result is used without a
+ * synchronisation, and are taken as max(0, min(T, offset)), none below the one before it.  An expert
+ * may have no rows.  Rows before offsets[0] and from offsets[E] on are left as they were, or with
+ * zero_rest set to 0.  a's codes are contiguous within a row.  E <= 1024.
+ */
+size_t emu_grouped_block_mm_workspace_bytes(const emu_block_operand_t* a, const emu_block_operand_t* b,
+                                            int64_t T, int64_t N, int64_t K, int64_t E);
+int emu_grouped_block_scaled_mm(const emu_block_operand_t* a, const emu_block_operand_t* b,
+                                const int32_t* offsets, int64_t E, int64_t T, int64_t N, int64_t K, void* out,
+                                emu_out_t out_dtype, int32_t zero_rest, void* workspace,
+                                size_t workspace_bytes, void* stream);
+
+/*
+ * Gradient of the experts' weights: out[e] = a[rows of e]^T b[rows of e], out [E,N,K] contiguous, with
+ * a [T,N] the gradients of the outputs and b [T,K] the inputs, both row-major.  As operands of a
+ * product over T they have N and K rows with row_stride 1, k_stride the distance of a token from
+ * the next, and blocks of 128 tokens, which count from row 0 whatever the groups are.
+ * offsets as above; an expert without rows gets zeros.
+ */
+size_t emu_grouped_block_wgrad_workspace_bytes(const emu_block_operand_t* a, const emu_block_operand_t* b,
+                                               int64_t T, int64_t N, int64_t K);
+int emu_grouped_block_scaled_wgrad(const emu_block_operand_t* a, const emu_block_operand_t* b,
+                                   const int32_t* offsets, int64_t E, int64_t T, int64_t N, int64_t K,
+                                   void* out, emu_out_t out_dtype, void* workspace, size_t workspace_bytes,
+                                   void* stream);
+
 /* Message of the last error an operator above returned on the calling host thread. */
 const char* emu_ops_last_error(void);
 
