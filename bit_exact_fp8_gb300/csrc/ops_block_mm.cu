@@ -3,15 +3,27 @@
 //   out[m, n] = sum over blocks kb of (sum over k in kb of a[m, k] b[n, k]) * (sa[m, kb] * sb[n, kb])
 #include "ops_block.cuh"
 
+#include <cuda.h>             // CUtensorMap (the type only; the driver is called through an entry point)
+#include <cudaTypedefs.h>
+
+#include <atomic>
 #include <type_traits>
 
 namespace emu_ops {
 
-constexpr int64_t kMaxExperts = 1024;
+// 1 once a bounded wait of the pipeline gave up (the outputs of that call are not valid)
+__device__ int g_block_status = 0;
 
-enum class BlockKind { dense, grouped, wgrad };
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();  // ops_int8.cu
+
+}  // namespace emu_ops
+
+#include "ops_block_tc.cuh"
+
+namespace emu_ops {
+
 struct BlockMm {
-  emu_block_operand_t a, b;                              // M and N rows; wgrad: rows by tokens
+  emu_block_operand_t a, b;                              // M and N rows
   BlockKind kind;
   int64_t M, N, K;                                       // grouped: M tokens; wgrad: K tokens
   const int32_t* offsets; int E;
@@ -19,65 +31,160 @@ struct BlockMm {
   void* out; int out_type;                               // [M, N], wgrad [E, M, N]
 };
 
-// rows [lo, hi) of expert e: the offsets within [0, T], none below the one before it
-__device__ __forceinline__ void group_of(const BlockMm& p, int e, int64_t T, int64_t& lo, int64_t& hi) {
-  lo = 0;
-  for (int i = 0; i <= e + 1; ++i) {
-    int64_t at = p.offsets[i];
-    at = at < 0 ? 0 : at > T ? T : at;
-    if (i == e + 1) hi = at > lo ? at : lo;
-    else lo = at > lo ? at : lo;
+// An operand's codes as `outer` vectors of `inner` contiguous codes, `stride` apart, in groups.
+struct CodesView {
+  const uint8_t* at;
+  int64_t inner, outer, stride, groups, group_stride;
+  bool mn;                                               // the contiguous codes are those of a K position
+  bool fits() const {                                    // what a tensor map asks for
+    return aligned(at, 16) && (outer <= 1 || stride % 16 == 0) && (groups <= 1 || group_stride % 16 == 0);
   }
-}
-__device__ __forceinline__ float scale_at(const emu_block_operand_t& o, int64_t row, int64_t kb, int64_t group) {
-  return __ldg(o.scale + group * o.scale_group_stride + (o.scale_rows == 1 ? row : row / kBlock) * o.scale_row_stride +
-               kb * o.scale_k_stride);
-}
-__device__ __forceinline__ void store_out(void* out, int type, int64_t i, float v) {
-  if (type == EMU_OUT_F32) static_cast<float*>(out)[i] = v;
-  else if (type == EMU_OUT_BF16) static_cast<__nv_bfloat16*>(out)[i] = __float2bfloat16_rn(v);
-  else static_cast<__half*>(out)[i] = __float2half_rn(v);
+  size_t laid_out() const { return fits() ? 0 : ((size_t)groups * (size_t)outer * (size_t)((inner + 15) / 16 * 16) + 255) / 256 * 256; }
+};
+CodesView view_of(const emu_block_operand_t& o, int64_t rows, int64_t K, int64_t groups, bool mn) {
+  const bool by_k = !mn && (o.k_stride == 1 || K == 1) && (rows <= 1 || o.row_stride >= K);
+  const uint8_t* at = static_cast<const uint8_t*>(o.codes);
+  if (by_k) return {at, K, rows, o.row_stride, groups, o.group_stride, false};
+  return {at, rows, K, o.k_stride, groups, o.group_stride, true};
 }
 
-// one output a thread
-__global__ void __launch_bounds__(256) block_mm_kernel(const BlockMm p) {
-  const int64_t per = p.M * p.N, total = per * (p.kind == BlockKind::wgrad ? p.E : 1);
+// Codes to rows whose length is a multiple of 16 (zeros behind their ends), for operands that a tensor map does
+// not take.  A thread takes 16 codes.
+struct LayOut {
+  const uint8_t* from; uintptr_t end;
+  int64_t inner, outer, stride, group_stride, vectors;   // vectors: of all groups
+  uint8_t* to; int64_t chunks;                           // 16 codes each, of a vector
+};
+__global__ void __launch_bounds__(256) lay_out_kernel(const LayOut a, const LayOut b) {
+  const int64_t na = a.vectors * a.chunks, total = na + b.vectors * b.chunks;
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
-    int64_t group = i / per, m = i % per / p.N, n = i % p.N, k0 = 0, k1 = p.K;
-    if (p.kind == BlockKind::wgrad) {
-      group_of(p, (int)group, p.K, k0, k1);
-    } else if (p.kind == BlockKind::grouped) {
-      int64_t lo = 0, hi = 0;
-      int e = 0;
-      for (; e < p.E; ++e) {
-        group_of(p, e, p.M, lo, hi);
-        if (m >= lo && m < hi) break;
-      }
-      if (e == p.E) {
-        if (p.zero_rest) store_out(p.out, p.out_type, i, 0.0f);
-        continue;
-      }
-      group = e;
-    }
-    const int64_t gb = p.kind == BlockKind::grouped ? group : 0;
-    const uint8_t* a = static_cast<const uint8_t*>(p.a.codes) + m * p.a.row_stride;
-    const uint8_t* b = static_cast<const uint8_t*>(p.b.codes) + gb * p.b.group_stride + n * p.b.row_stride;
-    float sum = 0.0f;
-    while (k0 < k1) {
-      const int64_t kb = k0 / kBlock, end = (kb + 1) * kBlock < k1 ? (kb + 1) * kBlock : k1;
-      float part = 0.0f;
-      for (; k0 < end; ++k0)
-        part = fmaf(code_value(a[k0 * p.a.k_stride], p.a.format), code_value(b[k0 * p.b.k_stride], p.b.format), part);
-      sum = fmaf(part, scale_at(p.a, m, kb, 0) * scale_at(p.b, n, kb, gb), sum);
-    }
-    store_out(p.out, p.out_type, i, sum);
+    const LayOut& s = i < na ? a : b;
+    const int64_t j = i < na ? i : i - na, v = j / s.chunks, k = (j - v * s.chunks) * 16, g = v / s.outer;
+    const int8_t* const row = reinterpret_cast<const int8_t*>(s.from + g * s.group_stride + (v - g * s.outer) * s.stride) + k;
+    const int left = s.inner - k < 16 ? (int)(s.inner - k) : 16;
+    Codes<false> codes;
+    codes.ask(row, 0, true, reinterpret_cast<const int8_t*>(s.from), s.end);
+    *reinterpret_cast<uint4*>(s.to + v * s.chunks * 16 + k) = codes.get(row, 0, left, true, reinterpret_cast<const int8_t*>(s.from), s.end);
   }
 }
+LayOut lay_out_of(CodesView& v, unsigned char*& ws) {
+  LayOut l = {};
+  if (v.fits()) return l;
+  const int64_t chunks = (v.inner + 15) / 16;
+  const int64_t span = (v.groups - 1) * v.group_stride + (v.outer - 1) * v.stride + v.inner;
+  l = {v.at, reinterpret_cast<uintptr_t>(v.at) + (size_t)span, v.inner, v.outer, v.stride, v.group_stride, v.groups * v.outer, ws, chunks};
+  const size_t bytes = v.laid_out();
+  v.at = ws;
+  v.stride = chunks * 16;
+  v.group_stride = v.outer * v.stride;
+  ws += bytes;
+  return l;
+}
 
-int run_block_mm(const BlockMm& p, cudaStream_t st) {
-  const int64_t total = p.M * p.N * (p.kind == BlockKind::wgrad ? p.E : 1), ctas = (total + 255) / 256;
-  block_mm_kernel<<<(unsigned)(ctas < 1 << 20 ? ctas : 1 << 20), 256, 0, st>>>(p);
-  return emu_ops_launched("emu_block_scaled_mm");
+// boxes of 128 contiguous codes by `box` vectors under the 128-byte swizzle
+int codes_map(CUtensorMap* map, const CodesView& v, int box) {
+  PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+  if (!enc) return emu_ops_fail(EMU_ECUDA, "cuTensorMapEncodeTiled is not available from the driver");
+  const cuuint64_t stride = v.outer > 1 ? (cuuint64_t)v.stride : (cuuint64_t)((v.inner + 15) / 16 * 16);
+  const cuuint64_t group = v.groups > 1 ? (cuuint64_t)v.group_stride : stride * (cuuint64_t)v.outer;
+  const cuuint64_t dims[3] = {(cuuint64_t)v.inner, (cuuint64_t)v.outer, (cuuint64_t)v.groups}, strides[2] = {stride, group};
+  const cuuint32_t boxes[3] = {128u, (cuuint32_t)box, 1u}, step[3] = {1u, 1u, 1u};
+  const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<uint8_t*>(v.at), dims, strides, boxes, step,
+                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? EMU_OK : emu_ops_fail(EMU_ECUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
+}
+
+BlockSide side_of(const emu_block_operand_t& o, int64_t rows, bool mn) {
+  return {o.scale, o.scale_rows == 1 ? 0 : 7, o.scale_row_stride, o.scale_k_stride, o.scale_group_stride, (int)rows, mn ? 1 : 0};
+}
+
+template <int BN> int launch_tc(const BlockTcParams& p, int mode, int64_t tiles, const CUtensorMap& map_l, const CUtensorMap& map_c,
+                                cudaStream_t st) {
+  using SH = BlockTcShape<BN>;
+  auto kernel = mode == kScaleLane ? block_tc_kernel<BN, kScaleLane> : mode == kScaleColumns ? block_tc_kernel<BN, kScaleColumns>
+                                                                                              : block_tc_kernel<BN, kScaleBoth>;
+  static std::atomic<bool> done[3][64];
+  if (!emu_ops_allow_smem(reinterpret_cast<const void*>(kernel), SH::smem(kMaxExperts), done[mode])) return emu_ops_launched("cudaFuncSetAttribute");
+  const int sms = emu_ops_sm_count();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(p.slices > 1 ? tiles * p.slices : tiles < sms ? tiles : sms));
+  cfg.blockDim = dim3(kTcThreads8);
+  cfg.dynamicSmemBytes = SH::smem(p.kind == BlockKind::dense ? 0 : p.E);
+  cfg.stream = st;
+  cudaLaunchAttribute at;
+  at.id = cudaLaunchAttributeClusterDimension;
+  at.val.clusterDim.x = (unsigned)p.slices;
+  at.val.clusterDim.y = at.val.clusterDim.z = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = p.slices > 1 ? 1 : 0;
+  if (cudaLaunchKernelEx(&cfg, kernel, p, map_l, map_c) != cudaSuccess) return emu_ops_launched("emu_block_scaled_mm");
+  return EMU_OK;
+}
+
+int run_block_mm(const BlockMm& p, void* workspace, cudaStream_t st) {
+  const bool wgrad = p.kind == BlockKind::wgrad, grouped = p.kind == BlockKind::grouped;
+  CodesView va = view_of(p.a, p.M, p.K, 1, wgrad), vb = view_of(p.b, p.N, p.K, grouped ? p.E : 1, wgrad);
+  const bool any = p.K > 0 && !(grouped && p.E == 0);    // anything to multiply
+  if (any) {
+    unsigned char* ws = static_cast<unsigned char*>(workspace);
+    const LayOut la = lay_out_of(va, ws), lb = lay_out_of(vb, ws);
+    const int64_t work = la.vectors * la.chunks + lb.vectors * lb.chunks, ctas = (work + 255) / 256;
+    if (work > 0) lay_out_kernel<<<(unsigned)(ctas < 16384 ? ctas : 16384), 256, 0, st>>>(la, lb);
+  }
+  const int64_t sms = emu_ops_sm_count(), kb = (p.K + kBlock - 1) / kBlock;
+  const int64_t groups = wgrad ? p.E : 1;
+  auto up = [](int64_t n, int64_t d) { return (n + d - 1) / d; };
+  // which form
+  int BN = 256, slices = 1;
+  const int64_t rows = grouped ? up(p.M, p.E > 0 ? p.E : 1) : p.M;                // of the tokens' side, about
+  if (up(p.M, 128) * up(p.N, 256) * groups < sms || (grouped && rows <= 128)) {
+    BN = va.mn || rows > 64 ? 128 : rows > 32 ? 64 : 32;
+    if (!grouped && !wgrad) {
+      const int64_t tiles = up(p.N, 128) * up(p.M, BN);
+      while (slices < 8 && tiles * slices * 2 <= sms && kb / (slices * 2) >= 2) slices *= 2;
+    }
+  }
+  const bool swap = BN < 256;
+  BlockTcParams q = {};
+  q.kind = p.kind;
+  q.l = swap ? side_of(p.b, p.N, vb.mn) : side_of(p.a, p.M, va.mn);
+  q.c = swap ? side_of(p.a, p.M, va.mn) : side_of(p.b, p.N, vb.mn);
+  const emu_block_operand_t& ol = swap ? p.b : p.a;
+  const emu_block_operand_t& oc = swap ? p.a : p.b;
+  q.idesc = (1u << 4) | ((ol.format == EMU_E5M2 ? 1u : 0u) << 7) | ((oc.format == EMU_E5M2 ? 1u : 0u) << 10) | ((uint32_t)q.l.mn << 15) |
+            ((uint32_t)q.c.mn << 16) | ((uint32_t)(BN >> 3) << 17) | (8u << 24);
+  const int64_t tl = up(q.l.rows, 128), tc = up(q.c.rows, BN);
+  // the most tiles there can be: of ragged groups, each may add one
+  const int64_t tiles = grouped ? (swap ? tl * (tc + p.E) : (tl + p.E) * tc) : tl * tc * groups;
+  if (tiles * slices >= (int64_t)1 << 31) return emu_ops_fail(EMU_EUNSUPPORTED, "too many tiles");
+  q.tiles_l = (int)tl;
+  q.tiles_c = (int)tc;
+  q.k_blocks = any ? (int)kb : 0;
+  q.slices = slices;
+  q.offsets = p.offsets;
+  q.E = p.E;
+  q.T = (int)(wgrad ? p.K : p.M);
+  q.zero_rest = p.zero_rest;
+  q.out = p.out;
+  q.out_type = p.out_type;
+  q.ldl = swap ? 1 : p.N;
+  q.ldc = swap ? p.N : 1;
+  q.out_group = p.M * p.N;
+  CUtensorMap map_l = {}, map_c = {};
+  if (any) {
+    int rc = codes_map(&map_l, swap ? vb : va, 128);
+    const CodesView& vc = swap ? va : vb;
+    if (rc == EMU_OK) rc = codes_map(&map_c, vc, vc.mn ? 128 : BN);
+    if (rc != EMU_OK) return rc;
+  }
+  // a lane's scale alone, where the columns of a warp share theirs; else the lanes' in the columns' if they all share it
+  const bool tokens_c = grouped && swap, tokens_l = grouped && !swap;
+  const int mode = q.c.shift == 7 && !tokens_c ? kScaleLane : q.l.shift == 7 && !tokens_l ? kScaleColumns : kScaleBoth;
+  if (BN == 256) return launch_tc<256>(q, mode, tiles, map_l, map_c, st);
+  if (BN == 128) return launch_tc<128>(q, mode, tiles, map_l, map_c, st);
+  if (BN == 64) return launch_tc<64>(q, mode, tiles, map_l, map_c, st);
+  return launch_tc<32>(q, mode, tiles, map_l, map_c, st);
 }
 
 // ------------------------------------------------------------------------------- checks
@@ -115,9 +222,9 @@ int check_sizes(emu_out_t type, int64_t M, int64_t N, int64_t K, int64_t E) {
   if (!is_float_type(type)) return emu_ops_fail(EMU_EINVAL, "the output is fp32, bf16 or fp16 (got %d)", (int)type);
   if (M < 0 || N < 0 || K < 0 || E < 0)
     return emu_ops_fail(EMU_EINVAL, "negative size (%lld, %lld, %lld, %lld)", (long long)M, (long long)N, (long long)K, (long long)E);
-  const int64_t most = (int64_t)1 << 31;
-  if (M >= most || N >= most || K >= most) return emu_ops_fail(EMU_EUNSUPPORTED, "sizes must be below 2^31");
-  if (E > kMaxExperts) return emu_ops_fail(EMU_EUNSUPPORTED, "more than %lld experts", (long long)kMaxExperts);
+  const int64_t most = ((int64_t)1 << 31) - 256;         // so that a tile's end is a 32-bit number
+  if (M >= most || N >= most || K >= most) return emu_ops_fail(EMU_EUNSUPPORTED, "sizes must be below 2^31 - 256");
+  if (E > kMaxExperts) return emu_ops_fail(EMU_EUNSUPPORTED, "more than %d experts", kMaxExperts);
   return EMU_OK;
 }
 int check_out(void* out, emu_out_t type, int64_t rows, int64_t cols, const int32_t* offsets, int64_t E, void* workspace,
@@ -138,15 +245,29 @@ int check_out(void* out, emu_out_t type, int64_t rows, int64_t cols, const int32
 
 using namespace emu_ops;
 
+int emu_ops_block_status(int* status, bool reset) {
+  const int zero = 0;
+  if (cudaMemcpyFromSymbol(status, g_block_status, sizeof *status) != cudaSuccess ||
+      (reset && cudaMemcpyToSymbol(g_block_status, &zero, sizeof zero) != cudaSuccess))
+    return emu_ops_launched("emu_ops_device_status");
+  return EMU_OK;
+}
+
 extern "C" {
 
-size_t emu_block_mm_workspace_bytes(const emu_block_operand_t*, const emu_block_operand_t*, int64_t, int64_t, int64_t) { return 0; }
-size_t emu_grouped_block_mm_workspace_bytes(const emu_block_operand_t*, const emu_block_operand_t*, int64_t, int64_t, int64_t,
-                                            int64_t) {
-  return 0;
+size_t emu_block_mm_workspace_bytes(const emu_block_operand_t* a, const emu_block_operand_t* b, int64_t M, int64_t N, int64_t K) {
+  if (!a || !b || M < 1 || N < 1 || K < 1) return 0;
+  return view_of(*a, M, K, 1, false).laid_out() + view_of(*b, N, K, 1, false).laid_out();
 }
-size_t emu_grouped_block_wgrad_workspace_bytes(const emu_block_operand_t*, const emu_block_operand_t*, int64_t, int64_t, int64_t) {
-  return 0;
+size_t emu_grouped_block_mm_workspace_bytes(const emu_block_operand_t* a, const emu_block_operand_t* b, int64_t T, int64_t N, int64_t K,
+                                            int64_t E) {
+  if (!a || !b || T < 1 || N < 1 || K < 1 || E < 1) return 0;
+  return view_of(*a, T, K, 1, false).laid_out() + view_of(*b, N, K, E, false).laid_out();
+}
+size_t emu_grouped_block_wgrad_workspace_bytes(const emu_block_operand_t* a, const emu_block_operand_t* b, int64_t T, int64_t N,
+                                               int64_t K) {
+  if (!a || !b || T < 1 || N < 1 || K < 1) return 0;
+  return view_of(*a, N, T, 1, true).laid_out() + view_of(*b, K, T, 1, true).laid_out();
 }
 
 int emu_block_scaled_mm(const emu_block_operand_t* a, const emu_block_operand_t* b, int64_t M, int64_t N, int64_t K, void* out,
@@ -159,8 +280,8 @@ int emu_block_scaled_mm(const emu_block_operand_t* a, const emu_block_operand_t*
   const size_t need = emu_block_mm_workspace_bytes(a, b, M, N, K);
   rc = check_out(out, out_dtype, M, N, nullptr, -1, workspace, workspace_bytes, need, *a, {M, K, 1}, *b, {N, K, 1});
   if (rc != EMU_OK) return rc;
-  BlockMm p = {*a, *b, BlockKind::dense, M, N, K, nullptr, 1, false, out, (int)out_dtype};
-  return run_block_mm(p, static_cast<cudaStream_t>(stream));
+  BlockMm p = {*a, *b, BlockKind::dense, M, N, K, nullptr, 0, false, out, (int)out_dtype};
+  return run_block_mm(p, workspace, static_cast<cudaStream_t>(stream));
 }
 
 int emu_grouped_block_scaled_mm(const emu_block_operand_t* a, const emu_block_operand_t* b, const int32_t* offsets, int64_t E,
@@ -177,7 +298,7 @@ int emu_grouped_block_scaled_mm(const emu_block_operand_t* a, const emu_block_op
   rc = check_out(out, out_dtype, T, N, offsets, E, workspace, workspace_bytes, need, *a, {T, K, 1}, *b, {N, K, E});
   if (rc != EMU_OK) return rc;
   BlockMm p = {*a, *b, BlockKind::grouped, T, N, K, offsets, (int)E, zero_rest != 0, out, (int)out_dtype};
-  return run_block_mm(p, static_cast<cudaStream_t>(stream));
+  return run_block_mm(p, workspace, static_cast<cudaStream_t>(stream));
 }
 
 int emu_grouped_block_scaled_wgrad(const emu_block_operand_t* a, const emu_block_operand_t* b, const int32_t* offsets, int64_t E,
@@ -195,7 +316,7 @@ int emu_grouped_block_scaled_wgrad(const emu_block_operand_t* a, const emu_block
   rc = check_out(out, out_dtype, E * N, K, offsets, E, workspace, workspace_bytes, need, *a, {N, T, 1}, *b, {K, T, 1});
   if (rc != EMU_OK) return rc;
   BlockMm p = {*a, *b, BlockKind::wgrad, N, K, T, offsets, (int)E, false, out, (int)out_dtype};
-  return run_block_mm(p, static_cast<cudaStream_t>(stream));
+  return run_block_mm(p, workspace, static_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

@@ -1,0 +1,545 @@
+// ops_block_tc.cuh -- the FP8 products with block scales on the 5th-generation tensor cores.
+//
+// tcgen05.mma kind::f8f6f4 multiplies the codes as they are; the four MMAs of a block of 128 of K
+// leave its sum in tensor memory (fp32; measured within 2^-21.5 of the sum of the products' magnitudes),
+// and eight warps read it back, multiply it by the block's two scales and add it to sums in
+// registers while the next block is multiplied.  One side of the product lies along the 128 lanes
+// (L), the other along the columns (C) of the tensor memory; either may be K-major or have its rows
+// contiguous: shared memory holds a block as 128 rows of 128 codes under the 128-byte swizzle both
+// ways, and the instruction descriptor says which.
+#pragma once
+#include "ops_block.cuh"
+
+namespace emu_ops {
+
+constexpr int kTcThreads8 = 384;                         // warps: loads, MMAs, tensor memory, zeros, eight that read
+constexpr int kMaxExperts = 1024;
+
+enum class BlockKind { dense, grouped, wgrad };
+// how the scales enter: one value for a lane's columns; a vector over the columns, the lanes' one value in it; both vectors
+enum ScaleMode { kScaleLane = 0, kScaleColumns = 1, kScaleBoth = 2 };
+
+struct BlockSide {
+  const float* scale;
+  int shift;                                             // of a row to its scale: 0 or 7
+  int64_t rs, ks, gs;                                    // the scales' strides by row, block of K, group
+  int rows;
+  int mn;                                                // rows contiguous instead of K
+};
+struct BlockTcParams {
+  BlockSide l, c;
+  int tiles_l, tiles_c, k_blocks, slices;
+  BlockKind kind;
+  const int32_t* offsets; int E, T;                      // groups of tokens (grouped: of rows, wgrad: of K)
+  int zero_rest;
+  void* out; int out_type;
+  int64_t ldl, ldc, out_group;                           // out[l * ldl + c * ldc], one of them 1
+  uint32_t idesc;
+};
+template <int BN> struct BlockTcShape {
+  static constexpr bool SWAP = BN < 256;                 // the output's rows are the columns C
+  static constexpr int NS = BN == 256 ? 4 : BN == 128 ? 6 : 8, STAGE = 128 * 128 + BN * 128, NB = BN == 256 ? 2 : 4;
+  static constexpr int OWN = BN / 2, CHUNK = OWN < 32 ? OWN : 32, TMEM = NB * BN;
+  static constexpr int OUT = NS * STAGE, CS = OUT + (SWAP ? 0 : 8 * 32 * 64), BARS = CS + 2 * BN * 4;
+  static constexpr int TABLE = BARS + 8 * (3 * NS + 2 * NB + 3) + 8 + 2 * 12 * 4;
+  static constexpr int smem(int E) { return TABLE + 2 * (E + 1) * 4 + 1024; }
+};
+static_assert(BlockTcShape<256>::smem(kMaxExperts) <= kMaxSmem && BlockTcShape<128>::smem(kMaxExperts) <= kMaxSmem &&
+              BlockTcShape<64>::smem(kMaxExperts) <= kMaxSmem && BlockTcShape<32>::smem(kMaxExperts) <= kMaxSmem, "one CTA an SM");
+
+__device__ __forceinline__ float scale_of(const BlockSide& s, int64_t row, int kb, int group) {
+  return __ldg(s.scale + group * s.gs + (row >> s.shift) * s.rs + kb * s.ks);
+}
+__device__ __forceinline__ void tma_load3(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
+      ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar) : "memory");
+}
+// shared-memory matrix descriptor: rows of 128 bytes under the 128-byte swizzle, eight of them 1024 bytes apart from
+// the next eight; with rows contiguous, 128 of them 16 KB apart from the next 128
+__device__ __forceinline__ uint64_t desc8(uint32_t addr) {
+  return (uint64_t)((addr >> 4) & 0x3FFFu) | (1024ull << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
+}
+__device__ __forceinline__ void mma8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t add) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(add)
+      : "memory");
+}
+// columns of this warp's 32 lanes, asked for, and waited for (whatever was asked for before)
+__device__ __forceinline__ void tmem_ask(uint32_t addr, float (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]), "=f"(r[8]),
+        "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15]), "=f"(r[16]),
+        "=f"(r[17]), "=f"(r[18]), "=f"(r[19]), "=f"(r[20]), "=f"(r[21]), "=f"(r[22]), "=f"(r[23]), "=f"(r[24]),
+        "=f"(r[25]), "=f"(r[26]), "=f"(r[27]), "=f"(r[28]), "=f"(r[29]), "=f"(r[30]), "=f"(r[31])
+      : "r"(addr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_ask(uint32_t addr, float (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]), "=f"(r[8]),
+        "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15])
+      : "r"(addr)
+      : "memory");
+}
+template <int N> __device__ __forceinline__ void tmem_wait(float (&r)[N]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < N; i += 8)                         // nothing that uses them goes before the wait
+    asm volatile("" : "+f"(r[i]), "+f"(r[i + 1]), "+f"(r[i + 2]), "+f"(r[i + 3]), "+f"(r[i + 4]), "+f"(r[i + 5]), "+f"(r[i + 6]),
+                      "+f"(r[i + 7]));
+}
+
+// The groups' first rows (within [0, T], none below the one before it) and, of `tile` rows each, how many tiles come
+// before them: a scan by all threads, three entries each.
+__device__ __forceinline__ void group_table(const int32_t* offsets, int E, int T, int tile, int* start, int* before, int* part) {
+  static_assert(kTcThreads8 * 3 > kMaxExperts, "three entries a thread");
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  int v[3];
+#pragma unroll
+  for (int j = 0; j < 3; ++j) {
+    const int i = tid * 3 + j, at = i <= E ? __ldg(offsets + i) : 0;
+    v[j] = at < 0 ? 0 : at > T ? T : at;
+    if (j > 0) v[j] = v[j] > v[j - 1] ? v[j] : v[j - 1];
+  }
+  int top = v[2];
+#pragma unroll
+  for (int o = 1; o < 32; o *= 2) {
+    const int w = __shfl_up_sync(0xFFFFFFFFu, top, o);
+    if (lane >= o && w > top) top = w;
+  }
+  int ahead = __shfl_up_sync(0xFFFFFFFFu, top, 1);
+  if (lane == 0) ahead = 0;
+  if (lane == 31) part[warp] = top;
+  __syncthreads();
+  for (int w = 0; w < warp; ++w) ahead = part[w] > ahead ? part[w] : ahead;
+#pragma unroll
+  for (int j = 0; j < 3; ++j)
+    if (tid * 3 + j <= E) start[tid * 3 + j] = v[j] > ahead ? v[j] : ahead;
+  __syncthreads();
+  int n[3], sum = 0;
+#pragma unroll
+  for (int j = 0; j < 3; ++j) {
+    const int i = tid * 3 + j;
+    n[j] = i < E ? (start[i + 1] - start[i] + tile - 1) / tile : 0;
+    sum += n[j];
+  }
+  int upto = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o *= 2) {
+    const int w = __shfl_up_sync(0xFFFFFFFFu, upto, o);
+    if (lane >= o) upto += w;
+  }
+  if (lane == 31) part[12 + warp] = upto;
+  __syncthreads();
+  int base = upto - sum;
+  for (int w = 0; w < warp; ++w) base += part[12 + w];
+#pragma unroll
+  for (int j = 0; j < 3; ++j) {
+    if (tid * 3 + j <= E) before[tid * 3 + j] = base;
+    base += n[j];
+  }
+  __syncthreads();
+}
+
+struct BlockTile {
+  int l0, c0, l_end, c_end, group;
+  int kb0, kb1, lo, hi;                                  // blocks of K; wgrad: of them the tokens [lo, hi)
+};
+// eight rows of tiles at a time, column by column, so that the CTAs at work share both sides' rows
+__device__ __forceinline__ void tile_order(int tile, int tiles_l, int tiles_c, int& l, int& c) {
+  const int group = tile / (8 * tiles_c), first = group * 8, rows = tiles_l - first < 8 ? tiles_l - first : 8;
+  const int in = tile - group * 8 * tiles_c;
+  l = first + in % rows;
+  c = in / rows;
+}
+template <int BN> __device__ __forceinline__ int tile_count(const BlockTcParams& p, const int* before) {
+  if (p.kind == BlockKind::dense) return p.tiles_l * p.tiles_c * p.slices;
+  if (p.kind == BlockKind::wgrad) return p.tiles_l * p.tiles_c * p.E;
+  return before[p.E] * (BlockTcShape<BN>::SWAP ? p.tiles_l : p.tiles_c);
+}
+template <int BN> __device__ __forceinline__ BlockTile tile_at(const BlockTcParams& p, const int* start, const int* before, int tile) {
+  BlockTile t;
+  t.group = 0;
+  t.kb0 = 0;
+  t.kb1 = p.k_blocks;
+  t.lo = 0;
+  t.hi = 0x7FFFFFFF;
+  t.l_end = p.l.rows;
+  t.c_end = p.c.rows;
+  int l, c;
+  if (p.kind == BlockKind::grouped) {
+    constexpr bool SWAP = BlockTcShape<BN>::SWAP;
+    const int weights = SWAP ? p.tiles_l : p.tiles_c, at = tile / weights;
+    int a = 0, b = p.E;                                  // before[a] <= at < before[b]
+    while (b - a > 1) {
+      const int m = (a + b) / 2;
+      if (before[m] <= at) a = m;
+      else b = m;
+    }
+    t.group = a;
+    const int in = tile - before[a] * weights, n = before[a + 1] - before[a];
+    const int token = in % n, weight = in / n;           // an expert's tiles that share weights one after the other
+    if (SWAP) {
+      l = weight;
+      t.c0 = start[a] + token * BN;
+      t.c_end = start[a + 1];
+      t.l0 = l * 128;
+    } else {
+      c = weight;
+      t.l0 = start[a] + token * 128;
+      t.l_end = start[a + 1];
+      t.c0 = c * BN;
+    }
+    return t;
+  }
+  if (p.kind == BlockKind::wgrad) {
+    t.group = tile / (p.tiles_l * p.tiles_c);
+    tile -= t.group * p.tiles_l * p.tiles_c;
+    t.lo = start[t.group];
+    t.hi = start[t.group + 1];
+    t.kb0 = t.lo / kBlock;
+    t.kb1 = t.hi > t.lo ? (t.hi + kBlock - 1) / kBlock : t.kb0;
+  } else if (p.slices > 1) {
+    const int slice = tile % p.slices;
+    tile /= p.slices;
+    t.kb0 = p.k_blocks * slice / p.slices;
+    t.kb1 = p.k_blocks * (slice + 1) / p.slices;
+  }
+  tile_order(tile, p.tiles_l, p.tiles_c, l, c);
+  t.l0 = l * 128;
+  t.c0 = c * BN;
+  return t;
+}
+
+template <class T> __device__ __forceinline__ void put(void* out, int64_t i, float v) { static_cast<T*>(out)[i] = from_f<T>(v); }
+__device__ __forceinline__ void put(void* out, int type, int64_t i, float v) {
+  if (type == EMU_OUT_F32) put<float>(out, i, v);
+  else if (type == EMU_OUT_BF16) put<__nv_bfloat16>(out, i, v);
+  else put<__half>(out, i, v);
+}
+// zeros over the elements [from, to) of the output, by `count` threads
+__device__ __forceinline__ void put_zeros(void* out, int type, int64_t from, int64_t to, int64_t who, int64_t count) {
+  for (int64_t i = from + who; i < to; i += count) put(out, type, i, 0.0f);
+}
+
+// A warp's 32 rows (lanes) x 128 columns of sums to row-major memory: 64 bytes of each row at a time go through shared
+// memory (16 bytes a lane, a row's chunks permuted by its number: no two lanes of a phase meet in a bank), so
+// that whole sectors are stored, or, where rows are not 16-byte aligned, elements.
+template <class T>
+__device__ __forceinline__ void write_rows(const BlockTcParams& p, const f2 (&acc)[64], unsigned char* stage, int64_t row0, int rows,
+                                           int64_t n0, int64_t group, int lane) {
+  constexpr int COLS = 64 / sizeof(T), VEC = 16 / sizeof(T);
+  T* const out = static_cast<T*>(p.out) + group * p.out_group;
+  const int64_t N = p.c.rows;
+  const bool vec = N % VEC == 0 && p.ldl % VEC == 0 && (reinterpret_cast<uintptr_t>(out) & 15u) == 0;
+#pragma unroll
+  for (int c = 0; c < 128; c += COLS) {
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < COLS; i += VEC) {
+      float v[VEC];
+#pragma unroll
+      for (int j = 0; j < VEC; j += 2) halves(acc[(c + i + j) / 2], v[j], v[j + 1]);
+      store_f<T, VEC>(reinterpret_cast<T*>(stage + lane * 64 + (((i / VEC) ^ ((lane >> 1) & 3)) * 16)), v);
+    }
+    __syncwarp();
+    if (vec) {
+      const int64_t n = n0 + c + (lane & 3) * VEC;
+      if (n < N) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int r = k * 8 + (lane >> 2);
+          if (r < rows)
+            *reinterpret_cast<uint4*>(out + (row0 + r) * p.ldl + n) =
+                *reinterpret_cast<const uint4*>(stage + r * 64 + (((lane & 3) ^ ((r >> 1) & 3)) * 16));
+        }
+      }
+    } else {
+      constexpr int EACH = 32 / COLS;                    // rows a warp stores at once
+      const int in = lane % COLS;
+      if (n0 + c + in < N) {
+#pragma unroll 4
+        for (int r = lane / COLS; r < rows; r += EACH)
+          out[(row0 + r) * p.ldl + n0 + c + in] =
+              *reinterpret_cast<const T*>(stage + r * 64 + (((in / VEC) ^ ((r >> 1) & 3)) * 16) + (in % VEC) * sizeof(T));
+      }
+    }
+  }
+}
+
+// Persistent: one CTA an SM, tiles of 128 x BN outputs in turn.  Warp 0 loads the blocks by TMA, warp 1 issues the
+// MMAs, warp 2 owns the tensor memory, warp 3 clears the tokens of other experts in a weights' gradient's first
+// and last block, warps 4 to 11 scale and add: each holds 32 lanes x BN / 2 columns of sums in registers.
+// Several slices of K (dense, BN < 256): the CTAs of a cluster, which share out the columns at the end.  All waits
+// are bounded; a role that gives up sets the status and takes the others along.
+template <int BN, int MODE>
+__global__ void __launch_bounds__(kTcThreads8, 1)
+block_tc_kernel(const __grid_constant__ BlockTcParams p, const __grid_constant__ CUtensorMap map_l,
+                const __grid_constant__ CUtensorMap map_c) {
+  using SH = BlockTcShape<BN>;
+  constexpr int NS = SH::NS, NB = SH::NB, OWN = SH::OWN, CHUNK = SH::CHUNK;
+  extern __shared__ unsigned char raw[];
+  unsigned char* const smem = raw + ((1024u - (smem_addr(raw) & 1023u)) & 1023u);
+  const uint32_t base = smem_addr(smem);
+  const uint32_t full = base + SH::BARS, empty = full + 8 * NS, fixed = empty + 8 * NS, tfull = fixed + 8 * NS, tempty = tfull + 8 * NB,
+                 cfull = tempty + 8 * NB, drained = cfull + 16;
+  uint32_t* const slot = reinterpret_cast<uint32_t*>(smem + SH::BARS + 8 * (3 * NS + 2 * NB + 3));
+  volatile int* const given_up = reinterpret_cast<volatile int*>(slot + 1);
+  int* const part = reinterpret_cast<int*>(slot + 2);
+  int* const start = reinterpret_cast<int*>(smem + SH::TABLE);
+  int* const before = start + p.E + 1;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+
+  if (tid == 0) {
+    for (int i = 0; i < NS; ++i) {
+      bar_init(full + 8 * i, 1);
+      bar_init(empty + 8 * i, 1);
+      bar_init(fixed + 8 * i, 1);
+    }
+    for (int i = 0; i < NB; ++i) {
+      bar_init(tfull + 8 * i, 1);
+      bar_init(tempty + 8 * i, 8);                       // one arrival a reading warp
+    }
+    for (int i = 0; i < 2; ++i) bar_init(cfull + 8 * i, 4);   // the columns' scales, one arrival a warp of the half
+    bar_init(drained, 1);
+    *given_up = 0;
+    bar_init_fence();
+  }
+  if (warp == 2) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(slot)), "r"(SH::TMEM) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  if (p.kind != BlockKind::dense) group_table(p.offsets, p.E, p.T, SH::SWAP ? BN : 128, start, before, part);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *slot;
+  const int tiles = tile_count<BN>(p, before);
+
+  if (warp < 4) {
+    if constexpr (BN == 256) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+    if (warp == 0 && lane == 0) {
+      uint32_t it = 0;
+      bool ok = true;
+      for (int tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
+        const BlockTile t = tile_at<BN>(p, start, before, tile);
+        const int gl = p.kind == BlockKind::grouped && SH::SWAP ? t.group : 0, gc = p.kind == BlockKind::grouped && !SH::SWAP ? t.group : 0;
+        for (int kb = t.kb0; kb < t.kb1; ++kb, ++it) {
+          const uint32_t s = it % NS, bar = full + 8 * s, dst = base + s * SH::STAGE;
+          if (it >= NS && !bar_wait_all(empty + 8 * s, (it / NS - 1) & 1, given_up)) {
+            ok = false;
+            break;
+          }
+          bar_expect(bar, SH::STAGE);
+          tma_load3(dst, &map_l, p.l.mn ? t.l0 : kb * kBlock, p.l.mn ? kb * kBlock : t.l0, gl, bar);
+          if (BN >= 128 && p.c.mn) {
+#pragma unroll
+            for (int x = 0; x < BN / 128; ++x) tma_load3(dst + (1 + x) * 16384, &map_c, t.c0 + x * 128, kb * kBlock, gc, bar);
+          } else {
+            tma_load3(dst + 16384, &map_c, kb * kBlock, t.c0, gc, bar);
+          }
+        }
+      }
+      if (!ok)                                           // the loads issued last, one stage each at most
+        for (uint32_t i = it > NS ? it - NS : 0; i < it; ++i) (void)bar_wait(full + 8 * (i % NS), (i / NS) & 1);
+    } else if (warp == 1 && lane == 0) {
+      uint32_t it = 0;
+      bool ok = true;
+      const uint32_t step_l = p.l.mn ? 256 : 2, step_c = p.c.mn ? 256 : 2;   // 32 of K, in 16 bytes
+      for (int tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
+        const BlockTile t = tile_at<BN>(p, start, before, tile);
+        for (int kb = t.kb0; kb < t.kb1; ++kb, ++it) {
+          const uint32_t s = it % NS, buf = it % NB;
+          ok = (it < NB || bar_wait_all(tempty + 8 * buf, (it / NB - 1) & 1, given_up)) && bar_wait_all(full + 8 * s, (it / NS) & 1, given_up);
+          if (ok && p.kind == BlockKind::wgrad) ok = bar_wait_all(fixed + 8 * s, (it / NS) & 1, given_up);
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t dl = desc8(base + s * SH::STAGE), dc = desc8(base + s * SH::STAGE + 16384);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) mma8(tmem + buf * BN, dl + k * step_l, dc + k * step_c, p.idesc, k > 0);
+          tc_commit(empty + 8 * s);
+          tc_commit(tfull + 8 * buf);
+        }
+      }
+      tc_commit(drained);                                // the MMAs are done before the tensor memory goes back
+      (void)bar_wait(drained, 0);
+    } else if (warp == 3 && p.kind == BlockKind::wgrad) {
+      uint32_t it = 0;
+      bool ok = true;
+      for (int tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
+        const BlockTile t = tile_at<BN>(p, start, before, tile);
+        for (int kb = t.kb0; kb < t.kb1; ++kb, ++it) {
+          const uint32_t s = it % NS;
+          ok = __all_sync(0xFFFFFFFFu, bar_wait_all(full + 8 * s, (it / NS) & 1, given_up));
+          if (!ok) break;
+          const int first = t.lo - kb * kBlock, last = t.hi - kb * kBlock;   // of the block's rows, [first, last) count
+          if (first > 0 || last < kBlock) {
+            uint4* const rows = reinterpret_cast<uint4*>(smem + s * SH::STAGE);
+            for (int i = lane; i < SH::STAGE / 16; i += 32) {
+              const int r = (i >> 3) & 127;              // a token's codes of 128 rows are 128 bytes
+              if (r < first || r >= last) rows[i] = make_uint4(0u, 0u, 0u, 0u);
+            }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          }
+          __syncwarp();
+          if (lane == 0) bar_arrive(fixed + 8 * s);
+        }
+      }
+    }
+    __syncwarp();
+  } else {
+    if constexpr (BN == 256) asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
+    const int quad = warp & 3, half = (warp - 4) >> 2, mine = quad * 32 + lane;
+    float* const cs = reinterpret_cast<float*>(smem + SH::CS) + half * OWN;   // the columns' scales, two slots BN apart
+    uint32_t it = 0;
+    bool ok = true, met = false;
+    for (int tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
+      const BlockTile t = tile_at<BN>(p, start, before, tile);
+      const int gl = p.kind == BlockKind::grouped && SH::SWAP ? t.group : 0, gc = p.kind == BlockKind::grouped && !SH::SWAP ? t.group : 0;
+      const int l = t.l0 + mine, c = t.c0 + half * OWN;
+      const bool l_in = l < t.l_end;
+      // the scales of a block, asked for two blocks ahead
+      const int c_at = MODE == kScaleLane ? c : c + mine;
+      const bool c_in = c_at < t.c_end && (MODE == kScaleLane || mine < OWN);
+      auto ask = [&](int kb, float& rl, float& rc) {
+        rl = rc = 0.0f;
+        if (kb < t.kb1) {
+          if (MODE == kScaleColumns) {
+            if (c_in) rl = scale_of(p.l, t.l0, kb, gl);
+          } else if (l_in) {
+            rl = scale_of(p.l, l, kb, gl);
+          }
+          if (c_in) rc = scale_of(p.c, c_at, kb, gc);
+        }
+      };
+      float rl0, rc0, rl1, rc1;
+      ask(t.kb0, rl0, rc0);
+      ask(t.kb0 + 1, rl1, rc1);
+      f2 acc[OWN / 2];
+#pragma unroll
+      for (int i = 0; i < OWN / 2; ++i) acc[i] = 0ull;
+      for (int kb = t.kb0; kb < t.kb1; ++kb, ++it) {
+        const uint32_t buf = it % NB;
+        const float rl = rl0, rc = rc0;
+        rl0 = rl1;
+        rc0 = rc1;
+        ask(kb + 2, rl1, rc1);
+        float* const cv = cs + (it & 1) * BN;
+        if (MODE != kScaleLane) {
+          if (mine < OWN) cv[mine] = MODE == kScaleColumns ? rl * rc : rc;
+          __syncwarp();
+          if (lane == 0) bar_arrive(cfull + 8 * half);
+          ok = bar_wait_all(cfull + 8 * half, it & 1, given_up);
+        }
+        ok = __all_sync(0xFFFFFFFFu, ok && bar_wait_all(tfull + 8 * buf, (it / NB) & 1, given_up));
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t at = tmem + ((uint32_t)(quad * 32) << 16) + buf * BN + half * OWN;
+        const f2 by = MODE == kScaleLane ? pair(rl * rc, rl * rc) : pair(rl, rl);
+        float r[2][CHUNK];
+        tmem_ask(at, r[0]);
+#pragma unroll
+        for (int k = 0; k < OWN / CHUNK; ++k) {
+          tmem_wait(r[k & 1]);
+          if (k + 1 < OWN / CHUNK) {
+            tmem_ask(at + (k + 1) * CHUNK, r[(k + 1) & 1]);
+          } else {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) bar_arrive(tempty + 8 * buf);
+          }
+#pragma unroll
+          for (int i = 0; i < CHUNK; i += 4) {
+            f2& a0 = acc[(k * CHUNK + i) / 2];
+            f2& a1 = acc[(k * CHUNK + i) / 2 + 1];
+            const f2 x0 = pair(r[k & 1][i], r[k & 1][i + 1]), x1 = pair(r[k & 1][i + 2], r[k & 1][i + 3]);
+            if (MODE == kScaleLane) {
+              a0 = fma2(x0, by, a0);
+              a1 = fma2(x1, by, a1);
+            } else {
+              const float4 s = *reinterpret_cast<const float4*>(cv + k * CHUNK + i);
+              const f2 s0 = pair(s.x, s.y), s1 = pair(s.z, s.w);
+              a0 = fma2(MODE == kScaleBoth ? mul2(x0, by) : x0, s0, a0);
+              a1 = fma2(MODE == kScaleBoth ? mul2(x1, by) : x1, s1, a1);
+            }
+          }
+        }
+      }
+      if (!ok) break;
+      if constexpr (!SH::SWAP) {
+        unsigned char* const stage = smem + SH::OUT + (warp - 4) * 32 * 64;
+        const int64_t row0 = t.l0 + quad * 32;
+        const int rows = t.l_end - row0 < 32 ? (int)(t.l_end - row0) : 32;
+        const int64_t group = p.kind == BlockKind::wgrad ? t.group : 0;
+        if (p.out_type == EMU_OUT_F32) write_rows<float>(p, acc, stage, row0, rows, c, group, lane);
+        else if (p.out_type == EMU_OUT_BF16) write_rows<__nv_bfloat16>(p, acc, stage, row0, rows, c, group, lane);
+        else write_rows<__half>(p, acc, stage, row0, rows, c, group, lane);
+      } else if (p.slices == 1) {
+        auto write = [&](auto* out) {
+          using T = std::remove_pointer_t<decltype(out)>;
+          T* const to = out + (p.kind == BlockKind::wgrad ? t.group * p.out_group : 0) + l * p.ldl;
+#pragma unroll
+          for (int i = 0; i < OWN; i += 2) {
+            float a, b;
+            halves(acc[i / 2], a, b);
+            if (l_in && c + i < t.c_end) to[(c + i) * p.ldc] = from_f<T>(a);
+            if (l_in && c + i + 1 < t.c_end) to[(c + i + 1) * p.ldc] = from_f<T>(b);
+          }
+        };
+        if (p.out_type == EMU_OUT_F32) write(static_cast<float*>(p.out));
+        else if (p.out_type == EMU_OUT_BF16) write(static_cast<__nv_bfloat16*>(p.out));
+        else write(static_cast<__half*>(p.out));
+      } else {
+        // slice s adds up columns s BN / S on: every slice writes its sums of them there, [S][BN / S][128], in the place of
+        // the operands, once that CTA is past its last MMA
+        cluster_sync();
+        met = true;
+        const int per = BN / p.slices, slice = tile % p.slices;
+        float* const sums = reinterpret_cast<float*>(smem);
+#pragma unroll
+        for (int i = 0; i < OWN; ++i) {
+          const int j = half * OWN + i, owner = j / per;
+          float a, b;
+          halves(acc[i / 2], a, b);
+          asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(in_cluster(sums + (slice * per + j % per) * 128 + mine, owner)),
+                       "f"(i & 1 ? b : a) : "memory");
+        }
+      }
+    }
+    if (p.kind == BlockKind::grouped && p.zero_rest) {
+      const int64_t N = SH::SWAP ? p.l.rows : p.c.rows, who = (int64_t)blockIdx.x * 256 + tid - 128, count = (int64_t)gridDim.x * 256;
+      put_zeros(p.out, p.out_type, 0, start[0] * N, who, count);
+      put_zeros(p.out, p.out_type, start[p.E] * N, (int64_t)p.T * N, who, count);
+    }
+    __syncwarp();
+    if (SH::SWAP && p.slices > 1 && !met) cluster_sync();   // a warp that gave up goes past the first barrier too
+  }
+  if constexpr (SH::SWAP) {
+    if (p.slices > 1) {                                  // one tile a CTA
+      if (warp < 4) cluster_sync();
+      cluster_sync();
+      const BlockTile t = tile_at<BN>(p, start, before, blockIdx.x);
+      const int per = BN / p.slices, slice = (int)blockIdx.x % p.slices;
+      const float* const sums = reinterpret_cast<const float*>(smem);
+      if (!*given_up)
+        for (int i = tid; i < per * 128; i += kTcThreads8) {
+          const int l = t.l0 + i % 128, c = t.c0 + slice * per + i / 128;
+          float v = 0.0f;
+          for (int s = 0; s < p.slices; ++s) v += sums[s * per * 128 + i];
+          if (l < t.l_end && c < t.c_end) put(p.out, p.out_type, l * p.ldl + c * p.ldc, v);
+        }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (tid == 0 && *given_up) atomicExch(&g_block_status, 1);
+  if (warp == 2) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(SH::TMEM) : "memory");
+}
+
+}  // namespace emu_ops

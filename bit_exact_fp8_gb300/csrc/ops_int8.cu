@@ -66,68 +66,6 @@ template <int N> __device__ __forceinline__ bool stores_together(const Int8Param
   return p.N % N == 0 && (reinterpret_cast<uintptr_t>(p.out) & (N * es - 1)) == 0;
 }
 
-// 16 bytes of the 32 in a and b, from the at-th on (0 to 16)
-__device__ __forceinline__ uint4 bytes_from(const uint4& a, const uint4& b, int at) {
-  const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-  uint32_t x[6], y[5];
-#pragma unroll
-  for (int i = 0; i < 6; ++i) x[i] = at & 8 ? w[i + 2] : w[i];
-#pragma unroll
-  for (int i = 0; i < 5; ++i) y[i] = at & 4 ? x[i + 1] : x[i];
-  const uint32_t shift = (uint32_t)(at & 3) * 8;
-  if (at == 16) return b;
-  return make_uint4(__funnelshift_r(y[0], y[1], shift), __funnelshift_r(y[1], y[2], shift),
-                    __funnelshift_r(y[2], y[3], shift), __funnelshift_r(y[3], y[4], shift));
-}
-
-// 16 codes of a row from the k-th on, zeros after the K-th, in two steps, so that a thread's loads are all
-// asked for before the first is waited for.  Rows that are 16-byte aligned (VEC): one load.  Else the two
-// 16-byte words that the codes touch, as far as these lie within the operand's memory (`from` to `end`),
-// shifted into place; at its very ends code by code.
-template <bool VEC> struct Codes;
-template <> struct Codes<true> {
-  uint4 w;
-  __device__ __forceinline__ void ask(const int8_t* row, int k, bool in, const int8_t*, uintptr_t) {
-    w = make_uint4(0u, 0u, 0u, 0u);
-    if (in) w = *reinterpret_cast<const uint4*>(row + k);
-  }
-  __device__ __forceinline__ uint4 get(const int8_t*, int, int, bool, const int8_t*, uintptr_t) const { return w; }
-};
-template <> struct Codes<false> {
-  uint4 a, b;
-  __device__ __forceinline__ void ask(const int8_t* row, int k, bool in, const int8_t* from, uintptr_t end) {
-    const uintptr_t word = reinterpret_cast<uintptr_t>(row + k) & ~(uintptr_t)15;
-    a = b = make_uint4(0u, 0u, 0u, 0u);
-    if (in && word >= reinterpret_cast<uintptr_t>(from) && word + 16 <= end) a = *reinterpret_cast<const uint4*>(word);
-    if (in && word + 32 <= end) b = *reinterpret_cast<const uint4*>(word + 16);
-  }
-  __device__ __forceinline__ uint4 get(const int8_t* row, int k, int K, bool in, const int8_t* from, uintptr_t end) const {
-    if (!in) return make_uint4(0u, 0u, 0u, 0u);
-    const uintptr_t at = reinterpret_cast<uintptr_t>(row + k), word = at & ~(uintptr_t)15;
-    const int n = K - k;
-    uint32_t r[4];
-    if (word >= reinterpret_cast<uintptr_t>(from) && word + 32 <= end) {
-      const uint4 q = bytes_from(a, b, (int)(at & 15));
-      r[0] = q.x; r[1] = q.y; r[2] = q.z; r[3] = q.w;
-    } else {
-      r[0] = r[1] = r[2] = r[3] = 0u;
-      for (int j = 0; j < 16 && j < n; ++j) {
-        const uint32_t c = (uint32_t)(uint8_t)row[k + j] << (8 * (j & 3));
-#pragma unroll
-        for (int i = 0; i < 4; ++i) r[i] |= j >> 2 == i ? c : 0u;
-      }
-    }
-    if (n < 16) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int left = n - 4 * i;
-        if (left < 4) r[i] = left <= 0 ? 0u : r[i] & ((1u << (8 * left)) - 1u);
-      }
-    }
-    return make_uint4(r[0], r[1], r[2], r[3]);
-  }
-};
-
 __device__ __forceinline__ int dot16(const uint4& a, const uint4& b, int acc) {
   acc = __dp4a((int)a.x, (int)b.x, acc);
   acc = __dp4a((int)a.y, (int)b.y, acc);

@@ -34,16 +34,7 @@ struct TcTiles {
   }
 };
 
-// ---- barriers, TMA and tcgen05 (inline PTX)
-// Waits for the phase of this parity; false once the limit is reached or another role gave up.
-__device__ __forceinline__ bool bar_wait_all(uint32_t bar, uint32_t parity, volatile int* given_up) {
-  for (uint32_t i = 0; i < kPolls; ++i) {
-    if (bar_try(bar, parity)) return true;
-    if (*given_up) return false;
-  }
-  *given_up = 1;
-  return false;
-}
+// ---- TMA and tcgen05 (inline PTX)
 __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
   asm volatile(
       "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
@@ -64,11 +55,6 @@ __device__ __forceinline__ void tc_mma(uint32_t d, uint64_t a, uint64_t b, uint3
       "l"(a), "l"(b), "r"(idesc), "r"(add)
       : "memory");
 }
-__device__ __forceinline__ void tc_commit(uint32_t bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
-}
-__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 // 32 columns of this warp's 32 lanes
 __device__ __forceinline__ void tc_read32(uint32_t addr, float (&r)[32]) {
   asm volatile(

@@ -1195,14 +1195,16 @@ int emu_ops_device_status(int32_t* status, int32_t reset) {
   emu_ops_begin();
   if (!status) return emu_ops_fail(EMU_EINVAL, "status is null");
   int v = 0;
-  const int rc = emu_ops_int8_status(&v, reset != 0);
+  int rc = emu_ops_int8_status(&v, reset != 0);
+  int b = 0;
+  if (rc == EMU_OK) rc = emu_ops_block_status(&b, reset != 0);
   if (rc != EMU_OK) return rc;
   int n = 0;
   if (cudaMemcpyFromSymbol(&n, g_norm_status, sizeof n) != cudaSuccess) return emu_ops_launched("emu_ops_device_status");
   const int zero = 0;
   if (reset && cudaMemcpyToSymbol(g_norm_status, &zero, sizeof zero) != cudaSuccess)
     return emu_ops_launched("emu_ops_device_status");
-  *status = v | n;
+  *status = v | b | n;
   return EMU_OK;
 }
 

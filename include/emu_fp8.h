@@ -464,7 +464,7 @@ typedef struct {
  * within 2^-20 of the sum of their magnitudes, the blocks in fp32.  Any mixture of the two
  * formats and of the strides above, so that a layer's forward product and both its gradients
  * read the same codes.  A NaN among a row's codes or scales gives NaN in that row's (column's)
- * outputs alone.  K == 0 gives zeros.  Sizes: M, N, K < 2^31.
+ * outputs alone.  K == 0 gives zeros.  Sizes: M, N, K < 2^31 - 256.
  *   workspace: emu_block_mm_workspace_bytes of the same operands (0 where both are 16-byte
  *   aligned with strides that are multiples of 16), 256-byte aligned
  */
