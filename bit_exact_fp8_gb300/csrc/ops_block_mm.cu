@@ -99,6 +99,22 @@ BlockSide side_of(const emu_block_operand_t& o, int64_t rows, bool mn) {
   return {o.scale, o.scale_rows == 1 ? 0 : 7, o.scale_row_stride, o.scale_k_stride, o.scale_group_stride, (int)rows, mn ? 1 : 0};
 }
 
+// pairs of CTAs that the device holds at once (SMs of a cluster share a part of the chip, which may have an odd number)
+int pairs_at_once(const void* kernel, cudaLaunchConfig_t cfg) {
+  static std::atomic<int> cached[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return emu_ops_sm_count() / 2;
+  int v = cached[dev].load(std::memory_order_relaxed);
+  if (v == 0) {
+    int n = 0;
+    cfg.gridDim = dim3(2);
+    cfg.dynamicSmemBytes = BlockTcShape<256>::smem(kMaxExperts);
+    v = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) == cudaSuccess && n > 0 ? n : emu_ops_sm_count() / 2;
+    cached[dev].store(v, std::memory_order_relaxed);
+  }
+  return v;
+}
+
 template <int BN> int launch_tc(const BlockTcParams& p, int mode, int64_t tiles, const CUtensorMap& map_l, const CUtensorMap& map_c,
                                 cudaStream_t st) {
   using SH = BlockTcShape<BN>;
@@ -106,18 +122,20 @@ template <int BN> int launch_tc(const BlockTcParams& p, int mode, int64_t tiles,
                                                                                               : block_tc_kernel<BN, kScaleBoth>;
   static std::atomic<bool> done[3][64];
   if (!emu_ops_allow_smem(reinterpret_cast<const void*>(kernel), SH::smem(kMaxExperts), done[mode])) return emu_ops_launched("cudaFuncSetAttribute");
-  const int sms = emu_ops_sm_count();
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(p.slices > 1 ? tiles * p.slices : tiles < sms ? tiles : sms));
   cfg.blockDim = dim3(kTcThreads8);
   cfg.dynamicSmemBytes = SH::smem(p.kind == BlockKind::dense ? 0 : p.E);
   cfg.stream = st;
+  const int cluster = SH::PAIR ? 2 : p.slices;
   cudaLaunchAttribute at;
   at.id = cudaLaunchAttributeClusterDimension;
-  at.val.clusterDim.x = (unsigned)p.slices;
+  at.val.clusterDim.x = (unsigned)cluster;
   at.val.clusterDim.y = at.val.clusterDim.z = 1;
   cfg.attrs = &at;
-  cfg.numAttrs = p.slices > 1 ? 1 : 0;
+  cfg.numAttrs = cluster > 1 ? 1 : 0;
+  int64_t room = emu_ops_sm_count();
+  if (SH::PAIR) room = pairs_at_once(reinterpret_cast<const void*>(kernel), cfg);
+  cfg.gridDim = dim3((unsigned)(p.slices > 1 ? tiles * p.slices : (tiles < room ? tiles : room) * cluster));
   if (cudaLaunchKernelEx(&cfg, kernel, p, map_l, map_c) != cudaSuccess) return emu_ops_launched("emu_block_scaled_mm");
   return EMU_OK;
 }
@@ -138,7 +156,7 @@ int run_block_mm(const BlockMm& p, void* workspace, cudaStream_t st) {
   // which form
   int BN = 256, slices = 1;
   const int64_t rows = grouped ? up(p.M, p.E > 0 ? p.E : 1) : p.M;                // of the tokens' side, about
-  if (up(p.M, 128) * up(p.N, 256) * groups < sms || (grouped && rows <= 128)) {
+  if (up(p.M, 256) * up(p.N, 256) * groups < sms / 2 || (grouped && rows <= 128)) {
     BN = va.mn || rows > 64 ? 128 : rows > 32 ? 64 : 32;
     if (!grouped && !wgrad) {
       const int64_t tiles = up(p.N, 128) * up(p.M, BN);
@@ -153,8 +171,8 @@ int run_block_mm(const BlockMm& p, void* workspace, cudaStream_t st) {
   const emu_block_operand_t& ol = swap ? p.b : p.a;
   const emu_block_operand_t& oc = swap ? p.a : p.b;
   q.idesc = (1u << 4) | ((ol.format == EMU_E5M2 ? 1u : 0u) << 7) | ((oc.format == EMU_E5M2 ? 1u : 0u) << 10) | ((uint32_t)q.l.mn << 15) |
-            ((uint32_t)q.c.mn << 16) | ((uint32_t)(BN >> 3) << 17) | (8u << 24);
-  const int64_t tl = up(q.l.rows, 128), tc = up(q.c.rows, BN);
+            ((uint32_t)q.c.mn << 16) | ((uint32_t)((swap ? BN : 128) >> 3) << 17) | ((swap ? 8u : 16u) << 24);
+  const int64_t tl = up(q.l.rows, swap ? 128 : 256), tc = up(q.c.rows, BN);
   // the most tiles there can be: of ragged groups, each may add one
   const int64_t tiles = grouped ? (swap ? tl * (tc + p.E) : (tl + p.E) * tc) : tl * tc * groups;
   if (tiles * slices >= (int64_t)1 << 31) return emu_ops_fail(EMU_EUNSUPPORTED, "too many tiles");
@@ -175,7 +193,7 @@ int run_block_mm(const BlockMm& p, void* workspace, cudaStream_t st) {
   if (any) {
     int rc = codes_map(&map_l, swap ? vb : va, 128);
     const CodesView& vc = swap ? va : vb;
-    if (rc == EMU_OK) rc = codes_map(&map_c, vc, vc.mn ? 128 : BN);
+    if (rc == EMU_OK) rc = codes_map(&map_c, vc, vc.mn || BN > 128 ? 128 : BN);
     if (rc != EMU_OK) return rc;
   }
   // a lane's scale alone, where the columns of a warp share theirs; else the lanes' in the columns' if they all share it

@@ -14,6 +14,7 @@ namespace emu_ops {
 
 constexpr int kTcThreads8 = 384;                         // warps: loads, MMAs, tensor memory, zeros, eight that read
 constexpr int kMaxExperts = 1024;
+constexpr int kOutRow = 256 + 16;                        // bytes from one staged output row to the next: no bank conflicts
 
 enum class BlockKind { dense, grouped, wgrad };
 // how the scales enter: one value for a lane's columns; a vector over the columns, the lanes' one value in it; both vectors
@@ -37,19 +38,19 @@ struct BlockTcParams {
   uint32_t idesc;
 };
 template <int BN> struct BlockTcShape {
-  static constexpr bool SWAP = BN < 256;                 // the output's rows are the columns C
-  static constexpr int NS = BN == 256 ? 4 : BN == 128 ? 6 : 8, STAGE = 128 * 128 + BN * 128, NB = BN == 256 ? 2 : 4;
-  static constexpr int OWN = BN / 2, CHUNK = OWN < 32 ? OWN : 32, TMEM = NB * BN;
-  static constexpr int OUT = NS * STAGE, CS = OUT + (SWAP ? 0 : 8 * 32 * 64), BARS = CS + 2 * BN * 4;
-  static constexpr int TABLE = BARS + 8 * (3 * NS + 2 * NB + 3) + 8 + 2 * 12 * 4;
+  static constexpr bool PAIR = BN == 256;                // two CTAs on a tile of 256 x 256, each with half of either side
+  static constexpr bool SWAP = !PAIR;                    // the output's rows are the columns C
+  static constexpr int L = PAIR ? 256 : 128, C_ROWS = PAIR ? 128 : BN;       // a tile's lanes; rows of C that a CTA loads
+  static constexpr int NS = PAIR ? 4 : BN == 128 ? 6 : 8, STAGE = 128 * 128 + C_ROWS * 128, NB = PAIR ? 2 : 4;
+  static constexpr int H = PAIR ? 2 : 1;                 // parts of a tile's columns, each with MMAs and barriers of its own
+  static constexpr int OWN = BN / 2, READ = OWN / H, TMEM = NB * BN;         // a warp's columns, and those of a part
+  static constexpr int OUT = NS * STAGE, CS = OUT + (PAIR ? 8 * 32 * kOutRow : 0), BARS = CS + 2 * BN * 4;
+  static constexpr int TABLE = BARS + 8 * (3 * NS + 2 * NB * H + 3) + 8 + 2 * 12 * 4;
   static constexpr int smem(int E) { return TABLE + 2 * (E + 1) * 4 + 1024; }
 };
 static_assert(BlockTcShape<256>::smem(kMaxExperts) <= kMaxSmem && BlockTcShape<128>::smem(kMaxExperts) <= kMaxSmem &&
               BlockTcShape<64>::smem(kMaxExperts) <= kMaxSmem && BlockTcShape<32>::smem(kMaxExperts) <= kMaxSmem, "one CTA an SM");
 
-__device__ __forceinline__ float scale_of(const BlockSide& s, int64_t row, int kb, int group) {
-  return __ldg(s.scale + group * s.gs + (row >> s.shift) * s.rs + kb * s.ks);
-}
 __device__ __forceinline__ void tma_load3(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
   asm volatile(
       "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
@@ -60,12 +61,57 @@ __device__ __forceinline__ void tma_load3(uint32_t dst, const CUtensorMap* map, 
 __device__ __forceinline__ uint64_t desc8(uint32_t addr) {
   return (uint64_t)((addr >> 4) & 0x3FFFu) | (1024ull << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
 }
-__device__ __forceinline__ void mma8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t add) {
-  asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(add)
-      : "memory");
+template <bool PAIR> __device__ __forceinline__ void mma8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t add) {
+  if constexpr (PAIR)
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(add)
+        : "memory");
+  else
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(add)
+        : "memory");
 }
+// the arrival of all MMAs issued before: of a pair, at the barriers of both CTAs
+template <bool PAIR> __device__ __forceinline__ void commit8(uint32_t bar) {
+  if constexpr (PAIR)
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+                 "h"((uint16_t)3) : "memory");
+  else
+    tc_commit(bar);
+}
+template <bool PAIR> __device__ __forceinline__ void tmem_alloc(uint32_t slot, int columns) {
+  if constexpr (PAIR) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(slot), "r"(columns) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  } else {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(slot), "r"(columns) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+}
+template <bool PAIR> __device__ __forceinline__ void tmem_free(uint32_t at, int columns) {
+  if constexpr (PAIR) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(at), "r"(columns) : "memory");
+  else asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(at), "r"(columns) : "memory");
+}
+// Arrival at a barrier of the pair's first CTA (an address in the cluster).  What it orders are reads of tensor memory and
+// TMA loads that have been waited for, not this thread's own stores: without a cluster-wide release, which waits for all
+// that the thread has under way (8192 x 5760 x 1920 170 us with it).
+__device__ __forceinline__ void bar_arrive_cluster(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void fence_cluster() { asm volatile("fence.acq_rel.cluster;" ::: "memory"); }
+__device__ __forceinline__ uint32_t in_cluster(uint32_t at, int rank) {
+  uint32_t a;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(at), "r"(rank));
+  return a;
+}
+// this thread's `bytes` (a multiple of 16) of shared memory to global memory, and the wait until all have been read
+__device__ __forceinline__ void bulk_store(void* dst, uint32_t src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(src), "r"(bytes) : "memory");
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+__device__ __forceinline__ void bulk_store_wait() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
 // columns of this warp's 32 lanes, asked for, and waited for (whatever was asked for before)
 __device__ __forceinline__ void tmem_ask(uint32_t addr, float (&r)[32]) {
   asm volatile(
@@ -86,12 +132,30 @@ __device__ __forceinline__ void tmem_ask(uint32_t addr, float (&r)[16]) {
       : "r"(addr)
       : "memory");
 }
-template <int N> __device__ __forceinline__ void tmem_wait(float (&r)[N]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-  for (int i = 0; i < N; i += 8)                         // nothing that uses them goes before the wait
-    asm volatile("" : "+f"(r[i]), "+f"(r[i + 1]), "+f"(r[i + 2]), "+f"(r[i + 3]), "+f"(r[i + 4]), "+f"(r[i + 5]), "+f"(r[i + 6]),
-                      "+f"(r[i + 7]));
+template <int N> __device__ __forceinline__ void tmem_ask_all(uint32_t at, float (&r)[N]) {
+  if constexpr (N == 64) {
+    tmem_ask(at, *reinterpret_cast<float(*)[32]>(r));
+    tmem_ask(at + 32, *reinterpret_cast<float(*)[32]>(r + 32));
+  } else {
+    tmem_ask(at, r);
+  }
+}
+__device__ __forceinline__ void tmem_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+// acc += (x, y) * by, of values asked for from tensor memory: volatile, so that it stays behind the wait for them
+__device__ __forceinline__ void add_scaled(f2& acc, float x, float y, f2 by) {
+  asm volatile("{\n .reg .b64 v;\n mov.b64 v, {%1, %2};\n fma.rn.f32x2 %0, v, %3, %0;\n}" : "+l"(acc) : "f"(x), "f"(y), "l"(by));
+}
+__device__ __forceinline__ void add_scaled(f2& acc, float x, float y, f2 by, f2 by2) {
+  asm volatile("{\n .reg .b64 v;\n mov.b64 v, {%1, %2};\n mul.rn.f32x2 v, v, %3;\n fma.rn.f32x2 %0, v, %4, %0;\n}"
+               : "+l"(acc) : "f"(x), "f"(y), "l"(by), "l"(by2));
+}
+
+// One lane of the warp, in code that the whole warp runs: its values are the warp's then, and the addresses and descriptors
+// of loads and MMAs need not be moved from a thread's registers (an MMA's issue took 100 cycles with a branch for lane 0).
+__device__ __forceinline__ bool one_of_warp() {
+  uint32_t one;
+  asm volatile("{\n .reg .pred P;\n elect.sync _|P, 0xFFFFFFFF;\n selp.u32 %0, 1, 0, P;\n}" : "=r"(one) :: "memory");
+  return one != 0u;
 }
 
 // The groups' first rows (within [0, T], none below the one before it) and, of `tile` rows each, how many tiles come
@@ -162,7 +226,8 @@ template <int BN> __device__ __forceinline__ int tile_count(const BlockTcParams&
   if (p.kind == BlockKind::wgrad) return p.tiles_l * p.tiles_c * p.E;
   return before[p.E] * (BlockTcShape<BN>::SWAP ? p.tiles_l : p.tiles_c);
 }
-template <int BN> __device__ __forceinline__ BlockTile tile_at(const BlockTcParams& p, const int* start, const int* before, int tile) {
+// (rank: which CTA of a pair)
+template <int BN> __device__ __forceinline__ BlockTile tile_at(const BlockTcParams& p, const int* start, const int* before, int tile, int rank) {
   BlockTile t;
   t.group = 0;
   t.kb0 = 0;
@@ -191,7 +256,7 @@ template <int BN> __device__ __forceinline__ BlockTile tile_at(const BlockTcPara
       t.l0 = l * 128;
     } else {
       c = weight;
-      t.l0 = start[a] + token * 128;
+      t.l0 = start[a] + token * 256 + rank * 128;
       t.l_end = start[a + 1];
       t.c0 = c * BN;
     }
@@ -211,7 +276,7 @@ template <int BN> __device__ __forceinline__ BlockTile tile_at(const BlockTcPara
     t.kb1 = p.k_blocks * (slice + 1) / p.slices;
   }
   tile_order(tile, p.tiles_l, p.tiles_c, l, c);
-  t.l0 = l * 128;
+  t.l0 = l * BlockTcShape<BN>::L + rank * 128;
   t.c0 = c * BN;
   return t;
 }
@@ -227,107 +292,100 @@ __device__ __forceinline__ void put_zeros(void* out, int type, int64_t from, int
   for (int64_t i = from + who; i < to; i += count) put(out, type, i, 0.0f);
 }
 
-// A warp's 32 rows (lanes) x 128 columns of sums to row-major memory: 64 bytes of each row at a time go through shared
-// memory (16 bytes a lane, a row's chunks permuted by its number: no two lanes of a phase meet in a bank), so
-// that whole sectors are stored, or, where rows are not 16-byte aligned, elements.
+// A warp's 32 rows (lanes) x 128 columns of sums to row-major memory, 256 bytes of a row at a time by way of shared
+// memory: a lane's row leaves by a bulk copy, which the next tile's blocks do not wait for, or, where rows are
+// not 16-byte aligned, by the warp's elements.
 template <class T>
 __device__ __forceinline__ void write_rows(const BlockTcParams& p, const f2 (&acc)[64], unsigned char* stage, int64_t row0, int rows,
                                            int64_t n0, int64_t group, int lane) {
-  constexpr int COLS = 64 / sizeof(T), VEC = 16 / sizeof(T);
-  T* const out = static_cast<T*>(p.out) + group * p.out_group;
-  const int64_t N = p.c.rows;
-  const bool vec = N % VEC == 0 && p.ldl % VEC == 0 && (reinterpret_cast<uintptr_t>(out) & 15u) == 0;
+  constexpr int COLS = 256 / sizeof(T), VEC = 16 / sizeof(T);
+  T* const out = static_cast<T*>(p.out) + group * p.out_group + row0 * p.ldl + n0;
+  const int cols = p.c.rows - n0 < 128 ? (int)(p.c.rows - n0) : 128;      // may be none
+  const bool vec = p.ldl % VEC == 0 && ((reinterpret_cast<uintptr_t>(p.out) | (uintptr_t)(p.out_group * sizeof(T))) & 15u) == 0;
 #pragma unroll
   for (int c = 0; c < 128; c += COLS) {
+    bulk_store_wait();                                   // the copy before has read this lane's row
     __syncwarp();
 #pragma unroll
     for (int i = 0; i < COLS; i += VEC) {
       float v[VEC];
 #pragma unroll
       for (int j = 0; j < VEC; j += 2) halves(acc[(c + i + j) / 2], v[j], v[j + 1]);
-      store_f<T, VEC>(reinterpret_cast<T*>(stage + lane * 64 + (((i / VEC) ^ ((lane >> 1) & 3)) * 16)), v);
+      store_f<T, VEC>(reinterpret_cast<T*>(stage + lane * kOutRow) + i, v);
     }
-    __syncwarp();
     if (vec) {
-      const int64_t n = n0 + c + (lane & 3) * VEC;
-      if (n < N) {
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int r = k * 8 + (lane >> 2);
-          if (r < rows)
-            *reinterpret_cast<uint4*>(out + (row0 + r) * p.ldl + n) =
-                *reinterpret_cast<const uint4*>(stage + r * 64 + (((lane & 3) ^ ((r >> 1) & 3)) * 16));
-        }
-      }
+      const int n = cols - c < COLS ? cols - c : COLS;
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      if (lane < rows && n > 0) bulk_store(out + lane * p.ldl + c, smem_addr(stage + lane * kOutRow), n * (uint32_t)sizeof(T));
     } else {
-      constexpr int EACH = 32 / COLS;                    // rows a warp stores at once
-      const int in = lane % COLS;
-      if (n0 + c + in < N) {
+      __syncwarp();
 #pragma unroll 4
-        for (int r = lane / COLS; r < rows; r += EACH)
-          out[(row0 + r) * p.ldl + n0 + c + in] =
-              *reinterpret_cast<const T*>(stage + r * 64 + (((in / VEC) ^ ((r >> 1) & 3)) * 16) + (in % VEC) * sizeof(T));
-      }
+      for (int r = 0; r < rows; ++r)
+#pragma unroll
+        for (int i = 0; i < COLS; i += 32)
+          if (c + i + lane < cols) out[r * p.ldl + c + i + lane] = *(reinterpret_cast<const T*>(stage + r * kOutRow) + i + lane);
     }
   }
 }
 
-// Persistent: one CTA an SM, tiles of 128 x BN outputs in turn.  Warp 0 loads the blocks by TMA, warp 1 issues the
-// MMAs, warp 2 owns the tensor memory, warp 3 clears the tokens of other experts in a weights' gradient's first
-// and last block, warps 4 to 11 scale and add: each holds 32 lanes x BN / 2 columns of sums in registers.
-// Several slices of K (dense, BN < 256): the CTAs of a cluster, which share out the columns at the end.  All waits
-// are bounded; a role that gives up sets the status and takes the others along.
+// Persistent: one CTA an SM, tiles in turn.  Warp 0 loads the blocks by TMA, warp 1 issues the MMAs, warp 2 owns the
+// tensor memory, warp 3 clears the tokens of other experts in a weights' gradient's first and last block (and
+// tells the pair's first CTA that its blocks are there), warps 4 to 11 scale and add: each holds 32 lanes x BN / 2
+// columns of sums in registers.  BN = 256: pairs of CTAs, whose MMAs the first one issues for both (an SM takes
+// in 64 bytes a cycle: a block of 128 x 256 outputs would need 48 KB every 512 cycles, of the pair each 32).
+// Several slices of K (dense, BN < 256): the CTAs of a cluster, which share out the columns at the end.  All
+// waits are bounded; a role that gives up sets the status and takes the others along.
 template <int BN, int MODE>
 __global__ void __launch_bounds__(kTcThreads8, 1)
 block_tc_kernel(const __grid_constant__ BlockTcParams p, const __grid_constant__ CUtensorMap map_l,
                 const __grid_constant__ CUtensorMap map_c) {
   using SH = BlockTcShape<BN>;
-  constexpr int NS = SH::NS, NB = SH::NB, OWN = SH::OWN, CHUNK = SH::CHUNK;
+  constexpr bool PAIR = SH::PAIR;
+  constexpr int NS = SH::NS, NB = SH::NB, H = SH::H, OWN = SH::OWN, READ = SH::READ;
   extern __shared__ unsigned char raw[];
   unsigned char* const smem = raw + ((1024u - (smem_addr(raw) & 1023u)) & 1023u);
   const uint32_t base = smem_addr(smem);
-  const uint32_t full = base + SH::BARS, empty = full + 8 * NS, fixed = empty + 8 * NS, tfull = fixed + 8 * NS, tempty = tfull + 8 * NB,
-                 cfull = tempty + 8 * NB, drained = cfull + 16;
-  uint32_t* const slot = reinterpret_cast<uint32_t*>(smem + SH::BARS + 8 * (3 * NS + 2 * NB + 3));
+  const uint32_t full = base + SH::BARS, empty = full + 8 * NS, fixed = empty + 8 * NS, tfull = fixed + 8 * NS, tempty = tfull + 8 * NB * H,
+                 cfull = tempty + 8 * NB * H, drained = cfull + 16;
+  uint32_t* const slot = reinterpret_cast<uint32_t*>(smem + SH::BARS + 8 * (3 * NS + 2 * NB * H + 3));
   volatile int* const given_up = reinterpret_cast<volatile int*>(slot + 1);
   int* const part = reinterpret_cast<int*>(slot + 2);
   int* const start = reinterpret_cast<int*>(smem + SH::TABLE);
   int* const before = start + p.E + 1;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0);   // the same for all, and known to be
+  const int rank = PAIR ? blockIdx.x & 1 : 0, first_tile = PAIR ? blockIdx.x >> 1 : blockIdx.x, step = PAIR ? gridDim.x >> 1 : gridDim.x;
 
   if (tid == 0) {
     for (int i = 0; i < NS; ++i) {
       bar_init(full + 8 * i, 1);
-      bar_init(empty + 8 * i, 1);
-      bar_init(fixed + 8 * i, 1);
+      bar_init(empty + 8 * i, H);
+      bar_init(fixed + 8 * i, PAIR ? 2 : 1);
     }
-    for (int i = 0; i < NB; ++i) {
+    for (int i = 0; i < NB * H; ++i) {
       bar_init(tfull + 8 * i, 1);
-      bar_init(tempty + 8 * i, 8);                       // one arrival a reading warp
+      bar_init(tempty + 8 * i, PAIR ? 16 : 8);           // one arrival a reading warp
     }
     for (int i = 0; i < 2; ++i) bar_init(cfull + 8 * i, 4);   // the columns' scales, one arrival a warp of the half
-    bar_init(drained, 1);
+    bar_init(drained, H);
     *given_up = 0;
     bar_init_fence();
   }
-  if (warp == 2) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(slot)), "r"(SH::TMEM) : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-  }
-  if (p.kind != BlockKind::dense) group_table(p.offsets, p.E, p.T, SH::SWAP ? BN : 128, start, before, part);
+  if (warp == 2) tmem_alloc<PAIR>(smem_addr(slot), SH::TMEM);
+  if (p.kind != BlockKind::dense) group_table(p.offsets, p.E, p.T, PAIR ? 256 : BN, start, before, part);
   tc_fence_before();
   __syncthreads();
+  if (PAIR) cluster_sync();                              // the other's barriers are there
   tc_fence_after();
   const uint32_t tmem = *slot;
   const int tiles = tile_count<BN>(p, before);
 
   if (warp < 4) {
     if constexpr (BN == 256) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
-    if (warp == 0 && lane == 0) {
+    if (warp == 0) {
       uint32_t it = 0;
       bool ok = true;
-      for (int tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
-        const BlockTile t = tile_at<BN>(p, start, before, tile);
+      for (int tile = first_tile; tile < tiles && ok; tile += step) {
+        const BlockTile t = tile_at<BN>(p, start, before, tile, rank);
         const int gl = p.kind == BlockKind::grouped && SH::SWAP ? t.group : 0, gc = p.kind == BlockKind::grouped && !SH::SWAP ? t.group : 0;
         for (int kb = t.kb0; kb < t.kb1; ++kb, ++it) {
           const uint32_t s = it % NS, bar = full + 8 * s, dst = base + s * SH::STAGE;
@@ -335,59 +393,67 @@ block_tc_kernel(const __grid_constant__ BlockTcParams p, const __grid_constant__
             ok = false;
             break;
           }
-          bar_expect(bar, SH::STAGE);
-          tma_load3(dst, &map_l, p.l.mn ? t.l0 : kb * kBlock, p.l.mn ? kb * kBlock : t.l0, gl, bar);
-          if (BN >= 128 && p.c.mn) {
-#pragma unroll
-            for (int x = 0; x < BN / 128; ++x) tma_load3(dst + (1 + x) * 16384, &map_c, t.c0 + x * 128, kb * kBlock, gc, bar);
-          } else {
-            tma_load3(dst + 16384, &map_c, kb * kBlock, t.c0, gc, bar);
+          if (one_of_warp()) {
+            bar_expect(bar, SH::STAGE);
+            tma_load3(dst, &map_l, p.l.mn ? t.l0 : kb * kBlock, p.l.mn ? kb * kBlock : t.l0, gl, bar);
+            const int c = PAIR ? t.c0 + rank * 128 : t.c0;
+            tma_load3(dst + 16384, &map_c, p.c.mn ? c : kb * kBlock, p.c.mn ? kb * kBlock : c, gc, bar);
           }
         }
       }
       if (!ok)                                           // the loads issued last, one stage each at most
         for (uint32_t i = it > NS ? it - NS : 0; i < it; ++i) (void)bar_wait(full + 8 * (i % NS), (i / NS) & 1);
-    } else if (warp == 1 && lane == 0) {
+    } else if (warp <= H && rank == 0) {                 // of a pair warp 2 too: a warp issues the MMAs of one part of the columns
       uint32_t it = 0;
       bool ok = true;
-      const uint32_t step_l = p.l.mn ? 256 : 2, step_c = p.c.mn ? 256 : 2;   // 32 of K, in 16 bytes
-      for (int tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
-        const BlockTile t = tile_at<BN>(p, start, before, tile);
+      const int h = warp - 1;
+      // a step of 32 of K, in 16 bytes; the parts' rows of C within each CTA's 128
+      const uint32_t step_l = p.l.mn ? 256 : 2, step_c = p.c.mn ? 256 : 2, part_c = h * (p.c.mn ? 4 : 512);
+      for (int tile = first_tile; tile < tiles && ok; tile += step) {
+        const BlockTile t = tile_at<BN>(p, start, before, tile, rank);
         for (int kb = t.kb0; kb < t.kb1; ++kb, ++it) {
           const uint32_t s = it % NS, buf = it % NB;
-          ok = (it < NB || bar_wait_all(tempty + 8 * buf, (it / NB - 1) & 1, given_up)) && bar_wait_all(full + 8 * s, (it / NS) & 1, given_up);
-          if (ok && p.kind == BlockKind::wgrad) ok = bar_wait_all(fixed + 8 * s, (it / NS) & 1, given_up);
+          ok = bar_wait_all((PAIR || p.kind == BlockKind::wgrad ? fixed : full) + 8 * s, (it / NS) & 1, given_up) &&
+               (it < NB || bar_wait_all(tempty + 8 * (buf * H + h), (it / NB - 1) & 1, given_up));
           if (!ok) break;
           tc_fence_after();
-          const uint64_t dl = desc8(base + s * SH::STAGE), dc = desc8(base + s * SH::STAGE + 16384);
+          if (one_of_warp()) {
+            const uint64_t dl = desc8(base + s * SH::STAGE), dc = desc8(base + s * SH::STAGE + 16384) + part_c;
 #pragma unroll
-          for (int k = 0; k < 4; ++k) mma8(tmem + buf * BN, dl + k * step_l, dc + k * step_c, p.idesc, k > 0);
-          tc_commit(empty + 8 * s);
-          tc_commit(tfull + 8 * buf);
+            for (int k = 0; k < 4; ++k)
+              mma8<PAIR>(tmem + buf * BN + h * (BN / H), dl + k * step_l, dc + k * step_c, p.idesc, k > 0);
+            commit8<PAIR>(tfull + 8 * (buf * H + h));
+            commit8<PAIR>(empty + 8 * s);
+          }
         }
       }
-      tc_commit(drained);                                // the MMAs are done before the tensor memory goes back
+      if (one_of_warp()) commit8<PAIR>(drained);         // the MMAs are done before the tensor memory goes back
       (void)bar_wait(drained, 0);
-    } else if (warp == 3 && p.kind == BlockKind::wgrad) {
+    } else if (warp == 3 && (PAIR || p.kind == BlockKind::wgrad)) {
       uint32_t it = 0;
       bool ok = true;
-      for (int tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
-        const BlockTile t = tile_at<BN>(p, start, before, tile);
+      const uint32_t ready = PAIR ? in_cluster(fixed, 0) : fixed;
+      for (int tile = first_tile; tile < tiles && ok; tile += step) {
+        const BlockTile t = tile_at<BN>(p, start, before, tile, rank);
         for (int kb = t.kb0; kb < t.kb1; ++kb, ++it) {
           const uint32_t s = it % NS;
           ok = __all_sync(0xFFFFFFFFu, bar_wait_all(full + 8 * s, (it / NS) & 1, given_up));
           if (!ok) break;
           const int first = t.lo - kb * kBlock, last = t.hi - kb * kBlock;   // of the block's rows, [first, last) count
-          if (first > 0 || last < kBlock) {
+          if (p.kind == BlockKind::wgrad && (first > 0 || last < kBlock)) {
             uint4* const rows = reinterpret_cast<uint4*>(smem + s * SH::STAGE);
             for (int i = lane; i < SH::STAGE / 16; i += 32) {
               const int r = (i >> 3) & 127;              // a token's codes of 128 rows are 128 bytes
               if (r < first || r >= last) rows[i] = make_uint4(0u, 0u, 0u, 0u);
             }
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            if (PAIR) fence_cluster();
           }
           __syncwarp();
-          if (lane == 0) bar_arrive(fixed + 8 * s);
+          if (lane == 0) {
+            if (PAIR) bar_arrive_cluster(ready + 8 * s);
+            else bar_arrive(ready + 8 * s);
+          }
         }
       }
     }
@@ -395,31 +461,31 @@ block_tc_kernel(const __grid_constant__ BlockTcParams p, const __grid_constant__
   } else {
     if constexpr (BN == 256) asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
     const int quad = warp & 3, half = (warp - 4) >> 2, mine = quad * 32 + lane;
+    const uint32_t released = PAIR ? in_cluster(tempty, 0) : tempty;
     float* const cs = reinterpret_cast<float*>(smem + SH::CS) + half * OWN;   // the columns' scales, two slots BN apart
     uint32_t it = 0;
     bool ok = true, met = false;
-    for (int tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
-      const BlockTile t = tile_at<BN>(p, start, before, tile);
+    for (int tile = first_tile; tile < tiles && ok; tile += step) {
+      const BlockTile t = tile_at<BN>(p, start, before, tile, rank);
       const int gl = p.kind == BlockKind::grouped && SH::SWAP ? t.group : 0, gc = p.kind == BlockKind::grouped && !SH::SWAP ? t.group : 0;
       const int l = t.l0 + mine, c = t.c0 + half * OWN;
       const bool l_in = l < t.l_end;
-      // the scales of a block, asked for two blocks ahead
+      // the scales of a block, asked for two blocks ahead, by addresses that step from block to block
       const int c_at = MODE == kScaleLane ? c : c + mine;
-      const bool c_in = c_at < t.c_end && (MODE == kScaleLane || mine < OWN);
-      auto ask = [&](int kb, float& rl, float& rc) {
-        rl = rc = 0.0f;
-        if (kb < t.kb1) {
-          if (MODE == kScaleColumns) {
-            if (c_in) rl = scale_of(p.l, t.l0, kb, gl);
-          } else if (l_in) {
-            rl = scale_of(p.l, l, kb, gl);
-          }
-          if (c_in) rc = scale_of(p.c, c_at, kb, gc);
-        }
+      const bool c_in = c_at < t.c_end && (MODE == kScaleLane || mine < OWN), r_in = MODE == kScaleColumns ? c_in : l_in;
+      const float* pl = p.l.scale + gl * p.l.gs + ((MODE == kScaleColumns ? t.l0 : l) >> p.l.shift) * p.l.rs + t.kb0 * p.l.ks;
+      const float* pc = p.c.scale + gc * p.c.gs + (c_at >> p.c.shift) * p.c.rs + t.kb0 * p.c.ks;
+      int left = t.kb1 - t.kb0;                          // blocks whose scales have not been asked for
+      auto ask = [&](float& rl, float& rc) {
+        rl = r_in && left > 0 ? __ldg(pl) : 0.0f;
+        rc = c_in && left > 0 ? __ldg(pc) : 0.0f;
+        pl += p.l.ks;
+        pc += p.c.ks;
+        --left;
       };
       float rl0, rc0, rl1, rc1;
-      ask(t.kb0, rl0, rc0);
-      ask(t.kb0 + 1, rl1, rc1);
+      ask(rl0, rc0);
+      ask(rl1, rc1);
       f2 acc[OWN / 2];
 #pragma unroll
       for (int i = 0; i < OWN / 2; ++i) acc[i] = 0ull;
@@ -428,7 +494,7 @@ block_tc_kernel(const __grid_constant__ BlockTcParams p, const __grid_constant__
         const float rl = rl0, rc = rc0;
         rl0 = rl1;
         rc0 = rc1;
-        ask(kb + 2, rl1, rc1);
+        ask(rl1, rc1);
         float* const cv = cs + (it & 1) * BN;
         if (MODE != kScaleLane) {
           if (mine < OWN) cv[mine] = MODE == kScaleColumns ? rl * rc : rc;
@@ -436,43 +502,48 @@ block_tc_kernel(const __grid_constant__ BlockTcParams p, const __grid_constant__
           if (lane == 0) bar_arrive(cfull + 8 * half);
           ok = bar_wait_all(cfull + 8 * half, it & 1, given_up);
         }
-        ok = __all_sync(0xFFFFFFFFu, ok && bar_wait_all(tfull + 8 * buf, (it / NB) & 1, given_up));
-        if (!ok) break;
-        tc_fence_after();
-        const uint32_t at = tmem + ((uint32_t)(quad * 32) << 16) + buf * BN + half * OWN;
         const f2 by = MODE == kScaleLane ? pair(rl * rc, rl * rc) : pair(rl, rl);
-        float r[2][CHUNK];
-        tmem_ask(at, r[0]);
 #pragma unroll
-        for (int k = 0; k < OWN / CHUNK; ++k) {
-          tmem_wait(r[k & 1]);
-          if (k + 1 < OWN / CHUNK) {
-            tmem_ask(at + (k + 1) * CHUNK, r[(k + 1) & 1]);
-          } else {
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) bar_arrive(tempty + 8 * buf);
+        for (int h = 0; h < H; ++h) {
+          const uint32_t full_of = tfull + 8 * (buf * H + h);
+          ok = __all_sync(0xFFFFFFFFu, ok && bar_wait_all(full_of, (it / NB) & 1, given_up));
+          if (!ok) break;
+          tc_fence_after();
+          // the part's columns of a warp: all asked for at once, and the tensor memory given back before they are used
+          float r[READ];
+          const uint32_t at = tmem + ((uint32_t)(quad * 32) << 16) + buf * BN + h * (BN / H) + half * READ;
+          tmem_ask_all<READ>(at, r);
+          tmem_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            if (PAIR) bar_arrive_cluster(released + 8 * (buf * H + h));
+            else bar_arrive(released + 8 * (buf * H + h));
           }
 #pragma unroll
-          for (int i = 0; i < CHUNK; i += 4) {
-            f2& a0 = acc[(k * CHUNK + i) / 2];
-            f2& a1 = acc[(k * CHUNK + i) / 2 + 1];
-            const f2 x0 = pair(r[k & 1][i], r[k & 1][i + 1]), x1 = pair(r[k & 1][i + 2], r[k & 1][i + 3]);
+          for (int i = 0; i < READ; i += 4) {
+            f2& a0 = acc[(h * READ + i) / 2];
+            f2& a1 = acc[(h * READ + i) / 2 + 1];
             if (MODE == kScaleLane) {
-              a0 = fma2(x0, by, a0);
-              a1 = fma2(x1, by, a1);
+              add_scaled(a0, r[i], r[i + 1], by);
+              add_scaled(a1, r[i + 2], r[i + 3], by);
             } else {
-              const float4 s = *reinterpret_cast<const float4*>(cv + k * CHUNK + i);
-              const f2 s0 = pair(s.x, s.y), s1 = pair(s.z, s.w);
-              a0 = fma2(MODE == kScaleBoth ? mul2(x0, by) : x0, s0, a0);
-              a1 = fma2(MODE == kScaleBoth ? mul2(x1, by) : x1, s1, a1);
+              const float4 s = *reinterpret_cast<const float4*>(cv + h * READ + i);
+              if (MODE == kScaleColumns) {
+                add_scaled(a0, r[i], r[i + 1], pair(s.x, s.y));
+                add_scaled(a1, r[i + 2], r[i + 3], pair(s.z, s.w));
+              } else {
+                add_scaled(a0, r[i], r[i + 1], by, pair(s.x, s.y));
+                add_scaled(a1, r[i + 2], r[i + 3], by, pair(s.z, s.w));
+              }
             }
           }
         }
+        if (!ok) break;
       }
       if (!ok) break;
       if constexpr (!SH::SWAP) {
-        unsigned char* const stage = smem + SH::OUT + (warp - 4) * 32 * 64;
+        unsigned char* const stage = smem + SH::OUT + (warp - 4) * 32 * kOutRow;
         const int64_t row0 = t.l0 + quad * 32;
         const int rows = t.l_end - row0 < 32 ? (int)(t.l_end - row0) : 32;
         const int64_t group = p.kind == BlockKind::wgrad ? t.group : 0;
@@ -516,6 +587,7 @@ block_tc_kernel(const __grid_constant__ BlockTcParams p, const __grid_constant__
       put_zeros(p.out, p.out_type, 0, start[0] * N, who, count);
       put_zeros(p.out, p.out_type, start[p.E] * N, (int64_t)p.T * N, who, count);
     }
+    if (PAIR) bulk_store_wait();                         // before the memory that they leave from is gone
     __syncwarp();
     if (SH::SWAP && p.slices > 1 && !met) cluster_sync();   // a warp that gave up goes past the first barrier too
   }
@@ -523,7 +595,7 @@ block_tc_kernel(const __grid_constant__ BlockTcParams p, const __grid_constant__
     if (p.slices > 1) {                                  // one tile a CTA
       if (warp < 4) cluster_sync();
       cluster_sync();
-      const BlockTile t = tile_at<BN>(p, start, before, blockIdx.x);
+      const BlockTile t = tile_at<BN>(p, start, before, blockIdx.x, 0);
       const int per = BN / p.slices, slice = (int)blockIdx.x % p.slices;
       const float* const sums = reinterpret_cast<const float*>(smem);
       if (!*given_up)
@@ -537,9 +609,10 @@ block_tc_kernel(const __grid_constant__ BlockTcParams p, const __grid_constant__
   }
   tc_fence_before();
   __syncthreads();
+  if (PAIR) cluster_sync();                              // the first CTA's MMAs and the other's arrivals are over
   tc_fence_after();
   if (tid == 0 && *given_up) atomicExch(&g_block_status, 1);
-  if (warp == 2) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(SH::TMEM) : "memory");
+  if (warp == 2) tmem_free<PAIR>(tmem, SH::TMEM);
 }
 
 }  // namespace emu_ops
