@@ -95,6 +95,20 @@ int codes_map(CUtensorMap* map, const CodesView& v, int box) {
   return r == CUDA_SUCCESS ? EMU_OK : emu_ops_fail(EMU_ECUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
 }
 
+// the output [groups, rows, cols], boxes of 128 bytes by 32 rows
+int out_map(CUtensorMap* map, void* out, int type, int64_t rows, int64_t cols, int64_t groups) {
+  PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+  if (!enc) return emu_ops_fail(EMU_ECUDA, "cuTensorMapEncodeTiled is not available from the driver");
+  const cuuint64_t es = elem_bytes((emu_out_t)type);
+  const cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)groups}, strides[2] = {cols * es, cols * es * (cuuint64_t)rows};
+  const cuuint32_t boxes[3] = {(cuuint32_t)(128 / es), 32u, 1u}, step[3] = {1u, 1u, 1u};
+  const CUtensorMapDataType t = type == EMU_OUT_F32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                : type == EMU_OUT_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  const CUresult r = enc(map, t, 3, out, dims, strides, boxes, step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                         CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? EMU_OK : emu_ops_fail(EMU_ECUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
+}
+
 BlockSide side_of(const emu_block_operand_t& o, int64_t rows, bool mn) {
   return {o.scale, o.scale_rows == 1 ? 0 : 7, o.scale_row_stride, o.scale_k_stride, o.scale_group_stride, (int)rows, mn ? 1 : 0};
 }
@@ -115,8 +129,7 @@ int pairs_at_once(const void* kernel, cudaLaunchConfig_t cfg) {
   return v;
 }
 
-template <int BN> int launch_tc(const BlockTcParams& p, int mode, int64_t tiles, const CUtensorMap& map_l, const CUtensorMap& map_c,
-                                cudaStream_t st) {
+template <int BN> int launch_tc(const BlockTcParams& p, int mode, int64_t tiles, const CUtensorMap (&maps)[3], cudaStream_t st) {
   using SH = BlockTcShape<BN>;
   auto kernel = mode == kScaleLane ? block_tc_kernel<BN, kScaleLane> : mode == kScaleColumns ? block_tc_kernel<BN, kScaleColumns>
                                                                                               : block_tc_kernel<BN, kScaleBoth>;
@@ -136,7 +149,7 @@ template <int BN> int launch_tc(const BlockTcParams& p, int mode, int64_t tiles,
   int64_t room = emu_ops_sm_count();
   if (SH::PAIR) room = pairs_at_once(reinterpret_cast<const void*>(kernel), cfg);
   cfg.gridDim = dim3((unsigned)(p.slices > 1 ? tiles * p.slices : (tiles < room ? tiles : room) * cluster));
-  if (cudaLaunchKernelEx(&cfg, kernel, p, map_l, map_c) != cudaSuccess) return emu_ops_launched("emu_block_scaled_mm");
+  if (cudaLaunchKernelEx(&cfg, kernel, p, maps[0], maps[1], maps[2]) != cudaSuccess) return emu_ops_launched("emu_block_scaled_mm");
   return EMU_OK;
 }
 
@@ -189,20 +202,25 @@ int run_block_mm(const BlockMm& p, void* workspace, cudaStream_t st) {
   q.ldl = swap ? 1 : p.N;
   q.ldc = swap ? p.N : 1;
   q.out_group = p.M * p.N;
-  CUtensorMap map_l = {}, map_c = {};
+  CUtensorMap maps[3] = {};
   if (any) {
-    int rc = codes_map(&map_l, swap ? vb : va, 128);
+    int rc = codes_map(&maps[0], swap ? vb : va, 128);
     const CodesView& vc = swap ? va : vb;
-    if (rc == EMU_OK) rc = codes_map(&map_c, vc, vc.mn || BN > 128 ? 128 : BN);
+    if (rc == EMU_OK) rc = codes_map(&maps[1], vc, vc.mn || BN > 128 ? 128 : BN);
     if (rc != EMU_OK) return rc;
+  }
+  if (!swap && aligned(p.out, 16) && p.N * (int64_t)elem_bytes((emu_out_t)p.out_type) % 16 == 0) {
+    const int rc = out_map(&maps[2], p.out, p.out_type, p.M, p.N, groups);
+    if (rc != EMU_OK) return rc;
+    q.out_map = 1;
   }
   // a lane's scale alone, where the columns of a warp share theirs; else the lanes' in the columns' if they all share it
   const bool tokens_c = grouped && swap, tokens_l = grouped && !swap;
   const int mode = q.c.shift == 7 && !tokens_c ? kScaleLane : q.l.shift == 7 && !tokens_l ? kScaleColumns : kScaleBoth;
-  if (BN == 256) return launch_tc<256>(q, mode, tiles, map_l, map_c, st);
-  if (BN == 128) return launch_tc<128>(q, mode, tiles, map_l, map_c, st);
-  if (BN == 64) return launch_tc<64>(q, mode, tiles, map_l, map_c, st);
-  return launch_tc<32>(q, mode, tiles, map_l, map_c, st);
+  if (BN == 256) return launch_tc<256>(q, mode, tiles, maps, st);
+  if (BN == 128) return launch_tc<128>(q, mode, tiles, maps, st);
+  if (BN == 64) return launch_tc<64>(q, mode, tiles, maps, st);
+  return launch_tc<32>(q, mode, tiles, maps, st);
 }
 
 // ------------------------------------------------------------------------------- checks

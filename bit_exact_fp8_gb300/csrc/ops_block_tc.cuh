@@ -14,7 +14,7 @@ namespace emu_ops {
 
 constexpr int kTcThreads8 = 384;                         // warps: loads, MMAs, tensor memory, zeros, eight that read
 constexpr int kMaxExperts = 1024;
-constexpr int kOutRow = 256 + 16;                        // bytes from one staged output row to the next: no bank conflicts
+constexpr int kOutStage = 8 * 2 * 4096;                  // staged outputs: two times 32 rows of 128 bytes a warp
 
 enum class BlockKind { dense, grouped, wgrad };
 // how the scales enter: one value for a lane's columns; a vector over the columns, the lanes' one value in it; both vectors
@@ -33,7 +33,7 @@ struct BlockTcParams {
   BlockKind kind;
   const int32_t* offsets; int E, T;                      // groups of tokens (grouped: of rows, wgrad: of K)
   int zero_rest;
-  void* out; int out_type;
+  void* out; int out_type, out_map;                      // out_map: its rows are 16-byte aligned, and there is a map of it
   int64_t ldl, ldc, out_group;                           // out[l * ldl + c * ldc], one of them 1
   uint32_t idesc;
 };
@@ -44,7 +44,7 @@ template <int BN> struct BlockTcShape {
   static constexpr int NS = PAIR ? 4 : BN == 128 ? 6 : 8, STAGE = 128 * 128 + C_ROWS * 128, NB = PAIR ? 2 : 4;
   static constexpr int H = PAIR ? 2 : 1;                 // parts of a tile's columns, each with MMAs and barriers of its own
   static constexpr int OWN = BN / 2, READ = OWN / H, TMEM = NB * BN;         // a warp's columns, and those of a part
-  static constexpr int OUT = NS * STAGE, CS = OUT + (PAIR ? 8 * 32 * kOutRow : 0), BARS = CS + 2 * BN * 4;
+  static constexpr int OUT = NS * STAGE, CS = OUT + (PAIR ? kOutStage : 0), BARS = CS + 2 * BN * 4;
   static constexpr int TABLE = BARS + 8 * (3 * NS + 2 * NB * H + 3) + 8 + 2 * 12 * 4;
   static constexpr int smem(int E) { return TABLE + 2 * (E + 1) * 4 + 1024; }
 };
@@ -106,12 +106,6 @@ __device__ __forceinline__ uint32_t in_cluster(uint32_t at, int rank) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(at), "r"(rank));
   return a;
 }
-// this thread's `bytes` (a multiple of 16) of shared memory to global memory, and the wait until all have been read
-__device__ __forceinline__ void bulk_store(void* dst, uint32_t src, uint32_t bytes) {
-  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(src), "r"(bytes) : "memory");
-  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-}
-__device__ __forceinline__ void bulk_store_wait() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
 // columns of this warp's 32 lanes, asked for, and waited for (whatever was asked for before)
 __device__ __forceinline__ void tmem_ask(uint32_t addr, float (&r)[32]) {
   asm volatile(
@@ -292,38 +286,64 @@ __device__ __forceinline__ void put_zeros(void* out, int type, int64_t from, int
   for (int64_t i = from + who; i < to; i += count) put(out, type, i, 0.0f);
 }
 
-// A warp's 32 rows (lanes) x 128 columns of sums to row-major memory, 256 bytes of a row at a time by way of shared
-// memory: a lane's row leaves by a bulk copy, which the next tile's blocks do not wait for, or, where rows are
-// not 16-byte aligned, by the warp's elements.
+// A warp's 32 rows (lanes) x 128 columns of sums to row-major memory, 128 bytes of a row at a time by way of shared
+// memory (a row's chunks permuted by its number, as the 128-byte swizzle does): by TMA, which the next tile's
+// blocks do not wait for, or, of a group's last rows and where rows are not 16-byte aligned, by the warp.  (A bulk
+// copy for each row instead takes the TMA unit as long as the loads of a tile.)
 template <class T>
-__device__ __forceinline__ void write_rows(const BlockTcParams& p, const f2 (&acc)[64], unsigned char* stage, int64_t row0, int rows,
-                                           int64_t n0, int64_t group, int lane) {
-  constexpr int COLS = 256 / sizeof(T), VEC = 16 / sizeof(T);
-  T* const out = static_cast<T*>(p.out) + group * p.out_group + row0 * p.ldl + n0;
-  const int cols = p.c.rows - n0 < 128 ? (int)(p.c.rows - n0) : 128;      // may be none
-  const bool vec = p.ldl % VEC == 0 && ((reinterpret_cast<uintptr_t>(p.out) | (uintptr_t)(p.out_group * sizeof(T))) & 15u) == 0;
+__device__ __forceinline__ void write_rows(const BlockTcParams& p, const CUtensorMap* map, const f2 (&acc)[64], unsigned char* stage,
+                                           int row0, int rows, int n0, int group, int lane) {
+  constexpr int COLS = 128 / sizeof(T), VEC = 16 / sizeof(T);
+  const int cols = p.c.rows - n0;                        // may be none
+  // TMA leaves out what is behind the last row and column of the output, not of a group
+  const bool whole = p.out_map && rows > 0 && (rows >= 32 || p.kind != BlockKind::grouped);
+  const bool vec = p.out_map;                            // 16-byte aligned rows
 #pragma unroll
-  for (int c = 0; c < 128; c += COLS) {
-    bulk_store_wait();                                   // the copy before has read this lane's row
+  for (int c0 = 0; c0 < 128; c0 += 2 * COLS) {           // two pieces at a time
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");   // those before have been read
     __syncwarp();
 #pragma unroll
-    for (int i = 0; i < COLS; i += VEC) {
+    for (int i = 0; i < 2 * COLS; i += VEC) {
       float v[VEC];
 #pragma unroll
-      for (int j = 0; j < VEC; j += 2) halves(acc[(c + i + j) / 2], v[j], v[j + 1]);
-      store_f<T, VEC>(reinterpret_cast<T*>(stage + lane * kOutRow) + i, v);
+      for (int j = 0; j < VEC; j += 2) halves(acc[(c0 + i + j) / 2], v[j], v[j + 1]);
+      store_f<T, VEC>(reinterpret_cast<T*>(stage + i / COLS * 4096 + lane * 128 + (((i % COLS / VEC) ^ (lane & 7)) * 16)), v);
     }
-    if (vec) {
-      const int n = cols - c < COLS ? cols - c : COLS;
+    if (whole) {
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-      if (lane < rows && n > 0) bulk_store(out + lane * p.ldl + c, smem_addr(stage + lane * kOutRow), n * (uint32_t)sizeof(T));
-    } else {
       __syncwarp();
-#pragma unroll 4
-      for (int r = 0; r < rows; ++r)
+      if (lane == 0) {
 #pragma unroll
-        for (int i = 0; i < COLS; i += 32)
-          if (c + i + lane < cols) out[r * p.ldl + c + i + lane] = *(reinterpret_cast<const T*>(stage + r * kOutRow) + i + lane);
+        for (int i = 0; i < 2; ++i)
+          if (c0 + i * COLS < cols)
+            asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];"
+                         ::"l"(reinterpret_cast<uint64_t>(map)), "r"(smem_addr(stage) + i * 4096), "r"(n0 + c0 + i * COLS), "r"(row0), "r"(group)
+                         : "memory");
+        asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+      }
+      continue;
+    }
+    __syncwarp();
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int c = c0 + k * COLS;
+      const unsigned char* const buf = stage + k * 4096;
+      T* const out = static_cast<T*>(p.out) + group * p.out_group + (int64_t)row0 * p.ldl + n0 + c;
+      if (vec) {
+        const int n = (lane & 7) * VEC;
+        if (c + n < cols) {
+#pragma unroll
+          for (int r = lane >> 3; r < 32; r += 4)
+            if (r < rows)
+              *reinterpret_cast<uint4*>(out + r * p.ldl + n) = *reinterpret_cast<const uint4*>(buf + r * 128 + (((lane & 7) ^ (r & 7)) * 16));
+        }
+      } else {
+#pragma unroll 4
+        for (int r = 0; r < rows; ++r)
+#pragma unroll
+          for (int i = lane; i < COLS; i += 32)
+            if (c + i < cols) out[r * p.ldl + i] = *reinterpret_cast<const T*>(buf + r * 128 + (((i / VEC) ^ (r & 7)) * 16) + (i % VEC) * sizeof(T));
+      }
     }
   }
 }
@@ -338,7 +358,7 @@ __device__ __forceinline__ void write_rows(const BlockTcParams& p, const f2 (&ac
 template <int BN, int MODE>
 __global__ void __launch_bounds__(kTcThreads8, 1)
 block_tc_kernel(const __grid_constant__ BlockTcParams p, const __grid_constant__ CUtensorMap map_l,
-                const __grid_constant__ CUtensorMap map_c) {
+                const __grid_constant__ CUtensorMap map_c, const __grid_constant__ CUtensorMap map_out) {
   using SH = BlockTcShape<BN>;
   constexpr bool PAIR = SH::PAIR;
   constexpr int NS = SH::NS, NB = SH::NB, H = SH::H, OWN = SH::OWN, READ = SH::READ;
@@ -465,31 +485,43 @@ block_tc_kernel(const __grid_constant__ BlockTcParams p, const __grid_constant__
     float* const cs = reinterpret_cast<float*>(smem + SH::CS) + half * OWN;   // the columns' scales, two slots BN apart
     uint32_t it = 0;
     bool ok = true, met = false;
-    for (int tile = first_tile; tile < tiles && ok; tile += step) {
-      const BlockTile t = tile_at<BN>(p, start, before, tile, rank);
+    // the scales of a block, asked for two blocks ahead, by addresses that step from block to block; those of a tile's
+    // first two blocks before the outputs of the tile before are written
+    BlockTile t;
+    const float *pl = nullptr, *pc = nullptr;
+    bool r_in = false, c_in = false;
+    int left = 0;                                        // blocks whose scales have not been asked for
+    float rl0 = 0.0f, rc0 = 0.0f, rl1 = 0.0f, rc1 = 0.0f;
+    auto ask = [&](float& rl, float& rc) {
+      rl = r_in && left > 0 ? __ldg(pl) : 0.0f;
+      rc = c_in && left > 0 ? __ldg(pc) : 0.0f;
+      pl += p.l.ks;
+      pc += p.c.ks;
+      --left;
+    };
+    auto begin = [&](int tile) {
+      if (tile >= tiles) return;
+      t = tile_at<BN>(p, start, before, tile, rank);
       const int gl = p.kind == BlockKind::grouped && SH::SWAP ? t.group : 0, gc = p.kind == BlockKind::grouped && !SH::SWAP ? t.group : 0;
-      const int l = t.l0 + mine, c = t.c0 + half * OWN;
-      const bool l_in = l < t.l_end;
-      // the scales of a block, asked for two blocks ahead, by addresses that step from block to block
-      const int c_at = MODE == kScaleLane ? c : c + mine;
-      const bool c_in = c_at < t.c_end && (MODE == kScaleLane || mine < OWN), r_in = MODE == kScaleColumns ? c_in : l_in;
-      const float* pl = p.l.scale + gl * p.l.gs + ((MODE == kScaleColumns ? t.l0 : l) >> p.l.shift) * p.l.rs + t.kb0 * p.l.ks;
-      const float* pc = p.c.scale + gc * p.c.gs + (c_at >> p.c.shift) * p.c.rs + t.kb0 * p.c.ks;
-      int left = t.kb1 - t.kb0;                          // blocks whose scales have not been asked for
-      auto ask = [&](float& rl, float& rc) {
-        rl = r_in && left > 0 ? __ldg(pl) : 0.0f;
-        rc = c_in && left > 0 ? __ldg(pc) : 0.0f;
-        pl += p.l.ks;
-        pc += p.c.ks;
-        --left;
-      };
-      float rl0, rc0, rl1, rc1;
+      const int l_at = MODE == kScaleColumns ? t.l0 : t.l0 + mine, c_at = t.c0 + half * OWN + (MODE == kScaleLane ? 0 : mine);
+      c_in = c_at < t.c_end && (MODE == kScaleLane || mine < OWN);
+      r_in = MODE == kScaleColumns ? c_in : l_at < t.l_end;
+      pl = p.l.scale + gl * p.l.gs + (l_at >> p.l.shift) * p.l.rs + t.kb0 * p.l.ks;
+      pc = p.c.scale + gc * p.c.gs + (c_at >> p.c.shift) * p.c.rs + t.kb0 * p.c.ks;
+      left = t.kb1 - t.kb0;
       ask(rl0, rc0);
       ask(rl1, rc1);
+    };
+    begin(first_tile);
+    for (int tile = first_tile; tile < tiles && ok; tile += step) {
+      const int l0 = t.l0, l_end = t.l_end, c = t.c0 + half * OWN, c_end = t.c_end, group = p.kind == BlockKind::wgrad ? t.group : 0;
+      const int l = l0 + mine;
+      const bool l_in = l < l_end;
+      const int kb0 = t.kb0, kb1 = t.kb1;
       f2 acc[OWN / 2];
 #pragma unroll
       for (int i = 0; i < OWN / 2; ++i) acc[i] = 0ull;
-      for (int kb = t.kb0; kb < t.kb1; ++kb, ++it) {
+      for (int kb = kb0; kb < kb1; ++kb, ++it) {
         const uint32_t buf = it % NB;
         const float rl = rl0, rc = rc0;
         rl0 = rl1;
@@ -542,24 +574,23 @@ block_tc_kernel(const __grid_constant__ BlockTcParams p, const __grid_constant__
         if (!ok) break;
       }
       if (!ok) break;
+      begin(tile + step);
       if constexpr (!SH::SWAP) {
-        unsigned char* const stage = smem + SH::OUT + (warp - 4) * 32 * kOutRow;
-        const int64_t row0 = t.l0 + quad * 32;
-        const int rows = t.l_end - row0 < 32 ? (int)(t.l_end - row0) : 32;
-        const int64_t group = p.kind == BlockKind::wgrad ? t.group : 0;
-        if (p.out_type == EMU_OUT_F32) write_rows<float>(p, acc, stage, row0, rows, c, group, lane);
-        else if (p.out_type == EMU_OUT_BF16) write_rows<__nv_bfloat16>(p, acc, stage, row0, rows, c, group, lane);
-        else write_rows<__half>(p, acc, stage, row0, rows, c, group, lane);
+        unsigned char* const stage = smem + SH::OUT + (warp - 4) * (kOutStage / 8);
+        const int row0 = l0 + quad * 32, rows = l_end - row0 < 32 ? l_end - row0 : 32;
+        if (p.out_type == EMU_OUT_F32) write_rows<float>(p, &map_out, acc, stage, row0, rows, c, group, lane);
+        else if (p.out_type == EMU_OUT_BF16) write_rows<__nv_bfloat16>(p, &map_out, acc, stage, row0, rows, c, group, lane);
+        else write_rows<__half>(p, &map_out, acc, stage, row0, rows, c, group, lane);
       } else if (p.slices == 1) {
         auto write = [&](auto* out) {
           using T = std::remove_pointer_t<decltype(out)>;
-          T* const to = out + (p.kind == BlockKind::wgrad ? t.group * p.out_group : 0) + l * p.ldl;
+          T* const to = out + group * p.out_group + l * p.ldl;
 #pragma unroll
           for (int i = 0; i < OWN; i += 2) {
             float a, b;
             halves(acc[i / 2], a, b);
-            if (l_in && c + i < t.c_end) to[(c + i) * p.ldc] = from_f<T>(a);
-            if (l_in && c + i + 1 < t.c_end) to[(c + i + 1) * p.ldc] = from_f<T>(b);
+            if (l_in && c + i < c_end) to[(c + i) * p.ldc] = from_f<T>(a);
+            if (l_in && c + i + 1 < c_end) to[(c + i + 1) * p.ldc] = from_f<T>(b);
           }
         };
         if (p.out_type == EMU_OUT_F32) write(static_cast<float*>(p.out));
@@ -587,7 +618,7 @@ block_tc_kernel(const __grid_constant__ BlockTcParams p, const __grid_constant__
       put_zeros(p.out, p.out_type, 0, start[0] * N, who, count);
       put_zeros(p.out, p.out_type, start[p.E] * N, (int64_t)p.T * N, who, count);
     }
-    if (PAIR) bulk_store_wait();                         // before the memory that they leave from is gone
+    if (PAIR && lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");   // before the memory is gone
     __syncwarp();
     if (SH::SWAP && p.slices > 1 && !met) cluster_sync();   // a warp that gave up goes past the first barrier too
   }
