@@ -8,9 +8,15 @@ namespace emu_ops {
 
 constexpr int kBlock = 128;                              // values that share a scale
 
-// one code's value; every FP8 value is exact in fp16
-__device__ __forceinline__ float code_value(uint8_t code, int fmt) {
-  return __half2float(__half(__nv_cvt_fp8_to_halfraw(code, fmt == EMU_E4M3FN ? __NV_E4M3 : __NV_E5M2)));
+template <class T> __device__ __forceinline__ void put(void* out, int64_t i, float v) { static_cast<T*>(out)[i] = from_f<T>(v); }
+__device__ __forceinline__ void put(void* out, int type, int64_t i, float v) {
+  if (type == EMU_OUT_F32) put<float>(out, i, v);
+  else if (type == EMU_OUT_BF16) put<__nv_bfloat16>(out, i, v);
+  else put<__half>(out, i, v);
+}
+// zeros over the elements [from, to) of the output, by `count` threads
+__device__ __forceinline__ void put_zeros(void* out, int type, int64_t from, int64_t to, int64_t who, int64_t count) {
+  for (int64_t i = from + who; i < to; i += count) put(out, type, i, 0.0f);
 }
 
 }  // namespace emu_ops

@@ -18,6 +18,7 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();  // ops_int8.cu
 
 }  // namespace emu_ops
 
+#include "ops_block_few.cuh"
 #include "ops_block_tc.cuh"
 
 namespace emu_ops {
@@ -153,9 +154,38 @@ template <int BN> int launch_tc(const BlockTcParams& p, int mode, int64_t tiles,
   return EMU_OK;
 }
 
+// Up to eight tokens of a dense product whose rows are whole 16-byte chunks, where latency counts; where bandwidth does,
+// the TMA's deep queues win.  As few and by tcgen05: 1 x 5760 x 1920 4.6 and 8.4 us, 8 x 4096 x 4096 5.7 and 8.3,
+// 8 x 8192 x 2048 6.6 and 8.4, 8 x 16384 x 2048 11.6 and 8.8, 8 x 8192 x 8192 22 and 17; of 16 tokens 8.1 and 8.4.
+bool few_tokens(const BlockMm& p, const CodesView& va, const CodesView& vb) {
+  return p.kind == BlockKind::dense && p.M <= 8 && p.K > 0 && p.K % 16 == 0 && !va.mn && !vb.mn && va.fits() && vb.fits() &&
+         p.N * p.K <= (int64_t)24 << 20;
+}
+void run_few_tokens(const BlockMm& p, const CodesView& va, const CodesView& vb, cudaStream_t st) {
+  BlockFewParams q = {};
+  q.w = vb.at; q.w_row = vb.stride;
+  q.ws = p.b.scale; q.ws_shift = p.b.scale_rows == 1 ? 0 : 7; q.ws_row = p.b.scale_row_stride; q.ws_k = p.b.scale_k_stride;
+  q.t = va.at; q.t_row = va.stride;
+  q.ts = p.a.scale; q.ts_shift = p.a.scale_rows == 1 ? 0 : 7; q.ts_row = p.a.scale_row_stride; q.ts_k = p.a.scale_k_stride;
+  q.M = (int)p.M; q.N = p.N; q.K = (int)p.K;
+  const int64_t kb = (p.K + kBlock - 1) / kBlock;
+  q.share = kb >= 8 ? 8 : kb >= 4 ? 4 : kb >= 2 ? 2 : 1;
+  q.out = p.out; q.out_type = p.out_type;
+  auto kernel = p.b.format == EMU_E4M3FN
+                    ? p.a.format == EMU_E4M3FN ? block_few_kernel<EMU_E4M3FN, EMU_E4M3FN> : block_few_kernel<EMU_E4M3FN, EMU_E5M2>
+                    : p.a.format == EMU_E4M3FN ? block_few_kernel<EMU_E5M2, EMU_E4M3FN> : block_few_kernel<EMU_E5M2, EMU_E5M2>;
+  const int64_t rows = 16 * (8 / q.share);
+  kernel<<<(unsigned)((p.N + rows - 1) / rows), 256, 0, st>>>(q);
+}
+
 int run_block_mm(const BlockMm& p, void* workspace, cudaStream_t st) {
   const bool wgrad = p.kind == BlockKind::wgrad, grouped = p.kind == BlockKind::grouped;
   CodesView va = view_of(p.a, p.M, p.K, 1, wgrad), vb = view_of(p.b, p.N, p.K, grouped ? p.E : 1, wgrad);
+  const int64_t rows_of_group = grouped ? (p.M + (p.E > 0 ? p.E : 1) - 1) / (p.E > 0 ? p.E : 1) : p.M;   // about
+  if (few_tokens(p, va, vb)) {
+    run_few_tokens(p, va, vb, st);
+    return emu_ops_launched("emu_block_scaled_mm");
+  }
   const bool any = p.K > 0 && !(grouped && p.E == 0);    // anything to multiply
   if (any) {
     unsigned char* ws = static_cast<unsigned char*>(workspace);
@@ -168,7 +198,7 @@ int run_block_mm(const BlockMm& p, void* workspace, cudaStream_t st) {
   auto up = [](int64_t n, int64_t d) { return (n + d - 1) / d; };
   // which form
   int BN = 256, slices = 1;
-  const int64_t rows = grouped ? up(p.M, p.E > 0 ? p.E : 1) : p.M;                // of the tokens' side, about
+  const int64_t rows = rows_of_group;
   if (up(p.M, 256) * up(p.N, 256) * groups < sms / 2 || (grouped && rows <= 128)) {
     BN = va.mn || rows > 64 ? 128 : rows > 32 ? 64 : 32;
     if (!grouped && !wgrad) {

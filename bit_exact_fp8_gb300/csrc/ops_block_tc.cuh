@@ -106,42 +106,48 @@ __device__ __forceinline__ uint32_t in_cluster(uint32_t at, int rank) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(at), "r"(rank));
   return a;
 }
-// columns of this warp's 32 lanes, asked for, and waited for (whatever was asked for before)
-__device__ __forceinline__ void tmem_ask(uint32_t addr, float (&r)[32]) {
+// columns of this warp's 32 lanes, read and waited for
+__device__ __forceinline__ void tmem_read(uint32_t addr, float (&r)[16]) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
-      : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]), "=f"(r[8]),
-        "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15]), "=f"(r[16]),
-        "=f"(r[17]), "=f"(r[18]), "=f"(r[19]), "=f"(r[20]), "=f"(r[21]), "=f"(r[22]), "=f"(r[23]), "=f"(r[24]),
-        "=f"(r[25]), "=f"(r[26]), "=f"(r[27]), "=f"(r[28]), "=f"(r[29]), "=f"(r[30]), "=f"(r[31])
-      : "r"(addr)
-      : "memory");
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {"
+        "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]), "=f"(r[8]),
+          "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15])
+        : "r"(addr)
+        : "memory");
 }
-__device__ __forceinline__ void tmem_ask(uint32_t addr, float (&r)[16]) {
+__device__ __forceinline__ void tmem_read(uint32_t addr, float (&r)[32]) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
-      : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]), "=f"(r[8]),
-        "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15])
-      : "r"(addr)
-      : "memory");
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {"
+        "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, "
+        "%21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]), "=f"(r[8]),
+          "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15]), "=f"(r[16]),
+          "=f"(r[17]), "=f"(r[18]), "=f"(r[19]), "=f"(r[20]), "=f"(r[21]), "=f"(r[22]), "=f"(r[23]), "=f"(r[24]),
+          "=f"(r[25]), "=f"(r[26]), "=f"(r[27]), "=f"(r[28]), "=f"(r[29]), "=f"(r[30]), "=f"(r[31])
+        : "r"(addr)
+        : "memory");
 }
-template <int N> __device__ __forceinline__ void tmem_ask_all(uint32_t at, float (&r)[N]) {
-  if constexpr (N == 64) {
-    tmem_ask(at, *reinterpret_cast<float(*)[32]>(r));
-    tmem_ask(at + 32, *reinterpret_cast<float(*)[32]>(r + 32));
-  } else {
-    tmem_ask(at, r);
-  }
-}
-__device__ __forceinline__ void tmem_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
-// acc += (x, y) * by, of values asked for from tensor memory: volatile, so that it stays behind the wait for them
-__device__ __forceinline__ void add_scaled(f2& acc, float x, float y, f2 by) {
-  asm volatile("{\n .reg .b64 v;\n mov.b64 v, {%1, %2};\n fma.rn.f32x2 %0, v, %3, %0;\n}" : "+l"(acc) : "f"(x), "f"(y), "l"(by));
-}
-__device__ __forceinline__ void add_scaled(f2& acc, float x, float y, f2 by, f2 by2) {
-  asm volatile("{\n .reg .b64 v;\n mov.b64 v, {%1, %2};\n mul.rn.f32x2 v, v, %3;\n fma.rn.f32x2 %0, v, %4, %0;\n}"
-               : "+l"(acc) : "f"(x), "f"(y), "l"(by), "l"(by2));
+__device__ __forceinline__ void tmem_read(uint32_t addr, float (&r)[64]) {
+  asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x64.b32 {"
+        "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, "
+        "%21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32, %33, %34, %35, %36, %37, %38, %39, "
+        "%40, %41, %42, %43, %44, %45, %46, %47, %48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, "
+        "%59, %60, %61, %62, %63}, [%64];\n"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]), "=f"(r[8]),
+          "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15]), "=f"(r[16]),
+          "=f"(r[17]), "=f"(r[18]), "=f"(r[19]), "=f"(r[20]), "=f"(r[21]), "=f"(r[22]), "=f"(r[23]), "=f"(r[24]),
+          "=f"(r[25]), "=f"(r[26]), "=f"(r[27]), "=f"(r[28]), "=f"(r[29]), "=f"(r[30]), "=f"(r[31]), "=f"(r[32]),
+          "=f"(r[33]), "=f"(r[34]), "=f"(r[35]), "=f"(r[36]), "=f"(r[37]), "=f"(r[38]), "=f"(r[39]), "=f"(r[40]),
+          "=f"(r[41]), "=f"(r[42]), "=f"(r[43]), "=f"(r[44]), "=f"(r[45]), "=f"(r[46]), "=f"(r[47]), "=f"(r[48]),
+          "=f"(r[49]), "=f"(r[50]), "=f"(r[51]), "=f"(r[52]), "=f"(r[53]), "=f"(r[54]), "=f"(r[55]), "=f"(r[56]),
+          "=f"(r[57]), "=f"(r[58]), "=f"(r[59]), "=f"(r[60]), "=f"(r[61]), "=f"(r[62]), "=f"(r[63])
+        : "r"(addr)
+        : "memory");
 }
 
 // One lane of the warp, in code that the whole warp runs: its values are the warp's then, and the addresses and descriptors
@@ -275,23 +281,12 @@ template <int BN> __device__ __forceinline__ BlockTile tile_at(const BlockTcPara
   return t;
 }
 
-template <class T> __device__ __forceinline__ void put(void* out, int64_t i, float v) { static_cast<T*>(out)[i] = from_f<T>(v); }
-__device__ __forceinline__ void put(void* out, int type, int64_t i, float v) {
-  if (type == EMU_OUT_F32) put<float>(out, i, v);
-  else if (type == EMU_OUT_BF16) put<__nv_bfloat16>(out, i, v);
-  else put<__half>(out, i, v);
-}
-// zeros over the elements [from, to) of the output, by `count` threads
-__device__ __forceinline__ void put_zeros(void* out, int type, int64_t from, int64_t to, int64_t who, int64_t count) {
-  for (int64_t i = from + who; i < to; i += count) put(out, type, i, 0.0f);
-}
-
 // A warp's 32 rows (lanes) x 128 columns of sums to row-major memory, 128 bytes of a row at a time by way of shared
 // memory (a row's chunks permuted by its number, as the 128-byte swizzle does): by TMA, which the next tile's
 // blocks do not wait for, or, of a group's last rows and where rows are not 16-byte aligned, by the warp.  (A bulk
 // copy for each row instead takes the TMA unit as long as the loads of a tile.)
 template <class T>
-__device__ __forceinline__ void write_rows(const BlockTcParams& p, const CUtensorMap* map, const f2 (&acc)[64], unsigned char* stage,
+__device__ __forceinline__ void write_rows(const BlockTcParams& p, const CUtensorMap* map, const float2 (&acc)[64], unsigned char* stage,
                                            int row0, int rows, int n0, int group, int lane) {
   constexpr int COLS = 128 / sizeof(T), VEC = 16 / sizeof(T);
   const int cols = p.c.rows - n0;                        // may be none
@@ -306,7 +301,10 @@ __device__ __forceinline__ void write_rows(const BlockTcParams& p, const CUtenso
     for (int i = 0; i < 2 * COLS; i += VEC) {
       float v[VEC];
 #pragma unroll
-      for (int j = 0; j < VEC; j += 2) halves(acc[(c0 + i + j) / 2], v[j], v[j + 1]);
+      for (int j = 0; j < VEC; j += 2) {
+        v[j] = acc[(c0 + i + j) / 2].x;
+        v[j + 1] = acc[(c0 + i + j) / 2].y;
+      }
       store_f<T, VEC>(reinterpret_cast<T*>(stage + i / COLS * 4096 + lane * 128 + (((i % COLS / VEC) ^ (lane & 7)) * 16)), v);
     }
     if (whole) {
@@ -518,9 +516,9 @@ block_tc_kernel(const __grid_constant__ BlockTcParams p, const __grid_constant__
       const int l = l0 + mine;
       const bool l_in = l < l_end;
       const int kb0 = t.kb0, kb1 = t.kb1;
-      f2 acc[OWN / 2];
+      float2 acc[OWN / 2];
 #pragma unroll
-      for (int i = 0; i < OWN / 2; ++i) acc[i] = 0ull;
+      for (int i = 0; i < OWN / 2; ++i) acc[i] = make_float2(0.0f, 0.0f);
       for (int kb = kb0; kb < kb1; ++kb, ++it) {
         const uint32_t buf = it % NB;
         const float rl = rl0, rc = rc0;
@@ -534,7 +532,7 @@ block_tc_kernel(const __grid_constant__ BlockTcParams p, const __grid_constant__
           if (lane == 0) bar_arrive(cfull + 8 * half);
           ok = bar_wait_all(cfull + 8 * half, it & 1, given_up);
         }
-        const f2 by = MODE == kScaleLane ? pair(rl * rc, rl * rc) : pair(rl, rl);
+        const float by = MODE == kScaleLane ? rl * rc : rl;
 #pragma unroll
         for (int h = 0; h < H; ++h) {
           const uint32_t full_of = tfull + 8 * (buf * H + h);
@@ -544,8 +542,7 @@ block_tc_kernel(const __grid_constant__ BlockTcParams p, const __grid_constant__
           // the part's columns of a warp: all asked for at once, and the tensor memory given back before they are used
           float r[READ];
           const uint32_t at = tmem + ((uint32_t)(quad * 32) << 16) + buf * BN + h * (BN / H) + half * READ;
-          tmem_ask_all<READ>(at, r);
-          tmem_wait();
+          tmem_read(at, r);
           tc_fence_before();
           __syncwarp();
           if (lane == 0) {
@@ -554,21 +551,21 @@ block_tc_kernel(const __grid_constant__ BlockTcParams p, const __grid_constant__
           }
 #pragma unroll
           for (int i = 0; i < READ; i += 4) {
-            f2& a0 = acc[(h * READ + i) / 2];
-            f2& a1 = acc[(h * READ + i) / 2 + 1];
-            if (MODE == kScaleLane) {
-              add_scaled(a0, r[i], r[i + 1], by);
-              add_scaled(a1, r[i + 2], r[i + 3], by);
-            } else {
+            float2& a0 = acc[(h * READ + i) / 2];
+            float2& a1 = acc[(h * READ + i) / 2 + 1];
+            float2 x0 = make_float2(r[i], r[i + 1]), x1 = make_float2(r[i + 2], r[i + 3]);
+            float2 s0 = make_float2(by, by), s1 = s0;
+            if (MODE != kScaleLane) {
               const float4 s = *reinterpret_cast<const float4*>(cv + h * READ + i);
-              if (MODE == kScaleColumns) {
-                add_scaled(a0, r[i], r[i + 1], pair(s.x, s.y));
-                add_scaled(a1, r[i + 2], r[i + 3], pair(s.z, s.w));
-              } else {
-                add_scaled(a0, r[i], r[i + 1], by, pair(s.x, s.y));
-                add_scaled(a1, r[i + 2], r[i + 3], by, pair(s.z, s.w));
+              if (MODE == kScaleBoth) {
+                x0 = __fmul2_rn(x0, s0);
+                x1 = __fmul2_rn(x1, s0);
               }
+              s0 = make_float2(s.x, s.y);
+              s1 = make_float2(s.z, s.w);
             }
+            a0 = __ffma2_rn(x0, s0, a0);
+            a1 = __ffma2_rn(x1, s1, a1);
           }
         }
         if (!ok) break;
@@ -586,12 +583,8 @@ block_tc_kernel(const __grid_constant__ BlockTcParams p, const __grid_constant__
           using T = std::remove_pointer_t<decltype(out)>;
           T* const to = out + group * p.out_group + l * p.ldl;
 #pragma unroll
-          for (int i = 0; i < OWN; i += 2) {
-            float a, b;
-            halves(acc[i / 2], a, b);
-            if (l_in && c + i < c_end) to[(c + i) * p.ldc] = from_f<T>(a);
-            if (l_in && c + i + 1 < c_end) to[(c + i + 1) * p.ldc] = from_f<T>(b);
-          }
+          for (int i = 0; i < OWN; ++i)
+            if (l_in && c + i < c_end) to[(c + i) * p.ldc] = from_f<T>(i & 1 ? acc[i / 2].y : acc[i / 2].x);
         };
         if (p.out_type == EMU_OUT_F32) write(static_cast<float*>(p.out));
         else if (p.out_type == EMU_OUT_BF16) write(static_cast<__nv_bfloat16*>(p.out));
@@ -606,10 +599,8 @@ block_tc_kernel(const __grid_constant__ BlockTcParams p, const __grid_constant__
 #pragma unroll
         for (int i = 0; i < OWN; ++i) {
           const int j = half * OWN + i, owner = j / per;
-          float a, b;
-          halves(acc[i / 2], a, b);
           asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(in_cluster(sums + (slice * per + j % per) * 128 + mine, owner)),
-                       "f"(i & 1 ? b : a) : "memory");
+                       "f"(i & 1 ? acc[i / 2].y : acc[i / 2].x) : "memory");
         }
       }
     }
