@@ -201,7 +201,7 @@ int run_block_mm(const BlockMm& p, void* workspace, cudaStream_t st) {
   const int64_t rows = rows_of_group;
   if (up(p.M, 256) * up(p.N, 256) * groups < sms / 2 || (grouped && rows <= 128)) {
     BN = va.mn || rows > 64 ? 128 : rows > 32 ? 64 : 32;
-    if (!grouped && !wgrad) {
+    if (!grouped && !wgrad && BN < 128) {
       const int64_t tiles = up(p.N, 128) * up(p.M, BN);
       while (slices < 8 && tiles * slices * 2 <= sms && kb / (slices * 2) >= 2) slices *= 2;
     }

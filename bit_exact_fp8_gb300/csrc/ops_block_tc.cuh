@@ -40,12 +40,13 @@ struct BlockTcParams {
 template <int BN> struct BlockTcShape {
   static constexpr bool PAIR = BN == 256;                // two CTAs on a tile of 256 x 256, each with half of either side
   static constexpr bool SWAP = !PAIR;                    // the output's rows are the columns C
+  static constexpr bool ALT = BN <= 64;                  // either four reading warps take every other block, with all columns
   static constexpr int L = PAIR ? 256 : 128, C_ROWS = PAIR ? 128 : BN;       // a tile's lanes; rows of C that a CTA loads
-  static constexpr int NS = PAIR ? 4 : BN == 128 ? 6 : 8, STAGE = 128 * 128 + C_ROWS * 128, NB = PAIR ? 2 : 4;
+  static constexpr int NS = PAIR ? 4 : BN == 128 ? 6 : BN == 64 ? 7 : 8, STAGE = 128 * 128 + C_ROWS * 128, NB = PAIR ? 2 : 4;
   static constexpr int H = PAIR ? 2 : 1;                 // parts of a tile's columns, each with MMAs and barriers of its own
-  static constexpr int OWN = BN / 2, READ = OWN / H, TMEM = NB * BN;         // a warp's columns, and those of a part
-  static constexpr int OUT = NS * STAGE, CS = OUT + (PAIR ? kOutStage : 0), BARS = CS + 2 * BN * 4;
-  static constexpr int TABLE = BARS + 8 * (3 * NS + 2 * NB * H + 3) + 8 + 2 * 12 * 4;
+  static constexpr int OWN = ALT ? BN : BN / 2, READ = OWN / H, TMEM = NB * BN;          // a warp's columns, and those of a part
+  static constexpr int OUT = NS * STAGE, CS = OUT + (PAIR ? kOutStage : ALT ? BN * 128 * 4 : 0), BARS = CS + 8 * 2 * OWN * 4;
+  static constexpr int BAR_COUNT = 3 * NS + 2 * NB * H + 10, TABLE = BARS + 8 * BAR_COUNT + 8 + 2 * 12 * 4;
   static constexpr int smem(int E) { return TABLE + 2 * (E + 1) * 4 + 1024; }
 };
 static_assert(BlockTcShape<256>::smem(kMaxExperts) <= kMaxSmem && BlockTcShape<128>::smem(kMaxExperts) <= kMaxSmem &&
@@ -99,6 +100,11 @@ template <bool PAIR> __device__ __forceinline__ void tmem_free(uint32_t at, int 
 // that the thread has under way (8192 x 5760 x 1920 170 us with it).
 __device__ __forceinline__ void bar_arrive_cluster(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// `bytes` of this CTA's shared memory to another's of the cluster, counted by a barrier there
+__device__ __forceinline__ void send(uint32_t dst, uint32_t src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "r"(src),
+               "r"(bytes), "r"(bar) : "memory");
 }
 __device__ __forceinline__ void fence_cluster() { asm volatile("fence.acq_rel.cluster;" ::: "memory"); }
 __device__ __forceinline__ uint32_t in_cluster(uint32_t at, int rank) {
@@ -351,7 +357,7 @@ __device__ __forceinline__ void write_rows(const BlockTcParams& p, const CUtenso
 // tells the pair's first CTA that its blocks are there), warps 4 to 11 scale and add: each holds 32 lanes x BN / 2
 // columns of sums in registers.  BN = 256: pairs of CTAs, whose MMAs the first one issues for both (an SM takes
 // in 64 bytes a cycle: a block of 128 x 256 outputs would need 48 KB every 512 cycles, of the pair each 32).
-// Several slices of K (dense, BN < 256): the CTAs of a cluster, which share out the columns at the end.  All
+// Several slices of K (dense, BN <= 64): the CTAs of a cluster, which share out the columns at the end.  All
 // waits are bounded; a role that gives up sets the status and takes the others along.
 template <int BN, int MODE>
 __global__ void __launch_bounds__(kTcThreads8, 1)
@@ -359,13 +365,14 @@ block_tc_kernel(const __grid_constant__ BlockTcParams p, const __grid_constant__
                 const __grid_constant__ CUtensorMap map_c, const __grid_constant__ CUtensorMap map_out) {
   using SH = BlockTcShape<BN>;
   constexpr bool PAIR = SH::PAIR;
+  constexpr bool ALT = SH::ALT;
   constexpr int NS = SH::NS, NB = SH::NB, H = SH::H, OWN = SH::OWN, READ = SH::READ;
   extern __shared__ unsigned char raw[];
   unsigned char* const smem = raw + ((1024u - (smem_addr(raw) & 1023u)) & 1023u);
   const uint32_t base = smem_addr(smem);
   const uint32_t full = base + SH::BARS, empty = full + 8 * NS, fixed = empty + 8 * NS, tfull = fixed + 8 * NS, tempty = tfull + 8 * NB * H,
-                 cfull = tempty + 8 * NB * H, drained = cfull + 16;
-  uint32_t* const slot = reinterpret_cast<uint32_t*>(smem + SH::BARS + 8 * (3 * NS + 2 * NB * H + 3));
+                 joined = tempty + 8 * NB * H, parted = joined + 32, drained = parted + 32, met_all = drained + 8;
+  uint32_t* const slot = reinterpret_cast<uint32_t*>(smem + SH::BARS + 8 * SH::BAR_COUNT);
   volatile int* const given_up = reinterpret_cast<volatile int*>(slot + 1);
   int* const part = reinterpret_cast<int*>(slot + 2);
   int* const start = reinterpret_cast<int*>(smem + SH::TABLE);
@@ -381,10 +388,12 @@ block_tc_kernel(const __grid_constant__ BlockTcParams p, const __grid_constant__
     }
     for (int i = 0; i < NB * H; ++i) {
       bar_init(tfull + 8 * i, 1);
-      bar_init(tempty + 8 * i, PAIR ? 16 : 8);           // one arrival a reading warp
+      bar_init(tempty + 8 * i, PAIR ? 16 : ALT ? 4 : 8); // one arrival a reading warp
     }
-    for (int i = 0; i < 2; ++i) bar_init(cfull + 8 * i, 4);   // the columns' scales, one arrival a warp of the half
-    bar_init(drained, H);
+    for (int i = 0; i < 8; ++i) bar_init(joined + 8 * i, 1);
+    bar_init(drained, 2);
+    bar_init(met_all, 1);
+    if (p.slices > 1) bar_expect(met_all, BN * 128 * 4);  // what the slices send of this one's columns
     *given_up = 0;
     bar_init_fence();
   }
@@ -421,16 +430,17 @@ block_tc_kernel(const __grid_constant__ BlockTcParams p, const __grid_constant__
       }
       if (!ok)                                           // the loads issued last, one stage each at most
         for (uint32_t i = it > NS ? it - NS : 0; i < it; ++i) (void)bar_wait(full + 8 * (i % NS), (i / NS) & 1);
-    } else if (warp <= H && rank == 0) {                 // of a pair warp 2 too: a warp issues the MMAs of one part of the columns
+    } else if (warp <= 2 && rank == 0) {                 // two warps: of a pair one for either part of the columns, else for every other block
       uint32_t it = 0;
       bool ok = true;
-      const int h = warp - 1;
+      const int mine = warp - 1, h = PAIR ? mine : 0;
       // a step of 32 of K, in 16 bytes; the parts' rows of C within each CTA's 128
       const uint32_t step_l = p.l.mn ? 256 : 2, step_c = p.c.mn ? 256 : 2, part_c = h * (p.c.mn ? 4 : 512);
       for (int tile = first_tile; tile < tiles && ok; tile += step) {
         const BlockTile t = tile_at<BN>(p, start, before, tile, rank);
         for (int kb = t.kb0; kb < t.kb1; ++kb, ++it) {
           const uint32_t s = it % NS, buf = it % NB;
+          if (!PAIR && (int)(it & 1) != mine) continue;
           ok = bar_wait_all((PAIR || p.kind == BlockKind::wgrad ? fixed : full) + 8 * s, (it / NS) & 1, given_up) &&
                (it < NB || bar_wait_all(tempty + 8 * (buf * H + h), (it / NB - 1) & 1, given_up));
           if (!ok) break;
@@ -480,68 +490,76 @@ block_tc_kernel(const __grid_constant__ BlockTcParams p, const __grid_constant__
     if constexpr (BN == 256) asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
     const int quad = warp & 3, half = (warp - 4) >> 2, mine = quad * 32 + lane;
     const uint32_t released = PAIR ? in_cluster(tempty, 0) : tempty;
-    float* const cs = reinterpret_cast<float*>(smem + SH::CS) + half * OWN;   // the columns' scales, two slots BN apart
+    float* const cs = reinterpret_cast<float*>(smem + SH::CS) + (warp - 4) * 2 * OWN;   // this warp's columns' scales, twice
+    constexpr int STEP = ALT ? 2 : 1, NC = MODE == kScaleLane ? 1 : OWN / 32;            // a lane's scales of columns
     uint32_t it = 0;
     bool ok = true, met = false;
-    // the scales of a block, asked for two blocks ahead, by addresses that step from block to block; those of a tile's
-    // first two blocks before the outputs of the tile before are written
+    // the scales of a block, asked for two of this warp's blocks ahead, by addresses that step from block to block; those of
+    // a tile's first before the outputs of the tile before are written
     BlockTile t;
     const float *pl = nullptr, *pc = nullptr;
-    bool r_in = false, c_in = false;
-    int left = 0;                                        // blocks whose scales have not been asked for
-    float rl0 = 0.0f, rc0 = 0.0f, rl1 = 0.0f, rc1 = 0.0f;
-    auto ask = [&](float& rl, float& rc) {
+    bool r_in = false;
+    int left = 0, c_at = 0;                              // blocks whose scales have not been asked for; a lane's first column
+    float rl0 = 0.0f, rl1 = 0.0f, rc0[NC] = {}, rc1[NC] = {};
+    auto ask = [&](float& rl, float (&rc)[NC]) {
       rl = r_in && left > 0 ? __ldg(pl) : 0.0f;
-      rc = c_in && left > 0 ? __ldg(pc) : 0.0f;
-      pl += p.l.ks;
-      pc += p.c.ks;
-      --left;
+#pragma unroll
+      for (int j = 0; j < NC; ++j)
+        rc[j] = left > 0 && c_at + 32 * j < t.c_end ? __ldg(pc + ((c_at + 32 * j) >> p.c.shift) * p.c.rs) : 0.0f;
+      pl += STEP * p.l.ks;
+      pc += STEP * p.c.ks;
+      left -= STEP;
     };
     auto begin = [&](int tile) {
       if (tile >= tiles) return;
       t = tile_at<BN>(p, start, before, tile, rank);
       const int gl = p.kind == BlockKind::grouped && SH::SWAP ? t.group : 0, gc = p.kind == BlockKind::grouped && !SH::SWAP ? t.group : 0;
-      const int l_at = MODE == kScaleColumns ? t.l0 : t.l0 + mine, c_at = t.c0 + half * OWN + (MODE == kScaleLane ? 0 : mine);
-      c_in = c_at < t.c_end && (MODE == kScaleLane || mine < OWN);
-      r_in = MODE == kScaleColumns ? c_in : l_at < t.l_end;
-      pl = p.l.scale + gl * p.l.gs + (l_at >> p.l.shift) * p.l.rs + t.kb0 * p.l.ks;
-      pc = p.c.scale + gc * p.c.gs + (c_at >> p.c.shift) * p.c.rs + t.kb0 * p.c.ks;
-      left = t.kb1 - t.kb0;
+      const int l_at = MODE == kScaleColumns ? t.l0 : t.l0 + mine, kb = t.kb0 + (ALT ? (int)(it ^ half) & 1 : 0);
+      r_in = l_at < t.l_end;
+      c_at = t.c0 + (ALT ? 0 : half * OWN) + (MODE == kScaleLane ? 0 : lane);
+      pl = p.l.scale + gl * p.l.gs + (l_at >> p.l.shift) * p.l.rs + kb * p.l.ks;
+      pc = p.c.scale + gc * p.c.gs + kb * p.c.ks;
+      left = t.kb1 - kb;
       ask(rl0, rc0);
       ask(rl1, rc1);
     };
     begin(first_tile);
-    for (int tile = first_tile; tile < tiles && ok; tile += step) {
-      const int l0 = t.l0, l_end = t.l_end, c = t.c0 + half * OWN, c_end = t.c_end, group = p.kind == BlockKind::wgrad ? t.group : 0;
+    uint32_t done = 0;                                   // tiles
+    for (int tile = first_tile; tile < tiles && ok; tile += step, ++done) {
+      const int l0 = t.l0, l_end = t.l_end, c = t.c0 + (ALT ? 0 : half * OWN), c_end = t.c_end, group = p.kind == BlockKind::wgrad ? t.group : 0;
       const int l = l0 + mine;
       const bool l_in = l < l_end;
-      const int kb0 = t.kb0, kb1 = t.kb1;
+      const int blocks = t.kb1 - t.kb0;
       float2 acc[OWN / 2];
 #pragma unroll
       for (int i = 0; i < OWN / 2; ++i) acc[i] = make_float2(0.0f, 0.0f);
-      for (int kb = kb0; kb < kb1; ++kb, ++it) {
-        const uint32_t buf = it % NB;
-        const float rl = rl0, rc = rc0;
+      for (int kb = ALT ? (int)(it ^ half) & 1 : 0; kb < blocks; kb += STEP) {
+        const uint32_t unit = it + kb, buf = unit % NB;
+        const float rl = rl0;
+        float rc[NC];
         rl0 = rl1;
-        rc0 = rc1;
-        ask(rl1, rc1);
-        float* const cv = cs + (it & 1) * BN;
-        if (MODE != kScaleLane) {
-          if (mine < OWN) cv[mine] = MODE == kScaleColumns ? rl * rc : rc;
-          __syncwarp();
-          if (lane == 0) bar_arrive(cfull + 8 * half);
-          ok = bar_wait_all(cfull + 8 * half, it & 1, given_up);
+#pragma unroll
+        for (int j = 0; j < NC; ++j) {
+          rc[j] = rc0[j];
+          rc0[j] = rc1[j];
         }
-        const float by = MODE == kScaleLane ? rl * rc : rl;
+        ask(rl1, rc1);
+        float* const cv = cs + (unit / STEP & 1) * OWN;
+        if (MODE != kScaleLane) {
+#pragma unroll
+          for (int j = 0; j < NC; ++j) cv[32 * j + lane] = MODE == kScaleColumns ? rl * rc[j] : rc[j];
+          __syncwarp();
+        }
+        const float by = MODE == kScaleLane ? rl * rc[0] : rl;
 #pragma unroll
         for (int h = 0; h < H; ++h) {
           const uint32_t full_of = tfull + 8 * (buf * H + h);
-          ok = __all_sync(0xFFFFFFFFu, ok && bar_wait_all(full_of, (it / NB) & 1, given_up));
+          ok = __all_sync(0xFFFFFFFFu, bar_wait_all(full_of, (unit / NB) & 1, given_up));
           if (!ok) break;
           tc_fence_after();
           // the part's columns of a warp: all asked for at once, and the tensor memory given back before they are used
           float r[READ];
-          const uint32_t at = tmem + ((uint32_t)(quad * 32) << 16) + buf * BN + h * (BN / H) + half * READ;
+          const uint32_t at = tmem + ((uint32_t)(quad * 32) << 16) + buf * BN + h * (BN / H) + (ALT ? 0 : half * READ);
           tmem_read(at, r);
           tc_fence_before();
           __syncwarp();
@@ -571,6 +589,7 @@ block_tc_kernel(const __grid_constant__ BlockTcParams p, const __grid_constant__
         if (!ok) break;
       }
       if (!ok) break;
+      it += blocks;
       begin(tile + step);
       if constexpr (!SH::SWAP) {
         unsigned char* const stage = smem + SH::OUT + (warp - 4) * (kOutStage / 8);
@@ -578,7 +597,44 @@ block_tc_kernel(const __grid_constant__ BlockTcParams p, const __grid_constant__
         if (p.out_type == EMU_OUT_F32) write_rows<float>(p, &map_out, acc, stage, row0, rows, c, group, lane);
         else if (p.out_type == EMU_OUT_BF16) write_rows<__nv_bfloat16>(p, &map_out, acc, stage, row0, rows, c, group, lane);
         else write_rows<__half>(p, &map_out, acc, stage, row0, rows, c, group, lane);
-      } else if (p.slices == 1) {
+      } else {
+        if (ALT) {                                       // the second four warps' sums join the first four's
+          float4* const sums = reinterpret_cast<float4*>(smem + SH::OUT) + mine;
+          if (half == 1) {
+            ok = __all_sync(0xFFFFFFFFu, done == 0 || bar_wait_all(parted + 8 * quad, (done - 1) & 1, given_up));
+            if (!ok) break;
+#pragma unroll
+            for (int i = 0; i < OWN / 4; ++i) sums[i * 128] = make_float4(acc[2 * i].x, acc[2 * i].y, acc[2 * i + 1].x, acc[2 * i + 1].y);
+            __syncwarp();
+            if (lane == 0) bar_arrive(joined + 8 * quad);
+            continue;
+          }
+          ok = __all_sync(0xFFFFFFFFu, bar_wait_all(joined + 8 * quad, done & 1, given_up));
+          if (!ok) break;
+#pragma unroll
+          for (int i = 0; i < OWN / 4; ++i) {
+            const float4 v = sums[i * 128];
+            acc[2 * i] = __fadd2_rn(acc[2 * i], make_float2(v.x, v.y));
+            acc[2 * i + 1] = __fadd2_rn(acc[2 * i + 1], make_float2(v.z, v.w));
+          }
+          __syncwarp();
+          if (lane == 0) bar_arrive(parted + 8 * quad);
+          if (p.slices > 1) {
+            // slice s adds up columns s BN / S on: every slice sends its sums of them there, in the place of that CTA's operands,
+            // [S][BN / S / 4][128][4], once all are past their last MMA
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < OWN / 4; ++i) sums[i * 128] = make_float4(acc[2 * i].x, acc[2 * i].y, acc[2 * i + 1].x, acc[2 * i + 1].y);
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            cluster_sync();
+            met = true;
+            const int per = OWN / 4 / p.slices, slice = tile % p.slices;        // groups of four columns
+            if (lane < OWN / 4)
+              send(in_cluster(base + ((slice * per + lane % per) * 128 + quad * 32) * 16, lane / per),
+                   smem_addr(smem + SH::OUT) + (lane * 128 + quad * 32) * 16, 32 * 16, in_cluster(met_all, lane / per));
+            continue;
+          }
+        }
         auto write = [&](auto* out) {
           using T = std::remove_pointer_t<decltype(out)>;
           T* const to = out + group * p.out_group + l * p.ldl;
@@ -589,19 +645,6 @@ block_tc_kernel(const __grid_constant__ BlockTcParams p, const __grid_constant__
         if (p.out_type == EMU_OUT_F32) write(static_cast<float*>(p.out));
         else if (p.out_type == EMU_OUT_BF16) write(static_cast<__nv_bfloat16*>(p.out));
         else write(static_cast<__half*>(p.out));
-      } else {
-        // slice s adds up columns s BN / S on: every slice writes its sums of them there, [S][BN / S][128], in the place of
-        // the operands, once that CTA is past its last MMA
-        cluster_sync();
-        met = true;
-        const int per = BN / p.slices, slice = tile % p.slices;
-        float* const sums = reinterpret_cast<float*>(smem);
-#pragma unroll
-        for (int i = 0; i < OWN; ++i) {
-          const int j = half * OWN + i, owner = j / per;
-          asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(in_cluster(sums + (slice * per + j % per) * 128 + mine, owner)),
-                       "f"(i & 1 ? acc[i / 2].y : acc[i / 2].x) : "memory");
-        }
       }
     }
     if (p.kind == BlockKind::grouped && p.zero_rest) {
@@ -611,22 +654,29 @@ block_tc_kernel(const __grid_constant__ BlockTcParams p, const __grid_constant__
     }
     if (PAIR && lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");   // before the memory is gone
     __syncwarp();
-    if (SH::SWAP && p.slices > 1 && !met) cluster_sync();   // a warp that gave up goes past the first barrier too
+    if (ALT && p.slices > 1 && !met) cluster_sync();   // a warp that gave up goes past the first barrier too
   }
-  if constexpr (SH::SWAP) {
+  if constexpr (ALT) {
     if (p.slices > 1) {                                  // one tile a CTA
       if (warp < 4) cluster_sync();
-      cluster_sync();
       const BlockTile t = tile_at<BN>(p, start, before, blockIdx.x, 0);
-      const int per = BN / p.slices, slice = (int)blockIdx.x % p.slices;
-      const float* const sums = reinterpret_cast<const float*>(smem);
-      if (!*given_up)
+      const int per = OWN / 4 / p.slices, slice = (int)blockIdx.x % p.slices;
+      const float4* const sums = reinterpret_cast<const float4*>(smem);
+      if (bar_wait_all(met_all, 0, given_up))
         for (int i = tid; i < per * 128; i += kTcThreads8) {
-          const int l = t.l0 + i % 128, c = t.c0 + slice * per + i / 128;
-          float v = 0.0f;
-          for (int s = 0; s < p.slices; ++s) v += sums[s * per * 128 + i];
-          if (l < t.l_end && c < t.c_end) put(p.out, p.out_type, l * p.ldl + c * p.ldc, v);
+          float4 v = sums[i];
+          for (int s = 1; s < p.slices; ++s) {
+            const float4 w = sums[s * per * 128 + i];
+            v = make_float4(v.x + w.x, v.y + w.y, v.z + w.z, v.w + w.w);
+          }
+          const int l = t.l0 + i % 128, c = t.c0 + (slice * per + i / 128) * 4;
+          const float each[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (l < t.l_end && c + j < t.c_end) put(p.out, p.out_type, l * p.ldl + (c + j) * p.ldc, each[j]);
         }
+      __syncwarp();
+      cluster_sync();                                    // what was sent has been read
     }
   }
   tc_fence_before();
