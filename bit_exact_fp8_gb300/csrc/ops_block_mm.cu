@@ -178,6 +178,38 @@ void run_few_tokens(const BlockMm& p, const CodesView& va, const CodesView& vb, 
   kernel<<<(unsigned)((p.N + rows - 1) / rows), 256, 0, st>>>(q);
 }
 
+int64_t up(int64_t n, int64_t d) { return (n + d - 1) / d; }
+// Which tiles: pairs of CTAs on 256 x 256, or 128 of the weights' rows by BN tokens, and of how many slices of K.
+// Measured, in us: a call takes `base`, and each of K's blocks `first` in the first round of tiles and `next` in
+// those after it (where more SMs share the memory); slices 0.9 more.  As BN 32, 64 and pairs: 64 x 5760 x 1920 6.9, 8.8
+// and 11.4, 128 x 5760 x 1920 10.8, 9.3 and 11.4, 256 x 4096 x 4096 16.2, 15.2 and 18.4, 512 x 5760 x 1920 22.6, 21.5 and
+// 11.9; 64 x 1920 x 5760 10.9 in one slice, 7.6 in four.
+struct Form { int BN, slices; };
+Form pick_form(const BlockMm& p, bool tokens_mn, int64_t rows, int64_t sms) {
+  if (p.kind == BlockKind::wgrad || tokens_mn) return {256, 1};          // (narrow tiles take the tokens K-major)
+  // by expert the tiles are not known, but the rows an expert has, about: 64 experts of 1920 x 1920 in BN 32, 64 and pairs
+  // with 16 rows 43, 48 and 63 us, with 64 64, 57 and 64, 32 experts with 128 rows 61, 51 and 41
+  if (p.kind == BlockKind::grouped) return {rows <= 32 ? 32 : rows <= 64 ? 64 : 256, 1};
+  struct Cost { int BN; double base, first, next; };
+  const Cost costs[3] = {{32, 4.7, 0.16, 0.25}, {64, 5.3, 0.22, 0.38}, {256, 5.5, 0.41, 0.49}};
+  const int64_t kb = up(p.K, kBlock);
+  Form best = {256, 1};
+  double least = 0.0;
+  for (const Cost& c : costs) {
+    const bool pair = c.BN == 256;
+    const int64_t tiles = up(p.N, pair ? 256 : 128) * up(p.M, c.BN), room = pair ? sms / 2 : sms;
+    for (int slices = 1; slices <= (pair ? 1 : 8); slices *= 2) {
+      if (slices > 1 && (tiles * slices > room || slices > kb)) break;
+      const double t = c.base + (double)up(kb, slices) * (c.first + (double)(up(tiles, room) - 1) * c.next) + (slices > 1 ? 0.9 : 0.0);
+      if (least == 0.0 || t < least) {
+        least = t;
+        best = {c.BN, slices};
+      }
+    }
+  }
+  return best;
+}
+
 int run_block_mm(const BlockMm& p, void* workspace, cudaStream_t st) {
   const bool wgrad = p.kind == BlockKind::wgrad, grouped = p.kind == BlockKind::grouped;
   CodesView va = view_of(p.a, p.M, p.K, 1, wgrad), vb = view_of(p.b, p.N, p.K, grouped ? p.E : 1, wgrad);
@@ -195,17 +227,8 @@ int run_block_mm(const BlockMm& p, void* workspace, cudaStream_t st) {
   }
   const int64_t sms = emu_ops_sm_count(), kb = (p.K + kBlock - 1) / kBlock;
   const int64_t groups = wgrad ? p.E : 1;
-  auto up = [](int64_t n, int64_t d) { return (n + d - 1) / d; };
-  // which form
-  int BN = 256, slices = 1;
-  const int64_t rows = rows_of_group;
-  if (up(p.M, 256) * up(p.N, 256) * groups < sms / 2 || (grouped && rows <= 128)) {
-    BN = va.mn || rows > 64 ? 128 : rows > 32 ? 64 : 32;
-    if (!grouped && !wgrad && BN < 128) {
-      const int64_t tiles = up(p.N, 128) * up(p.M, BN);
-      while (slices < 8 && tiles * slices * 2 <= sms && kb / (slices * 2) >= 2) slices *= 2;
-    }
-  }
+  const Form form = pick_form(p, va.mn, rows_of_group, sms);
+  const int BN = form.BN, slices = form.slices;
   const bool swap = BN < 256;
   BlockTcParams q = {};
   q.kind = p.kind;
@@ -248,7 +271,6 @@ int run_block_mm(const BlockMm& p, void* workspace, cudaStream_t st) {
   const bool tokens_c = grouped && swap, tokens_l = grouped && !swap;
   const int mode = q.c.shift == 7 && !tokens_c ? kScaleLane : q.l.shift == 7 && !tokens_l ? kScaleColumns : kScaleBoth;
   if (BN == 256) return launch_tc<256>(q, mode, tiles, maps, st);
-  if (BN == 128) return launch_tc<128>(q, mode, tiles, maps, st);
   if (BN == 64) return launch_tc<64>(q, mode, tiles, maps, st);
   return launch_tc<32>(q, mode, tiles, maps, st);
 }

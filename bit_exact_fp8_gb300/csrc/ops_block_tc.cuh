@@ -39,17 +39,17 @@ struct BlockTcParams {
 };
 template <int BN> struct BlockTcShape {
   static constexpr bool PAIR = BN == 256;                // two CTAs on a tile of 256 x 256, each with half of either side
-  static constexpr bool SWAP = !PAIR;                    // the output's rows are the columns C
-  static constexpr bool ALT = BN <= 64;                  // either four reading warps take every other block, with all columns
+  static constexpr bool SWAP = !PAIR;                    // the output's rows are the columns C, and either four reading
+                                                         // warps take every other block, with all columns
   static constexpr int L = PAIR ? 256 : 128, C_ROWS = PAIR ? 128 : BN;       // a tile's lanes; rows of C that a CTA loads
-  static constexpr int NS = PAIR ? 4 : BN == 128 ? 6 : BN == 64 ? 7 : 8, STAGE = 128 * 128 + C_ROWS * 128, NB = PAIR ? 2 : 4;
+  static constexpr int NS = PAIR ? 4 : BN == 64 ? 7 : 8, STAGE = 128 * 128 + C_ROWS * 128, NB = PAIR ? 2 : 4;
   static constexpr int H = PAIR ? 2 : 1;                 // parts of a tile's columns, each with MMAs and barriers of its own
-  static constexpr int OWN = ALT ? BN : BN / 2, READ = OWN / H, TMEM = NB * BN;          // a warp's columns, and those of a part
-  static constexpr int OUT = NS * STAGE, CS = OUT + (PAIR ? kOutStage : ALT ? BN * 128 * 4 : 0), BARS = CS + 8 * 2 * OWN * 4;
+  static constexpr int OWN = PAIR ? BN / 2 : BN, READ = OWN / H, TMEM = NB * BN;          // a warp's columns, and those of a part
+  static constexpr int OUT = NS * STAGE, CS = OUT + (PAIR ? kOutStage : BN * 128 * 4), BARS = CS + 8 * 2 * OWN * 4;
   static constexpr int BAR_COUNT = 3 * NS + 2 * NB * H + 10, TABLE = BARS + 8 * BAR_COUNT + 8 + 2 * 12 * 4;
   static constexpr int smem(int E) { return TABLE + 2 * (E + 1) * 4 + 1024; }
 };
-static_assert(BlockTcShape<256>::smem(kMaxExperts) <= kMaxSmem && BlockTcShape<128>::smem(kMaxExperts) <= kMaxSmem &&
+static_assert(BlockTcShape<256>::smem(kMaxExperts) <= kMaxSmem &&
               BlockTcShape<64>::smem(kMaxExperts) <= kMaxSmem && BlockTcShape<32>::smem(kMaxExperts) <= kMaxSmem, "one CTA an SM");
 
 __device__ __forceinline__ void tma_load3(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
@@ -365,7 +365,6 @@ block_tc_kernel(const __grid_constant__ BlockTcParams p, const __grid_constant__
                 const __grid_constant__ CUtensorMap map_c, const __grid_constant__ CUtensorMap map_out) {
   using SH = BlockTcShape<BN>;
   constexpr bool PAIR = SH::PAIR;
-  constexpr bool ALT = SH::ALT;
   constexpr int NS = SH::NS, NB = SH::NB, H = SH::H, OWN = SH::OWN, READ = SH::READ;
   extern __shared__ unsigned char raw[];
   unsigned char* const smem = raw + ((1024u - (smem_addr(raw) & 1023u)) & 1023u);
@@ -388,7 +387,7 @@ block_tc_kernel(const __grid_constant__ BlockTcParams p, const __grid_constant__
     }
     for (int i = 0; i < NB * H; ++i) {
       bar_init(tfull + 8 * i, 1);
-      bar_init(tempty + 8 * i, PAIR ? 16 : ALT ? 4 : 8); // one arrival a reading warp
+      bar_init(tempty + 8 * i, PAIR ? 16 : 4);            // one arrival a reading warp
     }
     for (int i = 0; i < 8; ++i) bar_init(joined + 8 * i, 1);
     bar_init(drained, 2);
@@ -491,7 +490,7 @@ block_tc_kernel(const __grid_constant__ BlockTcParams p, const __grid_constant__
     const int quad = warp & 3, half = (warp - 4) >> 2, mine = quad * 32 + lane;
     const uint32_t released = PAIR ? in_cluster(tempty, 0) : tempty;
     float* const cs = reinterpret_cast<float*>(smem + SH::CS) + (warp - 4) * 2 * OWN;   // this warp's columns' scales, twice
-    constexpr int STEP = ALT ? 2 : 1, NC = MODE == kScaleLane ? 1 : OWN / 32;            // a lane's scales of columns
+    constexpr int STEP = PAIR ? 1 : 2, NC = MODE == kScaleLane ? 1 : OWN / 32;            // a lane's scales of columns
     uint32_t it = 0;
     bool ok = true, met = false;
     // the scales of a block, asked for two of this warp's blocks ahead, by addresses that step from block to block; those of
@@ -514,9 +513,9 @@ block_tc_kernel(const __grid_constant__ BlockTcParams p, const __grid_constant__
       if (tile >= tiles) return;
       t = tile_at<BN>(p, start, before, tile, rank);
       const int gl = p.kind == BlockKind::grouped && SH::SWAP ? t.group : 0, gc = p.kind == BlockKind::grouped && !SH::SWAP ? t.group : 0;
-      const int l_at = MODE == kScaleColumns ? t.l0 : t.l0 + mine, kb = t.kb0 + (ALT ? (int)(it ^ half) & 1 : 0);
+      const int l_at = MODE == kScaleColumns ? t.l0 : t.l0 + mine, kb = t.kb0 + (PAIR ? 0 : (int)(it ^ half) & 1);
       r_in = l_at < t.l_end;
-      c_at = t.c0 + (ALT ? 0 : half * OWN) + (MODE == kScaleLane ? 0 : lane);
+      c_at = t.c0 + (PAIR ? half * OWN : 0) + (MODE == kScaleLane ? 0 : lane);
       pl = p.l.scale + gl * p.l.gs + (l_at >> p.l.shift) * p.l.rs + kb * p.l.ks;
       pc = p.c.scale + gc * p.c.gs + kb * p.c.ks;
       left = t.kb1 - kb;
@@ -526,14 +525,14 @@ block_tc_kernel(const __grid_constant__ BlockTcParams p, const __grid_constant__
     begin(first_tile);
     uint32_t done = 0;                                   // tiles
     for (int tile = first_tile; tile < tiles && ok; tile += step, ++done) {
-      const int l0 = t.l0, l_end = t.l_end, c = t.c0 + (ALT ? 0 : half * OWN), c_end = t.c_end, group = p.kind == BlockKind::wgrad ? t.group : 0;
+      const int l0 = t.l0, l_end = t.l_end, c = t.c0 + (PAIR ? half * OWN : 0), c_end = t.c_end, group = p.kind == BlockKind::wgrad ? t.group : 0;
       const int l = l0 + mine;
       const bool l_in = l < l_end;
       const int blocks = t.kb1 - t.kb0;
       float2 acc[OWN / 2];
 #pragma unroll
       for (int i = 0; i < OWN / 2; ++i) acc[i] = make_float2(0.0f, 0.0f);
-      for (int kb = ALT ? (int)(it ^ half) & 1 : 0; kb < blocks; kb += STEP) {
+      for (int kb = PAIR ? 0 : (int)(it ^ half) & 1; kb < blocks; kb += STEP) {
         const uint32_t unit = it + kb, buf = unit % NB;
         const float rl = rl0;
         float rc[NC];
@@ -559,7 +558,7 @@ block_tc_kernel(const __grid_constant__ BlockTcParams p, const __grid_constant__
           tc_fence_after();
           // the part's columns of a warp: all asked for at once, and the tensor memory given back before they are used
           float r[READ];
-          const uint32_t at = tmem + ((uint32_t)(quad * 32) << 16) + buf * BN + h * (BN / H) + (ALT ? 0 : half * READ);
+          const uint32_t at = tmem + ((uint32_t)(quad * 32) << 16) + buf * BN + h * (BN / H) + (PAIR ? half * READ : 0);
           tmem_read(at, r);
           tc_fence_before();
           __syncwarp();
@@ -598,7 +597,7 @@ block_tc_kernel(const __grid_constant__ BlockTcParams p, const __grid_constant__
         else if (p.out_type == EMU_OUT_BF16) write_rows<__nv_bfloat16>(p, &map_out, acc, stage, row0, rows, c, group, lane);
         else write_rows<__half>(p, &map_out, acc, stage, row0, rows, c, group, lane);
       } else {
-        if (ALT) {                                       // the second four warps' sums join the first four's
+        {                                                // the second four warps' sums join the first four's
           float4* const sums = reinterpret_cast<float4*>(smem + SH::OUT) + mine;
           if (half == 1) {
             ok = __all_sync(0xFFFFFFFFu, done == 0 || bar_wait_all(parted + 8 * quad, (done - 1) & 1, given_up));
@@ -654,9 +653,9 @@ block_tc_kernel(const __grid_constant__ BlockTcParams p, const __grid_constant__
     }
     if (PAIR && lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");   // before the memory is gone
     __syncwarp();
-    if (ALT && p.slices > 1 && !met) cluster_sync();   // a warp that gave up goes past the first barrier too
+    if (SH::SWAP && p.slices > 1 && !met) cluster_sync();   // a warp that gave up goes past the first barrier too
   }
-  if constexpr (ALT) {
+  if constexpr (SH::SWAP) {
     if (p.slices > 1) {                                  // one tile a CTA
       if (warp < 4) cluster_sync();
       const BlockTile t = tile_at<BN>(p, start, before, blockIdx.x, 0);
