@@ -140,7 +140,7 @@ template <int BN> int launch_tc(const BlockTcParams& p, int mode, int64_t tiles,
   cfg.blockDim = dim3(kTcThreads8);
   cfg.dynamicSmemBytes = SH::smem(p.kind == BlockKind::dense ? 0 : p.E);
   cfg.stream = st;
-  const int cluster = SH::PAIR ? 2 : p.slices;
+  const int cluster = (SH::PAIR ? 2 : 1) * p.slices;
   cudaLaunchAttribute at;
   at.id = cudaLaunchAttributeClusterDimension;
   at.val.clusterDim.x = (unsigned)cluster;
@@ -148,8 +148,8 @@ template <int BN> int launch_tc(const BlockTcParams& p, int mode, int64_t tiles,
   cfg.attrs = &at;
   cfg.numAttrs = cluster > 1 ? 1 : 0;
   int64_t room = emu_ops_sm_count();
-  if (SH::PAIR) room = pairs_at_once(reinterpret_cast<const void*>(kernel), cfg);
-  cfg.gridDim = dim3((unsigned)(p.slices > 1 ? tiles * p.slices : (tiles < room ? tiles : room) * cluster));
+  if (SH::PAIR && p.slices == 1) room = pairs_at_once(reinterpret_cast<const void*>(kernel), cfg);
+  cfg.gridDim = dim3((unsigned)(p.slices > 1 || tiles < room ? tiles : room) * cluster);
   if (cudaLaunchKernelEx(&cfg, kernel, p, maps[0], maps[1], maps[2]) != cudaSuccess) return emu_ops_launched("emu_block_scaled_mm");
   return EMU_OK;
 }
@@ -181,9 +181,9 @@ void run_few_tokens(const BlockMm& p, const CodesView& va, const CodesView& vb, 
 int64_t up(int64_t n, int64_t d) { return (n + d - 1) / d; }
 // Which tiles: pairs of CTAs on 256 x 256, or 128 of the weights' rows by BN tokens, and of how many slices of K.
 // Measured, in us: a call takes `base`, and each of K's blocks `first` in the first round of tiles and `next` in
-// those after it (where more SMs share the memory); slices 0.9 more.  As BN 32, 64 and pairs: 64 x 5760 x 1920 6.9, 8.8
+// those after it (where more SMs share the memory); slices 0.9 more, of pairs 3.  As BN 32, 64 and pairs: 64 x 5760 x 1920 6.9, 8.8
 // and 11.4, 128 x 5760 x 1920 10.8, 9.3 and 11.4, 256 x 4096 x 4096 16.2, 15.2 and 18.4, 512 x 5760 x 1920 22.6, 21.5 and
-// 11.9; 64 x 1920 x 5760 10.9 in one slice, 7.6 in four.
+// 11.9; 64 x 1920 x 5760 10.9 in one slice, 7.6 in four, 777 x 1920 x 5760 in pairs 23.5 and in two slices 18.4.
 struct Form { int BN, slices; };
 Form pick_form(const BlockMm& p, bool tokens_mn, int64_t rows, int64_t sms) {
   if (p.kind == BlockKind::wgrad || tokens_mn) return {256, 1};          // (narrow tiles take the tokens K-major)
@@ -198,9 +198,9 @@ Form pick_form(const BlockMm& p, bool tokens_mn, int64_t rows, int64_t sms) {
   for (const Cost& c : costs) {
     const bool pair = c.BN == 256;
     const int64_t tiles = up(p.N, pair ? 256 : 128) * up(p.M, c.BN), room = pair ? sms / 2 : sms;
-    for (int slices = 1; slices <= (pair ? 1 : 8); slices *= 2) {
+    for (int slices = 1; slices <= (pair ? 2 : 8); slices *= 2) {
       if (slices > 1 && (tiles * slices > room || slices > kb)) break;
-      const double t = c.base + (double)up(kb, slices) * (c.first + (double)(up(tiles, room) - 1) * c.next) + (slices > 1 ? 0.9 : 0.0);
+      const double t = c.base + (double)up(kb, slices) * (c.first + (double)(up(tiles, room) - 1) * c.next) + (slices == 1 ? 0.0 : pair ? 3.0 : 0.9);
       if (least == 0.0 || t < least) {
         least = t;
         best = {c.BN, slices};

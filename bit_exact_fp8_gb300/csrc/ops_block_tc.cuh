@@ -75,10 +75,10 @@ template <bool PAIR> __device__ __forceinline__ void mma8(uint32_t d, uint64_t a
         : "memory");
 }
 // the arrival of all MMAs issued before: of a pair, at the barriers of both CTAs
-template <bool PAIR> __device__ __forceinline__ void commit8(uint32_t bar) {
+template <bool PAIR> __device__ __forceinline__ void commit8(uint32_t bar, uint32_t both) {
   if constexpr (PAIR)
     asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
-                 "h"((uint16_t)3) : "memory");
+                 "h"((uint16_t)both) : "memory");
   else
     tc_commit(bar);
 }
@@ -107,6 +107,7 @@ __device__ __forceinline__ void send(uint32_t dst, uint32_t src, uint32_t bytes,
                "r"(bytes), "r"(bar) : "memory");
 }
 __device__ __forceinline__ void fence_cluster() { asm volatile("fence.acq_rel.cluster;" ::: "memory"); }
+// an address of this CTA's shared memory in that of the cluster's CTA `rank`
 __device__ __forceinline__ uint32_t in_cluster(uint32_t at, int rank) {
   uint32_t a;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(at), "r"(rank));
@@ -357,7 +358,7 @@ __device__ __forceinline__ void write_rows(const BlockTcParams& p, const CUtenso
 // tells the pair's first CTA that its blocks are there), warps 4 to 11 scale and add: each holds 32 lanes x BN / 2
 // columns of sums in registers.  BN = 256: pairs of CTAs, whose MMAs the first one issues for both (an SM takes
 // in 64 bytes a cycle: a block of 128 x 256 outputs would need 48 KB every 512 cycles, of the pair each 32).
-// Several slices of K (dense, BN <= 64): the CTAs of a cluster, which share out the columns at the end.  All
+// Several slices of K (dense): the CTAs of a cluster, of which each adds up some of the columns at the end.  All
 // waits are bounded; a role that gives up sets the status and takes the others along.
 template <int BN, int MODE>
 __global__ void __launch_bounds__(kTcThreads8, 1)
@@ -378,6 +379,8 @@ block_tc_kernel(const __grid_constant__ BlockTcParams p, const __grid_constant__
   int* const before = start + p.E + 1;
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0);   // the same for all, and known to be
   const int rank = PAIR ? blockIdx.x & 1 : 0, first_tile = PAIR ? blockIdx.x >> 1 : blockIdx.x, step = PAIR ? gridDim.x >> 1 : gridDim.x;
+  const int lead = PAIR && p.slices > 1 ? blockIdx.x & 2 : 0;             // the pair's first CTA in the cluster
+  const uint32_t both = 3u << lead;
 
   if (tid == 0) {
     for (int i = 0; i < NS; ++i) {
@@ -392,7 +395,7 @@ block_tc_kernel(const __grid_constant__ BlockTcParams p, const __grid_constant__
     for (int i = 0; i < 8; ++i) bar_init(joined + 8 * i, 1);
     bar_init(drained, 2);
     bar_init(met_all, 1);
-    if (p.slices > 1) bar_expect(met_all, BN * 128 * 4);  // what the slices send of this one's columns
+    if (p.slices > 1) bar_expect(met_all, OWN * 128 * 4); // what the slices send of this one's columns
     *given_up = 0;
     bar_init_fence();
   }
@@ -449,17 +452,17 @@ block_tc_kernel(const __grid_constant__ BlockTcParams p, const __grid_constant__
 #pragma unroll
             for (int k = 0; k < 4; ++k)
               mma8<PAIR>(tmem + buf * BN + h * (BN / H), dl + k * step_l, dc + k * step_c, p.idesc, k > 0);
-            commit8<PAIR>(tfull + 8 * (buf * H + h));
-            commit8<PAIR>(empty + 8 * s);
+            commit8<PAIR>(tfull + 8 * (buf * H + h), both);
+            commit8<PAIR>(empty + 8 * s, both);
           }
         }
       }
-      if (one_of_warp()) commit8<PAIR>(drained);         // the MMAs are done before the tensor memory goes back
+      if (one_of_warp()) commit8<PAIR>(drained, both);         // the MMAs are done before the tensor memory goes back
       (void)bar_wait(drained, 0);
     } else if (warp == 3 && (PAIR || p.kind == BlockKind::wgrad)) {
       uint32_t it = 0;
       bool ok = true;
-      const uint32_t ready = PAIR ? in_cluster(fixed, 0) : fixed;
+      const uint32_t ready = PAIR ? in_cluster(fixed, lead) : fixed;
       for (int tile = first_tile; tile < tiles && ok; tile += step) {
         const BlockTile t = tile_at<BN>(p, start, before, tile, rank);
         for (int kb = t.kb0; kb < t.kb1; ++kb, ++it) {
@@ -488,7 +491,7 @@ block_tc_kernel(const __grid_constant__ BlockTcParams p, const __grid_constant__
   } else {
     if constexpr (BN == 256) asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
     const int quad = warp & 3, half = (warp - 4) >> 2, mine = quad * 32 + lane;
-    const uint32_t released = PAIR ? in_cluster(tempty, 0) : tempty;
+    const uint32_t released = PAIR ? in_cluster(tempty, lead) : tempty;
     float* const cs = reinterpret_cast<float*>(smem + SH::CS) + (warp - 4) * 2 * OWN;   // this warp's columns' scales, twice
     constexpr int STEP = PAIR ? 1 : 2, NC = MODE == kScaleLane ? 1 : OWN / 32;            // a lane's scales of columns
     uint32_t it = 0;
@@ -592,6 +595,30 @@ block_tc_kernel(const __grid_constant__ BlockTcParams p, const __grid_constant__
       begin(tile + step);
       if constexpr (!SH::SWAP) {
         unsigned char* const stage = smem + SH::OUT + (warp - 4) * (kOutStage / 8);
+        if (p.slices > 1) {
+          // two slices: each adds up one half of the columns.  The other half's sums go to its place, behind where they are
+          // written here, once all are past their last MMA.
+          cluster_sync();
+          met = true;
+          float4* const sums = reinterpret_cast<float4*>(smem) + mine;   // [32][128][4]
+          if (half != (lead >> 1)) {
+#pragma unroll
+            for (int i = 0; i < OWN / 4; ++i) sums[i * 128] = make_float4(acc[2 * i].x, acc[2 * i].y, acc[2 * i + 1].x, acc[2 * i + 1].y);
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            const uint32_t at = (lane * 128 + quad * 32) * 16, other = (lead ^ 2) + rank;
+            send(in_cluster(base + OWN * 128 * 4 + at, other), base + at, 32 * 16, in_cluster(met_all, other));
+            continue;
+          }
+          ok = __all_sync(0xFFFFFFFFu, bar_wait_all(met_all, 0, given_up));
+          if (!ok) break;
+#pragma unroll
+          for (int i = 0; i < OWN / 4; ++i) {
+            const float4 v = sums[(OWN / 4 + i) * 128];
+            acc[2 * i] = __fadd2_rn(acc[2 * i], make_float2(v.x, v.y));
+            acc[2 * i + 1] = __fadd2_rn(acc[2 * i + 1], make_float2(v.z, v.w));
+          }
+        }
         const int row0 = l0 + quad * 32, rows = l_end - row0 < 32 ? l_end - row0 : 32;
         if (p.out_type == EMU_OUT_F32) write_rows<float>(p, &map_out, acc, stage, row0, rows, c, group, lane);
         else if (p.out_type == EMU_OUT_BF16) write_rows<__nv_bfloat16>(p, &map_out, acc, stage, row0, rows, c, group, lane);
@@ -653,11 +680,11 @@ block_tc_kernel(const __grid_constant__ BlockTcParams p, const __grid_constant__
     }
     if (PAIR && lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");   // before the memory is gone
     __syncwarp();
-    if (SH::SWAP && p.slices > 1 && !met) cluster_sync();   // a warp that gave up goes past the first barrier too
+    if (p.slices > 1 && !met) cluster_sync();   // a warp that gave up goes past the first barrier too
   }
+  if (p.slices > 1 && warp < 4) cluster_sync();
   if constexpr (SH::SWAP) {
     if (p.slices > 1) {                                  // one tile a CTA
-      if (warp < 4) cluster_sync();
       const BlockTile t = tile_at<BN>(p, start, before, blockIdx.x, 0);
       const int per = OWN / 4 / p.slices, slice = (int)blockIdx.x % p.slices;
       const float4* const sums = reinterpret_cast<const float4*>(smem);
