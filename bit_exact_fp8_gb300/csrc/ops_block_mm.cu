@@ -184,29 +184,34 @@ int64_t up(int64_t n, int64_t d) { return (n + d - 1) / d; }
 // those after it (where more SMs share the memory); slices 0.9 more, of pairs 3.  As BN 32, 64 and pairs: 64 x 5760 x 1920 6.9, 8.8
 // and 11.4, 128 x 5760 x 1920 10.8, 9.3 and 11.4, 256 x 4096 x 4096 16.2, 15.2 and 18.4, 512 x 5760 x 1920 22.6, 21.5 and
 // 11.9; 64 x 1920 x 5760 10.9 in one slice, 7.6 in four, 777 x 1920 x 5760 in pairs 23.5 and in two slices 18.4.
-struct Form { int BN, slices; };
+struct Form { int BN, slices; bool tail; };
 Form pick_form(const BlockMm& p, bool tokens_mn, int64_t rows, int64_t sms) {
-  if (p.kind == BlockKind::wgrad || tokens_mn) return {256, 1};          // (narrow tiles take the tokens K-major)
+  if (p.kind == BlockKind::wgrad) return {256, 1, false};
   // by expert the tiles are not known, but the rows an expert has, about: 64 experts of 1920 x 1920 in BN 32, 64 and pairs
   // with 16 rows 43, 48 and 63 us, with 64 64, 57 and 64, 32 experts with 128 rows 61, 51 and 41
-  if (p.kind == BlockKind::grouped) return {rows <= 32 ? 32 : rows <= 64 ? 64 : 256, 1};
+  if (p.kind == BlockKind::grouped) return {rows <= 32 ? 32 : rows <= 64 ? 64 : 256, 1, false};
   struct Cost { int BN; double base, first, next; };
   const Cost costs[3] = {{32, 4.7, 0.16, 0.25}, {64, 5.3, 0.22, 0.38}, {256, 5.5, 0.41, 0.49}};
   const int64_t kb = up(p.K, kBlock);
-  Form best = {256, 1};
+  Form best = {256, 1, false};
   double least = 0.0;
   for (const Cost& c : costs) {
     const bool pair = c.BN == 256;
+    if (tokens_mn && !pair) continue;                    // narrow tiles take the tokens K-major
     const int64_t tiles = up(p.N, pair ? 256 : 128) * up(p.M, c.BN), room = pair ? sms / 2 : sms;
     for (int slices = 1; slices <= (pair ? 2 : 8); slices *= 2) {
       if (slices > 1 && (tiles * slices > room || slices > kb)) break;
       const double t = c.base + (double)up(kb, slices) * (c.first + (double)(up(tiles, room) - 1) * c.next) + (slices == 1 ? 0.0 : pair ? 3.0 : 0.9);
       if (least == 0.0 || t < least) {
         least = t;
-        best = {c.BN, slices};
+        best = {c.BN, slices, false};
       }
     }
   }
+  // A last round of tiles that leaves half of the pairs without any goes in two slices, in a launch of its own, where half of
+  // K's blocks take longer than a launch and the slices' exchange: 5760 x 1920 x 8192 (184 tiles for 76 pairs) 150 -> 130 us.
+  const int64_t tiles = up(p.N, 256) * up(p.M, 256), rest = tiles % (sms / 2);
+  best.tail = best.BN == 256 && best.slices == 1 && tiles > sms / 2 && rest > 0 && rest <= sms / 4 - 2 && kb >= 32;
   return best;
 }
 
@@ -270,7 +275,17 @@ int run_block_mm(const BlockMm& p, void* workspace, cudaStream_t st) {
   // a lane's scale alone, where the columns of a warp share theirs; else the lanes' in the columns' if they all share it
   const bool tokens_c = grouped && swap, tokens_l = grouped && !swap;
   const int mode = q.c.shift == 7 && !tokens_c ? kScaleLane : q.l.shift == 7 && !tokens_l ? kScaleColumns : kScaleBoth;
-  if (BN == 256) return launch_tc<256>(q, mode, tiles, maps, st);
+  q.from = 0;
+  q.to = (int)tiles;
+  if (form.tail) {
+    q.to = (int)(tiles - tiles % (sms / 2));
+    const int rc = launch_tc<256>(q, mode, q.to, maps, st);
+    if (rc != EMU_OK) return rc;
+    q.from = q.to;
+    q.to = (int)tiles;
+    q.slices = 2;
+  }
+  if (BN == 256) return launch_tc<256>(q, mode, q.to - q.from, maps, st);
   if (BN == 64) return launch_tc<64>(q, mode, tiles, maps, st);
   return launch_tc<32>(q, mode, tiles, maps, st);
 }

@@ -30,6 +30,7 @@ struct BlockSide {
 struct BlockTcParams {
   BlockSide l, c;
   int tiles_l, tiles_c, k_blocks, slices;
+  int from, to;                                          // dense: the tiles of this launch
   BlockKind kind;
   const int32_t* offsets; int E, T;                      // groups of tokens (grouped: of rows, wgrad: of K)
   int zero_rest;
@@ -229,7 +230,7 @@ __device__ __forceinline__ void tile_order(int tile, int tiles_l, int tiles_c, i
   c = in / rows;
 }
 template <int BN> __device__ __forceinline__ int tile_count(const BlockTcParams& p, const int* before) {
-  if (p.kind == BlockKind::dense) return p.tiles_l * p.tiles_c * p.slices;
+  if (p.kind == BlockKind::dense) return (p.to - p.from) * p.slices;
   if (p.kind == BlockKind::wgrad) return p.tiles_l * p.tiles_c * p.E;
   return before[p.E] * (BlockTcShape<BN>::SWAP ? p.tiles_l : p.tiles_c);
 }
@@ -276,11 +277,14 @@ template <int BN> __device__ __forceinline__ BlockTile tile_at(const BlockTcPara
     t.hi = start[t.group + 1];
     t.kb0 = t.lo / kBlock;
     t.kb1 = t.hi > t.lo ? (t.hi + kBlock - 1) / kBlock : t.kb0;
-  } else if (p.slices > 1) {
-    const int slice = tile % p.slices;
-    tile /= p.slices;
-    t.kb0 = p.k_blocks * slice / p.slices;
-    t.kb1 = p.k_blocks * (slice + 1) / p.slices;
+  } else {
+    if (p.slices > 1) {
+      const int slice = tile % p.slices;
+      tile /= p.slices;
+      t.kb0 = (int)((int64_t)p.k_blocks * slice / p.slices);
+      t.kb1 = (int)((int64_t)p.k_blocks * (slice + 1) / p.slices);
+    }
+    tile += p.from;
   }
   tile_order(tile, p.tiles_l, p.tiles_c, l, c);
   t.l0 = l * BlockTcShape<BN>::L + rank * 128;

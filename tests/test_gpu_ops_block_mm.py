@@ -393,3 +393,10 @@ def test_grouped_refusals(fw):
             call()
     with pytest.raises(fw.UnsupportedFeatureError):
         f(a, b, off, sa, sb, out_dtype=torch.float64)
+
+
+@pytest.mark.parametrize("M,N,K,by_k", [(2600, 2100, 4200, (True, True)), (2500, 2048, 4096, (False, False)), (700, 1100, 3000, (True, False))])
+def test_tiles_in_rounds_and_slices(fw, M, N, K, by_k):
+    """More tiles than the device holds, the last few in slices of K; and few tiles in slices."""
+    for block in ((ROWS, SQUARES), (SQUARES, SQUARES), (ROWS, ROWS)):
+        dense(fw, M, N, K, by_k=by_k, block=block, dt=torch.bfloat16)
