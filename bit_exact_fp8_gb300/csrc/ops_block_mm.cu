@@ -224,11 +224,11 @@ int run_block_mm(const BlockMm& p, void* workspace, cudaStream_t st) {
     return emu_ops_launched("emu_block_scaled_mm");
   }
   const bool any = p.K > 0 && !(grouped && p.E == 0);    // anything to multiply
+  LayOut lay_a = {}, lay_b = {};
   if (any) {
     unsigned char* ws = static_cast<unsigned char*>(workspace);
-    const LayOut la = lay_out_of(va, ws), lb = lay_out_of(vb, ws);
-    const int64_t work = la.vectors * la.chunks + lb.vectors * lb.chunks, ctas = (work + 255) / 256;
-    if (work > 0) lay_out_kernel<<<(unsigned)(ctas < 16384 ? ctas : 16384), 256, 0, st>>>(la, lb);
+    lay_a = lay_out_of(va, ws);
+    lay_b = lay_out_of(vb, ws);
   }
   const int64_t sms = emu_ops_sm_count(), kb = (p.K + kBlock - 1) / kBlock;
   const int64_t groups = wgrad ? p.E : 1;
@@ -275,6 +275,8 @@ int run_block_mm(const BlockMm& p, void* workspace, cudaStream_t st) {
   // a lane's scale alone, where the columns of a warp share theirs; else the lanes' in the columns' if they all share it
   const bool tokens_c = grouped && swap, tokens_l = grouped && !swap;
   const int mode = q.c.shift == 7 && !tokens_c ? kScaleLane : q.l.shift == 7 && !tokens_l ? kScaleColumns : kScaleBoth;
+  const int64_t work = lay_a.vectors * lay_a.chunks + lay_b.vectors * lay_b.chunks, ctas = up(work, 256);
+  if (work > 0) lay_out_kernel<<<(unsigned)(ctas < 16384 ? ctas : 16384), 256, 0, st>>>(lay_a, lay_b);
   q.from = 0;
   q.to = (int)tiles;
   if (form.tail) {
