@@ -57,6 +57,7 @@ struct LayOut {
   uint8_t* to; int64_t chunks;                           // 16 codes each, of a vector
 };
 __global__ void __launch_bounds__(256) lay_out_kernel(const LayOut a, const LayOut b) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the product waits for this kernel's end
   const int64_t na = a.vectors * a.chunks, total = na + b.vectors * b.chunks;
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
     const LayOut& s = i < na ? a : b;
@@ -130,7 +131,8 @@ int pairs_at_once(const void* kernel, cudaLaunchConfig_t cfg) {
   return v;
 }
 
-template <int BN> int launch_tc(const BlockTcParams& p, int mode, int64_t tiles, const CUtensorMap (&maps)[3], cudaStream_t st) {
+// `early`: launched while its operands are still laid out (it waits for them itself)
+template <int BN> int launch_tc(const BlockTcParams& p, int mode, int64_t tiles, const CUtensorMap (&maps)[3], bool early, cudaStream_t st) {
   using SH = BlockTcShape<BN>;
   auto kernel = mode == kScaleLane ? block_tc_kernel<BN, kScaleLane> : mode == kScaleColumns ? block_tc_kernel<BN, kScaleColumns>
                                                                                               : block_tc_kernel<BN, kScaleBoth>;
@@ -141,15 +143,18 @@ template <int BN> int launch_tc(const BlockTcParams& p, int mode, int64_t tiles,
   cfg.dynamicSmemBytes = SH::smem(p.kind == BlockKind::dense ? 0 : p.E);
   cfg.stream = st;
   const int cluster = (SH::PAIR ? 2 : 1) * p.slices;
-  cudaLaunchAttribute at;
-  at.id = cudaLaunchAttributeClusterDimension;
-  at.val.clusterDim.x = (unsigned)cluster;
-  at.val.clusterDim.y = at.val.clusterDim.z = 1;
-  cfg.attrs = &at;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = (unsigned)cluster;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = cluster > 1 ? at : at + 1;
   cfg.numAttrs = cluster > 1 ? 1 : 0;
   int64_t room = emu_ops_sm_count();
   if (SH::PAIR && p.slices == 1) room = pairs_at_once(reinterpret_cast<const void*>(kernel), cfg);
   cfg.gridDim = dim3((unsigned)(p.slices > 1 || tiles < room ? tiles : room) * cluster);
+  if (early) ++cfg.numAttrs;
   if (cudaLaunchKernelEx(&cfg, kernel, p, maps[0], maps[1], maps[2]) != cudaSuccess) return emu_ops_launched("emu_block_scaled_mm");
   return EMU_OK;
 }
@@ -281,15 +286,15 @@ int run_block_mm(const BlockMm& p, void* workspace, cudaStream_t st) {
   q.to = (int)tiles;
   if (form.tail) {
     q.to = (int)(tiles - tiles % (sms / 2));
-    const int rc = launch_tc<256>(q, mode, q.to, maps, st);
+    const int rc = launch_tc<256>(q, mode, q.to, maps, work > 0, st);
     if (rc != EMU_OK) return rc;
     q.from = q.to;
     q.to = (int)tiles;
     q.slices = 2;
   }
-  if (BN == 256) return launch_tc<256>(q, mode, q.to - q.from, maps, st);
-  if (BN == 64) return launch_tc<64>(q, mode, tiles, maps, st);
-  return launch_tc<32>(q, mode, tiles, maps, st);
+  if (BN == 256) return launch_tc<256>(q, mode, q.to - q.from, maps, work > 0 && q.from == 0, st);
+  if (BN == 64) return launch_tc<64>(q, mode, tiles, maps, work > 0, st);
+  return launch_tc<32>(q, mode, tiles, maps, work > 0, st);
 }
 
 // ------------------------------------------------------------------------------- checks

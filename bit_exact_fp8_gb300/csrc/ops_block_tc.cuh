@@ -114,48 +114,27 @@ __device__ __forceinline__ uint32_t in_cluster(uint32_t at, int rank) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(at), "r"(rank));
   return a;
 }
-// columns of this warp's 32 lanes, read and waited for
-__device__ __forceinline__ void tmem_read(uint32_t addr, float (&r)[16]) {
+// 32 columns of this warp's 32 lanes, asked for, and waited for (whatever was asked for before)
+__device__ __forceinline__ void tmem_ask(uint32_t addr, float (&r)[32]) {
   asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {"
-        "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n"
-        "tcgen05.wait::ld.sync.aligned;"
-        : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]), "=f"(r[8]),
-          "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15])
-        : "r"(addr)
-        : "memory");
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]), "=f"(r[8]),
+        "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15]), "=f"(r[16]),
+        "=f"(r[17]), "=f"(r[18]), "=f"(r[19]), "=f"(r[20]), "=f"(r[21]), "=f"(r[22]), "=f"(r[23]), "=f"(r[24]),
+        "=f"(r[25]), "=f"(r[26]), "=f"(r[27]), "=f"(r[28]), "=f"(r[29]), "=f"(r[30]), "=f"(r[31])
+      : "r"(addr)
+      : "memory");
 }
-__device__ __forceinline__ void tmem_read(uint32_t addr, float (&r)[32]) {
-  asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {"
-        "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, "
-        "%21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n"
-        "tcgen05.wait::ld.sync.aligned;"
-        : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]), "=f"(r[8]),
-          "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15]), "=f"(r[16]),
-          "=f"(r[17]), "=f"(r[18]), "=f"(r[19]), "=f"(r[20]), "=f"(r[21]), "=f"(r[22]), "=f"(r[23]), "=f"(r[24]),
-          "=f"(r[25]), "=f"(r[26]), "=f"(r[27]), "=f"(r[28]), "=f"(r[29]), "=f"(r[30]), "=f"(r[31])
-        : "r"(addr)
-        : "memory");
+__device__ __forceinline__ void tmem_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+// acc += (x, y) * by, and (x, y) * by, of values asked for from tensor memory: volatile, so that they stay behind the wait
+__device__ __forceinline__ void add_scaled(f2& acc, float x, float y, f2 by) {
+  asm volatile("{\n .reg .b64 v;\n mov.b64 v, {%1, %2};\n fma.rn.f32x2 %0, v, %3, %0;\n}" : "+l"(acc) : "f"(x), "f"(y), "l"(by));
 }
-__device__ __forceinline__ void tmem_read(uint32_t addr, float (&r)[64]) {
-  asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x64.b32 {"
-        "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, "
-        "%21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32, %33, %34, %35, %36, %37, %38, %39, "
-        "%40, %41, %42, %43, %44, %45, %46, %47, %48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, "
-        "%59, %60, %61, %62, %63}, [%64];\n"
-        "tcgen05.wait::ld.sync.aligned;"
-        : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]), "=f"(r[8]),
-          "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15]), "=f"(r[16]),
-          "=f"(r[17]), "=f"(r[18]), "=f"(r[19]), "=f"(r[20]), "=f"(r[21]), "=f"(r[22]), "=f"(r[23]), "=f"(r[24]),
-          "=f"(r[25]), "=f"(r[26]), "=f"(r[27]), "=f"(r[28]), "=f"(r[29]), "=f"(r[30]), "=f"(r[31]), "=f"(r[32]),
-          "=f"(r[33]), "=f"(r[34]), "=f"(r[35]), "=f"(r[36]), "=f"(r[37]), "=f"(r[38]), "=f"(r[39]), "=f"(r[40]),
-          "=f"(r[41]), "=f"(r[42]), "=f"(r[43]), "=f"(r[44]), "=f"(r[45]), "=f"(r[46]), "=f"(r[47]), "=f"(r[48]),
-          "=f"(r[49]), "=f"(r[50]), "=f"(r[51]), "=f"(r[52]), "=f"(r[53]), "=f"(r[54]), "=f"(r[55]), "=f"(r[56]),
-          "=f"(r[57]), "=f"(r[58]), "=f"(r[59]), "=f"(r[60]), "=f"(r[61]), "=f"(r[62]), "=f"(r[63])
-        : "r"(addr)
-        : "memory");
+__device__ __forceinline__ f2 scaled(float x, float y, f2 by) {
+  f2 r;
+  asm volatile("{\n .reg .b64 v;\n mov.b64 v, {%1, %2};\n mul.rn.f32x2 %0, v, %3;\n}" : "=l"(r) : "f"(x), "f"(y), "l"(by));
+  return r;
 }
 
 // One lane of the warp, in code that the whole warp runs: its values are the warp's then, and the addresses and descriptors
@@ -216,6 +195,13 @@ __device__ __forceinline__ void group_table(const int32_t* offsets, int E, int T
     base += n[j];
   }
   __syncthreads();
+}
+
+__device__ __forceinline__ float4 four_of(f2 a, f2 b) {
+  float4 v;
+  halves(a, v.x, v.y);
+  halves(b, v.z, v.w);
+  return v;
 }
 
 struct BlockTile {
@@ -297,7 +283,7 @@ template <int BN> __device__ __forceinline__ BlockTile tile_at(const BlockTcPara
 // blocks do not wait for, or, of a group's last rows and where rows are not 16-byte aligned, by the warp.  (A bulk
 // copy for each row instead takes the TMA unit as long as the loads of a tile.)
 template <class T>
-__device__ __forceinline__ void write_rows(const BlockTcParams& p, const CUtensorMap* map, const float2 (&acc)[64], unsigned char* stage,
+__device__ __forceinline__ void write_rows(const BlockTcParams& p, const CUtensorMap* map, const f2 (&acc)[64], unsigned char* stage,
                                            int row0, int rows, int n0, int group, int lane) {
   constexpr int COLS = 128 / sizeof(T), VEC = 16 / sizeof(T);
   const int cols = p.c.rows - n0;                        // may be none
@@ -312,10 +298,7 @@ __device__ __forceinline__ void write_rows(const BlockTcParams& p, const CUtenso
     for (int i = 0; i < 2 * COLS; i += VEC) {
       float v[VEC];
 #pragma unroll
-      for (int j = 0; j < VEC; j += 2) {
-        v[j] = acc[(c0 + i + j) / 2].x;
-        v[j + 1] = acc[(c0 + i + j) / 2].y;
-      }
+      for (int j = 0; j < VEC; j += 2) halves(acc[(c0 + i + j) / 2], v[j], v[j + 1]);
       store_f<T, VEC>(reinterpret_cast<T*>(stage + i / COLS * 4096 + lane * 128 + (((i % COLS / VEC) ^ (lane & 7)) * 16)), v);
     }
     if (whole) {
@@ -415,6 +398,7 @@ block_tc_kernel(const __grid_constant__ BlockTcParams p, const __grid_constant__
   if (warp < 4) {
     if constexpr (BN == 256) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
     if (warp == 0) {
+      asm volatile("griddepcontrol.wait;" ::: "memory");       // the operands are laid out
       uint32_t it = 0;
       bool ok = true;
       for (int tile = first_tile; tile < tiles && ok; tile += step) {
@@ -536,11 +520,29 @@ block_tc_kernel(const __grid_constant__ BlockTcParams p, const __grid_constant__
       const int l = l0 + mine;
       const bool l_in = l < l_end;
       const int blocks = t.kb1 - t.kb0;
-      float2 acc[OWN / 2];
+      f2 acc[OWN / 2];
 #pragma unroll
-      for (int i = 0; i < OWN / 2; ++i) acc[i] = make_float2(0.0f, 0.0f);
-      for (int kb = PAIR ? 0 : (int)(it ^ half) & 1; kb < blocks; kb += STEP) {
-        const uint32_t unit = it + kb, buf = unit % NB;
+      for (int i = 0; i < OWN / 2; ++i) acc[i] = 0ull;
+      // Pieces of 32 columns.  Pairs: the next one is asked for before (of another part of the columns or block: while) one's
+      // values are used, so that neither the barriers' latency nor the tensor memory's adds to the multiplications'
+      // time (5760 x 1920 x 8192 94 -> 88 us).  Narrow tiles: a block's all at once.
+      constexpr int PIECES = OWN / 32, OF_PART = READ / 32;
+      float r[2][32];
+      auto full_of = [&](uint32_t unit, int h) { return tfull + 8 * (unit % NB * H + h); };
+      auto ask_piece = [&](uint32_t unit, int k) {
+        const int h = k / OF_PART;
+        tmem_ask(tmem + ((uint32_t)(quad * 32) << 16) + unit % NB * BN + h * (BN / H) + (PAIR ? half * READ : 0) + k % OF_PART * 32,
+                 r[k & 1]);
+      };
+      const int first = PAIR ? 0 : (int)(it ^ half) & 1;
+      if (PAIR && first < blocks) {
+        ok = __all_sync(0xFFFFFFFFu, bar_wait_all(full_of(it + first, 0), ((it + first) / NB) & 1, given_up));
+        if (!ok) break;
+        tc_fence_after();
+        ask_piece(it + first, 0);
+      }
+      for (int kb = first; kb < blocks; kb += STEP) {
+        const uint32_t unit = it + kb;
         const float rl = rl0;
         float rc[NC];
         rl0 = rl1;
@@ -556,41 +558,69 @@ block_tc_kernel(const __grid_constant__ BlockTcParams p, const __grid_constant__
           for (int j = 0; j < NC; ++j) cv[32 * j + lane] = MODE == kScaleColumns ? rl * rc[j] : rc[j];
           __syncwarp();
         }
-        const float by = MODE == kScaleLane ? rl * rc[0] : rl;
+        const float one = MODE == kScaleLane ? rl * rc[0] : rl;
+        const f2 by = pair(one, one);
+        auto use = [&](int k, int from, int to) {
+          const float* const v = r[k & 1];
 #pragma unroll
-        for (int h = 0; h < H; ++h) {
-          const uint32_t full_of = tfull + 8 * (buf * H + h);
-          ok = __all_sync(0xFFFFFFFFu, bar_wait_all(full_of, (unit / NB) & 1, given_up));
-          if (!ok) break;
-          tc_fence_after();
-          // the part's columns of a warp: all asked for at once, and the tensor memory given back before they are used
-          float r[READ];
-          const uint32_t at = tmem + ((uint32_t)(quad * 32) << 16) + buf * BN + h * (BN / H) + (PAIR ? half * READ : 0);
-          tmem_read(at, r);
+          for (int i = from; i < to; i += 4) {
+            f2& a0 = acc[(k * 32 + i) / 2];
+            f2& a1 = acc[(k * 32 + i) / 2 + 1];
+            if (MODE == kScaleLane) {
+              add_scaled(a0, v[i], v[i + 1], by);
+              add_scaled(a1, v[i + 2], v[i + 3], by);
+            } else {
+              const float4 s = *reinterpret_cast<const float4*>(cv + k * 32 + i);
+              if (MODE == kScaleColumns) {
+                add_scaled(a0, v[i], v[i + 1], pair(s.x, s.y));
+                add_scaled(a1, v[i + 2], v[i + 3], pair(s.z, s.w));
+              } else {
+                a0 = fma2(scaled(v[i], v[i + 1], by), pair(s.x, s.y), a0);
+                a1 = fma2(scaled(v[i + 2], v[i + 3], by), pair(s.z, s.w), a1);
+              }
+            }
+          }
+        };
+        auto release = [&](int h) {                      // the part has been read
           tc_fence_before();
           __syncwarp();
           if (lane == 0) {
-            if (PAIR) bar_arrive_cluster(released + 8 * (buf * H + h));
-            else bar_arrive(released + 8 * (buf * H + h));
+            if (PAIR) bar_arrive_cluster(released + 8 * (unit % NB * H + h));
+            else bar_arrive(released + 8 * (unit % NB * H + h));
           }
+        };
+        if constexpr (PAIR) {
 #pragma unroll
-          for (int i = 0; i < READ; i += 4) {
-            float2& a0 = acc[(h * READ + i) / 2];
-            float2& a1 = acc[(h * READ + i) / 2 + 1];
-            float2 x0 = make_float2(r[i], r[i + 1]), x1 = make_float2(r[i + 2], r[i + 3]);
-            float2 s0 = make_float2(by, by), s1 = s0;
-            if (MODE != kScaleLane) {
-              const float4 s = *reinterpret_cast<const float4*>(cv + h * READ + i);
-              if (MODE == kScaleBoth) {
-                x0 = __fmul2_rn(x0, s0);
-                x1 = __fmul2_rn(x1, s0);
-              }
-              s0 = make_float2(s.x, s.y);
-              s1 = make_float2(s.z, s.w);
+          for (int k = 0; k < PIECES; ++k) {
+            tmem_wait();
+            if ((k + 1) % OF_PART != 0) {
+              ask_piece(unit, k + 1);
+              use(k, 0, 32);
+              continue;
             }
-            a0 = __ffma2_rn(x0, s0, a0);
-            a1 = __ffma2_rn(x1, s1, a1);
+            release(k / OF_PART);
+            const bool last = k + 1 == PIECES, more = !last || kb + STEP < blocks;
+            const uint32_t next = last ? unit + STEP : unit, bar = full_of(next, last ? 0 : (k + 1) / OF_PART), parity = (next / NB) & 1;
+            const bool there = more && bar_try(bar, parity);
+            use(k, 0, 16);
+            if (more) {
+              ok = __all_sync(0xFFFFFFFFu, there || bar_wait_all(bar, parity, given_up));
+              if (!ok) break;
+              tc_fence_after();
+              ask_piece(next, last ? 0 : k + 1);
+            }
+            use(k, 16, 32);
           }
+        } else {
+          ok = __all_sync(0xFFFFFFFFu, bar_wait_all(full_of(unit, 0), (unit / NB) & 1, given_up));
+          if (!ok) break;
+          tc_fence_after();
+#pragma unroll
+          for (int k = 0; k < PIECES; ++k) ask_piece(unit, k);
+          tmem_wait();
+          release(0);
+#pragma unroll
+          for (int k = 0; k < PIECES; ++k) use(k, 0, 32);
         }
         if (!ok) break;
       }
@@ -607,7 +637,7 @@ block_tc_kernel(const __grid_constant__ BlockTcParams p, const __grid_constant__
           float4* const sums = reinterpret_cast<float4*>(smem) + mine;   // [32][128][4]
           if (half != (lead >> 1)) {
 #pragma unroll
-            for (int i = 0; i < OWN / 4; ++i) sums[i * 128] = make_float4(acc[2 * i].x, acc[2 * i].y, acc[2 * i + 1].x, acc[2 * i + 1].y);
+            for (int i = 0; i < OWN / 4; ++i) sums[i * 128] = four_of(acc[2 * i], acc[2 * i + 1]);
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
             const uint32_t at = (lane * 128 + quad * 32) * 16, other = (lead ^ 2) + rank;
@@ -619,8 +649,8 @@ block_tc_kernel(const __grid_constant__ BlockTcParams p, const __grid_constant__
 #pragma unroll
           for (int i = 0; i < OWN / 4; ++i) {
             const float4 v = sums[(OWN / 4 + i) * 128];
-            acc[2 * i] = __fadd2_rn(acc[2 * i], make_float2(v.x, v.y));
-            acc[2 * i + 1] = __fadd2_rn(acc[2 * i + 1], make_float2(v.z, v.w));
+            acc[2 * i] = add2(acc[2 * i], pair(v.x, v.y));
+            acc[2 * i + 1] = add2(acc[2 * i + 1], pair(v.z, v.w));
           }
         }
         const int row0 = l0 + quad * 32, rows = l_end - row0 < 32 ? l_end - row0 : 32;
@@ -634,7 +664,7 @@ block_tc_kernel(const __grid_constant__ BlockTcParams p, const __grid_constant__
             ok = __all_sync(0xFFFFFFFFu, done == 0 || bar_wait_all(parted + 8 * quad, (done - 1) & 1, given_up));
             if (!ok) break;
 #pragma unroll
-            for (int i = 0; i < OWN / 4; ++i) sums[i * 128] = make_float4(acc[2 * i].x, acc[2 * i].y, acc[2 * i + 1].x, acc[2 * i + 1].y);
+            for (int i = 0; i < OWN / 4; ++i) sums[i * 128] = four_of(acc[2 * i], acc[2 * i + 1]);
             __syncwarp();
             if (lane == 0) bar_arrive(joined + 8 * quad);
             continue;
@@ -644,8 +674,8 @@ block_tc_kernel(const __grid_constant__ BlockTcParams p, const __grid_constant__
 #pragma unroll
           for (int i = 0; i < OWN / 4; ++i) {
             const float4 v = sums[i * 128];
-            acc[2 * i] = __fadd2_rn(acc[2 * i], make_float2(v.x, v.y));
-            acc[2 * i + 1] = __fadd2_rn(acc[2 * i + 1], make_float2(v.z, v.w));
+            acc[2 * i] = add2(acc[2 * i], pair(v.x, v.y));
+            acc[2 * i + 1] = add2(acc[2 * i + 1], pair(v.z, v.w));
           }
           __syncwarp();
           if (lane == 0) bar_arrive(parted + 8 * quad);
@@ -654,7 +684,7 @@ block_tc_kernel(const __grid_constant__ BlockTcParams p, const __grid_constant__
             // [S][BN / S / 4][128][4], once all are past their last MMA
             __syncwarp();
 #pragma unroll
-            for (int i = 0; i < OWN / 4; ++i) sums[i * 128] = make_float4(acc[2 * i].x, acc[2 * i].y, acc[2 * i + 1].x, acc[2 * i + 1].y);
+            for (int i = 0; i < OWN / 4; ++i) sums[i * 128] = four_of(acc[2 * i], acc[2 * i + 1]);
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             cluster_sync();
             met = true;
@@ -669,8 +699,12 @@ block_tc_kernel(const __grid_constant__ BlockTcParams p, const __grid_constant__
           using T = std::remove_pointer_t<decltype(out)>;
           T* const to = out + group * p.out_group + l * p.ldl;
 #pragma unroll
-          for (int i = 0; i < OWN; ++i)
-            if (l_in && c + i < c_end) to[(c + i) * p.ldc] = from_f<T>(i & 1 ? acc[i / 2].y : acc[i / 2].x);
+          for (int i = 0; i < OWN; i += 2) {
+            float a, b;
+            halves(acc[i / 2], a, b);
+            if (l_in && c + i < c_end) to[(c + i) * p.ldc] = from_f<T>(a);
+            if (l_in && c + i + 1 < c_end) to[(c + i + 1) * p.ldc] = from_f<T>(b);
+          }
         };
         if (p.out_type == EMU_OUT_F32) write(static_cast<float*>(p.out));
         else if (p.out_type == EMU_OUT_BF16) write(static_cast<__nv_bfloat16*>(p.out));
