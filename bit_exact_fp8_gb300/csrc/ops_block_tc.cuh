@@ -490,12 +490,14 @@ block_tc_kernel(const __grid_constant__ BlockTcParams p, const __grid_constant__
     const float *pl = nullptr, *pc = nullptr;
     bool r_in = false;
     int left = 0, c_at = 0;                              // blocks whose scales have not been asked for; a lane's first column
+    // from one of a lane's columns to the next (a pair's 128 of a warp are within one block)
+    const int64_t next_c = p.c.shift == 0 ? 32 * p.c.rs : 0;
     float rl0 = 0.0f, rl1 = 0.0f, rc0[NC] = {}, rc1[NC] = {};
     auto ask = [&](float& rl, float (&rc)[NC]) {
       rl = r_in && left > 0 ? __ldg(pl) : 0.0f;
 #pragma unroll
       for (int j = 0; j < NC; ++j)
-        rc[j] = left > 0 && c_at + 32 * j < t.c_end ? __ldg(pc + ((c_at + 32 * j) >> p.c.shift) * p.c.rs) : 0.0f;
+        rc[j] = left > 0 && c_at + 32 * j < t.c_end ? __ldg(PAIR ? pc + j * next_c : pc + ((c_at + 32 * j) >> p.c.shift) * p.c.rs) : 0.0f;
       pl += STEP * p.l.ks;
       pc += STEP * p.c.ks;
       left -= STEP;
@@ -508,7 +510,7 @@ block_tc_kernel(const __grid_constant__ BlockTcParams p, const __grid_constant__
       r_in = l_at < t.l_end;
       c_at = t.c0 + (PAIR ? half * OWN : 0) + (MODE == kScaleLane ? 0 : lane);
       pl = p.l.scale + gl * p.l.gs + (l_at >> p.l.shift) * p.l.rs + kb * p.l.ks;
-      pc = p.c.scale + gc * p.c.gs + kb * p.c.ks;
+      pc = p.c.scale + gc * p.c.gs + kb * p.c.ks + (PAIR ? (c_at >> p.c.shift) * p.c.rs : 0);
       left = t.kb1 - kb;
       ask(rl0, rc0);
       ask(rl1, rc1);
