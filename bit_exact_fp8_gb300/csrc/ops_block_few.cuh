@@ -5,16 +5,16 @@
 // memory: the order of K within a block is free as long as both sides keep to one, so a quad's lanes take 16
 // contiguous codes each of either half of a row's block, four MMAs' worth together.  The warps of a CTA
 // share out the blocks of K, and their sums meet in shared memory in a fixed order.
-// 1 x 5760 x 1920 in 4.6 us, 2.5 of them the launch (the tcgen05 kernel 8.4, whose steps are longer).
+// 1 x 5760 x 1920 in 4.1 us, 2.3 of them the launch (by tcgen05 8.4: its steps are longer).
 #pragma once
 #include "ops_block.cuh"
 
 namespace emu_ops {
 
 struct BlockFewParams {
-  const uint8_t* w; int64_t w_row;                       // [N][K], 16-byte aligned rows
+  const uint8_t* w; int64_t w_row; uintptr_t w_end;      // [N][K], and where its memory ends
   const float* ws; int ws_shift; int64_t ws_row, ws_k;
-  const uint8_t* t; int64_t t_row;                       // [M][K], 16-byte aligned rows
+  const uint8_t* t; int64_t t_row; uintptr_t t_end;      // [M][K]
   const float* ts; int ts_shift; int64_t ts_row, ts_k;
   int64_t N;
   int M, K, share;                                          // warps that share out K: 1, 2, 4 or 8
@@ -33,7 +33,9 @@ template <int FW, int FT> __device__ __forceinline__ void mma_fp8(float (&d)[4],
 #undef EMU_MMA
 }
 
-template <int FW, int FT>
+// VEC: rows of whole 16-byte chunks; else a chunk is the two aligned words that hold it, shifted into place (1 x 5760 x 1921
+// 9.5 us so, 12.8 by way of aligned copies).
+template <int FW, int FT, bool VEC>
 __global__ void __launch_bounds__(256) block_few_kernel(const BlockFewParams p) {
   __shared__ float sums[8][8][17];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, q = lane & 3;
@@ -48,19 +50,29 @@ __global__ void __launch_bounds__(256) block_few_kernel(const BlockFewParams p) 
   const float* const s1 = p.ws + ((in1 ? n + 8 : 0) >> p.ws_shift) * p.ws_row;
   const float* const st0 = p.ts + ((q * 2) >> p.ts_shift) * p.ts_row;
   const float* const st1 = p.ts + ((q * 2 + 1) >> p.ts_shift) * p.ts_row;
-  const uint4 none = make_uint4(0u, 0u, 0u, 0u);
-  auto chunk = [&](bool in, const uint8_t* from) { return in ? __ldg(reinterpret_cast<const uint4*>(from)) : none; };
+  const int8_t* const w_at = reinterpret_cast<const int8_t*>(p.w);
+  const int8_t* const t_at = reinterpret_cast<const int8_t*>(p.t);
   float acc[4] = {};
-#pragma unroll 2
+#pragma unroll (VEC ? 2 : 1)
   for (int kb = part; kb < kb_all; kb += p.share) {
-    const int k = kb * kBlock + q * 16;                  // K is a multiple of 16: a chunk of 16 codes is there or not
-    const bool k0 = k < p.K, k1 = k + 64 < p.K;
+    const int left = p.K - (kb * kBlock + q * 16);       // codes of the row from the first chunk's on
     const int64_t at = (int64_t)kb * kBlock;
-    const uint4 a0 = chunk(in0 && k0, w0 + at), a1 = chunk(in0 && k1, w0 + at + 64);
-    const uint4 c0 = chunk(in1 && k0, w1 + at), c1 = chunk(in1 && k1, w1 + at + 64);
-    const uint4 b0 = chunk(tin && k0, tok + at), b1 = chunk(tin && k1, tok + at + 64);
+    Codes<VEC> ask[6];
+    const int8_t* const from[3] = {reinterpret_cast<const int8_t*>(w0 + at), reinterpret_cast<const int8_t*>(w1 + at),
+                                   reinterpret_cast<const int8_t*>(tok + at)};
+    const bool in[3] = {in0, in1, tin};
+#pragma unroll
+    for (int i = 0; i < 6; ++i)
+      ask[i].ask(from[i / 2] + i % 2 * 64, 0, in[i / 2] && left > i % 2 * 64, i < 4 ? w_at : t_at, i < 4 ? p.w_end : p.t_end);
     const float sw0 = __ldg(s0 + kb * p.ws_k), sw1 = __ldg(s1 + kb * p.ws_k);
     const float t0 = q * 2 < p.M ? __ldg(st0 + kb * p.ts_k) : 0.0f, t1 = q * 2 + 1 < p.M ? __ldg(st1 + kb * p.ts_k) : 0.0f;
+    uint4 v[6];
+#pragma unroll
+    for (int i = 0; i < 6; ++i) {
+      const int rest = left - i % 2 * 64;
+      v[i] = ask[i].get(from[i / 2] + i % 2 * 64, 0, rest < 16 ? rest : 16, in[i / 2] && rest > 0, i < 4 ? w_at : t_at, i < 4 ? p.w_end : p.t_end);
+    }
+    const uint4 &a0 = v[0], &a1 = v[1], &c0 = v[2], &c1 = v[3], &b0 = v[4], &b1 = v[5];
     float d[4] = {};
     mma_fp8<FW, FT>(d, a0.x, c0.x, a0.y, c0.y, b0.x, b0.y);
     mma_fp8<FW, FT>(d, a0.z, c0.z, a0.w, c0.w, b0.z, b0.w);

@@ -159,26 +159,31 @@ template <int BN> int launch_tc(const BlockTcParams& p, int mode, int64_t tiles,
   return EMU_OK;
 }
 
-// Up to eight tokens of a dense product whose rows are whole 16-byte chunks, where latency counts; where bandwidth does,
-// the TMA's deep queues win.  As few and by tcgen05: 1 x 5760 x 1920 4.6 and 8.4 us, 8 x 4096 x 4096 5.7 and 8.3,
-// 8 x 8192 x 2048 6.6 and 8.4, 8 x 16384 x 2048 11.6 and 8.8, 8 x 8192 x 8192 22 and 17; of 16 tokens 8.1 and 8.4.
-bool few_tokens(const BlockMm& p, const CodesView& va, const CodesView& vb) {
-  return p.kind == BlockKind::dense && p.M <= 8 && p.K > 0 && p.K % 16 == 0 && !va.mn && !vb.mn && va.fits() && vb.fits() &&
-         p.N * p.K <= (int64_t)24 << 20;
+// Up to eight tokens of a dense product, K-major on both sides, where latency counts; where bandwidth does, the TMA's
+// deep queues win.  As few and by tcgen05: 1 x 5760 x 1920 4.1 and 8.4 us, 8 x 4096 x 4096 5.4 and 8.3, 8 x 8192 x 2048 6.6 and
+// 8.4, 8 x 16384 x 2048 11.6 and 8.8, 8 x 8192 x 8192 22 and 17; of 16 tokens 8.1 and 8.4.
+bool few_tokens(int64_t M, int64_t N, int64_t K, const CodesView& va, const CodesView& vb) {
+  return M <= 8 && K > 0 && !va.mn && !vb.mn && N * K <= (int64_t)24 << 20;
 }
 void run_few_tokens(const BlockMm& p, const CodesView& va, const CodesView& vb, cudaStream_t st) {
   BlockFewParams q = {};
-  q.w = vb.at; q.w_row = vb.stride;
+  const uintptr_t w = reinterpret_cast<uintptr_t>(vb.at), t = reinterpret_cast<uintptr_t>(va.at);
+  q.w = vb.at; q.w_row = vb.stride; q.w_end = w + (size_t)((p.N - 1) * vb.stride + p.K);
   q.ws = p.b.scale; q.ws_shift = p.b.scale_rows == 1 ? 0 : 7; q.ws_row = p.b.scale_row_stride; q.ws_k = p.b.scale_k_stride;
-  q.t = va.at; q.t_row = va.stride;
+  q.t = va.at; q.t_row = va.stride; q.t_end = t + (size_t)((p.M - 1) * va.stride + p.K);
   q.ts = p.a.scale; q.ts_shift = p.a.scale_rows == 1 ? 0 : 7; q.ts_row = p.a.scale_row_stride; q.ts_k = p.a.scale_k_stride;
   q.M = (int)p.M; q.N = p.N; q.K = (int)p.K;
   const int64_t kb = (p.K + kBlock - 1) / kBlock;
   q.share = kb >= 8 ? 8 : kb >= 4 ? 4 : kb >= 2 ? 2 : 1;
   q.out = p.out; q.out_type = p.out_type;
-  auto kernel = p.b.format == EMU_E4M3FN
-                    ? p.a.format == EMU_E4M3FN ? block_few_kernel<EMU_E4M3FN, EMU_E4M3FN> : block_few_kernel<EMU_E4M3FN, EMU_E5M2>
-                    : p.a.format == EMU_E4M3FN ? block_few_kernel<EMU_E5M2, EMU_E4M3FN> : block_few_kernel<EMU_E5M2, EMU_E5M2>;
+  auto pick = [&](auto vec) {
+    constexpr bool VEC = decltype(vec)::value;
+    return p.b.format == EMU_E4M3FN
+               ? p.a.format == EMU_E4M3FN ? block_few_kernel<EMU_E4M3FN, EMU_E4M3FN, VEC> : block_few_kernel<EMU_E4M3FN, EMU_E5M2, VEC>
+               : p.a.format == EMU_E4M3FN ? block_few_kernel<EMU_E5M2, EMU_E4M3FN, VEC> : block_few_kernel<EMU_E5M2, EMU_E5M2, VEC>;
+  };
+  const bool vec = p.K % 16 == 0 && va.fits() && vb.fits();
+  auto kernel = vec ? pick(std::true_type()) : pick(std::false_type());
   const int64_t rows = 16 * (8 / q.share);
   kernel<<<(unsigned)((p.N + rows - 1) / rows), 256, 0, st>>>(q);
 }
@@ -224,7 +229,7 @@ int run_block_mm(const BlockMm& p, void* workspace, cudaStream_t st) {
   const bool wgrad = p.kind == BlockKind::wgrad, grouped = p.kind == BlockKind::grouped;
   CodesView va = view_of(p.a, p.M, p.K, 1, wgrad), vb = view_of(p.b, p.N, p.K, grouped ? p.E : 1, wgrad);
   const int64_t rows_of_group = grouped ? (p.M + (p.E > 0 ? p.E : 1) - 1) / (p.E > 0 ? p.E : 1) : p.M;   // about
-  if (few_tokens(p, va, vb)) {
+  if (p.kind == BlockKind::dense && few_tokens(p.M, p.N, p.K, va, vb)) {
     run_few_tokens(p, va, vb, st);
     return emu_ops_launched("emu_block_scaled_mm");
   }
@@ -367,7 +372,8 @@ extern "C" {
 
 size_t emu_block_mm_workspace_bytes(const emu_block_operand_t* a, const emu_block_operand_t* b, int64_t M, int64_t N, int64_t K) {
   if (!a || !b || M < 1 || N < 1 || K < 1) return 0;
-  return view_of(*a, M, K, 1, false).laid_out() + view_of(*b, N, K, 1, false).laid_out();
+  const CodesView va = view_of(*a, M, K, 1, false), vb = view_of(*b, N, K, 1, false);
+  return few_tokens(M, N, K, va, vb) ? 0 : va.laid_out() + vb.laid_out();
 }
 size_t emu_grouped_block_mm_workspace_bytes(const emu_block_operand_t* a, const emu_block_operand_t* b, int64_t T, int64_t N, int64_t K,
                                             int64_t E) {

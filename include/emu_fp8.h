@@ -423,7 +423,7 @@ int emu_block_quant(const void* x, int64_t ldx, emu_out_t type, int64_t T, int64
 /*
  * SwiGLU with an 8-bit output: gate_up [T, 2H] holds g in its first H columns and u in the others,
  *   y = g / (1 + e^-g) * u    (fp32)
- * quantised as by emu_block_quant in rows or squares (q [T,H], scale).  checkpoint [T, 2H] and
+ * (within (7 + 1.2 |g|) 2^-23 of its value) quantised as by emu_block_quant in rows or squares (q [T,H], scale).  checkpoint [T, 2H] and
  * checkpoint_scale [T, 2 ceil(H/128)] (both NULL: not wanted): g and u themselves as E4M3 codes
  * with a scale for each 1 x 128 block of either half, for the backward pass.
  */
@@ -465,8 +465,8 @@ typedef struct {
  * formats and of the strides above, so that a layer's forward product and both its gradients
  * read the same codes.  A NaN among a row's codes or scales gives NaN in that row's (column's)
  * outputs alone.  K == 0 gives zeros.  Sizes: M, N, K < 2^31 - 256.
- *   workspace: emu_block_mm_workspace_bytes of the same operands (0 where both are 16-byte
- *   aligned with strides that are multiples of 16), 256-byte aligned
+ *   workspace: emu_block_mm_workspace_bytes of the same operands and sizes (0 where both are
+ *   16-byte aligned with strides that are multiples of 16), 256-byte aligned
  */
 size_t emu_block_mm_workspace_bytes(const emu_block_operand_t* a, const emu_block_operand_t* b,
                                     int64_t M, int64_t N, int64_t K);
