@@ -400,3 +400,42 @@ def test_tiles_in_rounds_and_slices(fw, M, N, K, by_k):
     """More tiles than the device holds, the last few in slices of K; and few tiles in slices."""
     for block in ((ROWS, SQUARES), (SQUARES, SQUARES), (ROWS, ROWS)):
         dense(fw, M, N, K, by_k=by_k, block=block, dt=torch.bfloat16)
+
+
+def big_codes(g, rows, cols):
+    """FP8 codes of values within [1, 2) and their negatives, without a 32-bit copy of them."""
+    codes = torch.empty(rows, cols, dtype=torch.uint8, device=DEV)
+    codes.random_(0, 256, generator=g)
+    return codes.bitwise_and_(0x87).bitwise_or_(0x38).view(torch.float8_e4m3fn)
+
+
+def test_operands_past_32_bits(fw):
+    """More than 2^31 codes on a side: many rows, the same across its rows, and many experts' weights."""
+    g = gen(6)
+    M, K, N = 70000, 32768, 24
+    a, sa = big_codes(g, M, K), torch.rand(M, blocks(K), generator=g, device=DEV)
+    b, sb = operand(g, (N, K), SQUARES)
+    vb = value(b, sb, SQUARES).t()
+    got = fw.block_scaled_mm(a, b.t(), sa, sb.t(), out_dtype=torch.float32)
+    for rows in (slice(0, 70), slice(65500, 65600), slice(M - 70, M)):
+        check_product(got[rows], value(a[rows], sa[rows], ROWS), vb)
+    # [K, M] codes: rows of the product across them
+    st = torch.rand(blocks(M), K, generator=g, device=DEV)               # blocks along the M tokens that are summed over
+    x, sx = operand(g, (M, 48), COLUMNS)
+    got = fw.block_scaled_mm(a.t(), x, st.t(), sx, out_dtype=torch.float32)
+    vx = value(x, sx, COLUMNS)
+    for cols in (slice(0, 40), slice(K - 40, K)):
+        check_product(got[cols], value(a[:, cols], st[:, cols], COLUMNS).t(), vx)
+    del a, got
+    E, N, K = 36, 8192, 8192
+    w = big_codes(g, E * N, K).view(E, N, K)
+    sw = torch.rand(E, N // 128, K // 128, generator=g, device=DEV)
+    sizes = [0] * E
+    sizes[0], sizes[17], sizes[-1] = 3, 150, 41
+    offsets = ends_of(sizes)
+    t, st = operand(g, (sum(sizes), K), ROWS)
+    got = fw.grouped_block_scaled_mm(t, w.transpose(1, 2), offsets, st, sw.transpose(1, 2), out_dtype=torch.float32)
+    ends = offsets.tolist()
+    for e in (0, 17, E - 1):
+        r = slice(ends[e], ends[e + 1])
+        check_product(got[r], value(t[r], st[r], ROWS), value(w[e], sw[e], SQUARES).t())
