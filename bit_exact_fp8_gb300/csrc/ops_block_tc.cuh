@@ -43,12 +43,15 @@ template <int BN> struct BlockTcShape {
   static constexpr bool SWAP = !PAIR;                    // the output's rows are the columns C, and either four reading
                                                          // warps take every other block, with all columns
   static constexpr int L = PAIR ? 256 : 128, C_ROWS = PAIR ? 128 : BN;       // a tile's lanes; rows of C that a CTA loads
-  static constexpr int NS = PAIR ? 4 : BN == 64 ? 7 : 8, STAGE = 128 * 128 + C_ROWS * 128, NB = PAIR ? 2 : 4;
+  static constexpr int NS = PAIR ? 4 : BN == 64 ? 6 : 8, STAGE = 128 * 128 + C_ROWS * 128, NB = PAIR ? 2 : 4;
   static constexpr int H = PAIR ? 2 : 1;                 // parts of a tile's columns, each with MMAs and barriers of its own
   static constexpr int OWN = PAIR ? BN / 2 : BN, READ = OWN / H, TMEM = NB * BN;          // a warp's columns, and those of a part
   static constexpr int OUT = NS * STAGE, CS = OUT + (PAIR ? kOutStage : BN * 128 * 4), BARS = CS + 8 * 2 * OWN * 4;
   static constexpr int BAR_COUNT = 3 * NS + 2 * NB * H + 10, TABLE = BARS + 8 * BAR_COUNT + 8 + 2 * 12 * 4;
   static constexpr int smem(int E) { return TABLE + 2 * (E + 1) * 4 + 1024; }
+  // Narrow tiles' blocks go in turn to two issuing warps.  A wait for a phase tells it from the one before, not from the one
+  // before that: each of a stage's (and each of a buffer's) blocks has to be the same warp's.
+  static_assert(PAIR || (NS % 2 == 0 && NB % 2 == 0), "a stage's blocks are one issuing warp's");
 };
 static_assert(BlockTcShape<256>::smem(kMaxExperts) <= kMaxSmem &&
               BlockTcShape<64>::smem(kMaxExperts) <= kMaxSmem && BlockTcShape<32>::smem(kMaxExperts) <= kMaxSmem, "one CTA an SM");
