@@ -421,35 +421,39 @@ block_tc_kernel(const __grid_constant__ BlockTcParams p, const __grid_constant__
           }
         }
       }
-      if (!ok)                                           // the loads issued last, one stage each at most
-        for (uint32_t i = it > NS ? it - NS : 0; i < it; ++i) (void)bar_wait(full + 8 * (i % NS), (i / NS) & 1);
-    } else if (warp <= 2 && rank == 0) {                 // two warps: of a pair one for either part of the columns, else for every other block
-      uint32_t it = 0;
-      bool ok = true;
-      const int mine = warp - 1, h = PAIR ? mine : 0;
-      // a step of 32 of K, in 16 bytes; the parts' rows of C within each CTA's 128
-      const uint32_t step_l = p.l.mn ? 256 : 2, step_c = p.c.mn ? 256 : 2, part_c = h * (p.c.mn ? 4 : 512);
-      for (int tile = first_tile; tile < tiles && ok; tile += step) {
-        const BlockTile t = tile_at<BN>(p, start, before, tile, rank);
-        for (int kb = t.kb0; kb < t.kb1; ++kb, ++it) {
-          const uint32_t s = it % NS, buf = it % NB;
-          if (!PAIR && (int)(it & 1) != mine) continue;
-          ok = bar_wait_all((PAIR || p.kind == BlockKind::wgrad ? fixed : full) + 8 * s, (it / NS) & 1, given_up) &&
-               (it < NB || bar_wait_all(tempty + 8 * (buf * H + h), (it / NB - 1) & 1, given_up));
-          if (!ok) break;
-          tc_fence_after();
-          if (one_of_warp()) {
-            const uint64_t dl = desc8(base + s * SH::STAGE), dc = desc8(base + s * SH::STAGE + 16384) + part_c;
+      // The barriers outlive what arrives at them: the loads issued last, one stage each at most, or the MMAs of those (of a pair,
+      // the first CTA's at the second's barriers).
+      for (uint32_t i = it > NS ? it - NS : 0; i < it; ++i)
+        (void)(ok ? bar_wait_all(empty + 8 * (i % NS), (i / NS) & 1, given_up) : bar_wait(full + 8 * (i % NS), (i / NS) & 1));
+    } else if (warp <= 2) {                              // two warps: of a pair one for either part of the columns, else for every other block
+      if (rank == 0) {
+        uint32_t it = 0;
+        bool ok = true;
+        const int mine = warp - 1, h = PAIR ? mine : 0;
+        // a step of 32 of K, in 16 bytes; the parts' rows of C within each CTA's 128
+        const uint32_t step_l = p.l.mn ? 256 : 2, step_c = p.c.mn ? 256 : 2, part_c = h * (p.c.mn ? 4 : 512);
+        for (int tile = first_tile; tile < tiles && ok; tile += step) {
+          const BlockTile t = tile_at<BN>(p, start, before, tile, rank);
+          for (int kb = t.kb0; kb < t.kb1; ++kb, ++it) {
+            const uint32_t s = it % NS, buf = it % NB;
+            if (!PAIR && (int)(it & 1) != mine) continue;
+            ok = bar_wait_all((PAIR || p.kind == BlockKind::wgrad ? fixed : full) + 8 * s, (it / NS) & 1, given_up) &&
+                 (it < NB || bar_wait_all(tempty + 8 * (buf * H + h), (it / NB - 1) & 1, given_up));
+            if (!ok) break;
+            tc_fence_after();
+            if (one_of_warp()) {
+              const uint64_t dl = desc8(base + s * SH::STAGE), dc = desc8(base + s * SH::STAGE + 16384) + part_c;
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              mma8<PAIR>(tmem + buf * BN + h * (BN / H), dl + k * step_l, dc + k * step_c, p.idesc, k > 0);
-            commit8<PAIR>(tfull + 8 * (buf * H + h), both);
-            commit8<PAIR>(empty + 8 * s, both);
+              for (int k = 0; k < 4; ++k)
+                mma8<PAIR>(tmem + buf * BN + h * (BN / H), dl + k * step_l, dc + k * step_c, p.idesc, k > 0);
+              commit8<PAIR>(tfull + 8 * (buf * H + h), both);
+              commit8<PAIR>(empty + 8 * s, both);
+            }
           }
         }
+        if (one_of_warp()) commit8<PAIR>(drained, both);
       }
-      if (one_of_warp()) commit8<PAIR>(drained, both);         // the MMAs are done before the tensor memory goes back
-      (void)bar_wait(drained, 0);
+      (void)bar_wait(drained, 0);                        // the MMAs are done, before the tensor memory goes back, at both CTAs of a pair
     } else if (warp == 3 && (PAIR || p.kind == BlockKind::wgrad)) {
       uint32_t it = 0;
       bool ok = true;
