@@ -423,9 +423,11 @@ int emu_block_quant(const void* x, int64_t ldx, emu_out_t type, int64_t T, int64
 /*
  * SwiGLU with an 8-bit output: gate_up [T, 2H] holds g in its first H columns and u in the others,
  *   y = g / (1 + e^-g) * u    (fp32)
- * (within (7 + 1.2 |g|) 2^-23 of its value) quantised as by emu_block_quant in rows or squares (q [T,H], scale).  checkpoint [T, 2H] and
- * checkpoint_scale [T, 2 ceil(H/128)] (both NULL: not wanted): g and u themselves as E4M3 codes
- * with a scale for each 1 x 128 block of either half, for the backward pass.
+ * (within (7 + 1.2 |g|) 2^-23 of its value; below g = -87, where 1 / (1 + e^-g) leaves fp32's
+ * normal range, and |g u| 2^-147) quantised as by emu_block_quant in rows or squares (q [T,H],
+ * scale).  checkpoint [T, 2H] and checkpoint_scale [T, 2 ceil(H/128)] (both NULL: not wanted):
+ * g and u themselves as E4M3 codes with a scale for each 1 x 128 block of either half, for the
+ * backward pass.
  */
 int emu_swiglu_quant(const void* gate_up, int64_t ldx, emu_out_t type, int64_t T, int64_t H,
                      emu_block_t block, emu_fp8_t q_format, void* q, float* scale, void* checkpoint,

@@ -1,5 +1,5 @@
-"""The forms of the operators with block scales that only larger calls take, each with several rounds of its
-work, against the formulas in 64 bits."""
+"""The forms of the products with block scales that only larger calls take, each with several rounds of its work,
+against the formulas in 64 bits."""
 import itertools
 import random
 
