@@ -360,21 +360,23 @@ template <int N> __device__ __forceinline__ void values_of_codes(const uint32_t 
     v[2 * i + 1] = f.y * scale;
   }
 }
-// gradients by g and u, in their places, with 1 / (1 + e^-g) as in swiglu (here the root costs registers: 64 us against 57 by __expf)
-template <int N> __device__ __forceinline__ void swiglu_grads(const float (&gy)[N], float (&g)[N], float (&u)[N]) {
+// Gradients by g and u, in their places, with 1 / (1 + e^-g) as in swiglu: of fp32 with expf (the fast exponential is off by 1.2 |g| 2^-23,
+// which 16-bit gradients round away; 4096 x 5760 takes the same 50 us).  By a root as in swiglu: more registers, 64 us instead of 58.
+template <class T, int N> __device__ __forceinline__ void swiglu_grads(const float (&gy)[N], float (&g)[N], float (&u)[N]) {
 #pragma unroll
   for (int k = 0; k < N; ++k) {
-    const float e = __expf(-fabsf(g[k])), sig = (g[k] < 0.0f ? e : 1.0f) * fast_inverse(1.0f + e);
+    const float e = sizeof(T) == 4 ? expf(-fabsf(g[k])) : __expf(-fabsf(g[k]));
+    const float sig = (g[k] < 0.0f ? e : 1.0f) * fast_inverse(1.0f + e);
     const float a = gy[k] * sig, grad_u = a * g[k];
     g[k] = u[k] * fmaf(a, g[k] * (1.0f - sig), a);
     u[k] = grad_u;
   }
 }
 
-// Aligned rows: a vector of grad_y a thread at a time; its 1 x 128 blocks are those of both halves.  8192 x 5760 bf16 in 57 us:
-// 6.6 TB/s, 97% of a copy's rate.
+// Aligned rows: a vector of grad_y a thread at a time; its 1 x 128 blocks are those of both halves.  8192 x 5760 bf16 in 58 us:
+// 6.5 TB/s, 96% of a copy's rate.  (256, 8): 32 registers, so that the SM is full of warps (fp32 with 40 53 us instead of 50).
 template <class T>
-__global__ void __launch_bounds__(256) swiglu_grad_kernel(const SwigluGradParams p) {
+__global__ void __launch_bounds__(256, 8) swiglu_grad_kernel(const SwigluGradParams p) {
   constexpr int N = Vec<T>::N;
   const int64_t blocks = (p.H + 127) / 128, per_row = p.H / N, total = p.T * per_row;
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
@@ -387,7 +389,7 @@ __global__ void __launch_bounds__(256) swiglu_grad_kernel(const SwigluGradParams
     *reinterpret_cast<typename Piece<N>::type*>(wu) = *reinterpret_cast<const typename Piece<N>::type*>(p.kept + row * 2 * p.H + p.H + col);
     values_of_codes<N>(wg, s[0], g);
     values_of_codes<N>(wu, s[blocks], u);
-    swiglu_grads<N>(gy, g, u);
+    swiglu_grads<T, N>(gy, g, u);
     T* const out = static_cast<T*>(p.out) + row * 2 * p.H + col;
     store_f<T, N>(out, g);
     store_f<T, N>(out + p.H, u);
@@ -431,7 +433,7 @@ __global__ void __launch_bounds__(256) swiglu_grad_unaligned_kernel(const Swiglu
     au.get(p.H - col, in, p.kept, p.kept_end, wu);
     values_of_codes<N>(wg, sg, g);
     values_of_codes<N>(wu, su, u);
-    swiglu_grads<N>(gy, g, u);
+    swiglu_grads<T, N>(gy, g, u);
     Pack<T, N> og, ou;
 #pragma unroll
     for (int k = 0; k < N; ++k) {

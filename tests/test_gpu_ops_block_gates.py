@@ -94,3 +94,23 @@ def test_swiglu_backward_far_above_zero(fw):
     got = fw.swiglu_backward(gy, kept, scale)
     torch.testing.assert_close(got[:, :128], gy * scale[:, 1:], rtol=2.0 ** -20, atol=0)
     assert bool(got[:2, 128:].isposinf().all()) and bool(got[2:, 128:].isfinite().all())
+
+
+@pytest.mark.parametrize("T,H", [(300, 640), (77, 333)])
+def test_swiglu_backward_of_fp32(fw, T, H):
+    """By the exponential itself: the sigmoid within 8 2^-24 (the exponential 4, its sum with 1 one, the inverse 2, the product
+    one), s (1 + g (1 - s)) within twice that and one more of (1 + |g|) s, and four products and sums."""
+    g = gen(T)
+    n = blocks(H)
+    kept = (torch.randn(T, 2 * H, generator=g, device=DEV) * 60).clamp(-448, 448).to(QT["e4m3"])
+    scale = torch.exp(4 * torch.rand(T, 2 * n, generator=g, device=DEV)) / 100
+    gy = torch.randn(T, H, generator=g, device=DEV)
+    got = fw.swiglu_backward(gy, kept, scale)
+    held = kept.float() * torch.cat([spread(scale[:, :n], ROWS, (T, H)), spread(scale[:, n:], ROWS, (T, H))], 1)
+    gate, up = held[:, :H].double(), held[:, H:].double()
+    assert float(gate.min()) < -60 and float(gate.max()) > 60
+    y, s = gy.double(), torch.sigmoid(gate)
+    want = torch.cat([y * up * s * (1 + gate * (1 - s)), y * gate * s], 1)
+    tol = torch.cat([(y * up).abs() * (1 + gate.abs()) * (21 * 2.0 ** -24 * s + SMALLEST), (y * gate).abs() * (10 * 2.0 ** -24 * s + SMALLEST)], 1)
+    bad = ~((got.double() - want).abs() <= tol + 2.0 ** -149)
+    assert not bool(bad.any()), (int(bad.sum()), ((got.double() - want).abs() / tol.clamp_min(1e-300)).max())
