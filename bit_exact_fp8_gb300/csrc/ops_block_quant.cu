@@ -19,14 +19,12 @@ struct BlockQuantParams {
   int across;                                            // rows: warps of a CTA on one row, 1 or 8
 };
 
-// what a block's values are multiplied by, and its scale, from its largest magnitude (NaN if it holds
-// NaN; Inf counts as NaN: x / Inf would be 0 for the others)
-__device__ __forceinline__ void block_factor(float top, float qmax, float& by, float& scale) {
+// a block's scale from its largest magnitude (NaN if it holds NaN; Inf counts as NaN: x / Inf would be 0 for the others)
+__device__ __forceinline__ float block_scale(float top, float qmax) {
   const float m = top < __int_as_float(0x7F800000) ? top : __int_as_float(0x7FC00000);
-  scale = max_nan(m / qmax, kBlockScaleMin);
-  by = m < qmax * kBlockScaleMin ? 1.0f / kBlockScaleMin : qmax / m;
+  return max_nan(m / qmax, kBlockScaleMin);
 }
-// 1 / v of v in [1, 2]
+// 1 / v within 2^-23, of v and 1 / v in the normal range
 __device__ __forceinline__ float fast_inverse(float v) {
   float r;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
@@ -155,26 +153,47 @@ __device__ __forceinline__ void store_pieces(uint8_t* to, typename Piece<BYTES>:
   }
 }
 
-// codes of a vector's values, each times `by`
-template <int FMT, int N> __device__ __forceinline__ typename Piece<N>::type codes_of(const float (&v)[N], const float (&by)[N]) {
+// What values are divided by, one scale or S neighbours' each its own: the scale's inverse as the sum of two numbers, so that x hi + x lo,
+// the second rounded and the sum once more, is x / scale rounded to fp32 (up to 2^-40), and halfway between two codes where that is.
+// hi is below the inverse by some 2^-21 of it and lo not below 0: -0 stays -0.
+template <int S> struct Divisor {
+  float hi[S], lo[S];
+  __device__ __forceinline__ explicit Divisor(const float (&scale)[S]) {
+#pragma unroll
+    for (int i = 0; i < S; ++i) {
+      hi[i] = fast_inverse(scale[i]) * (1.0f - 4.76837158e-7f);
+      lo[i] = fmaf(-hi[i], scale[i], 1.0f) * hi[i];
+    }
+  }
+};
+// codes of a vector's values: their quotients to 8 bits, two at a time (PAIRS) or one by one
+template <int FMT, int N, bool PAIRS, int S> __device__ __forceinline__ typename Piece<N>::type codes_of(const float (&v)[N], const Divisor<S>& d) {
+  static_assert(S == 1 || S == N, "one scale or one each");
   uint32_t w[N / 4];
 #pragma unroll
   for (int i = 0; i < N / 4; ++i) {
     uint32_t two[2];
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
-      two[j] = __nv_cvt_float2_to_fp8x2(make_float2(v[4 * i + 2 * j] * by[4 * i + 2 * j], v[4 * i + 2 * j + 1] * by[4 * i + 2 * j + 1]),
-                                        __NV_SATFINITE, FMT == EMU_E4M3FN ? __NV_E4M3 : __NV_E5M2);
+    for (int j = 0; j < 2; ++j) {
+      const int k = 4 * i + 2 * j, a = S == 1 ? 0 : k, b = S == 1 ? 0 : k + 1;
+      float q0, q1;
+      if constexpr (PAIRS) {
+        const f2 x = pair(v[k], v[k + 1]);
+        halves(fma2(x, pair(d.hi[a], d.hi[b]), mul2(x, pair(d.lo[a], d.lo[b]))), q0, q1);
+      } else {
+        q0 = fmaf(v[k], d.hi[a], v[k] * d.lo[a]);
+        q1 = fmaf(v[k + 1], d.hi[b], v[k + 1] * d.lo[b]);
+      }
+      two[j] = __nv_cvt_float2_to_fp8x2(make_float2(q0, q1), __NV_SATFINITE, FMT == EMU_E4M3FN ? __NV_E4M3 : __NV_E5M2);
+    }
     w[i] = two[0] | two[1] << 16;
   }
   if constexpr (N == 4) return w[0];
   else return make_uint2(w[0], w[1]);
 }
-template <int FMT, int N> __device__ __forceinline__ typename Piece<N>::type codes_of(const float (&v)[N], float by) {
-  float all[N];
-#pragma unroll
-  for (int i = 0; i < N; ++i) all[i] = by;
-  return codes_of<FMT, N>(v, all);
+template <int FMT, int N> __device__ __forceinline__ typename Piece<N>::type codes_of(const float (&v)[N], float scale) {
+  const float one[1] = {scale};
+  return codes_of<FMT, N, true>(v, Divisor<1>(one));
 }
 
 // 1 x 128 blocks: 128 / N lanes hold one.  A warp takes UNROLL loads of a row (32 N values each) at a time, all asked for
@@ -200,7 +219,7 @@ __global__ void __launch_bounds__(256) block_rows_kernel(const BlockQuantParams 
       const int64_t col = (seg + i) * per + lane * N, left = (p.H - col) * (int64_t)sizeof(T);
       const int64_t block = (seg + i) * (per / 128) + lane / LANES, from = block * 128;
       const uint4 r = av[i].get(left, col < p.H, p.x, p.x_end);
-      float v[N], by, scale;
+      float v[N], scale;
       values_of<T>(r, v);
       uint32_t top;
       if constexpr (SWIGLU) {
@@ -208,12 +227,11 @@ __global__ void __launch_bounds__(256) block_rows_kernel(const BlockQuantParams 
         float g[N];
         values_of<T>(rg, g);
         if (p.kept) {
-          float bg, bu, sg, su;
-          block_factor(top_value<T>(top_of_lanes<LANES>(join_top<T>(top_words<T>(0u, rg)))), 448.0f, bg, sg);
-          block_factor(top_value<T>(top_of_lanes<LANES>(join_top<T>(top_words<T>(0u, r)))), 448.0f, bu, su);
+          const float sg = block_scale(top_value<T>(top_of_lanes<LANES>(join_top<T>(top_words<T>(0u, rg)))), 448.0f);
+          const float su = block_scale(top_value<T>(top_of_lanes<LANES>(join_top<T>(top_words<T>(0u, r)))), 448.0f);
           uint8_t* const to = p.kept + row * 2 * p.H + from;
-          store_pieces<BYTES, LANES, VEC>(to, codes_of<EMU_E4M3FN, N>(g, bg), p.H - from, in);
-          store_pieces<BYTES, LANES, VEC>(to + p.H, codes_of<EMU_E4M3FN, N>(v, bu), p.H - from, in);
+          store_pieces<BYTES, LANES, VEC>(to, codes_of<EMU_E4M3FN, N>(g, sg), p.H - from, in);
+          store_pieces<BYTES, LANES, VEC>(to + p.H, codes_of<EMU_E4M3FN, N>(v, su), p.H - from, in);
           if (in == 0 && block < blocks) {
             p.kept_scale[row * 2 * blocks + block] = sg;
             p.kept_scale[row * 2 * blocks + blocks + block] = su;
@@ -225,11 +243,11 @@ __global__ void __launch_bounds__(256) block_rows_kernel(const BlockQuantParams 
           v[k] = swiglu(g[k], v[k]);
           top = top_word<float>(top, __float_as_uint(v[k]) & 0x7FFFFFFFu);
         }
-        block_factor(__uint_as_float(top_of_lanes<LANES>(top)), p.qmax, by, scale);
+        scale = block_scale(__uint_as_float(top_of_lanes<LANES>(top)), p.qmax);
       } else {
-        block_factor(top_value<T>(top_of_lanes<LANES>(join_top<T>(top_words<T>(0u, r)))), p.qmax, by, scale);
+        scale = block_scale(top_value<T>(top_of_lanes<LANES>(join_top<T>(top_words<T>(0u, r)))), p.qmax);
       }
-      store_pieces<BYTES, LANES, VEC>(p.q + row * p.H + from, codes_of<FMT, N>(v, by), p.H - from, in);
+      store_pieces<BYTES, LANES, VEC>(p.q + row * p.H + from, codes_of<FMT, N>(v, scale), p.H - from, in);
       if (in == 0 && block < blocks) p.scale[row * blocks + block] = scale;
     }
   }
@@ -269,13 +287,12 @@ __global__ void __launch_bounds__(256) block_tile_kernel(const BlockQuantParams 
       values_of<T>(rg, g);
       values_of<T>(r, u);
       if (p.kept) {
-        float bg, bu, sg, su;
-        block_factor(top_value<T>(top_of_lanes<LANES>(join_top<T>(top_words<T>(0u, rg)))), 448.0f, bg, sg);
-        block_factor(top_value<T>(top_of_lanes<LANES>(join_top<T>(top_words<T>(0u, r)))), 448.0f, bu, su);
+        const float sg = block_scale(top_value<T>(top_of_lanes<LANES>(join_top<T>(top_words<T>(0u, rg)))), 448.0f);
+        const float su = block_scale(top_value<T>(top_of_lanes<LANES>(join_top<T>(top_words<T>(0u, r)))), 448.0f);
         uint8_t* const to = p.kept + row * 2 * p.H + from;
         const int64_t count = row < p.T ? p.H - from : 0;
-        store_pieces<N, LANES, VEC>(to, codes_of<EMU_E4M3FN, N>(g, bg), count, in);
-        store_pieces<N, LANES, VEC>(to + p.H, codes_of<EMU_E4M3FN, N>(u, bu), count, in);
+        store_pieces<N, LANES, VEC>(to, codes_of<EMU_E4M3FN, N>(g, sg), count, in);
+        store_pieces<N, LANES, VEC>(to + p.H, codes_of<EMU_E4M3FN, N>(u, su), count, in);
         if (in == 0 && row < p.T) {
           p.kept_scale[row * 2 * blocks + blockIdx.x] = sg;
           p.kept_scale[row * 2 * blocks + blocks + blockIdx.x] = su;
@@ -294,7 +311,7 @@ __global__ void __launch_bounds__(256) block_tile_kernel(const BlockQuantParams 
                               top_word<T>(tops4.w, r.w & M));
     }
   }
-  float by[N], scale[N];
+  float scale[SQUARE ? 1 : N];
   if constexpr (SQUARE) {
     uint32_t* const words = reinterpret_cast<uint32_t*>(tops);
     const uint32_t one = __reduce_max_sync(0xFFFFFFFFu, SWIGLU ? top : join_top<T>(top));
@@ -303,9 +320,7 @@ __global__ void __launch_bounds__(256) block_tile_kernel(const BlockQuantParams 
     uint32_t all = words[0];
 #pragma unroll
     for (int i = 1; i < 8; ++i) all = words[i] > all ? words[i] : all;
-    block_factor(SWIGLU ? __uint_as_float(all) : top_value<T>(all), p.qmax, by[0], scale[0]);
-#pragma unroll
-    for (int k = 1; k < N; ++k) by[k] = by[0];
+    scale[0] = block_scale(SWIGLU ? __uint_as_float(all) : top_value<T>(all), p.qmax);
     if (threadIdx.x == 0) p.scale[(int64_t)blockIdx.y * blocks + blockIdx.x] = scale[0];
   } else {
 #pragma unroll
@@ -323,13 +338,15 @@ __global__ void __launch_bounds__(256) block_tile_kernel(const BlockQuantParams 
     float of[N];
     values_of<T>(all, of);
 #pragma unroll
-    for (int k = 0; k < N; ++k) block_factor(of[k], p.qmax, by[k], scale[k]);
+    for (int k = 0; k < N; ++k) scale[k] = block_scale(of[k], p.qmax);
     if (r0 == 0) {
 #pragma unroll
       for (int k = 0; k < N; ++k)
         if (col + k < p.H) p.scale[(int64_t)blockIdx.y * p.H + col + k] = scale[k];
     }
   }
+  constexpr bool PAIRS = SWIGLU || !SQUARE || !VEC;       // squares of aligned rows: 22.7 us so, 25.8 in pairs; columns 26.6 and 26.0
+  const Divisor<SQUARE ? 1 : N> divisor(scale);
 #pragma unroll
   for (int i = 0; i < PASSES; ++i) {
     const int64_t row = row0 + r0 + i * ROWS;
@@ -340,7 +357,7 @@ __global__ void __launch_bounds__(256) block_tile_kernel(const BlockQuantParams 
     } else {
       values_of<T>(raw[i], v);
     }
-    store_pieces<N, LANES, VEC>(p.q + row * p.H + from, codes_of<FMT, N>(v, by), row < p.T ? p.H - from : 0, in);
+    store_pieces<N, LANES, VEC>(p.q + row * p.H + from, codes_of<FMT, N, PAIRS>(v, divisor), row < p.T ? p.H - from : 0, in);
   }
 }
 

@@ -145,7 +145,7 @@ def block_quant(x: torch.Tensor, *, block: Tuple[int, int] = (1, 128),
                 out_dtype: torch.dtype = torch.float8_e4m3fn, out: Optional[torch.Tensor] = None) -> BlockQuant:
     """``x`` [T, H] (fp32, bf16 or fp16, rows contiguous, any row stride) as FP8 codes
     (float8_e4m3fn or float8_e5m2) with an fp32 scale for each block, ``max|x| / qmax`` but at
-    least 2^-126.
+    least 2^-126.  The codes are those of ``x / scale`` in fp32.
 
     block (1, 128): for products over H, scales [T, ceil(H / 128)].  (128, 1): for products over T (a
     weight's gradient), scales [ceil(T / 128), H].  (128, 128): for both, scales [ceil(T / 128),
