@@ -466,7 +466,10 @@ typedef struct {
  * out[M,N] = sum over the blocks of K of (sum of the block's products) * (scale_a * scale_b),
  * contiguous, rounded once to out_dtype (fp32, bf16 or fp16).  a has M rows, b has N: b's rows
  * are the columns of the product's right-hand side.  A block's products are added up in fp32
- * within 2^-20 of the sum of their magnitudes, the blocks in fp32.  Any mixture of the two
+ * within 2^-20 of the sum of their magnitudes, the blocks in fp32.  What is multiplied first, the two
+ * scales or the sum and one of them (each rounded to fp32), depends on sizes and strides:
+ * scales are from 2^-90 to 2^88 (any of a block of zeros) and their products from 2^-126 to
+ * 2^127; beyond, forms may differ in what passes fp32's range.  Any mixture of the two
  * formats and of the strides above, so that a layer's forward product and both its gradients
  * read the same codes.  A NaN among a row's codes or scales gives NaN in that row's (column's)
  * outputs alone.  K == 0 gives zeros.  Sizes: M, N, K < 2^31 - 256.
