@@ -561,7 +561,7 @@ int emu_block_quant(const void* x, int64_t ldx, emu_out_t type, int64_t T, int64
   if (!apart({Span(q, T, H, H, 1), Span(scale, sr, sc, sc, 4)}, {Span(x, T, ldx, H, es)}))
     return emu_ops_fail(EMU_EINVAL, "an output overlaps the input, or the other");
   const int64_t v = 16 / (int64_t)es;
-  const bool vec = H % v == 0 && ldx % v == 0 && aligned(x, 16) && aligned(q, (size_t)v) && aligned(scale, 16);
+  const bool vec = H % v == 0 && ldx % v == 0 && aligned(x, 16) && aligned(q, (size_t)v);
   const BlockQuantParams p = {x, ldx, static_cast<const uint8_t*>(x) + ((T - 1) * ldx + H) * (int64_t)es, T, H, (int)q_format, q_format == EMU_E4M3FN ? 448.0f : 57344.0f,
                               static_cast<uint8_t*>(q), scale, nullptr, nullptr, 1};
   rc = pick_quant<false>(p, type, block, vec, static_cast<cudaStream_t>(stream));

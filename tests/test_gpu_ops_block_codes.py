@@ -85,3 +85,21 @@ def test_codes_of_the_checkpoint(fw, T, H, block, dt):
     n = blocks(H)
     for half, s in ((slice(0, H), slice(0, n)), (slice(H, 2 * H), slice(n, 2 * n))):
         check(r.checkpoint[:, half], r.checkpoint_scale[:, s], x[:, half], ROWS, "e4m3")
+
+
+@pytest.mark.parametrize("block", BLOCKS)
+def test_scales_at_any_address(fw, block):
+    """The C call with scales that start at any multiple of four bytes: the same codes and scales, and nothing beside them."""
+    from bit_exact_fp8_gb300 import _lib
+    x = values(gen(0), 300, 512, torch.bfloat16)
+    want = fw.block_quant(x, block=BLOCKS[block])
+    for off in (0, 1, 3):
+        held = torch.full((want.scale.numel() + 8,), -1.0, device=DEV)
+        q = torch.empty_like(want.q)
+        scale = held[off:off + want.scale.numel()]
+        rc = _lib.load().emu_block_quant(x.data_ptr(), 512, _lib.EMU_OUT_BF16, 300, 512, list(BLOCKS).index(block), 0, q.data_ptr(),
+                                         scale.data_ptr(), torch.cuda.current_stream().cuda_stream)
+        assert rc == 0
+        torch.cuda.synchronize()
+        assert torch.equal(q.view(torch.uint8), want.q.view(torch.uint8)) and torch.equal(scale.view_as(want.scale), want.scale)
+        assert bool((held[:off] == -1).all()) and bool((held[off + scale.numel():] == -1).all())
