@@ -115,18 +115,31 @@ BlockSide side_of(const emu_block_operand_t& o, int64_t rows, bool mn) {
   return {o.scale, o.scale_rows == 1 ? 0 : 7, o.scale_row_stride, o.scale_k_stride, o.scale_group_stride, (int)rows, mn ? 1 : 0};
 }
 
-// pairs of CTAs that the device holds at once (SMs of a cluster share a part of the chip, which may have an odd number)
-int pairs_at_once(const void* kernel, cudaLaunchConfig_t cfg) {
-  static std::atomic<int> cached[64];
+// Clusters of so many CTAs (1 to 8) that the device holds at once, each CTA with an SM to itself.  The SMs of a cluster share a part of
+// the chip, whose number need not be a multiple of it: of 152 SMs 76 clusters of two, but 36 of four and 15 of eight.
+int clusters_at_once(int ctas) {
+  static std::atomic<int> cached[64][9];
+  static std::atomic<bool> done[64];
+  const int sms = emu_ops_sm_count();
   int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return emu_ops_sm_count() / 2;
-  int v = cached[dev].load(std::memory_order_relaxed);
+  if (ctas == 1 || cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return sms / ctas;
+  int v = cached[dev][ctas].load(std::memory_order_relaxed);
   if (v == 0) {
-    int n = 0;
-    cfg.gridDim = dim3(2);
+    const void* const kernel = reinterpret_cast<const void*>(block_tc_kernel<256, kScaleLane>);
+    cudaLaunchAttribute at;
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim.x = (unsigned)ctas;
+    at.val.clusterDim.y = at.val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)ctas);
+    cfg.blockDim = dim3(kTcThreads8);
     cfg.dynamicSmemBytes = BlockTcShape<256>::smem(kMaxExperts);
-    v = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) == cudaSuccess && n > 0 ? n : emu_ops_sm_count() / 2;
-    cached[dev].store(v, std::memory_order_relaxed);
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    int n = 0;
+    v = emu_ops_allow_smem(kernel, (int)cfg.dynamicSmemBytes, done) && cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) == cudaSuccess && n > 0
+            ? n : sms / ctas;
+    cached[dev][ctas].store(v, std::memory_order_relaxed);
   }
   return v;
 }
@@ -151,8 +164,7 @@ template <int BN> int launch_tc(const BlockTcParams& p, int mode, int64_t tiles,
   at[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = cluster > 1 ? at : at + 1;
   cfg.numAttrs = cluster > 1 ? 1 : 0;
-  int64_t room = emu_ops_sm_count();
-  if (SH::PAIR && p.slices == 1) room = pairs_at_once(reinterpret_cast<const void*>(kernel), cfg);
+  const int64_t room = clusters_at_once(SH::PAIR ? 2 : 1);
   cfg.gridDim = dim3((unsigned)(p.slices > 1 || tiles < room ? tiles : room) * cluster);
   if (early) ++cfg.numAttrs;
   if (cudaLaunchKernelEx(&cfg, kernel, p, maps[0], maps[1], maps[2]) != cudaSuccess) return emu_ops_launched("emu_block_scaled_mm");
@@ -195,7 +207,7 @@ int64_t up(int64_t n, int64_t d) { return (n + d - 1) / d; }
 // and 11.4, 128 x 5760 x 1920 10.8, 9.3 and 11.4, 256 x 4096 x 4096 16.2, 15.2 and 18.4, 512 x 5760 x 1920 22.6, 21.5 and
 // 11.9; 64 x 1920 x 5760 10.9 in one slice, 7.6 in four, 777 x 1920 x 5760 in pairs 23.5 and in two slices 18.4.
 struct Form { int BN, slices; bool tail; };
-Form pick_form(const BlockMm& p, bool tokens_mn, int64_t rows, int64_t sms) {
+Form pick_form(const BlockMm& p, bool tokens_mn, int64_t rows) {
   if (p.kind == BlockKind::wgrad) return {256, 1, false};
   // by expert the tiles are not known, but the rows an expert has, about: 64 experts of 1920 x 1920 in BN 32, 64 and pairs
   // with 16 rows 43, 48 and 63 us, with 64 64, 57 and 64, 32 experts with 128 rows 61, 51 and 41
@@ -208,9 +220,9 @@ Form pick_form(const BlockMm& p, bool tokens_mn, int64_t rows, int64_t sms) {
   for (const Cost& c : costs) {
     const bool pair = c.BN == 256;
     if (tokens_mn && !pair) continue;                    // narrow tiles take the tokens K-major
-    const int64_t tiles = up(p.N, pair ? 256 : 128) * up(p.M, c.BN), room = pair ? sms / 2 : sms;
+    const int64_t tiles = up(p.N, pair ? 256 : 128) * up(p.M, c.BN), room = clusters_at_once(pair ? 2 : 1);
     for (int slices = 1; slices <= (pair ? 2 : 8); slices *= 2) {
-      if (slices > 1 && (tiles * slices > room || slices > kb)) break;
+      if (slices > 1 && (tiles > clusters_at_once((pair ? 2 : 1) * slices) || slices > kb)) break;
       const double t = c.base + (double)up(kb, slices) * (c.first + (double)(up(tiles, room) - 1) * c.next) + (slices == 1 ? 0.0 : pair ? 3.0 : 0.9);
       if (least == 0.0 || t < least) {
         least = t;
@@ -219,9 +231,9 @@ Form pick_form(const BlockMm& p, bool tokens_mn, int64_t rows, int64_t sms) {
     }
   }
   // A last round of tiles that leaves half of the pairs without any goes in two slices, in a launch of its own, where half of
-  // K's blocks take longer than a launch and the slices' exchange: 5760 x 1920 x 8192 (184 tiles for 76 pairs) 150 -> 130 us.
-  const int64_t tiles = up(p.N, 256) * up(p.M, 256), rest = tiles % (sms / 2);
-  best.tail = best.BN == 256 && best.slices == 1 && tiles > sms / 2 && rest > 0 && rest <= sms / 4 - 2 && kb >= 32;
+  // K's blocks take longer than a launch and the slices' exchange: 5760 x 1920 x 8192 (184 tiles for 76 pairs) 150 -> 138 us.
+  const int64_t tiles = up(p.N, 256) * up(p.M, 256), pairs = clusters_at_once(2), rest = tiles % pairs;
+  best.tail = best.BN == 256 && best.slices == 1 && tiles > pairs && rest > 0 && rest <= clusters_at_once(4) && kb >= 32;
   return best;
 }
 
@@ -240,9 +252,9 @@ int run_block_mm(const BlockMm& p, void* workspace, cudaStream_t st) {
     lay_a = lay_out_of(va, ws);
     lay_b = lay_out_of(vb, ws);
   }
-  const int64_t sms = emu_ops_sm_count(), kb = (p.K + kBlock - 1) / kBlock;
+  const int64_t kb = (p.K + kBlock - 1) / kBlock;
   const int64_t groups = wgrad ? p.E : 1;
-  const Form form = pick_form(p, va.mn, rows_of_group, sms);
+  const Form form = pick_form(p, va.mn, rows_of_group);
   const int BN = form.BN, slices = form.slices;
   const bool swap = BN < 256;
   BlockTcParams q = {};
@@ -290,7 +302,7 @@ int run_block_mm(const BlockMm& p, void* workspace, cudaStream_t st) {
   q.from = 0;
   q.to = (int)tiles;
   if (form.tail) {
-    q.to = (int)(tiles - tiles % (sms / 2));
+    q.to = (int)(tiles - tiles % clusters_at_once(2));
     const int rc = launch_tc<256>(q, mode, q.to, maps, work > 0, st);
     if (rc != EMU_OK) return rc;
     q.from = q.to;

@@ -45,3 +45,12 @@ def test_grouped_by_64_tokens(fw, sizes, N, K):
     assert 33 <= -(-T // E) <= 64
     grouped(fw, sizes, N, K, seed=E, dt=DT["bf16"])
     grouped(fw, sizes, N, K, seed=E, block=(ROWS, ROWS), by_k=False)
+
+
+# ------------------------------------------------------------------------------- slices of K
+@pytest.mark.parametrize("M,N,K,by_k", [(16, 1920, 2048, True), (16, 2048, 2048, True), (30, 2432, 4100, True), (9, 4608, 2048, True), (16, 4864, 1024, True),
+                                        (60, 1930, 2048, True), (1000, 2304, 4096, False), (1000, 2400, 4096, False), (250, 9700, 2048, False)])
+def test_few_tiles_in_slices(fw, M, N, K, by_k):
+    """As many tiles as there are clusters of two, four and eight CTAs at once, and a few more."""
+    dense(fw, M, N, K, by_k=(by_k, True), dt=DT["bf16"])
+    dense(fw, M, N, K, by_k=(by_k, True), block=(ROWS, ROWS))
