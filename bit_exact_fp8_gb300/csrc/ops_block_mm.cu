@@ -172,10 +172,13 @@ template <int BN> int launch_tc(const BlockTcParams& p, int mode, int64_t tiles,
 }
 
 // Up to eight tokens of a dense product, K-major on both sides, where latency counts; where bandwidth does, the TMA's
-// deep queues win.  As few and by tcgen05: 1 x 5760 x 1920 4.1 and 8.4 us, 8 x 4096 x 4096 5.4 and 8.3, 8 x 8192 x 2048 6.6 and
-// 8.4, 8 x 16384 x 2048 11.6 and 8.8, 8 x 8192 x 8192 22 and 17; of 16 tokens 8.1 and 8.4.
+// deep queues win, and where a long K does, the slices: eight warps share K's blocks, 0.58 us a round (unaligned 1.5).  In us, so
+// and by tcgen05: 1 x 5760 x 1920 4.2 and 7.4, 8 x 4096 x 4096 5.3 and 7.7, 8 x 4096 x 6144 7.4 and 9.0, 8 x 16384 x 2048 11.5 and 8.8;
+// 8 x 1024 x 8192 7.2 and 6.7, 1 x 2048 x 8192 7.1 and 7.8, 1 x 2304 x 10240 8.3 and 8.7, 8 x 512 x 16384 12.2 and 8.1,
+// 1 x 512 x 32768 21 and 10.5; unaligned 1 x 5760 x 1921 9.7 and 12.9, 1 x 2048 x 6001 11.9 and 13.5, 8 x 512 x 8200 15.3 and
+// 9.5; of 16 tokens 8.1 and 8.4.
 bool few_tokens(int64_t M, int64_t N, int64_t K, const CodesView& va, const CodesView& vb) {
-  return M <= 8 && K > 0 && !va.mn && !vb.mn && N * K <= (int64_t)24 << 20;
+  return M <= 8 && K > 0 && K <= 8192 && !va.mn && !vb.mn && N * K <= (int64_t)24 << 20;
 }
 void run_few_tokens(const BlockMm& p, const CodesView& va, const CodesView& vb, cudaStream_t st) {
   BlockFewParams q = {};

@@ -54,3 +54,9 @@ def test_few_tiles_in_slices(fw, M, N, K, by_k):
     """As many tiles as there are clusters of two, four and eight CTAs at once, and a few more."""
     dense(fw, M, N, K, by_k=(by_k, True), dt=DT["bf16"])
     dense(fw, M, N, K, by_k=(by_k, True), block=(ROWS, ROWS))
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 512, 8192), (8, 300, 8193), (3, 64, 16384), (8, 1000, 12290), (1, 130, 65535), (5, 512, 32768)])
+def test_few_tokens_of_a_long_k(fw, M, N, K):
+    dense(fw, M, N, K, dt=DT["bf16"])
+    dense(fw, M, N, K, block=(ROWS, ROWS), fmt=("e5m2", "e4m3"))
