@@ -5,7 +5,7 @@
 // memory: the order of K within a block is free as long as both sides keep to one, so a quad's lanes take 16
 // contiguous codes each of either half of a row's block, four MMAs' worth together.  The warps of a CTA
 // share out the blocks of K, and their sums meet in shared memory in a fixed order.
-// 1 x 5760 x 1920 in 4.1 us, 2.3 of them the launch (by tcgen05 8.4: its steps are longer).
+// 1 x 5760 x 1920 in 4.2 us, 2.0 of them the launch (by tcgen05 7.4: its steps are longer).
 #pragma once
 #include "ops_block.cuh"
 

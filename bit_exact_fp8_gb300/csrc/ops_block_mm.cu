@@ -206,14 +206,16 @@ void run_few_tokens(const BlockMm& p, const CodesView& va, const CodesView& vb, 
 int64_t up(int64_t n, int64_t d) { return (n + d - 1) / d; }
 // Which tiles: pairs of CTAs on 256 x 256, or 128 of the weights' rows by BN tokens, and of how many slices of K.
 // Measured, in us: a call takes `base`, and each of K's blocks `first` in the first round of tiles and `next` in
-// those after it (where more SMs share the memory); slices 0.9 more, of pairs 3.  As BN 32, 64 and pairs: 64 x 5760 x 1920 6.9, 8.8
-// and 11.4, 128 x 5760 x 1920 10.8, 9.3 and 11.4, 256 x 4096 x 4096 16.2, 15.2 and 18.4, 512 x 5760 x 1920 22.6, 21.5 and
-// 11.9; 64 x 1920 x 5760 10.9 in one slice, 7.6 in four, 777 x 1920 x 5760 in pairs 23.5 and in two slices 18.4.
+// those after it (where more SMs share the memory); slices 0.9 more, of pairs 3.  As BN 32, 64 and pairs: 64 x 5760 x 1920 7.4, 8.9
+// and 11.1, 128 x 5760 x 1920 11.3, 9.5 and 11.5, 256 x 4096 x 4096 17.0, 15.3 and 14.7, 512 x 5760 x 1920 24, 22 and
+// 12.5; 64 x 1920 x 5760 11.3 in one slice, 8.1 in four, 777 x 1920 x 5760 in pairs 24.4 and in two slices 19.1.
 struct Form { int BN, slices; bool tail; };
 Form pick_form(const BlockMm& p, bool tokens_mn, int64_t rows) {
   if (p.kind == BlockKind::wgrad) return {256, 1, false};
-  // by expert the tiles are not known, but the rows an expert has, about: 64 experts of 1920 x 1920 in BN 32, 64 and pairs
-  // with 16 rows 43, 48 and 63 us, with 64 64, 57 and 64, 32 experts with 128 rows 61, 51 and 41
+  // by expert the tiles are not known, but the rows an expert has, about (those behind the last group count as well).  In BN 32, 64
+  // and pairs: 32 experts of 5760 x 1920 with 32 rows each 60, 71 and 88 us, with 64 89, 78 and 89, with 128 167, 132 and 92; 8 of
+  // 1920 x 5760 with 16 20, 21 and 27, with 64 26, 23 and 27, with 128 41, 33 and 29; 16 of 1024 x 1024 with 64 11.0, 9.6 and
+  // 10.5, with 128 17.0, 15.0 and 10.9
   if (p.kind == BlockKind::grouped) return {rows <= 32 ? 32 : rows <= 64 ? 64 : 256, 1, false};
   struct Cost { int BN; double base, first, next; };
   const Cost costs[3] = {{32, 4.7, 0.16, 0.25}, {64, 5.3, 0.22, 0.38}, {256, 5.5, 0.41, 0.49}};

@@ -197,7 +197,7 @@ template <int FMT, int N> __device__ __forceinline__ typename Piece<N>::type cod
 }
 
 // 1 x 128 blocks: 128 / N lanes hold one.  A warp takes UNROLL loads of a row (32 N values each) at a time, all asked for
-// before the first is waited for.  Bound by memory: 8192 x 5760 bf16 in 28 us, 5.1 TB/s.
+// before the first is waited for.  Bound by the instructions around the maxima: 8192 x 5760 bf16 in 27 us, 5.2 TB/s.
 template <class T, bool VEC, int FMT, bool SWIGLU, int UNROLL>
 __global__ void __launch_bounds__(256) block_rows_kernel(const BlockQuantParams p) {
   constexpr int N = Vec<T>::N, LANES = 128 / N, BYTES = N;                // a lane's codes of a load are N bytes
@@ -254,8 +254,8 @@ __global__ void __launch_bounds__(256) block_rows_kernel(const BlockQuantParams 
 }
 
 // 128 x 1 and 128 x 128 blocks: a CTA of 256 threads holds 128 rows x 128 columns in registers, 128 / N threads a row, finds
-// the columns' or the tile's largest magnitudes and writes the codes.  8192 x 5760 bf16: squares in 22 us, 6.4 TB/s (94% of a
-// copy's rate), columns in 27.
+// the columns' or the tile's largest magnitudes and writes the codes.  8192 x 5760 bf16: squares in 23 us, 6.2 TB/s (91% of a
+// copy's rate), columns in 26.
 template <class T, bool VEC, int FMT, bool SWIGLU, bool SQUARE>
 __global__ void __launch_bounds__(256) block_tile_kernel(const BlockQuantParams p) {
   constexpr int N = Vec<T>::N, LANES = 128 / N, ROWS = 256 / LANES, PASSES = 128 / ROWS;
@@ -428,7 +428,7 @@ template <int N> struct KeptCodes {
   }
 };
 
-// Rows at any address: a warp's lanes take a row's neighbouring vectors.  8192 x 5761 bf16 in 120 us.
+// Rows at any address: a warp's lanes take a row's neighbouring vectors.  8192 x 5761 bf16 in 122 us.
 template <class T>
 __global__ void __launch_bounds__(256) swiglu_grad_unaligned_kernel(const SwigluGradParams p) {
   constexpr int N = Vec<T>::N;
@@ -474,8 +474,9 @@ int64_t rows_of_ctas(int64_t wide, int64_t an_sm) {
 template <class T, int FMT, bool SWIGLU> int launch_quant(const BlockQuantParams& p, emu_block_t block, bool vec, cudaStream_t st) {
   const int64_t blocks = (p.H + 127) / 128;
   if (block == EMU_BLOCK_ROWS) {
-    // Loads of a warp at a time, as long as the device is full: 8192 x 5760 bf16 28 us with four, 30 with two, 57 with one;
-    // unaligned 8192 x 5761 57 with two, 63 with four; SwiGLU 83 with two, 100 with one, unaligned 4096 x 5761 70 and 83.
+    // Loads of a warp at a time, as long as the device is full: 8192 x 5760 bf16 27 us with four or two, 39 with one, fp32 42, 48
+    // and 55; unaligned 8192 x 5761 49 with two, 62 with four, 53 with one; SwiGLU 79 with two, 86 with one, unaligned
+    // 4096 x 5761 71 with one, 81 with two.
     constexpr int MANY = SWIGLU ? 2 : 4, SOME = SWIGLU ? 1 : 2;
     const int64_t loads = (p.H + 32 * Vec<T>::N - 1) / (32 * Vec<T>::N);
     const int unroll = p.T * loads < (int64_t)emu_ops_sm_count() * 32 * MANY ? 1 : vec ? MANY : SOME;

@@ -415,7 +415,7 @@ typedef enum { EMU_BLOCK_ROWS = 0, EMU_BLOCK_COLUMNS = 1, EMU_BLOCK_SQUARES = 2 
  *   scale  fp32, contiguous: [T, ceil(H/128)], [ceil(T/128), H] or [ceil(T/128), ceil(H/128)]
  * x / scale is the quotient by the scale as it is returned, rounded to fp32 before it is rounded
  * to 8 bits (ties to even).  A block that holds NaN or Inf has NaN for its scale and all its codes,
- * and touches no other block.  Sizes: T, H < 2^31.
+ * and touches no other block.  Sizes: T < 2^31, H < 2^30.
  */
 int emu_block_quant(const void* x, int64_t ldx, emu_out_t type, int64_t T, int64_t H, emu_block_t block,
                     emu_fp8_t q_format, void* q, float* scale, void* stream);
