@@ -401,7 +401,7 @@ __global__ void __launch_bounds__(256, 8) swiglu_grad_kernel(const SwigluGradPar
     float gy[N], g[N], u[N];
     load_f<T, N>(static_cast<const T*>(p.gy) + row * p.ldy + col, gy);
     const float* const s = p.kept_scale + row * 2 * blocks + col / 128;
-    uint32_t wg[N / 4], wu[N / 4];
+    alignas(N) uint32_t wg[N / 4], wu[N / 4];
     *reinterpret_cast<typename Piece<N>::type*>(wg) = *reinterpret_cast<const typename Piece<N>::type*>(p.kept + row * 2 * p.H + col);
     *reinterpret_cast<typename Piece<N>::type*>(wu) = *reinterpret_cast<const typename Piece<N>::type*>(p.kept + row * 2 * p.H + p.H + col);
     values_of_codes<N>(wg, s[0], g);
