@@ -30,7 +30,7 @@ def ragged(seed, experts, average):
 
 @pytest.mark.parametrize("sizes", [ragged(1, 12, 230), ragged(2, 30, 150), [1500, 0, 5, 900]])
 @pytest.mark.parametrize("N,K", [(2048, 1024), (2100, 1111)])
-def test_grouped_pairs_in_rounds(fw, sizes, N, K):
+def test_grouped_pairs_large(fw, sizes, N, K):
     """More tiles of 256 x 256 than there are pairs of CTAs."""
     assert sum(-(-s // 256) for s in sizes) * -(-N // 256) > 76
     grouped(fw, sizes, N, K, dt=DT["bf16"], rest=300)
@@ -39,14 +39,14 @@ def test_grouped_pairs_in_rounds(fw, sizes, N, K):
 
 @pytest.mark.parametrize("sizes", [ragged(3, 8, 300), [1000, 0, 77]])
 @pytest.mark.parametrize("block", [COLUMNS, SQUARES])
-def test_wgrad_in_rounds(fw, sizes, block):
+def test_wgrad_large(fw, sizes, block):
     wgrad(fw, sizes, 1000, 1920, block=(block, block))
     wgrad(fw, sizes, 1040, 1300, block=(block, block), dt=DT["bf16"], rest=40)
 
 
 @pytest.mark.parametrize("dt", DT)
 @pytest.mark.parametrize("T,H", [(8192, 5760), (8192, 5761), (5000, 8200)])
-def test_quant_in_rounds(fw, dt, T, H):
+def test_quant_large(fw, dt, T, H):
     x = values(gen(H), T, H, DT[dt]).clamp(-6e4, 6e4)
     for block, fmt in ((ROWS, "e4m3"), (ROWS, "e5m2"), (COLUMNS, "e4m3"), (SQUARES, "e5m2")):
         r = fw.block_quant(x, block=block, out_dtype=QT[fmt])
@@ -61,7 +61,7 @@ def test_quant_in_rounds(fw, dt, T, H):
 @pytest.mark.parametrize("dt", DT)
 @pytest.mark.parametrize("T,H", [(8192, 2880), (8192, 2881), (3000, 8200)])
 @pytest.mark.parametrize("block", [ROWS, SQUARES])
-def test_swiglu_in_rounds(fw, dt, T, H, block):
+def test_swiglu_large(fw, dt, T, H, block):
     x = gates(gen(H), T, H, DT[dt])
     r = fw.swiglu_quant(x, block=block, checkpoint=True)
     n = blocks(H)
@@ -79,7 +79,7 @@ def test_swiglu_in_rounds(fw, dt, T, H, block):
 
 @pytest.mark.parametrize("dt", DT)
 @pytest.mark.parametrize("T,H", [(8192, 5760), (8192, 5761), (40000, 264), (40000, 265)])
-def test_swiglu_backward_in_rounds(fw, dt, T, H):
+def test_swiglu_backward_large(fw, dt, T, H):
     g = gen(H)
     kept, _ = operand(g, (T, 2 * H), ROWS)
     n = blocks(H)
